@@ -31,7 +31,12 @@ EXPORTS = ("vq_kivi_quantize", "vq_kivi_quantize_ex", "vq_kivi_append",
            "vq_kivi_cache_bytes", "vq_kivi_set_split_tokens",
            "vq_kivi_launch_count", "vq_kivi_decode_attend_static",
            "vq_kivi_device_status", "vq_kivi_decode_kernel",
-           "vq_kivi_debug_fail_chunk")
+           "vq_kivi_debug_fail_chunk", "vq_kivi_norm_rope",
+           "vq_kivi_paged_pool_bytes", "vq_kivi_paged_workspace_bytes",
+           "vq_kivi_paged_append", "vq_kivi_paged_attend",
+           "vq_kivi_paged_dequantize", "vq_kivi_paged_status")
+
+F16, BF16, F32 = 0, 1, 2
 
 
 class VqError(RuntimeError):
@@ -62,6 +67,32 @@ class Bytes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in
                 ("code_bytes", "meta_bytes", "residual_bytes", "fp16_bytes",
                  "sink_bytes", "value_fp16_bytes")]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("H_q", "H_kv", "D", "group", "page", "n_pages")] + \
+               [("pool", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -112,6 +143,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.vq_kivi_decode_attend_static.argtypes = [
             ctypes.POINTER(Params), ctypes.POINTER(Planes), P, P, P,
             ctypes.c_float, P]
+        PG, PB = ctypes.POINTER(Paged), ctypes.POINTER(PagedBatch)
+        RW, RP = ctypes.POINTER(Rows), ctypes.POINTER(RopeSpec)
+        f32, cint = ctypes.c_float, ctypes.c_int
+        L.vq_kivi_norm_rope.argtypes = [cint, i64, cint, RW, RW, RP, P, cint, i64, f32, P]
+        L.vq_kivi_paged_pool_bytes.restype = ctypes.c_size_t
+        L.vq_kivi_paged_pool_bytes.argtypes = [PG]
+        L.vq_kivi_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.vq_kivi_paged_workspace_bytes.argtypes = [PG, i32, i32]
+        L.vq_kivi_paged_append.argtypes = [PG, PB, cint, RW, RW, RW, RP, P, cint, i64, f32, P]
+        L.vq_kivi_paged_attend.argtypes = [PG, PB, cint, RW, i32, f32, P, ctypes.c_size_t, P]
+        L.vq_kivi_paged_dequantize.argtypes = [PG, PB, P, P, P]
+        L.vq_kivi_paged_status.argtypes = [PG, P]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
         L.vq_kivi_plane_bytes.restype = ctypes.c_size_t

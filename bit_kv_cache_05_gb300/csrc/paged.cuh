@@ -1,0 +1,136 @@
+// The paged 4-bit cache: layout, what a call says about its batch, and the
+// launchers of its operators.
+//
+// Pool: [n_pages][H_kv][page / 16][block], a block holding 16 tokens of one kv
+// head in one contiguous run of 16 D + 128 D / g bytes (2560 at D = 128,
+// g = 32), so that one bulk copy brings everything an attention step needs:
+//   key codes    16 rows of D / 2 bytes; word (D / 32) t + i of a row (t < 4)
+//                holds channels 32 i + 8 t ... + 7, lowest nibble first
+//   key meta     per token pair (2 p, 2 p + 1) and group: s, s', z, z' (fp16)
+//   value codes  word ((8 h + n) 4 + t) (D / 32) + i: channels 32 i + 4 n ... + 3
+//                of token 8 h + 2 t in the low half, of the next in the high half
+//   value meta   as key meta
+// In these orders lane (n = lane / 4, t = lane % 4) of a warp finds its
+// operands of mma.m16n8k16 in consecutive words: for the scores the codes of
+// token n (B fragments, one 16-byte load per 8 tokens at D = 128), for the
+// output the channel quads 4 n of its two token pairs.  Two neighbouring
+// 16-bit halves of a word shifted by 4 r always form one fp16 pair.
+//
+// A stored value stands for fp16(code * s + z), rounded once: what the
+// attention kernels multiply and vq_kivi_paged_dequantize returns.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rope.cuh"
+#include "vq_kivi.h"
+
+namespace vqk {
+
+constexpr int kMaxSeqs = 1024;   // sequences of one paged call
+constexpr int kBlk = 16;         // tokens of a block
+
+// status bits (device word)
+constexpr unsigned kBadPage = 1u;     // a block table entry outside the pool
+constexpr unsigned kBadLength = 2u;   // lens / cu_new outside their ranges
+constexpr unsigned kGaveUp = 4u;      // a bounded wait ran out
+
+__host__ __device__ constexpr int paged_meta_bytes(int D, int g) { return 64 * (D / g); }
+__host__ __device__ constexpr int paged_block_bytes(int D, int g) {
+  return 2 * (8 * D + paged_meta_bytes(D, g));
+}
+
+// bytes into a block: key codes, key meta, value codes, value meta
+__host__ __device__ constexpr int off_km(int D) { return 8 * D; }
+__host__ __device__ constexpr int off_vc(int D, int g) { return 8 * D + paged_meta_bytes(D, g); }
+__host__ __device__ constexpr int off_vm(int D, int g) {
+  return 16 * D + paged_meta_bytes(D, g);
+}
+
+struct PagedArgs {
+  uint8_t *pool;
+  unsigned *status;
+  const int32_t *table;      // [B][max_pages]
+  const int32_t *lens;       // [B] tokens of each sequence, the new ones among them
+  const int32_t *cu;         // [B + 1] offsets of the new tokens, nullptr: one each
+  int64_t table_stride;
+  int64_t tokens;            // new tokens the token tensors have room for
+  int n_pages, page_log2, max_pages, B;
+  int H_q, H_kv, g;
+};
+
+// sequence of new token i and its place in the sequence (-1: not in the
+// cache): the new tokens of a sequence are its last ones
+struct Place {
+  int b, pos;
+};
+
+__device__ __forceinline__ Place find_place(const PagedArgs &a, int64_t i) {
+  if (!a.cu) {
+    const int len = a.lens[i];
+    if (len < 0 || len > ((int64_t)a.max_pages << a.page_log2)) {
+      atomicOr(a.status, kBadLength);
+      return Place{(int)i, -1};
+    }
+    return Place{(int)i, len - 1};
+  }
+  if (i < a.cu[0] || i >= a.cu[a.B]) return Place{-1, -1};
+  int lo = 0, hi = a.B;   // cu[lo] <= i < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= i) lo = mid; else hi = mid;
+  }
+  const int len = a.lens[lo];
+  if (len < 0 || len > ((int64_t)a.max_pages << a.page_log2)) {
+    atomicOr(a.status, kBadLength);
+    return Place{lo, -1};
+  }
+  const int pos = len - (a.cu[hi] - (int)i);
+  return Place{lo, pos < 0 ? -1 : pos};
+}
+
+// the block of kv head h that holds position pos of sequence b, nullptr (and
+// the status bit) when its page is not one of the pool
+__device__ __forceinline__ uint8_t *find_block(const PagedArgs &a, int b, int pos, int h,
+                                               int block_bytes) {
+  const int p = a.table[(int64_t)b * a.table_stride + (pos >> a.page_log2)];
+  if ((unsigned)p >= (unsigned)a.n_pages) {
+    atomicOr(a.status, kBadPage);
+    return nullptr;
+  }
+  const int in = (pos & ((1 << a.page_log2) - 1)) >> 4;
+  return a.pool + ((((int64_t)p * a.H_kv + h) << (a.page_log2 - 4)) + in) * block_bytes;
+}
+
+cudaError_t launch_norm_rope(int dtype, const HeadRows &q, const HeadRows &k,
+                             const RopeArgs &r, int D, int64_t tokens, float eps,
+                             int sm_count, cudaStream_t st);
+cudaError_t launch_paged_append(int dtype, const PagedArgs &a, const HeadRows &q,
+                                const HeadRows &k, const HeadRows &v, const RopeArgs &r,
+                                bool rotate_by_place, int D, float eps, int sm_count,
+                                cudaStream_t st);
+cudaError_t launch_paged_dequantize(const PagedArgs &a, __half *K, __half *V, int D,
+                                    int sm_count, cudaStream_t st);
+
+struct PagedAttend {
+  const void *q;
+  void *out;
+  int64_t q_token, q_head;   // element strides; out is [tokens][H_q][D]
+  float scale;
+  int max_new;               // no sequence has more new tokens
+  float *ws;                 // workspace
+};
+
+// few rows: up to 8 (new token, query head) pairs per kv head
+size_t paged_decode_ws(int B, int H_kv, int D, int rows, int sm_count);
+cudaError_t launch_paged_decode(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
+                                int sm_count, cudaStream_t st);
+// any number of new tokens
+size_t paged_chunk_ws(int B, int H_kv, int D, int sm_count);
+cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
+                               int sm_count, cudaStream_t st);
+
+}  // namespace vqk

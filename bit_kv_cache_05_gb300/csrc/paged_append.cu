@@ -1,0 +1,298 @@
+// Append to the paged 4-bit cache with the norms and the rotation on the way
+// (vq_kivi_paged_append), and the stored tokens read back
+// (vq_kivi_paged_dequantize).
+//
+// Per new token: queries normed, rotated and written out; keys normed,
+// rotated, rounded to fp16 and quantized; values rounded to fp16 and
+// quantized.  Groups of g channels of one token, as the value groups of the
+// contiguous cache: scale = (max - min) / 15 and code = rint((x - min) /
+// scale) in fp32, scale and min stored in fp16.
+//
+// LPR = D / 16 lanes hold a row.  A rotated key row passes through shared
+// memory so that its lanes hold 16 neighbouring channels, as a value row's
+// do: a group is then g / 16 neighbouring lanes, whatever the rotation.
+#include "paged.cuh"
+#include "vqk_internal.cuh"
+
+namespace vqk {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr unsigned kFull = 0xffffffffu;
+
+// fp16 of x; values beyond the type's range (infinities too) become its
+// largest, NaN stays NaN
+__device__ __forceinline__ __half to_half_sat(float x) {
+  const float y = fminf(fmaxf(x, -65504.f), 65504.f);
+  return __float2half_rn(x != x ? x : y);
+}
+
+// One row's 16 neighbouring channels x per lane, quantized and stored in the
+// block `blk` (nullptr: not stored) at token tl.  `poison`: the token's key or
+// value row holds a NaN.  A key row then gets NaN zeros, so that the scores
+// of every query that sees the token are NaN; a value row is stored as
+// zeros, because a masked token's weight of 0 times NaN would reach rows
+// that do not see it.
+template <int D, bool VALUES>
+__device__ __forceinline__ void quantize_row(const float (&x)[16], int g, int l, bool poison,
+                                             uint8_t *blk, int tl) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int e = 1; e < 16; ++e) {
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+  }
+  for (int o = 1; o < (g >> 4); o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+  }
+  if (!blk) return;
+  lo += 0.f;                                  // -0 to +0
+  const float scale = (hi - lo) / 15.f;
+  uint32_t w[2] = {0u, 0u};
+  if (scale > 0.f && !poison) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float t = fminf(fmaxf(rintf((x[e] - lo) / scale), 0.f), 15.f);
+      w[e >> 3] |= (uint32_t)(int)t << (4 * (e & 7));
+    }
+  }
+  __half s = __float2half_rn(scale), z = __float2half_rn(lo);
+  // code 15 must stay inside fp16's range (it rounds to infinity from 65520)
+  if (fmaf(15.f, __half2float(s), lo) >= 65520.f)
+    s = __ushort_as_half((unsigned short)(__half_as_ushort(s) - 1));
+  if (poison) {
+    s = __float2half_rn(0.f);
+    z = VALUES ? s : __ushort_as_half((unsigned short)0x7fff);
+  }
+  constexpr int I = D / 32;
+  if (VALUES) {
+    // quads 4 (l % 2) ... + 3 of the 32-channel span l / 2
+    uint8_t *p = blk + off_vc(D, g) + 2 * (tl & 1) +
+                 4 * (((8 * (tl >> 3) + 4 * (l & 1)) * 4 + ((tl & 7) >> 1)) * I + (l >> 1));
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      *reinterpret_cast<uint16_t *>(p + 16 * I * n) =
+          (uint16_t)(w[n >> 1] >> (16 * (n & 1)));
+  } else {
+    // words 2 l and 2 l + 1 of the row: span l / 2, quarter 2 (l % 2) and next
+    uint32_t *p = reinterpret_cast<uint32_t *>(blk + tl * (D / 2)) + 2 * (l & 1) * I + (l >> 1);
+    p[0] = w[0];
+    p[I] = w[1];
+  }
+  if ((l & ((g >> 4) - 1)) == 0) {
+    __half *m = reinterpret_cast<__half *>(blk + (VALUES ? off_vm(D, g) : off_km(D))) +
+                ((tl >> 1) * (D / g) + 16 * l / g) * 4 + (tl & 1);
+    m[0] = s;
+    m[2] = z;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
+               bool rotate_by_place, float eps, int parts) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  __shared__ __align__(16) __half rows[kThreads / 32][RPW][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR, l = lane % LPR;
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  const int64_t t = w / parts;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (t >= a.tokens) return;
+  const Place at = find_place(a, t);
+  if (at.pos < 0) return;
+  int p0, p1;
+  chunk_places(r, l, p0, p1);
+  float c[8], s[8];
+  rope_angles<LPR>(r, [&](int ax) -> long long {
+    if (rotate_by_place) return at.pos;
+    const int64_t i = (int64_t)ax * r.pos_stride + t;
+    return r.pos64 ? static_cast<const long long *>(r.pos)[i]
+                   : (long long)static_cast<const int *>(r.pos)[i];
+  }, lane, c, s);
+
+  const int gq = (q.heads + RPW - 1) / RPW, gk = (a.H_kv + RPW - 1) / RPW;
+  for (int gi = (int)(w % parts); gi < gq + gk; gi += parts) {
+    const bool isk = gi >= gq;
+    const HeadRows &h = isk ? k : q;
+    const int row = (isk ? gi - gq : gi) * RPW + sub;
+    const bool valid = row < h.heads;
+    uint4 na[1] = {}, nb[1] = {};
+    float x0[8], x1[8];
+    if (valid) {
+      const T *x = static_cast<const T *>(h.x) + t * h.x_token + row * h.x_head;
+      load8<T>(x + p0, na);
+      load8<T>(x + p1, nb);
+    }
+    unpack8<T>(na, x0);
+    unpack8<T>(nb, x1);
+    float y[16];
+    if (isk) {
+      uint4 va[1] = {}, vb[1] = {};
+      if (valid) {
+        const T *x = static_cast<const T *>(v.x) + t * v.x_token + row * v.x_head + 16 * l;
+        load8<T>(x, va);
+        load8<T>(x + 8, vb);
+      }
+      float y0[8], y1[8];
+      unpack8<T>(va, y0);
+      unpack8<T>(vb, y1);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = __half2float(to_half_sat(y0[e]));
+        y[8 + e] = __half2float(to_half_sat(y1[e]));
+      }
+    }
+    if (h.weight) {
+      uint4 wa[1], wb[1];
+      float w0[8], w1[8];
+      load8<T>(static_cast<const T *>(h.weight) + p0, wa);
+      load8<T>(static_cast<const T *>(h.weight) + p1, wb);
+      unpack8<T>(wa, w0);
+      unpack8<T>(wb, w1);
+      norm_row<LPR>(x0, x1, w0, w1, D, eps);
+    }
+    if (8 * l < r.half) rotate_row(r.interleaved, c, s, x0, x1);
+    if (!isk) {
+      if (valid) {
+        T *o = static_cast<T *>(q.out) + t * q.out_token + row * q.out_head;
+        store8<T>(o + p0, x0);
+        store8<T>(o + p1, x1);
+      }
+      continue;
+    }
+    // the key row's lanes change from rotated pairs to neighbouring channels
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x0[e] = __half2float(to_half_sat(x0[e]));
+      x1[e] = __half2float(to_half_sat(x1[e]));
+    }
+    __syncwarp();
+    store8<__half>(&rows[warp][sub][p0], x0);
+    store8<__half>(&rows[warp][sub][p1], x1);
+    __syncwarp();
+    uint4 ka[1], kb[1];
+    load8<__half>(&rows[warp][sub][16 * l], ka);
+    load8<__half>(&rows[warp][sub][16 * l + 8], kb);
+    unpack8<__half>(ka, x0);
+    unpack8<__half>(kb, x1);
+    float x[16];
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = x0[e];
+      x[8 + e] = x1[e];
+      nan = nan || x0[e] != x0[e] || x1[e] != x1[e] || y[e] != y[e] || y[8 + e] != y[8 + e];
+    }
+    const unsigned mask = ((1u << LPR) - 1u) << (sub * LPR);
+    const bool poison = (__ballot_sync(kFull, nan) & mask) != 0u;
+    uint8_t *blk = valid ? find_block(a, at.b, at.pos, row, paged_block_bytes(D, a.g)) : nullptr;
+    quantize_row<D, false>(x, a.g, l, poison, blk, at.pos & 15);
+    quantize_row<D, true>(y, a.g, l, poison, blk, at.pos & 15);
+  }
+}
+
+// 8 codes in fp16 times s plus z, each rounded once; words of four
+// neighbouring nibbles per half (see paged.cuh)
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+k_paged_dequantize(PagedArgs a, __half *K, __half *V, int parts) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR, I = D / 32;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = w / parts;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (t >= a.tokens) return;
+  const Place at = find_place(a, t);
+  if (at.pos < 0) return;
+  const int tl = at.pos & 15;
+  for (int row = (int)(w % parts) * RPW + sub; row < a.H_kv; row += parts * RPW) {
+    const uint8_t *blk = find_block(a, at.b, at.pos, row, paged_block_bytes(D, a.g));
+    if (!blk) continue;
+#pragma unroll
+    for (int values = 0; values < 2; ++values) {
+      uint32_t x[2];
+      if (values) {
+        const uint8_t *p = blk + off_vc(D, a.g) + 2 * (tl & 1) +
+                           4 * (((8 * (tl >> 3) + 4 * (l & 1)) * 4 + ((tl & 7) >> 1)) * I +
+                                (l >> 1));
+        uint32_t u[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) u[n] = *reinterpret_cast<const uint16_t *>(p + 16 * I * n);
+        x[0] = u[0] | (u[1] << 16);
+        x[1] = u[2] | (u[3] << 16);
+      } else {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(blk + tl * (D / 2)) +
+                            2 * (l & 1) * I + (l >> 1);
+        x[0] = p[0];
+        x[1] = p[I];
+      }
+      const __half *m = reinterpret_cast<const __half *>(
+                            blk + (values ? off_vm(D, a.g) : off_km(D))) +
+                        ((tl >> 1) * (D / a.g) + 16 * l / a.g) * 4 + (tl & 1);
+      const __half s = m[0], z = m[2];
+      __half2 o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = x[e >> 2] >> (8 * (e & 3));
+        o[e] = __halves2half2(__hfma(__ushort2half_rn(u & 15u), s, z),
+                              __hfma(__ushort2half_rn((u >> 4) & 15u), s, z));
+      }
+      uint4 *dst = reinterpret_cast<uint4 *>((values ? V : K) + (t * a.H_kv + row) * D + 16 * l);
+      dst[0] = reinterpret_cast<const uint4 *>(o)[0];
+      dst[1] = reinterpret_cast<const uint4 *>(o)[1];
+    }
+  }
+}
+
+// warps per token: enough for about 16 per SM, at most one per row group
+int parts_for(int64_t tokens, int groups, int sm_count) {
+  int64_t p = (int64_t)sm_count * 16 / (tokens > 0 ? tokens : 1);
+  return (int)(p < 1 ? 1 : (p > groups ? groups : p));
+}
+
+template <typename T, int D>
+cudaError_t launch_append(const PagedArgs &a, const HeadRows &q, const HeadRows &k,
+                          const HeadRows &v, const RopeArgs &r, bool by_place, float eps,
+                          int sm_count, cudaStream_t st) {
+  constexpr int RPW = 32 / (D / 16);
+  const int groups = (q.heads + RPW - 1) / RPW + (a.H_kv + RPW - 1) / RPW;
+  const int parts = parts_for(a.tokens, groups, sm_count);
+  const int64_t wpc = kThreads / 32;
+  cudaError_t e = launch_pdl(k_paged_append<T, D>,
+                             dim3((unsigned)((a.tokens * parts + wpc - 1) / wpc)),
+                             dim3(kThreads), 0, st, a, q, k, v, r, by_place, eps, parts);
+  count_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(int dtype, const PagedArgs &a, const HeadRows &q,
+                                const HeadRows &k, const HeadRows &v, const RopeArgs &r,
+                                bool by_place, int D, float eps, int sm_count,
+                                cudaStream_t st) {
+  if (dtype == VQ_F16)
+    return D == 64 ? launch_append<__half, 64>(a, q, k, v, r, by_place, eps, sm_count, st)
+                   : launch_append<__half, 128>(a, q, k, v, r, by_place, eps, sm_count, st);
+  return D == 64
+             ? launch_append<__nv_bfloat16, 64>(a, q, k, v, r, by_place, eps, sm_count, st)
+             : launch_append<__nv_bfloat16, 128>(a, q, k, v, r, by_place, eps, sm_count, st);
+}
+
+cudaError_t launch_paged_dequantize(const PagedArgs &a, __half *K, __half *V, int D,
+                                    int sm_count, cudaStream_t st) {
+  const int rpw = 512 / D, parts = parts_for(a.tokens, (a.H_kv + rpw - 1) / rpw, sm_count);
+  const int64_t wpc = kThreads / 32;
+  const dim3 grid((unsigned)((a.tokens * parts + wpc - 1) / wpc));
+  cudaError_t e = D == 64 ? launch_pdl(k_paged_dequantize<64>, grid, dim3(kThreads), 0, st, a,
+                                       K, V, parts)
+                          : launch_pdl(k_paged_dequantize<128>, grid, dim3(kThreads), 0, st, a,
+                                       K, V, parts);
+  count_launch();
+  return e;
+}
+
+}  // namespace vqk

@@ -390,6 +390,175 @@ int vq_kivi_decode_attend_static(const vq_kivi_params *p,
                                  float *out, float softmax_scale,
                                  void *stream);
 
+/* ---- norm and rotation of query and key heads --------------------------- */
+
+/* The step before the cache: RMS norm over each head and the rotation by
+ * position (the caches take keys as the attention uses them).  The pages have
+ * no counterpart; any model with per-head norms or rotary positions calls it
+ * before vq_kivi_append, vq_kivi_decode_attend or vq_kivi_attend_multi, and
+ * vq_kivi_paged_append below does the same on the way into its pages. */
+#define VQ_F16 0
+#define VQ_BF16 1
+#define VQ_F32 2
+
+/* Rotation: pair j of a head turns by position * frequency j.
+ *   rot_dim      rotated channels, a multiple of 16 in [0, D]; the channels
+ *                behind them pass through
+ *   interleaved  0: pairs (j, j + rot_dim/2); else pairs (2 j, 2 j + 1)
+ *   n_axes       1 ... 4 rows of positions (time, height, width, ...)
+ *   scale        factor of cosine and sine (1 for a plain rotation)
+ *   turns        device uint64[rot_dim/2]: frequency j in turns per position
+ *                (radians / 2 pi), times 2^64, rounded; the angle of any
+ *                position is then exact to position * 2^-65 turns
+ *   axis         device uint8[rot_dim/2]: the axis of each pair, each below
+ *                n_axes; may be NULL when n_axes is 1 */
+typedef struct vq_kivi_rope {
+  int32_t rot_dim, interleaved, n_axes;
+  float scale;
+  const void *turns;
+  const void *axis;
+} vq_kivi_rope;
+
+/* Heads of a batch of tokens: element (token, head, channel) at x[token *
+ * x_token + head * x_head + channel].  Pointers 16-byte aligned, strides
+ * multiples of 16 bytes.  out and its strides: where an entry point writes.
+ * weight: device [D] in the rows' type, or NULL for no norm. */
+typedef struct vq_kivi_rows {
+  const void *x;
+  void *out;
+  const void *weight;
+  int64_t x_token, x_head, out_token, out_head;
+  int32_t heads;
+} vq_kivi_rows;
+
+/* out = R(position) (x * rsqrt(mean x^2 + eps) * weight) for each token and
+ * head of q and k, in fp32, rounded once; one kernel for both.
+ *   dtype      VQ_F16, VQ_BF16 or VQ_F32 (rows and weights)
+ *   D          head dimension, a multiple of 16, at most 256
+ *   k          NULL for queries alone
+ *   rope       NULL for the norms alone (positions are then not read)
+ *   positions  device int32 (positions_64 = 0) or int64 [n_axes][tokens],
+ *              positions_stride elements between axes; any sign
+ * out may be x itself with the same strides; other overlaps are not
+ * allowed. */
+int vq_kivi_norm_rope(int dtype, int64_t tokens, int D, const vq_kivi_rows *q,
+                      const vq_kivi_rows *k, const vq_kivi_rope *rope,
+                      const void *positions, int positions_64,
+                      int64_t positions_stride, float eps, void *stream);
+
+/* ---- paged 4-bit cache --------------------------------------------------- */
+
+/* A cache whose pages the caller hands out: one pool for all sequences, a
+ * block table per sequence, lengths in device memory.  Nothing is kept on the
+ * host, so every call can be captured into a graph and follows the lengths
+ * and tables that it finds when it runs.  Keys and values are quantized per
+ * token in 4 bits over groups of g channels with the quantizer above (scale =
+ * (max - min) / 15, code = rint((x - min) / scale), fp32; scale and min
+ * stored in fp16; where code 15 would leave fp16's range the scale stored is
+ * the next smaller one), after rounding to fp16 (values beyond its range,
+ * infinities too, become its largest).  A stored value stands for
+ * fp16(code * scale + min), rounded once.  A NaN in a token's key or value
+ * row makes the scores of every query that sees the token NaN, and touches no
+ * other row.
+ *   D       64 or 128
+ *   group   32, 64 or 128, at most D
+ *   page    tokens of a page: a power of two, 16 ... 1024
+ *   H_q     a multiple of H_kv, at most 8 H_kv
+ *   pool    device, vq_kivi_paged_pool_bytes, 16-byte aligned, owned by the
+ *           caller: uint8 [n_pages][H_kv][page/16][block].  A block holds 16
+ *           tokens: key codes, key (scale, min), value codes, value (scale,
+ *           min).  Key codes: 16 rows of D/8 words; word (D/32) t + i (t < 4)
+ *           holds channels 32 i + 8 t ... + 7, the lowest nibble first.  Value
+ *           codes: word ((8 h + n) 4 + t) (D/32) + i holds channels 32 i + 4 n
+ *           ... + 3 of token 8 h + 2 t in its low half and of the next token
+ *           in its high half.  (scale, min): fp16, per token pair and group
+ *           s, s', m, m'.
+ *   status  device uint32, zeroed by the caller once: set by kernels, read by
+ *           vq_kivi_paged_status
+ * Slots that hold no token may hold anything. */
+typedef struct vq_kivi_paged {
+  int32_t H_q, H_kv, D, group, page, n_pages;
+  void *pool;
+  void *status;
+} vq_kivi_paged;
+
+/* The sequences of a call.  The new tokens of sequence b are its last ones:
+ * with n_b = cu_new[b + 1] - cu_new[b] new tokens, row cu_new[b] + i of a
+ * token tensor is position lens[b] - n_b + i.
+ *   table    device int32 [B][max_pages], table_stride elements a row: page of
+ *            positions page * j ... in entry j.  Entries behind a sequence's
+ *            last page are not read.
+ *   lens     device int32 [B]: tokens with the new ones, at most max_pages *
+ *            page
+ *   cu_new   device int32 [B + 1], not decreasing, or NULL: one new token per
+ *            sequence (row b; tokens = B)
+ *   tokens   rows of the token tensors, at least cu_new[B]; rows behind
+ *            cu_new[B] are neither read nor written
+ * B <= 1024.  A new token at a negative position (lens[b] < n_b: padding) is
+ * not in the cache: it is not stored and its attention row is zero.  A page
+ * outside the pool or a length outside its range is left out and reported by
+ * vq_kivi_paged_status.  No two new tokens of an append may share a place. */
+typedef struct vq_kivi_paged_batch {
+  int32_t B, max_pages;
+  const int32_t *table;
+  int64_t table_stride;
+  const int32_t *lens;
+  const int32_t *cu_new;
+  int64_t tokens;
+} vq_kivi_paged_batch;
+
+/* Bytes of a cache's pool (0 for parameters that are not supported; the
+ * pool, status and n_pages >= 1 need not be valid otherwise). */
+size_t vq_kivi_paged_pool_bytes(const vq_kivi_paged *p);
+
+/* Bytes of workspace that vq_kivi_paged_attend needs on the current device
+ * for B sequences of at most max_new new tokens (0 on an error).  The
+ * workspace need not be zeroed, keeps nothing between calls, and must not be
+ * shared by calls that may overlap. */
+size_t vq_kivi_paged_workspace_bytes(const vq_kivi_paged *p, int32_t B,
+                                     int32_t max_new);
+
+/* Append: the new tokens' keys are normed (k->weight, or NULL) and rotated
+ * (rope, or NULL) in fp32 and quantized into their pages, the values
+ * quantized; the queries (q, or NULL) are normed, rotated and written to
+ * q->out in the same kernel.
+ *   dtype       VQ_F16 or VQ_BF16, of q, k, v and the weights
+ *   positions   as vq_kivi_norm_rope, [n_axes][tokens]; NULL: a token's place
+ *               in its sequence, on every axis */
+int vq_kivi_paged_append(const vq_kivi_paged *p,
+                         const vq_kivi_paged_batch *batch, int dtype,
+                         const vq_kivi_rows *q, const vq_kivi_rows *k,
+                         const vq_kivi_rows *v, const vq_kivi_rope *rope,
+                         const void *positions, int positions_64,
+                         int64_t positions_stride, float eps, void *stream);
+
+/* Attention of the new tokens (already appended) over their sequences, each
+ * seeing the positions up to its own: decode with one new token, drafts and
+ * prompt chunks with several.
+ *   q              rows [tokens][H_q][D]; out contiguous, in q's type
+ *   max_new        no sequence has more new tokens (1 without cu_new); up to
+ *                  8 (token, query head) pairs per kv head are served by the
+ *                  split-KV kernel, more by the tensor-memory kernel
+ *   softmax_scale  <= 0 selects 1/sqrt(D)
+ *   workspace      device, 16-byte aligned */
+int vq_kivi_paged_attend(const vq_kivi_paged *p,
+                         const vq_kivi_paged_batch *batch, int dtype,
+                         const vq_kivi_rows *q, int32_t max_new,
+                         float softmax_scale, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* The new tokens' rows as the values that the cache stands for: fp16
+ * [tokens][H_kv][D], 16-byte aligned.  Rows of tokens that are not in the
+ * cache are not written. */
+int vq_kivi_paged_dequantize(const vq_kivi_paged *p,
+                             const vq_kivi_paged_batch *batch, void *K_hat,
+                             void *V_hat, void *stream);
+
+/* Synchronizes `stream` and reports what kernels found since the last check:
+ * VQ_ERR_ARG for a page or a length outside its range, VQ_ERR_CUDA for a wait
+ * that gave up (the word is then cleared). */
+int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
