@@ -105,6 +105,11 @@ __device__ __forceinline__ uint8_t *find_block(const PagedArgs &a, int b, int po
   return a.pool + ((((int64_t)p * a.H_kv + h) << (a.page_log2 - 4)) + in) * block_bytes;
 }
 
+// The operators wait for the stream's previous kernel before they read
+// anything.  Those whose outputs a caller sees do not release their
+// dependents early: the contiguous cache's append loads its input rows before
+// its own programmatic wait, and those rows may come from norm_rope or from
+// the read-back.  Only the attention kernels release their merges early.
 cudaError_t launch_norm_rope(int dtype, const HeadRows &q, const HeadRows &k,
                              const RopeArgs &r, int D, int64_t tokens, float eps,
                              int sm_count, cudaStream_t st);

@@ -98,7 +98,6 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
   const int64_t t = w / parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   if (t >= a.tokens) return;
   const Place at = find_place(a, t);
   if (at.pos < 0) return;
@@ -203,7 +202,6 @@ k_paged_dequantize(PagedArgs a, __half *K, __half *V, int parts) {
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   if (t >= a.tokens) return;
   const Place at = find_place(a, t);
   if (at.pos < 0) return;

@@ -1,93 +1,909 @@
 // Causal attention of any number of new tokens over the paged 4-bit cache
-// (vq_kivi_paged_attend): one warp per (new token, query head), lanes over
-// channels, one key at a time, an online softmax in fp32.
+// (vq_kivi_paged_attend), on tcgen05 with tensor-memory accumulators.
+//
+//   out = sum_t softmax_t(scale q.k_hat_t) v_hat_t,  t <= the row's own token
+//
+// Rows: 128 (new token, query head) pairs of a kv head make a query tile, two
+// tiles a pair; a pair shares the keys that it walks, 128 at a time.  The
+// work is one line of key tiles over (sequence, kv head, pair, key tile), cut
+// evenly among one CTA per SM whatever the lengths, so no plan on the host; a
+// pair that is cut leaves partial rows, which a second kernel merges.
+//
+// A CTA's 16 warps:
+//   0-3, 4-7   softmax of query tile 0 and 1, one row a thread: scores from
+//              tensor memory, online softmax in fp32, weights back to tensor
+//              memory in fp16 (the A operand of the second product), the
+//              output read out at the end.  Rounding a weight to fp16 moves
+//              it by 2^-12 of itself at most, as one rounding of a 16-bit
+//              output does.
+//   8-11       rebuild k_hat and v_hat (fp16 by definition) from the codes,
+//              into two 128-byte-swizzled stages of each
+//   12         issues the products: S = Q k_hat^T, then O += P v_hat; while
+//              one query tile is in its softmax the other is multiplied
+//   13         copies the blocks (one bulk copy each), 64 tokens a stage
+// The running maximum of a row is raised only when it grows by more than 8
+// (base 2), so that O is rarely rescaled; a weight stays below 2^8.
+//
+// k_hat's channels lie in the order 0 4 1 5 2 6 3 7 within each 8, in which
+// a code word gives its fp16 pairs; the queries are laid out the same.
+// Every wait is bounded; a CTA that gives up sets the status word, drains and
+// frees its tensor memory.
+#include "bulk_pipe.cuh"
 #include "paged.cuh"
 #include "vqk_internal.cuh"
 
 namespace vqk {
-namespace {
+namespace chunk {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 512;
+constexpr int kTile = 128;           // keys of a tile, rows of a query tile
+constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLazy = 8.f;
+constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
+constexpr int kSlices = 16;          // CTAs that merge one pair's 256 rows
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-k_paged_chunk(PagedArgs a, PagedAttend t) {
-  constexpr int CPL = D / 32, I = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t i = w / a.H_q;
-  const int hq = (int)(w % a.H_q), h = hq / (a.H_q / a.H_kv);
-  if (i >= a.tokens) return;
-  const Place at = find_place(a, i);
-  if (at.b < 0) return;
-  float q[CPL], o[CPL], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < CPL; ++e) {
-    q[e] = (float)static_cast<const T *>(t.q)[i * t.q_token + hq * t.q_head + 32 * e + lane];
-    o[e] = 0.f;
+__device__ __forceinline__ uint32_t saddr(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) {
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ __half2 bits_h2(uint32_t u) {
+  return *reinterpret_cast<const __half2 *>(&u);
+}
+
+// ---- barriers ----------------------------------------------------------------
+
+__device__ __forceinline__ void bar_init(uint64_t *b, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+// bounded (about half a second), given up at once when another role has
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *dead) {
+  if (mbar_try_wait(b, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(b, parity)) {
+    if (*dead) return false;
+    if (global_ns() - t0 > 500000000ull) {
+      *dead = 1;
+      return false;
+    }
   }
-  const uint8_t *blk = nullptr;
-  for (int p = 0; p <= at.pos; ++p) {
-    const int tl = p & 15;
-    if (tl == 0) blk = find_block(a, at.b, p, h, paged_block_bytes(D, a.g));
-    if (!blk) continue;
-    float kv[2][CPL];
+  return true;
+}
+
+// ---- tcgen05 -----------------------------------------------------------------
+
+// 128-byte-swizzled K-major operand whose 8-row atoms (1024 B) follow one
+// another: address >> 4, stride 1024 B between atoms, version 1, swizzle 2
+__device__ __forceinline__ uint64_t desc128(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, fp16 operands, fp32 accumulator, both K-major
+__host__ __device__ constexpr uint32_t idesc(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          saddr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+#define VQK_R8(v, i)                                                              \
+  "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]),     \
+      "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define VQK_S8(v, i)                                                              \
+  "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]),          \
+      "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tm_ld32(uint32_t t, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : VQK_R8(v, 0), VQK_R8(v, 8), VQK_R8(v, 16), VQK_R8(v, 24)
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t t, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(t),
+      VQK_S8(v, 0), VQK_S8(v, 8), VQK_S8(v, 16), VQK_S8(v, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(t),
+      VQK_S8(v, 0), VQK_S8(v, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ---- the work line -------------------------------------------------------------
+
+struct Seq {
+  int len, n, first;   // tokens, new tokens, row of the first new token
+};
+
+__device__ __forceinline__ Seq seq_of(const PagedArgs &a, int b, int max_new) {
+  Seq s{a.lens[b], 1, b};
+  if (a.cu) {
+    s.first = a.cu[b];
+    s.n = a.cu[b + 1] - s.first;
+  }
+  if (s.len < 0 || s.len > ((int64_t)a.max_pages << a.page_log2) || s.n < 0 || s.n > max_new ||
+      s.first < 0 || (int64_t)s.first + s.n > a.tokens) {
+    atomicOr(a.status, kBadLength);
+    s.len = s.n = 0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int pairs_of(const Seq &s, int tpt) {
+  return (s.n + 2 * tpt - 1) / (2 * tpt);
+}
+// key tiles that pair p of a sequence walks (one at least, so that rows
+// without keys are written too)
+__device__ __forceinline__ int tiles_of(const Seq &s, int p, int tpt) {
+  const int limit = s.len - s.n + min(s.n, (p + 1) * 2 * tpt);
+  return limit > kTile ? (limit + kTile - 1) / kTile : 1;
+}
+
+// prefix[b] = key tiles of sequences before b over all kv heads, b <= B; the
+// whole CTA takes part
+__device__ void tile_prefix(const PagedArgs &a, int max_new, int tpt, long long *prefix) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  for (int b = warp; b < a.B; b += nw) {
+    const Seq s = seq_of(a, b, max_new);
+    const int np = pairs_of(s, tpt);
+    long long sum = 0;
+    for (int p = lane; p < np; p += 32) sum += tiles_of(s, p, tpt);
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) {
-      const int c = 32 * e + lane;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) prefix[b + 1] = sum * a.H_kv;
+  }
+  if (threadIdx.x == 0) prefix[0] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      long long v = b0 + lane < a.B ? prefix[b0 + lane + 1] : 0;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int off = v ? off_vc(D, a.g) + 2 * (tl & 1) + (c % 4) / 2 +
-                                4 * (((8 * (tl >> 3) + c % 32 / 4) * 4 + (tl & 7) / 2) * I + c / 32)
-                          : tl * (D / 2) + 4 * (c % 32 / 8 * I + c / 32) + c % 8 / 2;
-        const int code = (blk[off] >> (4 * (c & 1))) & 15;
-        const __half *mt = reinterpret_cast<const __half *>(
-                               blk + (v ? off_vm(D, a.g) : off_km(D))) +
-                           ((tl >> 1) * (D / a.g) + c / a.g) * 4 + (tl & 1);
-        kv[v][e] = __half2float(__hfma(__int2half_rn(code), mt[0], mt[2]));
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += x;
+      }
+      if (b0 + lane < a.B) prefix[b0 + lane + 1] = base + v;
+      base += __shfl_sync(kFull, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int ctas_used(long long units, int ctas) {
+  const long long c = (units + kMinTiles - 1) / kMinTiles;
+  return (int)(c < ctas ? c : ctas);
+}
+__device__ __forceinline__ long long first_unit(long long units, int ctas, int c) {
+  return units / ctas * c + units % ctas * c / ctas;
+}
+
+struct Item {
+  Seq s;
+  int b, h, pair;
+  int k0, k1, nk;   // key tiles [k0, k1) of nk
+};
+
+struct Walk {
+  long long u, end;
+  int b, h, pair, k;
+  Seq s;
+  __device__ void seek(const PagedArgs &a, const long long *prefix, long long u0, long long u1,
+                       int max_new, int tpt) {
+    u = u0;
+    end = u1;
+    if (u >= end) return;
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= u) lo = mid; else hi = mid;
+    }
+    b = lo;
+    s = seq_of(a, b, max_new);
+    const long long per = (prefix[b + 1] - prefix[b]) / a.H_kv;
+    long long v = u - prefix[b];
+    h = (int)(v / per);
+    v -= h * per;
+    pair = 0;
+    for (int t = tiles_of(s, 0, tpt); v >= t; t = tiles_of(s, pair, tpt)) {
+      v -= t;
+      ++pair;
+    }
+    k = (int)v;
+  }
+  __device__ bool next(const PagedArgs &a, const long long *prefix, int max_new, int tpt,
+                       Item &it) {
+    if (u >= end) return false;
+    it.s = s;
+    it.b = b;
+    it.h = h;
+    it.pair = pair;
+    it.nk = tiles_of(s, pair, tpt);
+    it.k0 = k;
+    it.k1 = (int)min((long long)it.nk, k + (end - u));
+    u += it.k1 - it.k0;
+    k = 0;
+    if (++pair >= pairs_of(s, tpt)) {
+      pair = 0;
+      if (++h == a.H_kv) {
+        h = 0;
+        if (u < end) {
+          do { ++b; } while (b < a.B && prefix[b + 1] == prefix[b]);
+          if (b < a.B) s = seq_of(a, b, max_new);
+        }
       }
     }
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) x = fmaf(q[e], kv[0][e], x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
-    x *= t.scale;
-    const float mn = fmaxf(m, x);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float y = exp2f(x - (mn == -INFINITY ? 0.f : mn));
-    m = mn;
-    l = l * f + y;
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) o[e] = o[e] * f + y * kv[1][e];
+    return true;
   }
+};
+
+// ---- shared memory --------------------------------------------------------------
+
+template <int D, int NG>
+struct Smem {
+  static constexpr int KB = D / 64;
+  static constexpr int OP = KB * 16384;            // one 128 x D fp16 operand
+  static constexpr int BLK = 16 * D + 128 * NG;
+  static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, RAW = 6 * OP;
+  static constexpr int BAR = RAW + kRaw * 4 * BLK;
+  static constexpr int ALLOC = BAR + 512 + 1024;   // room to align the base
+};
+
+// byte of 16-byte chunk `c` of row `r` in a tile of 128-byte swizzled rows
+__device__ __forceinline__ int sw(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+struct Bars {
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  uint32_t good[kRaw];    // which of a stage's 4 blocks arrived
+  uint32_t tmem;
+  int dead;
+};
+
+template <typename T, int D, int NG>
+__global__ void __launch_bounds__(kThreads, 1)
+k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
+  using SM = Smem<D, NG>;
+  constexpr int I = D / 32, G = D / NG, KB = SM::KB, BLK = SM::BLK;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *sm = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+  Bars &B = *reinterpret_cast<Bars *>(sm + SM::BAR);
+  static_assert(sizeof(Bars) <= 512, "barriers fit");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
+  if (tid == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      bar_init(&B.raw_full[i], 1);
+      bar_init(&B.raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&B.k_full[i], 4);
+      bar_init(&B.v_full[i], 4);
+      bar_init(&B.k_empty[i], 1);
+      bar_init(&B.v_empty[i], 1);
+      bar_init(&B.q_full[i], 4);
+      bar_init(&B.s_full[i], 1);
+      bar_init(&B.p_full[i], 4);
+      bar_init(&B.o_full[i], 1);
+    }
+    bar_init(&B.drain, 1);
+    B.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+        saddr(&B.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  long long *prefix = prefixes + (long long)blockIdx.x * (a.B + 1);
+  tile_prefix(a, t.max_new, tpt, prefix);
+  fence_after();
+  const uint32_t tmem = B.tmem;
+  volatile int *dead = &B.dead;
+  const long long units = prefix[a.B];
+  const int ctas = units > 0 ? ctas_used(units, gridDim.x) : 0;
+  Walk walk;
+  Item it;
+  const bool busy = (int)blockIdx.x < ctas;
+  walk.u = walk.end = 0;
+  if (busy)
+    walk.seek(a, prefix, first_unit(units, ctas, blockIdx.x),
+              first_unit(units, ctas, blockIdx.x + 1), t.max_new, tpt);
+
+  if (warp < 8) {
+    // ---- softmax ----
+    const int wg = warp >> 2, row = tid & 127;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
+    uint32_t ph_s = 0, ph_o = 0;
+    float sl2 = 0.f;
+    // this thread's query row into shared memory
+    auto load_q = [&](const Item &x) {
+      const int tok = x.pair * 2 * tpt + wg * tpt + row / GQ;
+      const bool valid = row < tpt * GQ && tok < x.s.n;
+      const T *q = static_cast<const T *>(t.q) + (int64_t)(x.s.first + tok) * t.q_token +
+                   (int64_t)(x.h * GQ + row % GQ) * t.q_head;
+      sl2 = t.scale;
+      float up = 1.f;
+      if constexpr (!std::is_same<T, __half>::value) {
+        // a bf16 row as fp16: scaled by a power of two to a maximum near 2^14
+        float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < CPL; ++e) {
-    const float y = l == 0.f ? 0.f : o[e] / l;
-    static_cast<T *>(t.out)[(i * a.H_q + hq) * D + 32 * e + lane] = (T)y;
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 r = valid ? reinterpret_cast<const uint4 *>(q)[c]
+                                : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            m = fmaxf(m, fabsf(__uint_as_float(w[e] << 16)));
+            m = fmaxf(m, fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+          }
+        }
+        int f = 14 - ((int)(__float_as_uint(m) >> 23) - 127);
+        f = m > 0.f ? (f > 126 ? 126 : f) : 0;
+        f = f < -100 ? -100 : f;
+        up = __uint_as_float((uint32_t)(127 + f) << 23);
+        sl2 *= __uint_as_float((uint32_t)(127 - f) << 23);
+      }
+      unsigned char *dst = sm + SM::Q + wg * SM::OP;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 r = valid ? reinterpret_cast<const uint4 *>(q)[c] : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (!std::is_same<T, __half>::value) {
+          uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = h2_bits(__floats2half2_rn(__uint_as_float(w[e] << 16) * up,
+                                             __uint_as_float(w[e] & 0xffff0000u) * up));
+          r = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + sw(row, c & 7)) =
+            make_uint4(__byte_perm(r.x, r.z, 0x5410), __byte_perm(r.x, r.z, 0x7632),
+                       __byte_perm(r.y, r.w, 0x5410), __byte_perm(r.y, r.w, 0x7632));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(&B.q_full[wg]);
+    };
+    // the next item of this query tile
+    auto fetch = [&](Item &x) {
+      while (walk.next(a, prefix, t.max_new, tpt, x))
+        if (wg == 0 || x.pair * 2 * tpt + tpt < x.s.n) return true;
+      return false;
+    };
+    bool have = fetch(it), ok = true;
+    if (have) load_q(it);
+    while (have && ok) {
+      const int tok = it.pair * 2 * tpt + wg * tpt + row / GQ;
+      const bool valid = row < tpt * GQ && tok < it.s.n;
+      const int pos = valid ? it.s.len - it.s.n + tok : -1;
+      const float scale = sl2;
+      float m = -INFINITY, l = 0.f;
+      for (int kt = it.k0; kt < it.k1; ++kt) {
+        ok = bar_wait(&B.s_full[wg], ph_s, dead);
+        ph_s ^= 1u;
+        if (!__all_sync(kFull, ok)) { ok = false; break; }
+        fence_after();
+        const int vis = pos - kt * kTile;            // columns up to vis are seen
+        const bool all = __all_sync(kFull, vis >= kTile - 1);
+        uint32_t v[32];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          tm_ld32(ts + c, v);
+          if (all) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              mx = fmaxf(mx, c + j <= vis ? __uint_as_float(v[j]) : -INFINITY);
+          }
+        }
+        mx *= scale;
+        const bool raise = mx > m + kLazy;
+        float f = 1.f;
+        if (raise) {
+          f = m == -INFINITY ? 0.f : ex2(m - mx);
+          m = mx;
+          l *= f;
+        }
+        if (kt > it.k0 && __any_sync(kFull, raise)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            tm_ld32(to + c, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            tm_st32(to + c, v);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          tm_ld32(ts + c, v);
+          if (!all) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j > vis) v[j] = __float_as_uint(-INFINITY);
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                make_float2(scale, scale), make_float2(-base, -base));
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            sum = __fadd2_rn(sum, y);
+            p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
+          }
+          // fp16 pairs of these 32 columns take 16, all behind what is read
+          tm_st16(ts + c / 2, p);
+        }
+        l += sum.x + sum.y;
+        tm_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&B.p_full[wg]);
+      }
+      if (!ok) break;
+      // the next queries: this tile's last scores have been read
+      const Item done = it;
+      have = fetch(it);
+      if (have) load_q(it);
+      ok = bar_wait(&B.o_full[wg], ph_o, dead);
+      ph_o ^= 1u;
+      if (!__all_sync(kFull, ok)) { ok = false; break; }
+      fence_after();
+      const bool whole = done.k0 == 0 && done.k1 == done.nk;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float *pr = part + ((int64_t)(2 * blockIdx.x + (done.k0 > 0 ? 0 : 1)) * 2 * kTile +
+                          wg * kTile + row) * (D + 4);
+      T *orow = static_cast<T *>(t.out) +
+                ((int64_t)(done.s.first + tok) * a.H_q + done.h * GQ + row % GQ) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        __syncwarp();
+        tm_ld32(to + c, v);
+        if (valid && whole) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[j + e]) * inv;
+            store8<T>(orow + c + j, y);
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4 *>(pr + c + j) =
+                make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+      }
+      if (valid && !whole) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
+      __syncwarp();
+      fence_before();
+    }
+  } else if (warp < 12) {
+    // ---- k_hat and v_hat ----
+    const int w = warp - 8, n8 = lane >> 2, t4 = lane & 3;
+    uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
+    bool ok = true;
+    const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
+                  k64 = bits_h2(0xd400d400u);
+    while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
+      for (int kt = it.k0; ok && kt < it.k1; ++kt) {
+        ok = bar_wait(&B.k_empty[st], ph_e, dead) && bar_wait(&B.v_empty[st], ph_e, dead);
+        unsigned char *kd = sm + SM::K + st * SM::OP, *vd = sm + SM::V + st * SM::OP;
+        for (int hf = 0; hf < 2; ++hf) {
+          ok = ok && bar_wait(&B.raw_full[raw], ph_raw, dead);
+          if (!__all_sync(kFull, ok)) { ok = false; break; }
+          // warp w takes block w of the stage
+          const unsigned char *blk = sm + SM::RAW + (raw * 4 + w) * BLK;
+          const bool good = (B.good[raw] >> w) & 1u;
+          const int r0 = 64 * hf + 16 * w;             // its first key in the tile
+          const int left = it.s.len - (kt * kTile + r0);   // its tokens in the sequence
+#pragma unroll
+          for (int oct = 0; oct < 2; ++oct) {
+            const int tk = 8 * oct + n8, r = r0 + tk;
+            uint32_t kw[I];
+            if constexpr (I == 4) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(blk + tk * (D / 2) + t4 * 16);
+              kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2 *>(blk + tk * (D / 2) + t4 * 8);
+              kw[0] = x.x; kw[1] = x.y;
+            }
+            const uint2 *km = reinterpret_cast<const uint2 *>(blk + off_km(D)) + (tk >> 1) * NG;
+            const unsigned sel = (tk & 1) ? 0x3232u : 0x1010u;
+            // neighbouring rows store the two halves of a 128-byte row in
+            // turn, so that 8 lanes' 16-byte stores meet 8 bank groups
+            const int odd = n8 & 1;
+#pragma unroll
+            for (int i2 = 0; i2 < I; ++i2) {
+              const int i = i2 ^ odd;
+              uint32_t x = odd ? kw[i2 ^ 1] : kw[i2];
+              const uint2 y = km[32 * i / G];
+              const __half2 s = bits_h2(good ? __byte_perm(y.x, 0u, sel) : 0u),
+                            z = bits_h2(good ? __byte_perm(y.y, 0u, sel) : 0u);
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const __half2 c0 = __hsub2(bits_h2((x & 0x000f000fu) | 0x64006400u), k1024);
+                const __half2 c1 = __hfma2(bits_h2((x & 0x00f000f0u) | 0x64006400u), k16, k64);
+                o[2 * j] = h2_bits(__hfma2(c0, s, z));
+                o[2 * j + 1] = h2_bits(__hfma2(c1, s, z));
+                x >>= 8;
+              }
+              *reinterpret_cast<uint4 *>(kd + (i >> 1) * 16384 + sw(r, 4 * (i & 1) + t4)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          // values: lane (n8, t4) reads the words of token pair t4, then the
+          // four lanes of n8 exchange them, so that lane j has the four pairs
+          // (8 tokens) of the 32-channel span j
+#pragma unroll
+          for (int oct = 0; oct < 2; ++oct) {
+            uint32_t x[4] = {0u, 0u, 0u, 0u};
+            const unsigned char *vp = blk + off_vc(D, G) + (32 * oct + lane) * (4 * I);
+            if constexpr (I == 4) {
+              const uint4 y = *reinterpret_cast<const uint4 *>(vp);
+              x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2 *>(vp);
+              x[0] = y.x; x[1] = y.y;
+            }
+            // 4 x 4 transposition over the lanes t4 in two exchanges
+            {
+              const bool o1 = t4 & 1, o2 = t4 & 2;
+              uint32_t s0 = o1 ? x[0] : x[1], s1 = o1 ? x[2] : x[3];
+              s0 = __shfl_xor_sync(kFull, s0, 1);
+              s1 = __shfl_xor_sync(kFull, s1, 1);
+              if (o1) { x[0] = s0; x[2] = s1; } else { x[1] = s0; x[3] = s1; }
+              s0 = o2 ? x[0] : x[2];
+              s1 = o2 ? x[1] : x[3];
+              s0 = __shfl_xor_sync(kFull, s0, 2);
+              s1 = __shfl_xor_sync(kFull, s1, 2);
+              if (o2) { x[0] = s0; x[1] = s1; } else { x[2] = s0; x[3] = s1; }
+            }
+            const int span = t4;
+            if (I == 4 || span < I) {
+              const uint2 *vm = reinterpret_cast<const uint2 *>(blk + off_vm(D, G)) +
+                                4 * oct * NG + 32 * span / G;
+              __half2 s[4], z[4];
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                const uint2 y = vm[p * NG];
+                // tokens behind the sequence hold anything: their values are 0
+                const int e = left - (8 * oct + 2 * p);
+                const unsigned keep = !good || e <= 0 ? 0u : (e == 1 ? 0x0000ffffu : kFull);
+                s[p] = bits_h2(y.x & keep);
+                z[p] = bits_h2(y.y & keep);
+              }
+              const int chunk = 2 * w + oct;           // octet within the 64 tokens
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                // the lanes of a store differ in the channel's low bits
+                const int r = (q + span) & 3, c = 32 * span + 4 * n8 + r;
+                uint32_t o[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  const __half2 cc =
+                      __hsub2(bits_h2(((x[p] >> (4 * r)) & 0x000f000fu) | 0x64006400u), k1024);
+                  o[p] = h2_bits(__hfma2(cc, s[p], z[p]));
+                }
+                *reinterpret_cast<uint4 *>(vd + hf * (D * 128) + sw(c, chunk)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&B.raw_empty[raw]);
+          raw = raw + 1 == kRaw ? 0 : raw + 1;
+          ph_raw ^= raw == 0;
+        }
+        if (!ok) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&B.k_full[st]);
+          bar_arrive(&B.v_full[st]);
+        }
+        st ^= 1u;
+        ph_e ^= st == 0;
+      }
+    }
+  } else if (warp == 12) {
+    // ---- the products ----
+    if (lane == 0) {
+      const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
+      const uint32_t sb = saddr(sm);
+      uint32_t ks = 0, ph_k = 0, vs = 0, ph_v = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int i, uint32_t stage) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + 128 * i,
+                 desc128(sb + SM::Q + i * SM::OP + (k >> 2) * 16384 + 32 * (k & 3)),
+                 desc128(sb + SM::K + stage * SM::OP + (k >> 2) * 16384 + 32 * (k & 3)), id_s,
+                 k > 0);
+        mma_commit(&B.s_full[i]);
+      };
+      auto outputs = [&](int i, uint32_t stage, bool more) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k,
+                 desc128(sb + SM::V + stage * SM::OP + (k >> 2) * (D * 128) + 32 * (k & 3)),
+                 id_o, more || k > 0);
+      };
+      while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
+        const int two = it.pair * 2 * tpt + tpt < it.s.n ? 2 : 1;
+        const int nt = it.k1 - it.k0;
+        for (int i = 0; ok && i < two; ++i) {
+          ok = bar_wait(&B.q_full[i], ph_q[i], dead);
+          ph_q[i] ^= 1u;
+          if (ok && i == 0) ok = bar_wait(&B.k_full[ks], ph_k, dead);
+          if (!ok) break;
+          fence_after();
+          scores(i, ks);
+        }
+        if (!ok) break;
+        mma_commit(&B.k_empty[ks]);
+        ks ^= 1u;
+        ph_k ^= ks == 0;
+        for (int j = 0; ok && j < nt; ++j) {
+          const bool last = j + 1 == nt;
+          ok = bar_wait(&B.v_full[vs], ph_v, dead);
+          for (int i = 0; ok && i < two; ++i) {
+            ok = bar_wait(&B.p_full[i], ph_p[i], dead);
+            ph_p[i] ^= 1u;
+            if (!ok) break;
+            fence_after();
+            outputs(i, vs, j > 0);
+            if (last) {
+              mma_commit(&B.o_full[i]);
+            } else {
+              if (i == 0) ok = bar_wait(&B.k_full[ks], ph_k, dead);
+              if (!ok) break;
+              fence_after();
+              scores(i, ks);
+            }
+          }
+          if (!ok) break;
+          mma_commit(&B.v_empty[vs]);
+          vs ^= 1u;
+          ph_v ^= vs == 0;
+          if (!last) {
+            mma_commit(&B.k_empty[ks]);
+            ks ^= 1u;
+            ph_k ^= ks == 0;
+          }
+        }
+      }
+      // products in flight end before the tensor memory is given up
+      mma_commit(&B.drain);
+      int never = 0;
+      bar_wait(&B.drain, 0, &never);
+    }
+  } else if (warp == 13) {
+    // ---- copies ----
+    const int bpp = a.page_log2 - 4;
+    uint32_t raw = 0, ph_e = 1;
+    uint32_t used = 0;             // stages with copies not known to have landed
+    bool ok = true;
+    while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
+      const int nblk = (it.s.len + kBlk - 1) / kBlk;
+      for (int k4 = 2 * it.k0; ok && k4 < 2 * it.k1; ++k4) {
+        const int blk = 4 * k4 + lane;
+        bool good = lane < 4 && blk < nblk;
+        int p = -1;
+        if (good) {
+          p = a.table[(int64_t)it.b * a.table_stride + (blk >> bpp)];
+          if ((unsigned)p >= (unsigned)a.n_pages) {
+            atomicOr(a.status, kBadPage);
+            good = false;
+          }
+        }
+        ok = bar_wait(&B.raw_empty[raw], ph_e, dead);
+        if (!__all_sync(kFull, ok)) { ok = false; break; }
+        const unsigned mask = __ballot_sync(kFull, good);
+        if (lane == 0) {
+          B.good[raw] = mask;
+          mbar_expect_tx(&B.raw_full[raw], __popc(mask) * BLK);
+        }
+        __syncwarp();
+        if (good) {
+          const int64_t src = ((((int64_t)p * a.H_kv + it.h) << bpp) + (blk & ((1 << bpp) - 1)));
+          bulk_g2s(sm + SM::RAW + (raw * 4 + lane) * BLK, a.pool + src * BLK, BLK,
+                   &B.raw_full[raw]);
+        }
+        used |= 1u << raw;
+        raw = raw + 1 == kRaw ? 0 : raw + 1;
+        ph_e ^= raw == 0;
+      }
+    }
+    // copies in flight land before the shared memory is given up: the phase
+    // of a stage's last copies is the one before its next turn's
+    if (lane == 0) {
+      for (int i = 0; i < kRaw; ++i) {
+        int never = 0;
+        const uint32_t turn = (uint32_t)i < raw ? ph_e ^ 1u : ph_e;   // parity of its last full
+        if ((used >> i) & 1u) bar_wait(&B.raw_full[i], turn, &never);
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && B.dead) atomicOr(a.status, kGaveUp);
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, cudaStream_t st) {
-  const int64_t warps = a.tokens * a.H_q, wpc = kThreads / 32;
-  const dim3 grid((unsigned)((warps + wpc - 1) / wpc));
-  cudaError_t e = D == 64 ? launch_pdl(k_paged_chunk<T, 64>, grid, dim3(kThreads), 0, st, a, t)
-                          : launch_pdl(k_paged_chunk<T, 128>, grid, dim3(kThreads), 0, st, a, t);
+// Merge of a pair whose keys were cut: CTA (c, slice) merges 16 rows of the
+// pair that ends CTA c's piece of the line, when that pair starts in it and
+// goes on.  One warp per row, lanes over channels.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, long long *prefixes,
+                    int grid) {
+  constexpr int CPL = D / 32, ROW = D + 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the attention's CTA 0 has left the prefix
+  const long long *prefix = prefixes;
+  const long long units = prefix[a.B];
+  if (units == 0) return;
+  const int ctas = ctas_used(units, grid), c = blockIdx.x / kSlices,
+            slice = blockIdx.x % kSlices;
+  if (c + 1 >= ctas) return;
+  const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
+  const long long u1 = first_unit(units, ctas, c + 1);
+  Walk w;
+  w.seek(a, prefix, u1 - 1, u1, t.max_new, tpt);
+  const Seq s = w.s;
+  const int nk = tiles_of(s, w.pair, tpt), k = w.k, h = w.h, pair = w.pair;
+  // the pair's first tile lies k tiles before unit u1 - 1
+  if (k + 1 >= nk || u1 - 1 - k < first_unit(units, ctas, c)) return;
+  const long long ulast = u1 - 1 - k + nk - 1;
+  int cl = c + 1;
+  while (cl + 1 < ctas && first_unit(units, ctas, cl + 1) <= ulast) ++cl;
+  const int lane = threadIdx.x & 31;
+  for (int r = slice * 16 + (threadIdx.x >> 5); r < slice * 16 + 16; r += 4) {
+    const int wg = r >> 7, row = r & 127, tok = pair * 2 * tpt + wg * tpt + row / GQ;
+    if (row >= tpt * GQ || tok >= s.n) continue;
+    auto at = [&](int i) {
+      return part + ((int64_t)(i == c ? 2 * c + 1 : 2 * i) * 2 * kTile + r) * ROW;
+    };
+    float M = -INFINITY;
+    for (int i = c + lane; i <= cl; i += 32) M = fmaxf(M, at(i)[D]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float L = 0.f, acc[CPL];
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = c; i <= cl; ++i) {
+      const float *p = at(i);
+      const float2 ml = *reinterpret_cast<const float2 *>(p + D);
+      const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+      L = fmaf(f, ml.y, L);
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) acc[e] = fmaf(f, p[32 * e + lane], acc[e]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    T *o = static_cast<T *>(t.out) +
+           ((int64_t)(s.first + tok) * a.H_q + h * GQ + row % GQ) * D;
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) {
+      if constexpr (std::is_same<T, __half>::value) o[32 * e + lane] = __float2half_rn(acc[e] * inv);
+      else o[32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
+    }
+  }
+}
+
+size_t part_bytes(int D, int sm_count) {
+  return (size_t)2 * sm_count * 2 * kTile * (D + 4) * sizeof(float);
+}
+
+template <typename T, int D, int NG>
+cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cudaStream_t st) {
+  using SM = Smem<D, NG>;
+  cudaError_t e = cudaFuncSetAttribute(k_paged_chunk<T, D, NG>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SM::ALLOC);
+  if (e != cudaSuccess) return e;
+  float *part = t.ws;
+  long long *prefixes =
+      reinterpret_cast<long long *>(reinterpret_cast<uint8_t *>(t.ws) + part_bytes(D, sm_count));
+  e = launch_pdl(k_paged_chunk<T, D, NG>, dim3(sm_count), dim3(kThreads), SM::ALLOC, st, a, t,
+                 part, prefixes);
+  count_launch();
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_paged_chunk_merge<T, D>, dim3(sm_count * kSlices), dim3(128), 0, st, a, t,
+                 (const float *)part, prefixes, sm_count);
   count_launch();
   return e;
 }
 
-}  // namespace
+template <typename T>
+cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_count,
+                     cudaStream_t st) {
+  const int ng = D / a.g;
+  if (D == 64)
+    return ng == 1 ? launch_d<T, 64, 1>(a, t, sm_count, st)
+                   : launch_d<T, 64, 2>(a, t, sm_count, st);
+  return ng == 1   ? launch_d<T, 128, 1>(a, t, sm_count, st)
+         : ng == 2 ? launch_d<T, 128, 2>(a, t, sm_count, st)
+                   : launch_d<T, 128, 4>(a, t, sm_count, st);
+}
 
-size_t paged_chunk_ws(int, int, int, int) { return 0; }
+}  // namespace chunk
 
-cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D, int,
-                               cudaStream_t st) {
-  return dtype == VQ_F16 ? launch_t<__half>(a, t, D, st) : launch_t<__nv_bfloat16>(a, t, D, st);
+size_t paged_chunk_ws(int B, int, int D, int sm_count) {
+  return chunk::part_bytes(D, sm_count) + (size_t)sm_count * (B + 1) * sizeof(long long);
+}
+
+cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
+                               int sm_count, cudaStream_t st) {
+  return dtype == VQ_F16 ? chunk::launch_t<__half>(a, t, D, sm_count, st)
+                         : chunk::launch_t<__nv_bfloat16>(a, t, D, sm_count, st);
 }
 
 }  // namespace vqk

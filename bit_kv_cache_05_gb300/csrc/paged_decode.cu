@@ -468,7 +468,6 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max) {
   __shared__ int wsum[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   block_prefix(a, t.max_new, prefix, wsum);
   const int H = a.H_kv, GQ = a.H_q / H, R = t.max_new * GQ;
   const int row = blockIdx.x % R, seg = blockIdx.x / R, b = seg / H, h = seg % H;

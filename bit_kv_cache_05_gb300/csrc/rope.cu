@@ -27,7 +27,6 @@ k_norm_rope(HeadRows q, HeadRows k, RopeArgs r, int D, int64_t tokens, float eps
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   if (t >= tokens) return;
   const int gq = (q.heads + RPW - 1) / RPW, gk = (k.heads + RPW - 1) / RPW;
   const bool active = 16 * l < D;
