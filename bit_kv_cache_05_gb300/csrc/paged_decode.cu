@@ -3,17 +3,20 @@
 //
 //   out = sum_t softmax_t(scale q.k_hat_t) v_hat_t,  t <= the row's own token
 //
-// The work is one line of 16-token blocks over (sequence, kv head, block),
-// cut evenly among the resident warps, whatever the lengths: no plan on the
-// host, so a captured call follows the lengths that it finds.  A warp copies
-// its blocks (one bulk copy each) into its own ring of shared-memory stages
-// and keeps one online softmax per row; a second kernel merges the warps'
-// partials of a (sequence, kv head).
+// The work is one line of 32-token steps (two blocks) over (sequence, kv head,
+// step), cut evenly among the resident warps, whatever the lengths: no plan
+// on the host, so a captured call follows the lengths that it finds.  A warp
+// copies its steps (one bulk copy each, two where a page holds one block) into
+// its own ring of shared-memory stages and keeps one online softmax per row; a
+// second kernel merges the warps' partials of a (sequence, kv head).
 //
-// Products on mma.m16n8k16 with fp32 accumulators.  Scores: A = queries
-// (rows 0-7), B = k_hat of 8 tokens; output: A = weights, B = v_hat.  The
-// weights enter as fp16 hi (rows 0-7) plus the remainder lo (rows 8-15, free
-// in a 16-row product), so only the output is rounded to 16 bits.  k_hat and
+// Products on mma.m16n8k16 with fp32 accumulators.  Scores: A = k_hat of 16
+// tokens (row n the even token of pair n, row 8 + n the odd one, so that a
+// pair's scales are the halves of one word), B = up to 8 query rows; output:
+// A = weights, turned over by movmatrix, B = v_hat.  The weights enter as
+// fp16 hi (rows 0-7) plus the remainder lo (rows 8-15, free in a 16-row
+// product), so only the output is rounded to 16 bits.  Both operands that
+// change are made where the product reads them: no register is moved.  k_hat and
 // v_hat are fp16 by definition; a bf16 query row is scaled by a power of two
 // to a maximum near 2^14 and taken as fp16, which keeps every bit of values
 // down to 2^-28 of the row's largest.
@@ -30,7 +33,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMinBlocks = 2;      // blocks a warp takes at least
+constexpr int kStep = 32;          // tokens of a step: two blocks
+constexpr int kMinSteps = 1;       // steps a warp takes at least
 constexpr float kLazy = 8.f;       // a maximum is raised when it grows by more
 
 __device__ __forceinline__ float ex2(float x) {
@@ -47,11 +51,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// an 8 x 8 matrix of 16-bit values, a row per four lanes, turned over
+__device__ __forceinline__ uint32_t turn(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) {
   return *reinterpret_cast<const __half2 *>(&u);
+}
+
+// (w & mask) | 0x64006400 in one instruction: 0x6400 | c is 1024 + c
+template <uint32_t mask>
+__device__ __forceinline__ __half2 field(uint32_t w, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(mask), "r"(magic));
+  return bits_h2(d);
 }
 
 // the four fp16 pairs of a word: nibbles r of its two halves, times s plus z
@@ -60,17 +79,16 @@ __device__ __forceinline__ void word_values(uint32_t w, __half2 s, __half2 z, ui
                 k64 = bits_h2(0xd400d400u);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    // 0x6400 | c is 1024 + c, 0x6400 | 16 c is 1024 + 16 c: both exact
-    const __half2 c0 = __hsub2(bits_h2((w & 0x000f000fu) | 0x64006400u), k1024);
-    const __half2 c1 = __hfma2(bits_h2((w & 0x00f000f0u) | 0x64006400u), k16, k64);
+    // 1024 + c and 1024 + 16 c: both steps to c are exact
+    const __half2 c0 = __hsub2(field<0x000f000fu>(w, 0x64006400u), k1024);
+    const __half2 c1 = __hfma2(field<0x00f000f0u>(w, 0x64006400u), k16, k64);
     v[2 * j] = h2_bits(__hfma2(c0, s, z));
     v[2 * j + 1] = h2_bits(__hfma2(c1, s, z));
     w >>= 8;
   }
 }
 
-// Blocks of every sequence as a running sum over (sequence, kv head), in
-// shared memory; one entry per sequence.  Faulty lengths count as empty.
+// A sequence's lengths; faulty ones count as empty.
 struct Lengths {
   int len, n;   // tokens, new tokens (rows)
 };
@@ -90,18 +108,18 @@ __device__ __forceinline__ Lengths lengths_of(const PagedArgs &a, int b, int max
   return r;
 }
 
-__device__ __forceinline__ int blocks_of(const Lengths &r) {
-  return r.n > 0 ? (r.len + kBlk - 1) / kBlk : 0;
+__device__ __forceinline__ int steps_of(const Lengths &r) {
+  return r.n > 0 ? (r.len + kStep - 1) / kStep : 0;
 }
 
-// prefix[b] = blocks of sequences 0 ... b - 1 times H_kv, for b <= B
-__device__ void block_prefix(const PagedArgs &a, int max_new, int *prefix, int *warp_sum) {
+// prefix[b] = steps of sequences 0 ... b - 1 times H_kv, for b <= B
+__device__ void step_prefix(const PagedArgs &a, int max_new, int *prefix, int *warp_sum) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + nt - 1) / nt;
   int sum = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < a.B) sum += blocks_of(lengths_of(a, b, max_new)) * a.H_kv;
+    if (b < a.B) sum += steps_of(lengths_of(a, b, max_new)) * a.H_kv;
   }
   int inc = sum;
 #pragma unroll
@@ -117,22 +135,22 @@ __device__ void block_prefix(const PagedArgs &a, int max_new, int *prefix, int *
     const int b = tid * per + i;
     if (b < a.B) {
       prefix[b] = base;
-      base += blocks_of(lengths_of(a, b, max_new)) * a.H_kv;
+      base += steps_of(lengths_of(a, b, max_new)) * a.H_kv;
       if (b == a.B - 1) prefix[a.B] = base;
     }
   }
   __syncthreads();
 }
 
-// warps that share `units` blocks, and the first block of warp w
+// warps that share `units` steps, and the first step of warp w
 __device__ __forceinline__ int warps_used(int units, int warps_max) {
-  const int w = (units + kMinBlocks - 1) / kMinBlocks;
+  const int w = (units + kMinSteps - 1) / kMinSteps;
   return w < warps_max ? w : warps_max;
 }
 __device__ __forceinline__ int first_unit(int units, int warps, int w) {
   return (int)((int64_t)units * w / warps);
 }
-// the warp that owns block u
+// the warp that owns step u
 __device__ __forceinline__ int owner(int units, int warps, int u) {
   return (int)((((int64_t)u + 1) * warps - 1) / units);
 }
@@ -145,18 +163,47 @@ struct Part {   // a partial: rows x (D outputs, maximum, sum, padding)
 template <int D, int NG>
 struct DecSmem {
   static constexpr int BLK = 16 * D + 128 * NG;
-  static constexpr int STAGES = D == 128 ? 4 : 6;
-  static constexpr int PER_WARP = STAGES * BLK;          // a multiple of 128
+  static constexpr int STEP = 2 * BLK;
+  // 12 warps an SM at D = 128 (64 accumulators a thread), 16 at D = 64
+  static constexpr int CTAS = D == 128 ? 3 : 4;
+  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int PER_WARP = STAGES * STEP;         // a multiple of 128
   static constexpr int BAR = kWarps * PER_WARP;
   static constexpr int PREFIX = BAR + kWarps * STAGES * 8;
   static_assert(BLK % 128 == 0, "stages stay 128-byte aligned");
 };
 
+// the (scale, zero) words of a token pair, all groups
+template <int NG>
+__device__ __forceinline__ void load_meta(const unsigned char *p, uint2 (&m)[NG]) {
+  if constexpr (NG == 1) {
+    m[0] = *reinterpret_cast<const uint2 *>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) {
+      const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
+      m[2 * i] = make_uint2(x.x, x.y);
+      m[2 * i + 1] = make_uint2(x.z, x.w);
+    }
+  }
+}
+
+template <int I>
+__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[I]) {
+  if constexpr (I == 4) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x; w[1] = x.y;
+  }
+}
+
 template <typename T, int D, int NG>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, DecSmem<D, NG>::CTAS)
 k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
   using SM = DecSmem<D, NG>;
-  constexpr int I = D / 32, BLK = SM::BLK, ST = SM::STAGES, G = D / NG;
+  constexpr int I = D / 32, BLK = SM::BLK, STEP = SM::STEP, ST = SM::STAGES, G = D / NG;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int wsum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, t4 = lane & 3;
@@ -169,7 +216,7 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  block_prefix(a, t.max_new, prefix, wsum);
+  step_prefix(a, t.max_new, prefix, wsum);
 
   const int units = prefix[a.B];
   const int warps = warps_used(units, warps_max);
@@ -180,48 +227,69 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
   const int u_end = first_unit(units, warps, w + 1);
   const int H = a.H_kv, GQ = a.H_q / a.H_kv;
 
-  // the sequence of block u
-  int b = 0;
-  {
+  auto find = [&](int uu) {   // the sequence of step uu
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= u) lo = mid; else hi = mid;
+      if (prefix[mid] <= uu) lo = mid; else hi = mid;
     }
-    b = lo;
-  }
-  // cursor of the copies: block iu of sequence ib, head ih, at place ik
-  int iu = u, ib = b, inb, ih, ik;
+    return lo;
+  };
   auto enter = [&](int bb, int uu, int &nb, int &h, int &k) {
     nb = (prefix[bb + 1] - prefix[bb]) / H;
     h = (uu - prefix[bb]) / nb;
     k = (uu - prefix[bb]) - h * nb;
   };
-  enter(ib, iu, inb, ih, ik);
+  int b = find(u);
   const int bpp = a.page_log2 - 4;                     // log2 blocks of a page
-  unsigned ok_mask = 0u;                               // stages with a good page
+  // The copies of 32 steps are prepared at once, lane j those of step ibase +
+  // j: where its blocks lie and whether their pages are in the pool.
+  int iu = u, ibase = u;
+  const uint8_t *src0 = nullptr, *src1 = nullptr;
+  unsigned g0 = 0u, g1 = 0u;                           // of the 32 steps
+  auto prepare = [&]() {
+    ibase = iu;
+    const int v = iu + lane;
+    bool ok0 = false, ok1 = false;
+    if (v < u_end) {
+      int nb, h, k;
+      const int bb = find(v);
+      enter(bb, v, nb, h, k);
+      const int32_t *row = a.table + (int64_t)bb * a.table_stride;
+      const int blk = 2 * k, nblk = (a.lens[bb] + kBlk - 1) / kBlk;
+      const int p0 = row[blk >> bpp];
+      ok0 = (unsigned)p0 < (unsigned)a.n_pages;
+      src0 = a.pool + ((((int64_t)p0 * H + h) << bpp) + (blk & ((1 << bpp) - 1))) * BLK;
+      bool bad = !ok0;
+      if (blk + 1 < nblk) {
+        const int p1 = bpp ? p0 : row[blk + 1];
+        ok1 = (unsigned)p1 < (unsigned)a.n_pages;
+        src1 = bpp ? src0 + BLK : a.pool + ((int64_t)p1 * H + h) * BLK;
+        bad = bad || !ok1;
+      }
+      if (bad) atomicOr(a.status, kBadPage);
+    }
+    g0 = __ballot_sync(kFull, ok0);
+    g1 = __ballot_sync(kFull, ok1);
+  };
+  prepare();
+  unsigned good = 0u;                                  // two bits a stage
   auto issue = [&](int s) {
-    const int p = a.table[(int64_t)ib * a.table_stride + (ik >> bpp)];
-    const bool good = (unsigned)p < (unsigned)a.n_pages;
-    ok_mask = good ? ok_mask | (1u << s) : ok_mask & ~(1u << s);
-    if (lane == 0) {
-      if (good) {
-        const int64_t blk = (((int64_t)p * H + ih) << bpp) + (ik & ((1 << bpp) - 1));
-        mbar_expect_tx(&bar[s], BLK);
-        bulk_g2s(stage + s * BLK, a.pool + blk * BLK, BLK, &bar[s]);
+    if (iu - ibase == 32) prepare();
+    const int j = iu - ibase;
+    const unsigned gd = ((g0 >> j) & 1u) | (((g1 >> j) & 1u) << 1);
+    good = (good & ~(3u << (2 * s))) | (gd << (2 * s));
+    if (lane == j && gd) {
+      unsigned char *dst = stage + s * STEP;
+      mbar_expect_tx(&bar[s], gd == 3u ? STEP : BLK);
+      if (bpp && gd == 3u) {
+        bulk_g2s(dst, src0, STEP, &bar[s]);
       } else {
-        atomicOr(a.status, kBadPage);
+        if (gd & 1u) bulk_g2s(dst, src0, BLK, &bar[s]);
+        if (gd & 2u) bulk_g2s(dst + BLK, src1, BLK, &bar[s]);
       }
     }
     ++iu;
-    if (++ik == inb) {
-      ik = 0;
-      if (++ih == H) {
-        ih = 0;
-        do { ++ib; } while (ib < a.B && prefix[ib + 1] == prefix[ib]);
-        if (ib < a.B) inb = (prefix[ib + 1] - prefix[ib]) / H;
-      }
-    }
   };
 #pragma unroll
   for (int s = 0; s < ST; ++s)
@@ -237,8 +305,10 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
     const Lengths L = lengths_of(a, b, t.max_new);
     const int row0 = a.cu ? a.cu[b] : b, rows = L.n * GQ;
     const int tok = n8 / GQ;
-    // the newest token this lane's row sees (rows without a query: none)
-    const int last = n8 < rows ? L.len - L.n + tok : -1;
+    // the newest tokens that rows 2 t4 and 2 t4 + 1 see (rows without a
+    // query: none)
+    const int see0 = 2 * t4 < rows ? L.len - L.n + 2 * t4 / GQ : -1;
+    const int see1 = 2 * t4 + 1 < rows ? L.len - L.n + (2 * t4 + 1) / GQ : -1;
     const int all_see = L.len - L.n;      // tokens up to here are seen by all rows
     uint32_t qa[I][4];
     float sl2 = t.scale;
@@ -288,7 +358,10 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
         qa[i][3] = __byte_perm(raw[i].y, raw[i].w, 0x7632);
       }
     }
-    float m = -INFINITY, l = 0.f;
+    // of rows 2 t4 and 2 t4 + 1
+    const float2 sc = make_float2(__shfl_sync(kFull, sl2, 8 * t4),
+                                  __shfl_sync(kFull, sl2, 8 * t4 + 4));
+    float2 m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
     float o[I][4][4];
 #pragma unroll
     for (int i = 0; i < I; ++i)
@@ -300,8 +373,8 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
     const int k_end = min(nb, k + (u_end - u));
     u += k_end - k;
     for (; k < k_end; ++k) {
-      const bool good = (ok_mask >> s) & 1u;
-      if (good) {
+      const unsigned gd = (good >> (2 * s)) & 3u;
+      if (gd) {
         const bool ok = mbar_wait(&bar[s], (phases >> s) & 1u);
         phases ^= 1u << s;
         if (!__all_sync(kFull, ok)) {
@@ -309,54 +382,59 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
           dead = true;
           break;
         }
-        const unsigned char *st = stage + s * BLK;
-        const int t0 = k * kBlk;
-        float sc[2][4];
+        const unsigned char *st = stage + s * STEP;
+        const int t0 = k * kStep;
+        // raw scores of rows 2 t4, 2 t4 + 1: tokens 16 bk + 2 n8 and the next
+        float x[2][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int tl = 8 * nt + n8;
-          uint32_t kw[I];
-          if constexpr (I == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(st + tl * (D / 2) + t4 * 16);
-            kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(st + tl * (D / 2) + t4 * 8);
-            kw[0] = x.x; kw[1] = x.y;
-          }
-          const uint2 *km = reinterpret_cast<const uint2 *>(st + off_km(D)) + (tl >> 1) * NG;
-          const unsigned sel = (tl & 1) ? 0x3232u : 0x1010u;
+        for (int bk = 0; bk < 2; ++bk) {
+          const unsigned char *blk = st + bk * BLK;
+          uint32_t k0[I], k1[I];
+          uint2 km[NG];
+          load_words<I>(blk + 2 * n8 * (D / 2) + t4 * (4 * I), k0);
+          load_words<I>(blk + (2 * n8 + 1) * (D / 2) + t4 * (4 * I), k1);
+          load_meta<NG>(blk + off_km(D) + n8 * (8 * NG), km);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-          __half2 ks, kz;
+          for (int e = 0; e < 4; ++e) x[bk][e] = 0.f;
 #pragma unroll
           for (int i = 0; i < I; ++i) {
-            if ((32 * i) % G == 0) {
-              const uint2 x = km[32 * i / G];
-              ks = bits_h2(__byte_perm(x.x, 0u, sel));
-              kz = bits_h2(__byte_perm(x.y, 0u, sel));
-            }
-            uint32_t v[4];
-            word_values(kw[i], ks, kz, v);
-            mma16816(sc[nt], qa[i][0], 0u, qa[i][1], 0u, v[0], v[1]);
-            mma16816(sc[nt], qa[i][2], 0u, qa[i][3], 0u, v[2], v[3]);
+            const __half2 s2 = bits_h2(km[32 * i / G].x), z2 = bits_h2(km[32 * i / G].y);
+            uint32_t v0[4], v1[4];
+            word_values(k0[i], __low2half2(s2), __low2half2(z2), v0);
+            word_values(k1[i], __high2half2(s2), __high2half2(z2), v1);
+            mma16816(x[bk], v0[0], v1[0], v0[1], v1[1], qa[i][0], qa[i][1]);
+            mma16816(x[bk], v0[2], v1[2], v0[3], v1[3], qa[i][2], qa[i][3]);
           }
         }
-        // scores of row n8: tokens 2 t4, 2 t4 + 1 of both octets
-        float x[4] = {sc[0][0] * sl2, sc[0][1] * sl2, sc[1][0] * sl2, sc[1][1] * sl2};
-        const bool tail = t0 + kBlk - 1 > all_see;
-        if (tail) {
+        const bool special = t0 + kStep - 1 > all_see || gd != 3u;
+        if (special) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (t0 + 8 * (e >> 1) + 2 * t4 + (e & 1) > last) x[e] = -INFINITY;
+          for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t0 + 16 * bk + 2 * n8 + (e >> 1) > ((e & 1) ? see1 : see0) ||
+                  !((gd >> bk) & 1u))
+                x[bk][e] = -INFINITY;
         }
-        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        if (__any_sync(kFull, mx > m + kLazy)) {
-          float mn = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-          mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 2));
-          mn = fmaxf(m, mn);
-          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+        const float mx0 = sc.x * fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+        const float mx1 = sc.y * fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+        if (__any_sync(kFull, mx0 > m.x + kLazy || mx1 > m.y + kLazy)) {
+          float2 mn = make_float2(mx0, mx1);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            mn.x = fmaxf(mn.x, __shfl_xor_sync(kFull, mn.x, d));
+            mn.y = fmaxf(mn.y, __shfl_xor_sync(kFull, mn.y, d));
+          }
+          mn.x = fmaxf(m.x, mn.x);
+          mn.y = fmaxf(m.y, mn.y);
+          const float f0 = m.x == -INFINITY ? 0.f : ex2(m.x - mn.x);
+          const float f1 = m.y == -INFINITY ? 0.f : ex2(m.y - mn.y);
           m = mn;
-          l *= f;
+          l.x *= f0;
+          l.y *= f1;
+          // row n8's factor
+          const float g0 = __shfl_sync(kFull, f0, n8 >> 1), g1 = __shfl_sync(kFull, f1, n8 >> 1);
+          const float f = (n8 & 1) ? g1 : g0;
 #pragma unroll
           for (int i = 0; i < I; ++i)
 #pragma unroll
@@ -364,60 +442,59 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[i][r][e] *= f;
         }
-        const float base = m == -INFINITY ? 0.f : m;
-        float p[4];
+        const float2 base = make_float2(m.x == -INFINITY ? 0.f : -m.x,
+                                        m.y == -INFINITY ? 0.f : -m.y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2(x[e] - base);
-          l += p[e];
-        }
-        uint32_t hi[2], lo[2];
+        for (int bk = 0; bk < 2; ++bk) {
+          // weights as fp16 hi + lo of the even (0) and the odd (1) tokens
+          uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const __half2 hh = __floats2half2_rn(p[2 * e], p[2 * e + 1]);
-          const float2 hf = __half22float2(hh);
-          hi[e] = h2_bits(hh);
-          lo[e] = h2_bits(__floats2half2_rn(p[2 * e] - hf.x, p[2 * e + 1] - hf.y));
-        }
-        uint32_t vw[2][I];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const unsigned char *vp = st + off_vc(D, G) + (32 * hf + lane) * (4 * I);
-          if constexpr (I == 4) {
-            const uint4 y = *reinterpret_cast<const uint4 *>(vp);
-            vw[hf][0] = y.x; vw[hf][1] = y.y; vw[hf][2] = y.z; vw[hf][3] = y.w;
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2 *>(vp);
-            vw[hf][0] = y.x; vw[hf][1] = y.y;
+          for (int e = 0; e < 2; ++e) {
+            const float2 y = __ffma2_rn(make_float2(x[bk][2 * e], x[bk][2 * e + 1]), sc, base);
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            l = __fadd2_rn(l, p);
+            const __half2 hh = __floats2half2_rn(p.x, p.y);
+            const float2 hf = __half22float2(hh);
+            hi[e] = turn(h2_bits(hh));
+            lo[e] = turn(h2_bits(__floats2half2_rn(p.x - hf.x, p.y - hf.y)));
           }
-        }
-        const uint2 *vm = reinterpret_cast<const uint2 *>(st + off_vm(D, G)) + t4 * NG;
-        // tokens behind the sequence hold anything: their values become 0
-        unsigned keep[2] = {kFull, kFull};
-        if (tail) {
+          // row n8's weights of token pairs 2 t4 and 2 t4 + 1
+          const uint32_t a0 = __byte_perm(hi[0], hi[1], 0x5410),
+                         a1 = __byte_perm(lo[0], lo[1], 0x5410),
+                         a2 = __byte_perm(hi[0], hi[1], 0x7632),
+                         a3 = __byte_perm(lo[0], lo[1], 0x7632);
+          const unsigned char *blk = st + bk * BLK;
+          uint32_t vw[2][I];
+          uint2 vm[2][NG];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int tp = t0 + 8 * hf + 2 * t4;
-            keep[hf] = (tp < L.len ? 0x0000ffffu : 0u) | (tp + 1 < L.len ? 0xffff0000u : 0u);
+          for (int j = 0; j < 2; ++j) {
+            const int pair = 2 * t4 + j;
+            load_words<I>(blk + off_vc(D, G) + ((8 * (pair >> 2) + n8) * 4 + (pair & 3)) * (4 * I),
+                          vw[j]);
+            load_meta<NG>(blk + off_vm(D, G) + pair * (8 * NG), vm[j]);
           }
-        }
-        __half2 vs[2], vz[2];
+          if (special) {
+            // tokens behind the sequence hold anything: their values become 0
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-          if ((32 * i) % G == 0) {
+            for (int j = 0; j < 2; ++j) {
+              const int tp = t0 + 16 * bk + 2 * (2 * t4 + j);
+              unsigned keep = (tp < L.len ? 0x0000ffffu : 0u) | (tp + 1 < L.len ? 0xffff0000u : 0u);
+              if (!((gd >> bk) & 1u)) keep = 0u;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint2 y = vm[4 * hf * NG + 32 * i / G];
-              vs[hf] = bits_h2(y.x & keep[hf]);
-              vz[hf] = bits_h2(y.y & keep[hf]);
+              for (int g = 0; g < NG; ++g) {
+                vm[j][g].x &= keep;
+                vm[j][g].y &= keep;
+              }
             }
           }
-          uint32_t v0[4], v1[4];
-          word_values(vw[0][i], vs[0], vz[0], v0);
-          word_values(vw[1][i], vs[1], vz[1], v1);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            mma16816(o[i][r], hi[0], lo[0], hi[1], lo[1], v0[r], v1[r]);
+          for (int i = 0; i < I; ++i) {
+            uint32_t v0[4], v1[4];
+            word_values(vw[0][i], bits_h2(vm[0][32 * i / G].x), bits_h2(vm[0][32 * i / G].y), v0);
+            word_values(vw[1][i], bits_h2(vm[1][32 * i / G].x), bits_h2(vm[1][32 * i / G].y), v1);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mma16816(o[i][r], a0, a1, a2, a3, v0[r], v1[r]);
+          }
         }
       }
       // every lane has read the stage
@@ -426,10 +503,17 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
       s = s + 1 == ST ? 0 : s + 1;
     }
     // the partial of this (sequence, kv head): row n8's channels 32 i + 8 t4 ...
-    l += __shfl_xor_sync(kFull, l, 1);
-    l += __shfl_xor_sync(kFull, l, 2);
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      l.x += __shfl_xor_sync(kFull, l.x, d);
+      l.y += __shfl_xor_sync(kFull, l.y, d);
+    }
+    float *first = t.ws + (int64_t)(w + b * H + h) * (t.max_new * GQ) * Part<D>::ROW;
+    if (n8 < 2 && 2 * t4 + n8 < rows)
+      *reinterpret_cast<float2 *>(first + (2 * t4 + n8) * Part<D>::ROW + D) =
+          n8 ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
     if (n8 < rows) {
-      float *part = t.ws + ((int64_t)(w + b * H + h) * (t.max_new * GQ) + n8) * Part<D>::ROW;
+      float *part = first + n8 * Part<D>::ROW;
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         float4 c0, c1;
@@ -440,17 +524,16 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
         reinterpret_cast<float4 *>(part + 32 * i + 8 * t4)[0] = c0;
         reinterpret_cast<float4 *>(part + 32 * i + 8 * t4)[1] = c1;
       }
-      if (t4 == 0) *reinterpret_cast<float2 *>(part + D) = make_float2(m, l);
     }
-    // the next head or sequence with blocks
-    if (h + 1 == H) {
-      do { ++b; } while (b < a.B && prefix[b + 1] == prefix[b]);
+    // the next head or sequence with steps
+    if (h + 1 == H && u < u_end) {
+      do { ++b; } while (prefix[b + 1] == prefix[b]);
     }
   }
   if (dead) {
     // let the copies in flight land before the CTA's memory is given up
     for (int i = 0; i < ST; ++i)
-      if ((ok_mask >> i) & 1u) mbar_wait(&bar[i], (phases >> i) & 1u);
+      if ((good >> (2 * i)) & 3u) mbar_wait(&bar[i], (phases >> i) & 1u);
   }
 }
 
@@ -468,7 +551,7 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max) {
   __shared__ int wsum[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  block_prefix(a, t.max_new, prefix, wsum);
+  step_prefix(a, t.max_new, prefix, wsum);
   const int H = a.H_kv, GQ = a.H_q / H, R = t.max_new * GQ;
   const int row = blockIdx.x % R, seg = blockIdx.x / R, b = seg / H, h = seg % H;
   const Lengths L = lengths_of(a, b, t.max_new);
@@ -535,7 +618,8 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max) {
   }
 }
 
-int decode_ctas(int sm_count) { return 4 * sm_count; }
+// CTAs of one wave
+int decode_ctas(int D, int sm_count) { return (D == 128 ? 3 : 4) * sm_count; }
 
 template <typename T, int D, int NG>
 cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
@@ -545,7 +629,7 @@ cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
   cudaError_t e = cudaFuncSetAttribute(k_paged_decode<T, D, NG>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int ctas = decode_ctas(sm_count), warps_max = ctas * kWarps;
+  const int ctas = decode_ctas(D, sm_count), warps_max = ctas * kWarps;
   e = launch_pdl(k_paged_decode<T, D, NG>, dim3(ctas), dim3(kThreads), smem, st, a, t,
                  warps_max);
   count_launch();
@@ -572,7 +656,7 @@ cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_cou
 }  // namespace
 
 size_t paged_decode_ws(int B, int H_kv, int D, int rows, int sm_count) {
-  return ((size_t)decode_ctas(sm_count) * kWarps + (size_t)B * H_kv) * rows * (D + 4) *
+  return ((size_t)decode_ctas(D, sm_count) * kWarps + (size_t)B * H_kv) * rows * (D + 4) *
          sizeof(float);
 }
 
