@@ -105,6 +105,8 @@ def lib_path() -> str:
 
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -14,8 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .cache import _stream_handle
-from .rope import DTYPES, Rope, _on, _positions, _rows
+from .rope import DTYPES, Rope, _current_device, _on, _positions, _raw_stream, _rows
 
 
 class PagedKiviCache:
@@ -51,27 +50,39 @@ class PagedKiviCache:
         self.pool, self.device = pool, pool.device
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._spec.pool, self._spec.status = pool.data_ptr(), self._status.data_ptr()
+        self._lib, self._index = L, self.device.index
+        self._ws = {}      # workspace bytes by (B, max_new)
 
     # -- arguments -------------------------------------------------------------
 
-    def _batch(self, table, lens, cu_new, tokens: int) -> _lib.PagedBatch:
-        dev = self.device
+    def _check_batch(self, table, lens, cu_new):
+        """Say what is wrong with a batch, or nothing."""
         for t, name in ((table, "table"), (lens, "lens"), (cu_new, "cu_new")):
-            if t is not None and (t.dtype != torch.int32 or t.device != dev):
-                raise ValueError(f"{name} must be int32 on {dev}")
+            if t is not None and (t.dtype != torch.int32 or t.device != self.device):
+                raise ValueError(f"{name} must be int32 on {self.device}")
         if lens.dim() != 1 or not lens.is_contiguous():
             raise ValueError("lens must be a contiguous [B]")
         B = lens.shape[0]
         if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and
                                                        table.stride(1) != 1):
             raise ValueError(f"table must be [{B}][max_pages] with contiguous rows")
-        if cu_new is None:
-            if tokens != B:
-                raise ValueError(f"without cu_new every sequence has one new token: {tokens} "
-                                 f"rows for {B} sequences")
-        elif tuple(cu_new.shape) != (B + 1,) or not cu_new.is_contiguous():
+        if cu_new is not None and (tuple(cu_new.shape) != (B + 1,) or
+                                   not cu_new.is_contiguous()):
             raise ValueError(f"cu_new must be a contiguous [{B + 1}]")
-        mp = table.shape[1]
+
+    def _batch(self, table, lens, cu_new, tokens: int) -> _lib.PagedBatch:
+        dev, i32, ts, ls = self.device, torch.int32, table.shape, lens.shape
+        B = ls[0] if len(ls) == 1 else -1
+        if not (len(ts) == 2 and ts[0] == B and table.stride(1) == 1 and lens.is_contiguous() and
+                table.dtype is i32 and lens.dtype is i32 and table.device == dev and
+                lens.device == dev and
+                (cu_new is None or (cu_new.dtype is i32 and cu_new.device == dev and
+                                    cu_new.shape == (B + 1,) and cu_new.is_contiguous()))):
+            self._check_batch(table, lens, cu_new)
+        if cu_new is None and tokens != B:
+            raise ValueError(f"without cu_new every sequence has one new token: {tokens} rows "
+                             f"for {B} sequences")
+        mp = ts[1]
         return _lib.PagedBatch(B, mp, table.data_ptr() or None,
                                table.stride(0) if B > 1 else max(mp, 1), lens.data_ptr() or None,
                                None if cu_new is None else cu_new.data_ptr(), tokens)
@@ -79,12 +90,13 @@ class PagedKiviCache:
     def _dtype(self, t: torch.Tensor, name: str) -> int:
         if not t.is_cuda or t.device != self.device:
             raise ValueError(f"{name} must be a CUDA tensor on {self.device}")
-        if t.dtype not in (torch.float16, torch.bfloat16):
-            raise ValueError(f"{name} must be fp16 or bf16, got {t.dtype}")
-        return DTYPES[t.dtype]
+        dt = t.dtype
+        if dt is not torch.float16 and dt is not torch.bfloat16:
+            raise ValueError(f"{name} must be fp16 or bf16, got {dt}")
+        return DTYPES[dt]
 
     def _elsewhere(self, stream) -> bool:
-        return stream is not None or self.device.index != torch.cuda.current_device()
+        return stream is not None or self._index != _current_device()
 
     # -- steps -------------------------------------------------------------------
 
@@ -106,33 +118,36 @@ class PagedKiviCache:
                 return self.append(k, v, table, lens, cu_new, q=q, rope=rope,
                                    positions=positions, q_weight=q_weight, k_weight=k_weight,
                                    eps=eps, q_out=q_out)
-        dt = self._dtype(k, "k")
+        dt, dtype, device = self._dtype(k, "k"), k.dtype, self.device
         if k.shape != v.shape:
             raise ValueError("k and v must have one shape")
         T = k.shape[0]
-        rk = _rows(k, self.H_kv, self.D, k.dtype, self.device, "k", k_weight)
-        rv = _rows(v, self.H_kv, self.D, k.dtype, self.device, "v")
+        rk = _rows(k, self.H_kv, self.D, dtype, device, "k", k_weight)
+        rv = _rows(v, self.H_kv, self.D, dtype, device, "v")
         rq = None
         if q is not None:
             if q.shape[0] != T:
                 raise ValueError(f"q has {q.shape[0]} tokens, k {T}")
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            rq = _rows(q, self.H_q, self.D, k.dtype, self.device, "q", q_weight, q_out)
+            fresh = q_out is None
+            if fresh:
+                q_out = torch.empty(q.shape, dtype=dtype, device=device)
+            rq = _rows(q, self.H_q, self.D, dtype, device, "q", q_weight, q_out, fresh)
         elif q_weight is not None or q_out is not None:
             raise ValueError("q_weight or q_out without q")
         batch = self._batch(table, lens, cu_new, T)
-        pos, pos64, pstride = 0, 0, 0
+        pos, pos64, pstride = None, 0, 0
         if rope is not None:
-            if rope.device != self.device:
-                raise ValueError(f"the rope is on {rope.device}, the cache on {self.device}")
+            if rope.device != device:
+                raise ValueError(f"the rope is on {rope.device}, the cache on {device}")
             if positions is not None:
-                pos, pos64, pstride = _positions(positions, rope.n_axes, T, self.device)
+                pos, pos64, pstride = _positions(positions, rope.n_axes, T, device)
         elif positions is not None:
             raise ValueError("positions without a rope")
-        _lib.check(_lib.load().vq_kivi_paged_append(
-            self._spec, batch, dt, rq, rk, rv, None if rope is None else rope.spec, pos or None,
-            pos64, pstride, float(eps), _stream_handle(None, self.device.index)))
+        rc = self._lib.vq_kivi_paged_append(
+            self._spec, batch, dt, rq, rk, rv, None if rope is None else rope.spec, pos, pos64,
+            pstride, eps, _raw_stream(self._index))
+        if rc:
+            _lib.check(rc)
         return q_out
 
     def attend(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -146,23 +161,29 @@ class PagedKiviCache:
         if self._elsewhere(stream):
             with _on(self.device, stream):
                 return self.attend(q, table, lens, cu_new, max_new=max_new, scale=scale, out=out)
-        dt = self._dtype(q, "q")
-        T = q.shape[0]
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dt, shape = self._dtype(q, "q"), q.shape
+        fresh = out is None
+        if fresh:
+            out = torch.empty(shape, dtype=q.dtype, device=self.device)
         elif not out.is_contiguous():
             raise ValueError("out must be contiguous")
-        rq = _rows(q, self.H_q, self.D, q.dtype, self.device, "q", None, out)
+        rq = _rows(q, self.H_q, self.D, q.dtype, self.device, "q", None, out, fresh)
         rq.out_token, rq.out_head = self.H_q * self.D, self.D
-        batch = self._batch(table, lens, cu_new, T)
+        batch = self._batch(table, lens, cu_new, shape[0])
         if max_new is None:
-            max_new = 1 if cu_new is None else max(T, 1)
-        L = _lib.load()
-        nbytes = L.vq_kivi_paged_workspace_bytes(self._spec, batch.B, int(max_new))
+            max_new = 1 if cu_new is None else max(shape[0], 1)
+        key = (batch.B, max_new)
+        nbytes = self._ws.get(key)
+        if nbytes is None:
+            nbytes = self._lib.vq_kivi_paged_workspace_bytes(self._spec, batch.B, int(max_new))
+            if nbytes and len(self._ws) < 4096:
+                self._ws[key] = nbytes
         ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        _lib.check(L.vq_kivi_paged_attend(
-            self._spec, batch, dt, rq, int(max_new), float(scale), ws.data_ptr(), nbytes,
-            _stream_handle(None, self.device.index)))
+        rc = self._lib.vq_kivi_paged_attend(
+            self._spec, batch, dt, rq, int(max_new), scale, ws.data_ptr(), nbytes,
+            _raw_stream(self._index))
+        if rc:
+            _lib.check(rc)
         return out
 
     def dequantize(self, table: torch.Tensor, lens: torch.Tensor,
@@ -182,21 +203,23 @@ class PagedKiviCache:
         if out is None:
             out = (torch.empty(shape, dtype=torch.float16, device=self.device),
                    torch.empty(shape, dtype=torch.float16, device=self.device))
+        else:
+            for t in out:
+                if tuple(t.shape) != shape or t.dtype != torch.float16 or \
+                        t.device != self.device or not t.is_contiguous():
+                    raise ValueError(f"outputs must be contiguous fp16 {list(shape)} on "
+                                     f"{self.device}")
         K, V = out
-        for t in out:
-            if tuple(t.shape) != shape or t.dtype != torch.float16 or \
-                    t.device != self.device or not t.is_contiguous():
-                raise ValueError(f"outputs must be contiguous fp16 {list(shape)} on "
-                                 f"{self.device}")
         batch = self._batch(table, lens, cu_new, shape[0])
-        _lib.check(_lib.load().vq_kivi_paged_dequantize(
+        rc = self._lib.vq_kivi_paged_dequantize(
             self._spec, batch, K.data_ptr() or None, V.data_ptr() or None,
-            _stream_handle(None, self.device.index)))
+            _raw_stream(self._index))
+        if rc:
+            _lib.check(rc)
         return K, V
 
     def status(self):
         """Raise if a kernel since the last check found a page or a length
         outside its range, or gave up a wait (synchronizes)."""
         with torch.cuda.device(self.device):
-            _lib.check(_lib.load().vq_kivi_paged_status(
-                self._spec, _stream_handle(None, self.device.index)))
+            _lib.check(self._lib.vq_kivi_paged_status(self._spec, _raw_stream(self._index)))

@@ -16,7 +16,13 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from .cache import _stream_handle
+
+# the current stream's handle and the current device without the objects that
+# torch.cuda builds
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 _TWO_PI = Fraction("6.28318530717958647692528676655900576839433879875021164194988918")
 DTYPES = {torch.float16: _lib.F16, torch.bfloat16: _lib.BF16, torch.float32: _lib.F32}
@@ -76,10 +82,8 @@ class Rope:
                                   self.turns.data_ptr(), self.axis.data_ptr())
 
 
-def _rows(t: torch.Tensor, heads: Optional[int], D: Optional[int], dtype, device, name: str,
-          weight: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> _lib.Rows:
-    """The C description of rows [tokens][heads][D] (last dimension
-    contiguous)."""
+def _check_rows(t, heads, D, dtype, device, name, weight, out):
+    """Say what is wrong with rows, or nothing."""
     if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (
             D is not None and t.shape[2] != D):
         raise ValueError(f"{name} must be [tokens][{heads or 'heads'}][{D or 'D'}], got "
@@ -98,8 +102,6 @@ def _rows(t: torch.Tensor, heads: Optional[int], D: Optional[int], dtype, device
             raise ValueError(f"{what}: the last dimension must be contiguous")
     if weight is not None and tuple(weight.shape) != (D,):
         raise ValueError(f"{name}_weight must be [{D}], got {tuple(weight.shape)}")
-    s0, s1 = (t.stride(0) if T > 1 else 0), (t.stride(1) if H > 1 else 0)
-    o0 = o1 = po = 0
     if out is not None:
         if out.shape != t.shape:
             raise ValueError(f"{name}_out must be {tuple(t.shape)}, got {tuple(out.shape)}")
@@ -107,22 +109,41 @@ def _rows(t: torch.Tensor, heads: Optional[int], D: Optional[int], dtype, device
         if out.numel() and ((T > 1 and o0 < D) or (H > 1 and o1 < D) or (
                 T > 1 and H > 1 and o0 < (H - 1) * o1 + D and o1 < (T - 1) * o0 + D)):
             raise ValueError(f"{name}_out: rows overlap")
-        po = out.data_ptr()
-    return _lib.Rows(t.data_ptr(), po, None if weight is None else weight.data_ptr(), s0, s1,
-                     o0, o1, H)
+
+
+def _rows(t: torch.Tensor, heads: Optional[int], D: Optional[int], dtype, device, name: str,
+          weight: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+          fresh: bool = False) -> _lib.Rows:
+    """The C description of rows [tokens][heads][D] (last dimension
+    contiguous).  fresh: `out` was just made for these rows."""
+    shape, st = t.shape, t.stride()
+    # what nearly every call passes, in few steps; anything else is looked at
+    # one by one
+    if not (len(shape) == 3 and (heads is None or shape[1] == heads) and
+            (D is None or shape[2] == D) and t.dtype is dtype and t.device == device and
+            not t.requires_grad and st[2] == 1 and (out is None or fresh) and
+            (weight is None or (weight.dtype is dtype and weight.device == device and
+                                weight.shape == shape[2:] and not weight.requires_grad and
+                                weight.is_contiguous()))):
+        _check_rows(t, heads, D, dtype, device, name, weight, out)
+    T, H, _ = shape
+    po, so = (0, (0, 0)) if out is None else (out.data_ptr(), out.stride())
+    # the stride of a dimension of one element may be anything
+    t1, h1 = T > 1, H > 1
+    return _lib.Rows(t.data_ptr(), po, None if weight is None else weight.data_ptr(),
+                     st[0] if t1 else 0, st[1] if h1 else 0, so[0] if t1 else 0,
+                     so[1] if h1 else 0, H)
 
 
 def _positions(p: torch.Tensor, n_axes: int, T: int, device):
-    if p.dim() == 1 and n_axes == 1:
-        p = p[None]
-    if tuple(p.shape) != (n_axes, T):
-        raise ValueError(f"positions must be [{n_axes}][{T}], got {tuple(p.shape)}")
-    if p.device != device or p.dtype not in (torch.int32, torch.int64):
+    shape, st, dt = p.shape, p.stride(), p.dtype
+    if not (shape == (n_axes, T) or (n_axes == 1 and shape == (T,))):
+        raise ValueError(f"positions must be [{n_axes}][{T}], got {tuple(shape)}")
+    if p.device != device or (dt is not torch.int64 and dt is not torch.int32):
         raise ValueError(f"positions must be int32 or int64 on {device}")
-    if T > 1 and p.stride(1) != 1:
+    if T > 1 and st[-1] != 1:
         raise ValueError("positions: the last dimension must be contiguous")
-    return (p.data_ptr(), int(p.dtype == torch.int64),
-            p.stride(0) if n_axes > 1 else T)
+    return p.data_ptr() or None, int(dt is torch.int64), st[0] if n_axes > 1 else T
 
 
 @contextlib.contextmanager
@@ -147,12 +168,13 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[to
     fp32, any token and head strides -> (q_out, k_out).  positions: int32 or
     int64 [T], or [n_axes][T] (unused without a rope).  The outputs may be the
     inputs themselves."""
+    dt, device = q.dtype, q.device
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    if q.dtype not in DTYPES:
-        raise ValueError(f"q must be fp16, bf16 or fp32, got {q.dtype}")
-    if stream is not None or q.device.index != torch.cuda.current_device():
-        with _on(q.device, stream):
+    if dt not in DTYPES:
+        raise ValueError(f"q must be fp16, bf16 or fp32, got {dt}")
+    if stream is not None or device.index != _current_device():
+        with _on(device, stream):
             return norm_rope(q, k, positions, rope, q_weight=q_weight, k_weight=k_weight,
                              eps=eps, q_out=q_out, k_out=k_out)
     if q.dim() != 3:
@@ -162,21 +184,25 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[to
         raise ValueError(f"k must be [{T}][heads][{D}], got {tuple(k.shape)}")
     if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight or k_out without k")
+    fq = fk = False
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    rq = _rows(q, None, None, q.dtype, q.device, "q", q_weight, q_out)
-    rk = None if k is None else _rows(k, None, D, q.dtype, q.device, "k", k_weight, k_out)
-    pos, pos64, pstride = 0, 0, 0
+        q_out, fq = torch.empty(q.shape, dtype=dt, device=device), True
+    rk = None
+    if k is not None:
+        if k_out is None:
+            k_out, fk = torch.empty(k.shape, dtype=dt, device=device), True
+        rk = _rows(k, None, D, dt, device, "k", k_weight, k_out, fk)
+    rq = _rows(q, None, None, dt, device, "q", q_weight, q_out, fq)
+    pos, pos64, pstride = None, 0, 0
     if rope is not None and rope.rot_dim > 0:
-        if rope.device != q.device:
-            raise ValueError(f"the rope is on {rope.device}, q on {q.device}")
+        if rope.device != device:
+            raise ValueError(f"the rope is on {rope.device}, q on {device}")
         if positions is None:
             raise ValueError("positions are needed for the rotation")
-        pos, pos64, pstride = _positions(positions, rope.n_axes, T, q.device)
-    _lib.check(_lib.load().vq_kivi_norm_rope(
-        DTYPES[q.dtype], T, D, ctypes.byref(rq), None if rk is None else ctypes.byref(rk),
-        None if rope is None else ctypes.byref(rope.spec), pos or None, pos64, pstride,
-        float(eps), _stream_handle(None, q.device.index)))
+        pos, pos64, pstride = _positions(positions, rope.n_axes, T, device)
+    rc = _lib.load().vq_kivi_norm_rope(
+        DTYPES[dt], T, D, rq, rk, None if rope is None else rope.spec, pos, pos64, pstride, eps,
+        _raw_stream(device.index))
+    if rc:
+        _lib.check(rc)
     return q_out, k_out
