@@ -4,23 +4,26 @@
 //   out = sum_t softmax_t(scale q.k_hat_t) v_hat_t,  t <= the row's own token
 //
 // Rows: 128 (new token, query head) pairs of a kv head make a query tile, two
-// tiles a pair; a pair shares the keys that it walks, 128 at a time.  The
-// work is one line of key tiles over (sequence, kv head, pair, key tile), cut
-// evenly among one CTA per SM whatever the lengths, so no plan on the host; a
-// pair that is cut leaves partial rows, which a second kernel merges.
+// tiles a pair; a pair walks its keys 128 at a time.  The work is one line of
+// key tiles over (sequence, kv head, pair, key tile), cut evenly among one CTA
+// per SM whatever the lengths, so no plan on the host; a pair that is cut
+// leaves partial rows, which a second kernel merges.
 //
-// A CTA's 16 warps:
-//   0-3, 4-7   softmax of query tile 0 and 1, one row a thread: scores from
-//              tensor memory, online softmax in fp32, weights back to tensor
-//              memory in fp16 (the A operand of the second product), the
-//              output read out at the end.  Rounding a weight to fp16 moves
-//              it by 2^-12 of itself at most, as one rounding of a 16-bit
-//              output does.
-//   8-11       rebuild k_hat and v_hat (fp16 by definition) from the codes,
-//              into two 128-byte-swizzled stages of each
-//   12         issues the products: S = Q k_hat^T, then O += P v_hat; while
-//              one query tile is in its softmax the other is multiplied
-//   13         copies the blocks (one bulk copy each), 64 tokens a stage
+// A CTA works in two slots, so that one is multiplied while the other is in
+// its softmax: the two query tiles of a pair, or, where the second would be
+// empty, the even and the odd key tiles of one query tile (joined at the
+// end).  Its warps:
+//   0-3, 4-7   softmax of slot 0 and 1, one row a thread: scores from tensor
+//              memory, online softmax in fp32, weights back to tensor memory
+//              in fp16 (the A operand of the second product), the output
+//              read out at the end.  Rounding a weight to fp16 moves it by
+//              2^-12 of itself at most, as one rounding of a 16-bit output
+//              does.
+//   8-11       rebuild k_hat (fp16 by definition) from the codes into two
+//   12-15      128-byte-swizzled stages, and v_hat likewise
+//   16         issues the products: S = Q k_hat^T, then O += P v_hat
+//   17, 18     copy the key and the value halves of the blocks (one bulk copy
+//              each), 64 tokens a stage
 // The running maximum of a row is raised only when it grows by more than 8
 // (base 2), so that O is rarely rescaled; a weight stays below 2^8.
 //
@@ -35,13 +38,13 @@
 namespace vqk {
 namespace chunk {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLazy = 8.f;
 constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
-constexpr int kSlices = 16;          // CTAs that merge one pair's 256 rows
+constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes
 
 __device__ __forceinline__ uint32_t saddr(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -56,6 +59,14 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) {
 }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) {
   return *reinterpret_cast<const __half2 *>(&u);
+}
+
+// (w & mask) | 0x64006400 in one instruction: 0x6400 | c is 1024 + c
+template <uint32_t mask>
+__device__ __forceinline__ __half2 field(uint32_t w) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(mask), "r"(0x64006400u));
+  return bits_h2(d);
 }
 
 // ---- barriers ----------------------------------------------------------------
@@ -224,14 +235,19 @@ __device__ __forceinline__ int ctas_used(long long units, int ctas) {
   const long long c = (units + kMinTiles - 1) / kMinTiles;
   return (int)(c < ctas ? c : ctas);
 }
-__device__ __forceinline__ long long first_unit(long long units, int ctas, int c) {
-  return units / ctas * c + units % ctas * c / ctas;
-}
+// the line's pieces differ by one tile at most
+struct Cut {
+  long long each;
+  int more;
+  __device__ Cut(long long units, int ctas) : each(units / ctas), more((int)(units % ctas)) {}
+  __device__ long long first(int c) const { return each * c + (c < more ? c : more); }
+};
 
 struct Item {
   Seq s;
   int b, h, pair;
   int k0, k1, nk;   // key tiles [k0, k1) of nk
+  bool two;         // both query tiles have rows
 };
 
 struct Walk {
@@ -269,6 +285,7 @@ struct Walk {
     it.h = h;
     it.pair = pair;
     it.nk = tiles_of(s, pair, tpt);
+    it.two = pair * 2 * tpt + tpt < s.n;
     it.k0 = k;
     it.k1 = (int)min((long long)it.nk, k + (end - u));
     u += it.k1 - it.k0;
@@ -293,7 +310,7 @@ template <int D, int NG>
 struct Smem {
   static constexpr int KB = D / 64;
   static constexpr int OP = KB * 16384;            // one 128 x D fp16 operand
-  static constexpr int BLK = 16 * D + 128 * NG;
+  static constexpr int BLK = 16 * D + 128 * NG, HALF = BLK / 2;   // keys, values
   static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, RAW = 6 * OP;
   static constexpr int BAR = RAW + kRaw * 4 * BLK;
   static constexpr int ALLOC = BAR + 512 + 1024;   // room to align the base
@@ -303,18 +320,18 @@ struct Smem {
 __device__ __forceinline__ int sw(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t raw_full[2][kRaw], raw_empty[2][kRaw];   // keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  uint64_t drain;
-  uint32_t good[kRaw];    // which of a stage's 4 blocks arrived
+  uint64_t x_full, drain;
+  uint32_t good[2][kRaw];   // which of a stage's 4 blocks arrived
   uint32_t tmem;
   int dead;
 };
 
 template <typename T, int D, int NG>
 __global__ void __launch_bounds__(kThreads, 1)
-k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
+k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *prefixes) {
   using SM = Smem<D, NG>;
   constexpr int I = D / 32, G = D / NG, KB = SM::KB, BLK = SM::BLK;
   extern __shared__ unsigned char smem_raw[];
@@ -324,9 +341,9 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
   if (tid == 0) {
-    for (int i = 0; i < kRaw; ++i) {
-      bar_init(&B.raw_full[i], 1);
-      bar_init(&B.raw_empty[i], 4);
+    for (int i = 0; i < 2 * kRaw; ++i) {
+      bar_init(&B.raw_full[0][0] + i, 1);
+      bar_init(&B.raw_empty[0][0] + i, 4);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&B.k_full[i], 4);
@@ -338,6 +355,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
       bar_init(&B.p_full[i], 4);
       bar_init(&B.o_full[i], 1);
     }
+    bar_init(&B.x_full, 4);
     bar_init(&B.drain, 1);
     B.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -361,21 +379,27 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
   Item it;
   const bool busy = (int)blockIdx.x < ctas;
   walk.u = walk.end = 0;
-  if (busy)
-    walk.seek(a, prefix, first_unit(units, ctas, blockIdx.x),
-              first_unit(units, ctas, blockIdx.x + 1), t.max_new, tpt);
+  if (busy) {
+    const Cut cut(units, ctas);
+    walk.seek(a, prefix, cut.first(blockIdx.x), cut.first(blockIdx.x + 1), t.max_new, tpt);
+  }
 
   if (warp < 8) {
     // ---- softmax ----
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
-    uint32_t ph_s = 0, ph_o = 0;
+    uint32_t ph_s = 0, ph_o = 0, ph_x = 0;
     float sl2 = 0.f;
+    // query row of this thread, of the slot's query tile
+    auto token = [&](const Item &x) {
+      return x.pair * 2 * tpt + (x.two ? wg * tpt : 0) + row / GQ;
+    };
+    auto has_row = [&](const Item &x) { return row < tpt * GQ && token(x) < x.s.n; };
     // this thread's query row into shared memory
     auto load_q = [&](const Item &x) {
-      const int tok = x.pair * 2 * tpt + wg * tpt + row / GQ;
-      const bool valid = row < tpt * GQ && tok < x.s.n;
+      const int tok = token(x);
+      const bool valid = has_row(x);
       const T *q = static_cast<const T *>(t.q) + (int64_t)(x.s.first + tok) * t.q_token +
                    (int64_t)(x.h * GQ + row % GQ) * t.q_head;
       sl2 = t.scale;
@@ -420,25 +444,35 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
       __syncwarp();
       if (lane == 0) bar_arrive(&B.q_full[wg]);
     };
-    // the next item of this query tile
+    // the next item that this slot works on
     auto fetch = [&](Item &x) {
       while (walk.next(a, prefix, t.max_new, tpt, x))
-        if (wg == 0 || x.pair * 2 * tpt + tpt < x.s.n) return true;
+        if (wg == 0 || x.two || x.k1 - x.k0 > 1) return true;
       return false;
     };
     bool have = fetch(it), ok = true;
     if (have) load_q(it);
     while (have && ok) {
-      const int tok = it.pair * 2 * tpt + wg * tpt + row / GQ;
-      const bool valid = row < tpt * GQ && tok < it.s.n;
-      const int pos = valid ? it.s.len - it.s.n + tok : -1;
+      const int tok = token(it);
+      const bool valid = has_row(it);
+      // warps without a row leave the weights as they are: their rows of the
+      // output are not read.  Rows without a query see everything.
+      const bool idle = !__any_sync(kFull, valid);
+      const int pos = valid ? it.s.len - it.s.n + tok : 0x3fffffff;
       const float scale = sl2;
       float m = -INFINITY, l = 0.f;
-      for (int kt = it.k0; kt < it.k1; ++kt) {
+      const int kfirst = it.k0 + (it.two ? 0 : wg), kstep = it.two ? 1 : 2;
+      for (int kt = kfirst; kt < it.k1; kt += kstep) {
         ok = bar_wait(&B.s_full[wg], ph_s, dead);
         ph_s ^= 1u;
         if (!__all_sync(kFull, ok)) { ok = false; break; }
         fence_after();
+        if (idle) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&B.p_full[wg]);
+          continue;
+        }
         const int vis = pos - kt * kTile;            // columns up to vis are seen
         const bool all = __all_sync(kFull, vis >= kTile - 1);
         uint32_t v[32];
@@ -463,7 +497,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
           m = mx;
           l *= f;
         }
-        if (kt > it.k0 && __any_sync(kFull, raise)) {
+        if (kt > kfirst && __any_sync(kFull, raise)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             tm_ld32(to + c, v);
@@ -502,7 +536,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
         if (lane == 0) bar_arrive(&B.p_full[wg]);
       }
       if (!ok) break;
-      // the next queries: this tile's last scores have been read
+      // the next queries: this slot's last scores have been read
       const Item done = it;
       have = fetch(it);
       if (have) load_q(it);
@@ -510,166 +544,199 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
       ph_o ^= 1u;
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
-      const bool whole = done.k0 == 0 && done.k1 == done.nk;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      float *pr = part + ((int64_t)(2 * blockIdx.x + (done.k0 > 0 ? 0 : 1)) * 2 * kTile +
-                          wg * kTile + row) * (D + 4);
-      T *orow = static_cast<T *>(t.out) +
-                ((int64_t)(done.s.first + tok) * a.H_q + done.h * GQ + row % GQ) * D;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t v[32];
-        __syncwarp();
-        tm_ld32(to + c, v);
-        if (valid && whole) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[j + e]) * inv;
-            store8<T>(orow + c + j, y);
-          }
-        } else if (valid) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4 *>(pr + c + j) =
-                make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      // slot 1 of a single query tile hands its sums to slot 0
+      const bool halves = !done.two && done.k1 - done.k0 > 1;
+      const bool give = halves && wg == 1;
+      float *xr = swap + ((int64_t)blockIdx.x * kTile + row) * (D + 4);
+      float f0 = 1.f, f1 = 0.f;
+      if (halves && wg == 0) {
+        ok = bar_wait(&B.x_full, ph_x, dead);
+        ph_x ^= 1u;
+        if (!__all_sync(kFull, ok)) { ok = false; break; }
+        if (valid) {
+          const float2 ml = *reinterpret_cast<const float2 *>(xr + D);
+          const float M = fmaxf(m, ml.x);
+          // a part without a seen token weighs nothing (NaN sums stay)
+          f0 = m == -INFINITY ? (l != l ? l : 0.f) : ex2(m - M);
+          f1 = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+          l = l * f0 + ml.y * f1;
+          m = M;
         }
       }
-      if (valid && !whole) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
+      const bool whole = done.k0 == 0 && done.k1 == done.nk;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float *pr = give ? xr
+                       : part + ((int64_t)(2 * blockIdx.x + (done.k0 > 0 ? 0 : 1)) * 2 * kTile +
+                                 (done.two ? wg * kTile : 0) + row) * (D + 4);
+      T *orow = static_cast<T *>(t.out) +
+                ((int64_t)(done.s.first + tok) * a.H_q + done.h * GQ + row % GQ) * D;
+      if (!idle) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tm_ld32(to + c, v);
+          if (halves && wg == 0 && valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(xr + c + j);
+              v[j] = __float_as_uint(__uint_as_float(v[j]) * f0 + x.x * f1);
+              v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f0 + x.y * f1);
+              v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f0 + x.z * f1);
+              v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f0 + x.w * f1);
+            }
+          }
+          if (valid && whole && !give) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[j + e]) * inv;
+              store8<T>(orow + c + j, y);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4 *>(pr + c + j) =
+                  make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          }
+        }
+        if (valid && (give || !whole)) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
+      }
       __syncwarp();
+      if (give && lane == 0) bar_arrive(&B.x_full);
       fence_before();
     }
-  } else if (warp < 12) {
-    // ---- k_hat and v_hat ----
-    const int w = warp - 8, n8 = lane >> 2, t4 = lane & 3;
+  } else if (warp < 16) {
+    // ---- k_hat (warps 8-11) and v_hat (12-15) ----
+    const int kv = (warp - 8) >> 2, w = warp & 3, n8 = lane >> 2, t4 = lane & 3;
+    uint64_t *full = kv ? B.v_full : B.k_full, *empty = kv ? B.v_empty : B.k_empty;
     uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
     bool ok = true;
     const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
                   k64 = bits_h2(0xd400d400u);
     while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
       for (int kt = it.k0; ok && kt < it.k1; ++kt) {
-        ok = bar_wait(&B.k_empty[st], ph_e, dead) && bar_wait(&B.v_empty[st], ph_e, dead);
-        unsigned char *kd = sm + SM::K + st * SM::OP, *vd = sm + SM::V + st * SM::OP;
+        ok = bar_wait(&empty[st], ph_e, dead);
+        unsigned char *dst = sm + (kv ? SM::V : SM::K) + st * SM::OP;
         for (int hf = 0; hf < 2; ++hf) {
-          ok = ok && bar_wait(&B.raw_full[raw], ph_raw, dead);
+          ok = ok && bar_wait(&B.raw_full[kv][raw], ph_raw, dead);
           if (!__all_sync(kFull, ok)) { ok = false; break; }
           // warp w takes block w of the stage
-          const unsigned char *blk = sm + SM::RAW + (raw * 4 + w) * BLK;
-          const bool good = (B.good[raw] >> w) & 1u;
+          const unsigned char *blk = sm + SM::RAW + ((kv * kRaw + raw) * 4 + w) * SM::HALF;
+          const bool good = (B.good[kv][raw] >> w) & 1u;
           const int r0 = 64 * hf + 16 * w;             // its first key in the tile
-          const int left = it.s.len - (kt * kTile + r0);   // its tokens in the sequence
+          if (!kv) {
 #pragma unroll
-          for (int oct = 0; oct < 2; ++oct) {
-            const int tk = 8 * oct + n8, r = r0 + tk;
-            uint32_t kw[I];
-            if constexpr (I == 4) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(blk + tk * (D / 2) + t4 * 16);
-              kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2 *>(blk + tk * (D / 2) + t4 * 8);
-              kw[0] = x.x; kw[1] = x.y;
-            }
-            const uint2 *km = reinterpret_cast<const uint2 *>(blk + off_km(D)) + (tk >> 1) * NG;
-            const unsigned sel = (tk & 1) ? 0x3232u : 0x1010u;
-            // neighbouring rows store the two halves of a 128-byte row in
-            // turn, so that 8 lanes' 16-byte stores meet 8 bank groups
-            const int odd = n8 & 1;
-#pragma unroll
-            for (int i2 = 0; i2 < I; ++i2) {
-              const int i = i2 ^ odd;
-              uint32_t x = odd ? kw[i2 ^ 1] : kw[i2];
-              const uint2 y = km[32 * i / G];
-              const __half2 s = bits_h2(good ? __byte_perm(y.x, 0u, sel) : 0u),
-                            z = bits_h2(good ? __byte_perm(y.y, 0u, sel) : 0u);
-              uint32_t o[4];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const __half2 c0 = __hsub2(bits_h2((x & 0x000f000fu) | 0x64006400u), k1024);
-                const __half2 c1 = __hfma2(bits_h2((x & 0x00f000f0u) | 0x64006400u), k16, k64);
-                o[2 * j] = h2_bits(__hfma2(c0, s, z));
-                o[2 * j + 1] = h2_bits(__hfma2(c1, s, z));
-                x >>= 8;
+            for (int oct = 0; oct < 2; ++oct) {
+              const int tk = 8 * oct + n8, r = r0 + tk;
+              uint32_t kw[I];
+              if constexpr (I == 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(blk + tk * (D / 2) + t4 * 16);
+                kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(blk + tk * (D / 2) + t4 * 8);
+                kw[0] = x.x; kw[1] = x.y;
               }
-              *reinterpret_cast<uint4 *>(kd + (i >> 1) * 16384 + sw(r, 4 * (i & 1) + t4)) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
-          // values: lane (n8, t4) reads the words of token pair t4, then the
-          // four lanes of n8 exchange them, so that lane j has the four pairs
-          // (8 tokens) of the 32-channel span j
+              const uint2 *km = reinterpret_cast<const uint2 *>(blk + off_km(D)) + (tk >> 1) * NG;
+              const unsigned sel = !good ? 0x4444u : (tk & 1) ? 0x3232u : 0x1010u;
+              // neighbouring rows store the two halves of a 128-byte row in
+              // turn, so that 8 lanes' 16-byte stores meet 8 bank groups
+              const int odd = n8 & 1;
 #pragma unroll
-          for (int oct = 0; oct < 2; ++oct) {
-            uint32_t x[4] = {0u, 0u, 0u, 0u};
-            const unsigned char *vp = blk + off_vc(D, G) + (32 * oct + lane) * (4 * I);
-            if constexpr (I == 4) {
-              const uint4 y = *reinterpret_cast<const uint4 *>(vp);
-              x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-            } else {
-              const uint2 y = *reinterpret_cast<const uint2 *>(vp);
-              x[0] = y.x; x[1] = y.y;
-            }
-            // 4 x 4 transposition over the lanes t4 in two exchanges
-            {
-              const bool o1 = t4 & 1, o2 = t4 & 2;
-              uint32_t s0 = o1 ? x[0] : x[1], s1 = o1 ? x[2] : x[3];
-              s0 = __shfl_xor_sync(kFull, s0, 1);
-              s1 = __shfl_xor_sync(kFull, s1, 1);
-              if (o1) { x[0] = s0; x[2] = s1; } else { x[1] = s0; x[3] = s1; }
-              s0 = o2 ? x[0] : x[2];
-              s1 = o2 ? x[1] : x[3];
-              s0 = __shfl_xor_sync(kFull, s0, 2);
-              s1 = __shfl_xor_sync(kFull, s1, 2);
-              if (o2) { x[0] = s0; x[1] = s1; } else { x[2] = s0; x[3] = s1; }
-            }
-            const int span = t4;
-            if (I == 4 || span < I) {
-              const uint2 *vm = reinterpret_cast<const uint2 *>(blk + off_vm(D, G)) +
-                                4 * oct * NG + 32 * span / G;
-              __half2 s[4], z[4];
-#pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                const uint2 y = vm[p * NG];
-                // tokens behind the sequence hold anything: their values are 0
-                const int e = left - (8 * oct + 2 * p);
-                const unsigned keep = !good || e <= 0 ? 0u : (e == 1 ? 0x0000ffffu : kFull);
-                s[p] = bits_h2(y.x & keep);
-                z[p] = bits_h2(y.y & keep);
-              }
-              const int chunk = 2 * w + oct;           // octet within the 64 tokens
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                // the lanes of a store differ in the channel's low bits
-                const int r = (q + span) & 3, c = 32 * span + 4 * n8 + r;
+              for (int i2 = 0; i2 < I; ++i2) {
+                const int i = i2 ^ odd;
+                uint32_t x = odd ? kw[i2 ^ 1] : kw[i2];
+                const uint2 y = km[32 * i / G];
+                const __half2 s = bits_h2(__byte_perm(y.x, 0u, sel)),
+                              z = bits_h2(__byte_perm(y.y, 0u, sel));
                 uint32_t o[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                  const __half2 cc =
-                      __hsub2(bits_h2(((x[p] >> (4 * r)) & 0x000f000fu) | 0x64006400u), k1024);
-                  o[p] = h2_bits(__hfma2(cc, s[p], z[p]));
+                for (int j = 0; j < 2; ++j) {
+                  const __half2 c0 = __hsub2(field<0x000f000fu>(x), k1024);
+                  const __half2 c1 = __hfma2(field<0x00f000f0u>(x), k16, k64);
+                  o[2 * j] = h2_bits(__hfma2(c0, s, z));
+                  o[2 * j + 1] = h2_bits(__hfma2(c1, s, z));
+                  x >>= 8;
                 }
-                *reinterpret_cast<uint4 *>(vd + hf * (D * 128) + sw(c, chunk)) =
+                *reinterpret_cast<uint4 *>(dst + (i >> 1) * 16384 + sw(r, 4 * (i & 1) + t4)) =
                     make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          } else {
+            const int left = it.s.len - (kt * kTile + r0);   // its tokens in the sequence
+            // lane (n8, t4) reads the words of token pair t4, then the four
+            // lanes of n8 exchange them, so that lane j has the four pairs (8
+            // tokens) of the 32-channel span j
+#pragma unroll
+            for (int oct = 0; oct < 2; ++oct) {
+              uint32_t x[4] = {0u, 0u, 0u, 0u};
+              const unsigned char *vp = blk + (32 * oct + lane) * (4 * I);
+              if constexpr (I == 4) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(vp);
+                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2 *>(vp);
+                x[0] = y.x; x[1] = y.y;
+              }
+              // 4 x 4 transposition over the lanes t4 in two exchanges
+              {
+                const bool o1 = t4 & 1, o2 = t4 & 2;
+                uint32_t s0 = o1 ? x[0] : x[1], s1 = o1 ? x[2] : x[3];
+                s0 = __shfl_xor_sync(kFull, s0, 1);
+                s1 = __shfl_xor_sync(kFull, s1, 1);
+                if (o1) { x[0] = s0; x[2] = s1; } else { x[1] = s0; x[3] = s1; }
+                s0 = o2 ? x[0] : x[2];
+                s1 = o2 ? x[1] : x[3];
+                s0 = __shfl_xor_sync(kFull, s0, 2);
+                s1 = __shfl_xor_sync(kFull, s1, 2);
+                if (o2) { x[0] = s0; x[1] = s1; } else { x[2] = s0; x[3] = s1; }
+              }
+              const int span = t4;
+              if (I == 4 || span < I) {
+                const uint2 *vm = reinterpret_cast<const uint2 *>(blk + 8 * D) + 4 * oct * NG +
+                                  32 * span / G;
+                __half2 s[4], z[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  const uint2 y = vm[p * NG];
+                  // tokens behind the sequence hold anything: their values are 0
+                  const int e = left - (8 * oct + 2 * p);
+                  const unsigned keep = !good || e <= 0 ? 0u : (e == 1 ? 0x0000ffffu : kFull);
+                  s[p] = bits_h2(y.x & keep);
+                  z[p] = bits_h2(y.y & keep);
+                }
+                const int chunk = 2 * w + oct;         // octet within the 64 tokens
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  // the lanes of a store differ in the channel's low bits
+                  const int r = (q + span) & 3, c = 32 * span + 4 * n8 + r;
+                  uint32_t o[4];
+#pragma unroll
+                  for (int p = 0; p < 4; ++p) {
+                    const __half2 cc = __hsub2(field<0x000f000fu>(x[p] >> (4 * r)), k1024);
+                    o[p] = h2_bits(__hfma2(cc, s[p], z[p]));
+                  }
+                  *reinterpret_cast<uint4 *>(dst + hf * (D * 128) + sw(c, chunk)) =
+                      make_uint4(o[0], o[1], o[2], o[3]);
+                }
               }
             }
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(&B.raw_empty[raw]);
+          if (lane == 0) bar_arrive(&B.raw_empty[kv][raw]);
           raw = raw + 1 == kRaw ? 0 : raw + 1;
           ph_raw ^= raw == 0;
         }
         if (!ok) break;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          bar_arrive(&B.k_full[st]);
-          bar_arrive(&B.v_full[st]);
-        }
+        if (lane == 0) bar_arrive(&full[st]);
         st ^= 1u;
         ph_e ^= st == 0;
       }
     }
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // ---- the products ----
     if (lane == 0) {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
@@ -692,48 +759,53 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
                  desc128(sb + SM::V + stage * SM::OP + (k >> 2) * (D * 128) + 32 * (k & 3)),
                  id_o, more || k > 0);
       };
-      while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
-        const int two = it.pair * 2 * tpt + tpt < it.s.n ? 2 : 1;
-        const int nt = it.k1 - it.k0;
-        for (int i = 0; ok && i < two; ++i) {
-          ok = bar_wait(&B.q_full[i], ph_q[i], dead);
-          ph_q[i] ^= 1u;
-          if (ok && i == 0) ok = bar_wait(&B.k_full[ks], ph_k, dead);
-          if (!ok) break;
-          fence_after();
-          scores(i, ks);
-        }
-        if (!ok) break;
+      // waits for the keys of the next tile, and gives them back
+      auto keys = [&]() {
+        const bool r = bar_wait(&B.k_full[ks], ph_k, dead);
+        fence_after();
+        return r;
+      };
+      auto keys_done = [&]() {
         mma_commit(&B.k_empty[ks]);
         ks ^= 1u;
         ph_k ^= ks == 0;
+      };
+      while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
+        const int nt = it.k1 - it.k0;
+        const int slots = it.two || nt > 1 ? 2 : 1;
+        // first scores of both slots: one key tile for two query tiles, or a
+        // key tile each for one
+        for (int i = 0; ok && i < slots; ++i) {
+          ok = bar_wait(&B.q_full[i], ph_q[i], dead);
+          ph_q[i] ^= 1u;
+          if (ok && (i == 0 || !it.two)) ok = keys();
+          if (!ok) break;
+          fence_after();
+          scores(i, ks);
+          if (!it.two || i + 1 == slots) keys_done();
+        }
         for (int j = 0; ok && j < nt; ++j) {
-          const bool last = j + 1 == nt;
           ok = bar_wait(&B.v_full[vs], ph_v, dead);
-          for (int i = 0; ok && i < two; ++i) {
+          const bool last = it.two ? j + 1 == nt : j + 2 >= nt;
+          for (int i = it.two ? 0 : j & 1, n = it.two ? 2 : i + 1; ok && i < n; ++i) {
             ok = bar_wait(&B.p_full[i], ph_p[i], dead);
             ph_p[i] ^= 1u;
             if (!ok) break;
             fence_after();
-            outputs(i, vs, j > 0);
+            outputs(i, vs, it.two ? j > 0 : j > 1);
             if (last) {
               mma_commit(&B.o_full[i]);
             } else {
-              if (i == 0) ok = bar_wait(&B.k_full[ks], ph_k, dead);
+              if (i == 0 || !it.two) ok = keys();
               if (!ok) break;
-              fence_after();
               scores(i, ks);
+              if (!it.two || i == 1) keys_done();
             }
           }
           if (!ok) break;
           mma_commit(&B.v_empty[vs]);
           vs ^= 1u;
           ph_v ^= vs == 0;
-          if (!last) {
-            mma_commit(&B.k_empty[ks]);
-            ks ^= 1u;
-            ph_k ^= ks == 0;
-          }
         }
       }
       // products in flight end before the tensor memory is given up
@@ -741,9 +813,9 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
       int never = 0;
       bar_wait(&B.drain, 0, &never);
     }
-  } else if (warp == 13) {
-    // ---- copies ----
-    const int bpp = a.page_log2 - 4;
+  } else if (warp < 19) {
+    // ---- copies: keys (17) and values (18) ----
+    const int kv = warp - 17, bpp = a.page_log2 - 4;
     uint32_t raw = 0, ph_e = 1;
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
@@ -760,18 +832,18 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
             good = false;
           }
         }
-        ok = bar_wait(&B.raw_empty[raw], ph_e, dead);
+        ok = bar_wait(&B.raw_empty[kv][raw], ph_e, dead);
         if (!__all_sync(kFull, ok)) { ok = false; break; }
         const unsigned mask = __ballot_sync(kFull, good);
         if (lane == 0) {
-          B.good[raw] = mask;
-          mbar_expect_tx(&B.raw_full[raw], __popc(mask) * BLK);
+          B.good[kv][raw] = mask;
+          mbar_expect_tx(&B.raw_full[kv][raw], __popc(mask) * SM::HALF);
         }
         __syncwarp();
         if (good) {
           const int64_t src = ((((int64_t)p * a.H_kv + it.h) << bpp) + (blk & ((1 << bpp) - 1)));
-          bulk_g2s(sm + SM::RAW + (raw * 4 + lane) * BLK, a.pool + src * BLK, BLK,
-                   &B.raw_full[raw]);
+          bulk_g2s(sm + SM::RAW + ((kv * kRaw + raw) * 4 + lane) * SM::HALF,
+                   a.pool + src * BLK + kv * SM::HALF, SM::HALF, &B.raw_full[kv][raw]);
         }
         used |= 1u << raw;
         raw = raw + 1 == kRaw ? 0 : raw + 1;
@@ -784,7 +856,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
       for (int i = 0; i < kRaw; ++i) {
         int never = 0;
         const uint32_t turn = (uint32_t)i < raw ? ph_e ^ 1u : ph_e;   // parity of its last full
-        if ((used >> i) & 1u) bar_wait(&B.raw_full[i], turn, &never);
+        if ((used >> i) & 1u) bar_wait(&B.raw_full[kv][i], turn, &never);
       }
     }
   }
@@ -798,35 +870,36 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, long long *prefixes) {
   }
 }
 
-// Merge of a pair whose keys were cut: CTA (c, slice) merges 16 rows of the
+// Merge of a pair whose keys were cut: CTA (slice, c) merges 16 rows of the
 // pair that ends CTA c's piece of the line, when that pair starts in it and
 // goes on.  One warp per row, lanes over channels.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
 k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, long long *prefixes,
                     int grid) {
+  const int c = blockIdx.y, slice = blockIdx.x;
   constexpr int CPL = D / 32, ROW = D + 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the attention's CTA 0 has left the prefix
   const long long *prefix = prefixes;
   const long long units = prefix[a.B];
   if (units == 0) return;
-  const int ctas = ctas_used(units, grid), c = blockIdx.x / kSlices,
-            slice = blockIdx.x % kSlices;
+  const int ctas = ctas_used(units, grid);
   if (c + 1 >= ctas) return;
+  const Cut cut(units, ctas);
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
-  const long long u1 = first_unit(units, ctas, c + 1);
+  const long long u1 = cut.first(c + 1);
   Walk w;
   w.seek(a, prefix, u1 - 1, u1, t.max_new, tpt);
   const Seq s = w.s;
   const int nk = tiles_of(s, w.pair, tpt), k = w.k, h = w.h, pair = w.pair;
   // the pair's first tile lies k tiles before unit u1 - 1
-  if (k + 1 >= nk || u1 - 1 - k < first_unit(units, ctas, c)) return;
+  if (k + 1 >= nk || u1 - 1 - k < cut.first(c)) return;
   const long long ulast = u1 - 1 - k + nk - 1;
   int cl = c + 1;
-  while (cl + 1 < ctas && first_unit(units, ctas, cl + 1) <= ulast) ++cl;
+  while (cl + 1 < ctas && cut.first(cl + 1) <= ulast) ++cl;
   const int lane = threadIdx.x & 31;
-  for (int r = slice * 16 + (threadIdx.x >> 5); r < slice * 16 + 16; r += 4) {
+  for (int r = slice * kSliceRows + (threadIdx.x >> 5); r < (slice + 1) * kSliceRows; r += 4) {
     const int wg = r >> 7, row = r & 127, tok = pair * 2 * tpt + wg * tpt + row / GQ;
     if (row >= tpt * GQ || tok >= s.n) continue;
     auto at = [&](int i) {
@@ -859,9 +932,10 @@ k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, long long *pr
   }
 }
 
-size_t part_bytes(int D, int sm_count) {
-  return (size_t)2 * sm_count * 2 * kTile * (D + 4) * sizeof(float);
-}
+// two partials (pairs cut at either end of a CTA's piece) of 256 rows a CTA,
+// and 128 rows for what slot 1 hands to slot 0
+size_t part_floats(int D, int sm_count) { return (size_t)2 * sm_count * 2 * kTile * (D + 4); }
+size_t swap_floats(int D, int sm_count) { return (size_t)sm_count * kTile * (D + 4); }
 
 template <typename T, int D, int NG>
 cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cudaStream_t st) {
@@ -869,14 +943,17 @@ cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cud
   cudaError_t e = cudaFuncSetAttribute(k_paged_chunk<T, D, NG>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SM::ALLOC);
   if (e != cudaSuccess) return e;
-  float *part = t.ws;
-  long long *prefixes =
-      reinterpret_cast<long long *>(reinterpret_cast<uint8_t *>(t.ws) + part_bytes(D, sm_count));
+  float *part = t.ws, *swap = part + part_floats(D, sm_count);
+  long long *prefixes = reinterpret_cast<long long *>(swap + swap_floats(D, sm_count));
   e = launch_pdl(k_paged_chunk<T, D, NG>, dim3(sm_count), dim3(kThreads), SM::ALLOC, st, a, t,
-                 part, prefixes);
+                 part, swap, prefixes);
   count_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_paged_chunk_merge<T, D>, dim3(sm_count * kSlices), dim3(128), 0, st, a, t,
+  // rows of a pair that can hold queries: one tile's, or both tiles'
+  const int GQ = a.H_q / a.H_kv;
+  const int slices = t.max_new <= kTile / GQ ? (t.max_new * GQ + kSliceRows - 1) / kSliceRows
+                                             : 2 * kTile / kSliceRows;
+  e = launch_pdl(k_paged_chunk_merge<T, D>, dim3(slices, sm_count), dim3(128), 0, st, a, t,
                  (const float *)part, prefixes, sm_count);
   count_launch();
   return e;
@@ -897,7 +974,8 @@ cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_cou
 }  // namespace chunk
 
 size_t paged_chunk_ws(int B, int, int D, int sm_count) {
-  return chunk::part_bytes(D, sm_count) + (size_t)sm_count * (B + 1) * sizeof(long long);
+  return (chunk::part_floats(D, sm_count) + chunk::swap_floats(D, sm_count)) * sizeof(float) +
+         (size_t)sm_count * (B + 1) * sizeof(long long);
 }
 
 cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
