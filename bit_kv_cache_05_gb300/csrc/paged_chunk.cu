@@ -38,7 +38,7 @@
 namespace vqk {
 namespace chunk {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 608;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
@@ -103,11 +103,13 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr) {
 __host__ __device__ constexpr uint32_t idesc(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// The issuing warp runs as a whole (its operands are then known to be uniform
+// and stay in uniform registers); one elected lane issues.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
                                        uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
@@ -115,14 +117,15 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                        uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
           saddr(bar))
       : "memory");
 }
@@ -165,6 +168,11 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&v)[16]) {
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(t),
       VQK_S8(v, 0), VQK_S8(v, 8)
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ void tm_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -333,7 +341,7 @@ template <typename T, int D, int NG>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *prefixes) {
   using SM = Smem<D, NG>;
-  constexpr int I = D / 32, G = D / NG, KB = SM::KB, BLK = SM::BLK;
+  constexpr int I = D / 32, G = D / NG, BLK = SM::BLK;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
   Bars &B = *reinterpret_cast<Bars *>(sm + SM::BAR);
@@ -475,6 +483,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         }
         const int vis = pos - kt * kTile;            // columns up to vis are seen
         const bool all = __all_sync(kFull, vis >= kTile - 1);
+        // two passes over the scores: the maximum, then the weights
         uint32_t v[32];
         float mx = -INFINITY;
 #pragma unroll
@@ -482,7 +491,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           tm_ld32(ts + c, v);
           if (all) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
+            for (int j = 0; j < 32; j += 2)
+              mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -506,7 +516,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
             tm_st32(to + c, v);
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        const float base = m == -INFINITY ? 0.f : -m;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) {
@@ -521,12 +531,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           for (int j = 0; j < 16; ++j) {
             const float2 x = __ffma2_rn(
                 make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                make_float2(scale, scale), make_float2(-base, -base));
+                make_float2(scale, scale), make_float2(base, base));
             const float2 y = make_float2(ex2(x.x), ex2(x.y));
             sum = __fadd2_rn(sum, y);
             p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
           }
-          // fp16 pairs of these 32 columns take 16, all behind what is read
+          // the weights of these 32 columns take 16, all behind what is read
           tm_st16(ts + c / 2, p);
         }
         l += sum.x + sum.y;
@@ -738,30 +748,33 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     }
   } else if (warp == 16) {
     // ---- the products ----
-    if (lane == 0) {
+    {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
       const uint32_t sb = saddr(sm);
       uint32_t ks = 0, ph_k = 0, vs = 0, ph_v = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
       bool ok = true;
+      // descriptors of the operands' starts; a step of 16 in K adds 32 bytes,
+      // 64 in K the next block of 128-byte rows
+      const uint64_t dq = desc128(sb + SM::Q), dk = desc128(sb + SM::K),
+                     dv = desc128(sb + SM::V);
       auto scores = [&](int i, uint32_t stage) {
+        const uint64_t q = dq + i * (SM::OP >> 4), k = dk + stage * (SM::OP >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + 128 * i,
-                 desc128(sb + SM::Q + i * SM::OP + (k >> 2) * 16384 + 32 * (k & 3)),
-                 desc128(sb + SM::K + stage * SM::OP + (k >> 2) * 16384 + 32 * (k & 3)), id_s,
-                 k > 0);
+        for (int e = 0; e < D / 16; ++e)
+          mma_ss(tmem + 128 * i, q + (e >> 2) * 1024 + 2 * (e & 3),
+                 k + (e >> 2) * 1024 + 2 * (e & 3), id_s, e > 0);
         mma_commit(&B.s_full[i]);
       };
       auto outputs = [&](int i, uint32_t stage, bool more) {
+        const uint64_t v = dv + stage * (SM::OP >> 4);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k,
-                 desc128(sb + SM::V + stage * SM::OP + (k >> 2) * (D * 128) + 32 * (k & 3)),
-                 id_o, more || k > 0);
+        for (int e = 0; e < kTile / 16; ++e)
+          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * e,
+                 v + (e >> 2) * (D * 8) + 2 * (e & 3), id_o, more || e > 0);
       };
       // waits for the keys of the next tile, and gives them back
       auto keys = [&]() {
-        const bool r = bar_wait(&B.k_full[ks], ph_k, dead);
+        const bool r = __all_sync(kFull, bar_wait(&B.k_full[ks], ph_k, dead));
         fence_after();
         return r;
       };
@@ -776,7 +789,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         // first scores of both slots: one key tile for two query tiles, or a
         // key tile each for one
         for (int i = 0; ok && i < slots; ++i) {
-          ok = bar_wait(&B.q_full[i], ph_q[i], dead);
+          ok = __all_sync(kFull, bar_wait(&B.q_full[i], ph_q[i], dead));
           ph_q[i] ^= 1u;
           if (ok && (i == 0 || !it.two)) ok = keys();
           if (!ok) break;
@@ -785,10 +798,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           if (!it.two || i + 1 == slots) keys_done();
         }
         for (int j = 0; ok && j < nt; ++j) {
-          ok = bar_wait(&B.v_full[vs], ph_v, dead);
+          ok = __all_sync(kFull, bar_wait(&B.v_full[vs], ph_v, dead));
           const bool last = it.two ? j + 1 == nt : j + 2 >= nt;
           for (int i = it.two ? 0 : j & 1, n = it.two ? 2 : i + 1; ok && i < n; ++i) {
-            ok = bar_wait(&B.p_full[i], ph_p[i], dead);
+            ok = __all_sync(kFull, bar_wait(&B.p_full[i], ph_p[i], dead));
             ph_p[i] ^= 1u;
             if (!ok) break;
             fence_after();
@@ -813,7 +826,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       int never = 0;
       bar_wait(&B.drain, 0, &never);
     }
-  } else if (warp < 19) {
+  } else {
     // ---- copies: keys (17) and values (18) ----
     const int kv = warp - 17, bpp = a.page_log2 - 4;
     uint32_t raw = 0, ph_e = 1;
