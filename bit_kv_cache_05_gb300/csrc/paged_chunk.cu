@@ -13,17 +13,20 @@
 // its softmax: the two query tiles of a pair, or, where the second would be
 // empty, the even and the odd key tiles of one query tile (joined at the
 // end).  Its warps:
-//   0-3, 4-7   softmax of slot 0 and 1, one row a thread: scores from tensor
-//              memory, online softmax in fp32, weights back to tensor memory
-//              in fp16 (the A operand of the second product), the output
-//              read out at the end.  Rounding a weight to fp16 moves it by
-//              2^-12 of itself at most, as one rounding of a 16-bit output
-//              does.
-//   8-11       rebuild k_hat (fp16 by definition) from the codes into two
-//   12-15      128-byte-swizzled stages, and v_hat likewise
-//   16         issues the products: S = Q k_hat^T, then O += P v_hat
-//   17, 18     copy the key and the value halves of the blocks (one bulk copy
+//   0-7, 8-15  softmax of slot 0 and 1, two threads a row, 64 of its columns
+//              each: scores from tensor memory, online softmax in fp32 (the
+//              row's maximum exchanged through shared memory), weights back
+//              to tensor memory in fp16 (the A operand of the second
+//              product), the output read out at the end.  Rounding a weight
+//              to fp16 moves it by 2^-12 of itself at most, as one rounding
+//              of a 16-bit output does.
+//   16-19      rebuild k_hat (fp16 by definition) from the codes into two
+//   20-23      128-byte-swizzled stages, and v_hat likewise
+//   24         issues the products: S = Q k_hat^T, then O += P v_hat
+//   25, 26     copy the key and the value halves of the blocks (one bulk copy
 //              each), 64 tokens a stage
+// A slot's chain is scores, softmax, output, scores of the next tile; two
+// threads a row halve its longest part.
 // The running maximum of a row is raised only when it grows by more than 8
 // (base 2), so that O is rarely rescaled; a weight stays below 2^8.
 //
@@ -38,7 +41,7 @@
 namespace vqk {
 namespace chunk {
 
-constexpr int kThreads = 608;
+constexpr int kThreads = 864;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
@@ -321,7 +324,7 @@ struct Smem {
   static constexpr int BLK = 16 * D + 128 * NG, HALF = BLK / 2;   // keys, values
   static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, RAW = 6 * OP;
   static constexpr int BAR = RAW + kRaw * 4 * BLK;
-  static constexpr int ALLOC = BAR + 512 + 1024;   // room to align the base
+  static constexpr int ALLOC = BAR + 512 + 2048 + 1024;   // room to align the base
 };
 
 // byte of 16-byte chunk `c` of row `r` in a tile of 128-byte swizzled rows
@@ -331,6 +334,7 @@ struct Bars {
   uint64_t raw_full[2][kRaw], raw_empty[2][kRaw];   // keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t pair[2][4];      // the two warps of a slot's 32 rows
   uint64_t x_full, drain;
   uint32_t good[2][kRaw];   // which of a stage's 4 blocks arrived
   uint32_t tmem;
@@ -358,12 +362,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       bar_init(&B.v_full[i], 4);
       bar_init(&B.k_empty[i], 1);
       bar_init(&B.v_empty[i], 1);
-      bar_init(&B.q_full[i], 4);
+      bar_init(&B.q_full[i], 8);
       bar_init(&B.s_full[i], 1);
-      bar_init(&B.p_full[i], 4);
+      bar_init(&B.p_full[i], 8);
       bar_init(&B.o_full[i], 1);
+      for (int j = 0; j < 4; ++j) bar_init(&B.pair[i][j], 2);
     }
-    bar_init(&B.x_full, 4);
+    bar_init(&B.x_full, 8);
     bar_init(&B.drain, 1);
     B.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -392,12 +397,26 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     walk.seek(a, prefix, cut.first(blockIdx.x), cut.first(blockIdx.x + 1), t.max_new, tpt);
   }
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ---- softmax ----
-    const int wg = warp >> 2, row = tid & 127;
+    const int wg = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
-    uint32_t ph_s = 0, ph_o = 0, ph_x = 0;
+    // this thread's 64 columns of the scores, its D / 2 of the output
+    const uint32_t ts = tl + 128 * wg + 64 * half, to = tl + 256 + 128 * wg + half * (D / 2);
+    uint32_t ph_s = 0, ph_o = 0, ph_x = 0, ph_2 = 0;
+    // a value of the row's other thread, for one of its own
+    float *mine = reinterpret_cast<float *>(sm + SM::BAR + 512) + wg * 256 + half * 128 + row;
+    const float *other = reinterpret_cast<float *>(sm + SM::BAR + 512) + wg * 256 +
+                         (half ^ 1) * 128 + row;
+    auto exchange = [&](float x, float &y) {
+      *mine = x;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&B.pair[wg][warp & 3]);
+      const bool r = bar_wait(&B.pair[wg][warp & 3], ph_2, dead);
+      ph_2 ^= 1u;
+      y = *other;
+      return __all_sync(kFull, r);
+    };
     float sl2 = 0.f;
     // query row of this thread, of the slot's query tile
     auto token = [&](const Item &x) {
@@ -434,7 +453,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       }
       unsigned char *dst = sm + SM::Q + wg * SM::OP;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
+      for (int ch = 0; ch < D / 16; ++ch) {
+        const int c = half * (D / 16) + ch;
         uint4 r = valid ? reinterpret_cast<const uint4 *>(q)[c] : make_uint4(0u, 0u, 0u, 0u);
         if constexpr (!std::is_same<T, __half>::value) {
           uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -481,13 +501,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           if (lane == 0) bar_arrive(&B.p_full[wg]);
           continue;
         }
-        const int vis = pos - kt * kTile;            // columns up to vis are seen
-        const bool all = __all_sync(kFull, vis >= kTile - 1);
+        const int vis = pos - kt * kTile - 64 * half;   // columns up to vis are seen
+        const bool all = __all_sync(kFull, vis >= kTile / 2 - 1);
         // two passes over the scores: the maximum, then the weights
         uint32_t v[32];
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
+        for (int c = 0; c < kTile / 2; c += 32) {
           tm_ld32(ts + c, v);
           if (all) {
 #pragma unroll
@@ -499,7 +519,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
               mx = fmaxf(mx, c + j <= vis ? __uint_as_float(v[j]) : -INFINITY);
           }
         }
-        mx *= scale;
+        float my;
+        ok = exchange(mx, my);
+        if (!ok) break;
+        mx = scale * fmaxf(mx, my);
         const bool raise = mx > m + kLazy;
         float f = 1.f;
         if (raise) {
@@ -509,7 +532,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         }
         if (kt > kfirst && __any_sync(kFull, raise)) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D / 2; c += 32) {
             tm_ld32(to + c, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
@@ -519,7 +542,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         const float base = m == -INFINITY ? 0.f : -m;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
+        for (int c = 0; c < kTile / 2; c += 32) {
           tm_ld32(ts + c, v);
           if (!all) {
 #pragma unroll
@@ -536,7 +559,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
             sum = __fadd2_rn(sum, y);
             p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
           }
-          // the weights of these 32 columns take 16, all behind what is read
+          // the weights of these 32 columns take 16, all behind what this
+          // thread reads and none of the other thread's
           tm_st16(ts + c / 2, p);
         }
         l += sum.x + sum.y;
@@ -546,6 +570,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         if (lane == 0) bar_arrive(&B.p_full[wg]);
       }
       if (!ok) break;
+      // before the next queries are announced, so that this value is read before
+      // the next tile's maximum takes its place
+      if (!idle) {
+        float ly;
+        ok = exchange(l, ly);
+        if (!ok) break;
+        l = half ? ly + l : l + ly;
+      }
       // the next queries: this slot's last scores have been read
       const Item done = it;
       have = fetch(it);
@@ -558,6 +590,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       const bool halves = !done.two && done.k1 - done.k0 > 1;
       const bool give = halves && wg == 1;
       float *xr = swap + ((int64_t)blockIdx.x * kTile + row) * (D + 4);
+      const int c0 = half * (D / 2);
       float f0 = 1.f, f1 = 0.f;
       if (halves && wg == 0) {
         ok = bar_wait(&B.x_full, ph_x, dead);
@@ -582,14 +615,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
                 ((int64_t)(done.s.first + tok) * a.H_q + done.h * GQ + row % GQ) * D;
       if (!idle) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
           uint32_t v[32];
           __syncwarp();
           tm_ld32(to + c, v);
           if (halves && wg == 0 && valid) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 x = *reinterpret_cast<const float4 *>(xr + c + j);
+              const float4 x = *reinterpret_cast<const float4 *>(xr + c0 + c + j);
               v[j] = __float_as_uint(__uint_as_float(v[j]) * f0 + x.x * f1);
               v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f0 + x.y * f1);
               v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f0 + x.z * f1);
@@ -602,24 +635,24 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
               float y[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[j + e]) * inv;
-              store8<T>(orow + c + j, y);
+              store8<T>(orow + c0 + c + j, y);
             }
           } else if (valid) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4 *>(pr + c + j) =
+              *reinterpret_cast<uint4 *>(pr + c0 + c + j) =
                   make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
         }
-        if (valid && (give || !whole)) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
+        if (valid && !half && (give || !whole)) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
       }
       __syncwarp();
       if (give && lane == 0) bar_arrive(&B.x_full);
       fence_before();
     }
-  } else if (warp < 16) {
-    // ---- k_hat (warps 8-11) and v_hat (12-15) ----
-    const int kv = (warp - 8) >> 2, w = warp & 3, n8 = lane >> 2, t4 = lane & 3;
+  } else if (warp < 24) {
+    // ---- k_hat (warps 16-19) and v_hat (20-23) ----
+    const int kv = (warp - 16) >> 2, w = warp & 3, n8 = lane >> 2, t4 = lane & 3;
     uint64_t *full = kv ? B.v_full : B.k_full, *empty = kv ? B.v_empty : B.k_empty;
     uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
     bool ok = true;
@@ -746,7 +779,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         ph_e ^= st == 0;
       }
     }
-  } else if (warp == 16) {
+  } else if (warp == 24) {
     // ---- the products ----
     {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
@@ -769,7 +802,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         const uint64_t v = dv + stage * (SM::OP >> 4);
 #pragma unroll
         for (int e = 0; e < kTile / 16; ++e)
-          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * e,
+          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 64 * (e >> 2) + 8 * (e & 3),
                  v + (e >> 2) * (D * 8) + 2 * (e & 3), id_o, more || e > 0);
       };
       // waits for the keys of the next tile, and gives them back
@@ -827,8 +860,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       bar_wait(&B.drain, 0, &never);
     }
   } else {
-    // ---- copies: keys (17) and values (18) ----
-    const int kv = warp - 17, bpp = a.page_log2 - 4;
+    // ---- copies: keys (25) and values (26) ----
+    const int kv = warp - 25, bpp = a.page_log2 - 4;
     uint32_t raw = 0, ph_e = 1;
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
