@@ -14,8 +14,8 @@
 // empty, the even and the odd key tiles of one query tile (joined at the
 // end).  Its warps:
 //   0-7, 8-15  softmax of slot 0 and 1, two threads a row, 64 of its columns
-//              each: scores from tensor memory, online softmax in fp32 (the
-//              row's maximum exchanged through shared memory), weights back
+//              each: scores from tensor memory, online softmax in fp32 (their
+//              maxima compared through shared memory), weights back
 //              to tensor memory in fp16 (the A operand of the second
 //              product), the output read out at the end.  Rounding a weight
 //              to fp16 moves it by 2^-12 of itself at most, as one rounding
@@ -27,8 +27,10 @@
 //              each), 64 tokens a stage
 // A slot's chain is scores, softmax, output, scores of the next tile; two
 // threads a row halve its longest part.
-// The running maximum of a row is raised only when it grows by more than 8
-// (base 2), so that O is rarely rescaled; a weight stays below 2^8.
+// The running maximum of a row is a whole number (base 2) and is raised only
+// when a score passes it by more than 15: a weight stays below 2^15, which
+// fp16 holds, one pass over a tile's scores is enough, and what was weighed
+// with the old maximum is brought to a new one by an exact power of two.
 //
 // k_hat's channels lie in the order 0 4 1 5 2 6 3 7 within each 8, in which
 // a code word gives its fp16 pairs; the queries are laid out the same.
@@ -45,7 +47,8 @@ constexpr int kThreads = 864;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 15.f;
+constexpr int kNear = 64;            // sequences whose prefix fits in shared memory
 constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
 constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes
 
@@ -157,12 +160,13 @@ __device__ __forceinline__ void tm_ld32(uint32_t t, uint32_t (&v)[32]) {
       : "r"(t)
       : "memory");
 }
-__device__ __forceinline__ void tm_st32(uint32_t t, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tm_ld16(uint32_t t, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(t),
-      VQK_S8(v, 0), VQK_S8(v, 8), VQK_S8(v, 16), VQK_S8(v, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : VQK_R8(v, 0), VQK_R8(v, 8)
+      : "r"(t)
       : "memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&v)[16]) {
@@ -171,6 +175,10 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&v)[16]) {
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(t),
       VQK_S8(v, 0), VQK_S8(v, 8)
       : "memory");
+}
+// 2^d for a whole d <= 0 or -infinity
+__device__ __forceinline__ float pow2(float d) {
+  return d < -126.f ? 0.f : __int_as_float(((int)d + 127) << 23);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -324,7 +332,10 @@ struct Smem {
   static constexpr int BLK = 16 * D + 128 * NG, HALF = BLK / 2;   // keys, values
   static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, RAW = 6 * OP;
   static constexpr int BAR = RAW + kRaw * 4 * BLK;
-  static constexpr int ALLOC = BAR + 512 + 2048 + 1024;   // room to align the base
+  static constexpr int SWAP = BAR + 384;           // what a row's two threads exchange
+  static constexpr int EXP = SWAP + 2048;
+  static constexpr int PREFIX = EXP + 512;
+  static constexpr int ALLOC = PREFIX + 8 * (kNear + 1) + 8 + 1024;   // room to align the base
 };
 
 // byte of 16-byte chunk `c` of row `r` in a tile of 128-byte swizzled rows
@@ -349,7 +360,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
   Bars &B = *reinterpret_cast<Bars *>(sm + SM::BAR);
-  static_assert(sizeof(Bars) <= 512, "barriers fit");
+  static_assert(sizeof(Bars) <= 384, "barriers fit");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
   if (tid == 0) {
@@ -381,7 +392,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
   fence_before();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  long long *prefix = prefixes + (long long)blockIdx.x * (a.B + 1);
+  // (the merge reads CTA 0's)
+  long long *prefix = a.B <= kNear && blockIdx.x > 0
+                          ? reinterpret_cast<long long *>(sm + SM::PREFIX)
+                          : prefixes + (long long)blockIdx.x * (a.B + 1);
   tile_prefix(a, t.max_new, tpt, prefix);
   fence_after();
   const uint32_t tmem = B.tmem;
@@ -405,17 +419,21 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     const uint32_t ts = tl + 128 * wg + 64 * half, to = tl + 256 + 128 * wg + half * (D / 2);
     uint32_t ph_s = 0, ph_o = 0, ph_x = 0, ph_2 = 0;
     // a value of the row's other thread, for one of its own
-    float *mine = reinterpret_cast<float *>(sm + SM::BAR + 512) + wg * 256 + half * 128 + row;
-    const float *other = reinterpret_cast<float *>(sm + SM::BAR + 512) + wg * 256 +
+    float *mine = reinterpret_cast<float *>(sm + SM::SWAP) + wg * 256 + half * 128 + row;
+    const float *other = reinterpret_cast<float *>(sm + SM::SWAP) + wg * 256 +
                          (half ^ 1) * 128 + row;
-    auto exchange = [&](float x, float &y) {
-      *mine = x;
+    auto meet = [&]() {
       __syncwarp();
       if (lane == 0) bar_arrive(&B.pair[wg][warp & 3]);
       const bool r = bar_wait(&B.pair[wg][warp & 3], ph_2, dead);
       ph_2 ^= 1u;
-      y = *other;
       return __all_sync(kFull, r);
+    };
+    auto exchange = [&](float x, float &y) {
+      *mine = x;
+      const bool r = meet();
+      y = *other;
+      return r;
     };
     float sl2 = 0.f;
     // query row of this thread, of the slot's query tile
@@ -429,48 +447,56 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       const bool valid = has_row(x);
       const T *q = static_cast<const T *>(t.q) + (int64_t)(x.s.first + tok) * t.q_token +
                    (int64_t)(x.h * GQ + row % GQ) * t.q_head;
+      uint4 r[D / 16];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          r[c] = reinterpret_cast<const uint4 *>(q)[half * (D / 16) + c];
+      }
       sl2 = t.scale;
-      float up = 1.f;
+      bool met = true;
       if constexpr (!std::is_same<T, __half>::value) {
         // a bf16 row as fp16: scaled by a power of two to a maximum near 2^14
-        float m = 0.f;
+        uint32_t m = 0u;               // largest magnitude, as bits
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 r = valid ? reinterpret_cast<const uint4 *>(q)[c]
-                                : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            m = fmaxf(m, fabsf(__uint_as_float(w[e] << 16)));
-            m = fmaxf(m, fabsf(__uint_as_float(w[e] & 0xffff0000u)));
-          }
+          for (int e = 0; e < 4; ++e)
+            m = max(m, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
         }
-        int f = 14 - ((int)(__float_as_uint(m) >> 23) - 127);
-        f = m > 0.f ? (f > 126 ? 126 : f) : 0;
-        f = f < -100 ? -100 : f;
-        up = __uint_as_float((uint32_t)(127 + f) << 23);
+        uint8_t *ex = sm + SM::EXP + wg * 256 + row;
+        ex[half * 128] = (uint8_t)(m >> 23);
+        met = meet();
+        const int e = max((int)(m >> 23), (int)ex[(half ^ 1) * 128]);
+        int f = e > 0 ? 14 - (e - 127) : 0;
+        f = f > 126 ? 126 : (f < -100 ? -100 : f);
+        const float up = __uint_as_float((uint32_t)(127 + f) << 23);
         sl2 *= __uint_as_float((uint32_t)(127 - f) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * up,
+                                             __uint_as_float(w[i] & 0xffff0000u) * up));
+          r[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
       unsigned char *dst = sm + SM::Q + wg * SM::OP;
 #pragma unroll
-      for (int ch = 0; ch < D / 16; ++ch) {
-        const int c = half * (D / 16) + ch;
-        uint4 r = valid ? reinterpret_cast<const uint4 *>(q)[c] : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (!std::is_same<T, __half>::value) {
-          uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = h2_bits(__floats2half2_rn(__uint_as_float(w[e] << 16) * up,
-                                             __uint_as_float(w[e] & 0xffff0000u) * up));
-          r = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+      for (int i = 0; i < D / 16; ++i) {
+        const int c = half * (D / 16) + i;
         *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + sw(row, c & 7)) =
-            make_uint4(__byte_perm(r.x, r.z, 0x5410), __byte_perm(r.x, r.z, 0x7632),
-                       __byte_perm(r.y, r.w, 0x5410), __byte_perm(r.y, r.w, 0x7632));
+            make_uint4(__byte_perm(r[i].x, r[i].z, 0x5410), __byte_perm(r[i].x, r[i].z, 0x7632),
+                       __byte_perm(r[i].y, r[i].w, 0x5410), __byte_perm(r[i].y, r[i].w, 0x7632));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(&B.q_full[wg]);
+      return met;
     };
     // the next item that this slot works on
     auto fetch = [&](Item &x) {
@@ -479,7 +505,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       return false;
     };
     bool have = fetch(it), ok = true;
-    if (have) load_q(it);
+    if (have) ok = load_q(it);
     while (have && ok) {
       const int tok = token(it);
       const bool valid = has_row(it);
@@ -503,52 +529,46 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         }
         const int vis = pos - kt * kTile - 64 * half;   // columns up to vis are seen
         const bool all = __all_sync(kFull, vis >= kTile / 2 - 1);
-        // two passes over the scores: the maximum, then the weights
-        uint32_t v[32];
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kTile / 2; c += 32) {
-          tm_ld32(ts + c, v);
-          if (all) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              mx = fmaxf(mx, c + j <= vis ? __uint_as_float(v[j]) : -INFINITY);
-          }
-        }
-        float my;
-        ok = exchange(mx, my);
-        if (!ok) break;
-        mx = scale * fmaxf(mx, my);
-        const bool raise = mx > m + kLazy;
-        float f = 1.f;
-        if (raise) {
-          f = m == -INFINITY ? 0.f : ex2(m - mx);
-          m = mx;
-          l *= f;
-        }
-        if (kt > kfirst && __any_sync(kFull, raise)) {
-#pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) {
-            tm_ld32(to + c, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-            tm_st32(to + c, v);
-          }
-        }
-        const float base = m == -INFINITY ? 0.f : -m;
+        // `mo`: the maximum that this thread's weights of the tile stand on
+        float mo = m;
         float2 sum = make_float2(0.f, 0.f);
+        // the weights of this tile so far (16 columns of pairs a time), times f
+        auto rescale_weights = [&](int columns, float f) {
+          const __half2 f2 = __float2half2_rn(f);
+          tm_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < columns; c += 16) {
+            uint32_t p[16];
+            tm_ld16(ts + c, p);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = h2_bits(__hmul2(bits_h2(p[j]), f2));
+            tm_st16(ts + c, p);
+          }
+        };
 #pragma unroll
         for (int c = 0; c < kTile / 2; c += 32) {
+          uint32_t v[32];
           tm_ld32(ts + c, v);
           if (!all) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (c + j > vis) v[j] = __float_as_uint(-INFINITY);
           }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+          mx *= scale;
+          if (__any_sync(kFull, mx > mo + kLazy)) {
+            const float mn = mx > mo + kLazy ? ceilf(mx) : mo;
+            const float f = mn > mo ? pow2(mo - mn) : 1.f;
+            l *= f;
+            sum.x *= f;
+            sum.y *= f;
+            if (c > 0) rescale_weights(c / 2, f);
+            mo = mn;
+          }
+          const float base = mo == -INFINITY ? 0.f : -mo;
           uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -564,6 +584,28 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           tm_st16(ts + c / 2, p);
         }
         l += sum.x + sum.y;
+        // both threads of a row, and O, go to the larger maximum
+        float my;
+        ok = exchange(mo, my);
+        if (!ok) break;
+        my = fmaxf(mo, my);
+        if (__any_sync(kFull, my > mo)) {
+          const float f = my > mo ? pow2(mo - my) : 1.f;
+          l *= f;
+          rescale_weights(kTile / 4, f);
+        }
+        if (kt > kfirst && __any_sync(kFull, my > m)) {
+          const float f = my > m ? pow2(m - my) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 16) {
+            uint32_t v[16];
+            tm_ld16(to + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            tm_st16(to + c, v);
+          }
+        }
+        m = my;
         tm_wait_st();
         fence_before();
         __syncwarp();
@@ -581,8 +623,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       // the next queries: this slot's last scores have been read
       const Item done = it;
       have = fetch(it);
-      if (have) load_q(it);
-      ok = bar_wait(&B.o_full[wg], ph_o, dead);
+      if (have) ok = load_q(it);
+      ok = ok && bar_wait(&B.o_full[wg], ph_o, dead);
       ph_o ^= 1u;
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
