@@ -262,22 +262,21 @@ struct Cut {
   __device__ long long first(int c) const { return each * c + (c < more ? c : more); }
 };
 
-struct Item {
-  Seq s;
-  int b, h, pair;
-  int k0, k1, nk;   // key tiles [k0, k1) of nk
-  bool two;         // both query tiles have rows
-};
-
+// A place on the line: key tile k of pair `pair` of kv head h of sequence b,
+// and how many tiles of the CTA's piece are left from here.  Kept small: every
+// role holds one across its inner loop.
 struct Walk {
-  long long u, end;
-  int b, h, pair, k;
+  int left, b, h, pair, k;
   Seq s;
-  __device__ void seek(const PagedArgs &a, const long long *prefix, long long u0, long long u1,
+  __device__ int tiles(int tpt) const { return tiles_of(s, pair, tpt); }
+  // tiles of this pair in the piece
+  __device__ int steps(int tpt) const { return min(tiles(tpt) - k, left); }
+  // both query tiles have rows
+  __device__ bool two(int tpt) const { return pair * 2 * tpt + tpt < s.n; }
+  // to tile u of the line, with n tiles left
+  __device__ void seek(const PagedArgs &a, const long long *prefix, long long u, int n,
                        int max_new, int tpt) {
-    u = u0;
-    end = u1;
-    if (u >= end) return;
+    left = n;
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -296,27 +295,17 @@ struct Walk {
     }
     k = (int)v;
   }
-  __device__ bool next(const PagedArgs &a, const long long *prefix, int max_new, int tpt,
-                       Item &it) {
-    if (u >= end) return false;
-    it.s = s;
-    it.b = b;
-    it.h = h;
-    it.pair = pair;
-    it.nk = tiles_of(s, pair, tpt);
-    it.two = pair * 2 * tpt + tpt < s.n;
-    it.k0 = k;
-    it.k1 = (int)min((long long)it.nk, k + (end - u));
-    u += it.k1 - it.k0;
+  // to the next pair; false at the end of the piece
+  __device__ bool advance(const PagedArgs &a, const long long *prefix, int max_new, int tpt) {
+    left -= steps(tpt);
+    if (left <= 0) return false;
     k = 0;
     if (++pair >= pairs_of(s, tpt)) {
       pair = 0;
       if (++h == a.H_kv) {
         h = 0;
-        if (u < end) {
-          do { ++b; } while (b < a.B && prefix[b + 1] == prefix[b]);
-          if (b < a.B) s = seq_of(a, b, max_new);
-        }
+        do { ++b; } while (prefix[b + 1] == prefix[b]);
+        s = seq_of(a, b, max_new);
       }
     }
     return true;
@@ -403,13 +392,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
   const long long units = prefix[a.B];
   const int ctas = units > 0 ? ctas_used(units, gridDim.x) : 0;
   Walk walk;
-  Item it;
-  const bool busy = (int)blockIdx.x < ctas;
-  walk.u = walk.end = 0;
-  if (busy) {
+  bool have = (int)blockIdx.x < ctas;
+  if (have) {
     const Cut cut(units, ctas);
-    walk.seek(a, prefix, cut.first(blockIdx.x), cut.first(blockIdx.x + 1), t.max_new, tpt);
+    const long long u = cut.first(blockIdx.x);
+    walk.seek(a, prefix, u, (int)(cut.first(blockIdx.x + 1) - u), t.max_new, tpt);
   }
+  auto advance = [&]() { return walk.advance(a, prefix, t.max_new, tpt); };
 
   if (warp < 16) {
     // ---- softmax ----
@@ -437,16 +426,15 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     };
     float sl2 = 0.f;
     // query row of this thread, of the slot's query tile
-    auto token = [&](const Item &x) {
-      return x.pair * 2 * tpt + (x.two ? wg * tpt : 0) + row / GQ;
+    auto token = [&]() {
+      return walk.pair * 2 * tpt + (walk.two(tpt) ? wg * tpt : 0) + row / GQ;
     };
-    auto has_row = [&](const Item &x) { return row < tpt * GQ && token(x) < x.s.n; };
     // this thread's query row into shared memory
-    auto load_q = [&](const Item &x) {
-      const int tok = token(x);
-      const bool valid = has_row(x);
-      const T *q = static_cast<const T *>(t.q) + (int64_t)(x.s.first + tok) * t.q_token +
-                   (int64_t)(x.h * GQ + row % GQ) * t.q_head;
+    auto load_q = [&]() {
+      const int tok = token();
+      const bool valid = row < tpt * GQ && tok < walk.s.n;
+      const T *q = static_cast<const T *>(t.q) + (int64_t)(walk.s.first + tok) * t.q_token +
+                   (int64_t)(walk.h * GQ + row % GQ) * t.q_head;
       uint4 r[D / 16];
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -498,25 +486,28 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       if (lane == 0) bar_arrive(&B.q_full[wg]);
       return met;
     };
-    // the next item that this slot works on
-    auto fetch = [&](Item &x) {
-      while (walk.next(a, prefix, t.max_new, tpt, x))
-        if (wg == 0 || x.two || x.k1 - x.k0 > 1) return true;
-      return false;
+    // past the pairs that this slot has no part in
+    auto settle = [&]() {
+      while (have && wg == 1 && !walk.two(tpt) && walk.steps(tpt) < 2) have = advance();
     };
-    bool have = fetch(it), ok = true;
-    if (have) ok = load_q(it);
+    bool ok = true;
+    settle();
+    if (have) ok = load_q();
     while (have && ok) {
-      const int tok = token(it);
-      const bool valid = has_row(it);
+      const int tok = token();
+      const bool valid = row < tpt * GQ && tok < walk.s.n;
       // warps without a row leave the weights as they are: their rows of the
       // output are not read.  Rows without a query see everything.
       const bool idle = !__any_sync(kFull, valid);
-      const int pos = valid ? it.s.len - it.s.n + tok : 0x3fffffff;
+      const bool two = walk.two(tpt);
+      const int steps = walk.steps(tpt);
       const float scale = sl2;
       float m = -INFINITY, l = 0.f;
-      const int kfirst = it.k0 + (it.two ? 0 : wg), kstep = it.two ? 1 : 2;
-      for (int kt = kfirst; kt < it.k1; kt += kstep) {
+      // columns up to vis are seen
+      int vis = (valid ? walk.s.len - walk.s.n + tok : 0x3fffffff) -
+                (walk.k + (two ? 0 : wg)) * kTile - 64 * half;
+      const int ahead = two ? kTile : 2 * kTile;
+      for (int j = two ? 0 : wg; j < steps; j += two ? 1 : 2, vis -= ahead) {
         ok = bar_wait(&B.s_full[wg], ph_s, dead);
         ph_s ^= 1u;
         if (!__all_sync(kFull, ok)) { ok = false; break; }
@@ -527,7 +518,6 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           if (lane == 0) bar_arrive(&B.p_full[wg]);
           continue;
         }
-        const int vis = pos - kt * kTile - 64 * half;   // columns up to vis are seen
         const bool all = __all_sync(kFull, vis >= kTile / 2 - 1);
         // `mo`: the maximum that this thread's weights of the tile stand on
         float mo = m;
@@ -594,7 +584,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           l *= f;
           rescale_weights(kTile / 4, f);
         }
-        if (kt > kfirst && __any_sync(kFull, my > m)) {
+        if (j >= (two ? 1 : 2) && __any_sync(kFull, my > m)) {
           const float f = my > m ? pow2(m - my) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D / 2; c += 16) {
@@ -620,19 +610,25 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         if (!ok) break;
         l = half ? ly + l : l + ly;
       }
+      // slot 1 of a single query tile hands its sums to slot 0
+      const bool halves = !two && steps > 1;
+      const bool give = halves && wg == 1;
+      const bool whole = walk.k == 0 && steps == walk.tiles(tpt);
+      const int c0 = half * (D / 2);
+      float *xr = swap + (blockIdx.x * kTile + row) * (D + 4);
+      float *pr = give ? xr
+                       : part + ((2 * blockIdx.x + (walk.k > 0 ? 0 : 1)) * 2 * kTile +
+                                 (two ? wg * kTile : 0) + row) * (D + 4);
+      T *orow = static_cast<T *>(t.out) +
+                ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D + c0;
       // the next queries: this slot's last scores have been read
-      const Item done = it;
-      have = fetch(it);
-      if (have) ok = load_q(it);
+      have = advance();
+      settle();
+      if (have) ok = load_q();
       ok = ok && bar_wait(&B.o_full[wg], ph_o, dead);
       ph_o ^= 1u;
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
-      // slot 1 of a single query tile hands its sums to slot 0
-      const bool halves = !done.two && done.k1 - done.k0 > 1;
-      const bool give = halves && wg == 1;
-      float *xr = swap + ((int64_t)blockIdx.x * kTile + row) * (D + 4);
-      const int c0 = half * (D / 2);
       float f0 = 1.f, f1 = 0.f;
       if (halves && wg == 0) {
         ok = bar_wait(&B.x_full, ph_x, dead);
@@ -648,13 +644,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           m = M;
         }
       }
-      const bool whole = done.k0 == 0 && done.k1 == done.nk;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float *pr = give ? xr
-                       : part + ((int64_t)(2 * blockIdx.x + (done.k0 > 0 ? 0 : 1)) * 2 * kTile +
-                                 (done.two ? wg * kTile : 0) + row) * (D + 4);
-      T *orow = static_cast<T *>(t.out) +
-                ((int64_t)(done.s.first + tok) * a.H_q + done.h * GQ + row % GQ) * D;
       if (!idle) {
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
@@ -677,7 +667,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
               float y[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[j + e]) * inv;
-              store8<T>(orow + c0 + c + j, y);
+              store8<T>(orow + c + j, y);
             }
           } else if (valid) {
 #pragma unroll
@@ -700,8 +690,11 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     bool ok = true;
     const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
                   k64 = bits_h2(0xd400d400u);
-    while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
-      for (int kt = it.k0; ok && kt < it.k1; ++kt) {
+    for (; ok && have; have = advance()) {
+      const int steps = walk.steps(tpt);
+      // the sequence's tokens from this tile on
+      int left = walk.s.len - walk.k * kTile;
+      for (int j = 0; ok && j < steps; ++j, left -= kTile) {
         ok = bar_wait(&empty[st], ph_e, dead);
         unsigned char *dst = sm + (kv ? SM::V : SM::K) + st * SM::OP;
         for (int hf = 0; hf < 2; ++hf) {
@@ -749,7 +742,6 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
               }
             }
           } else {
-            const int left = it.s.len - (kt * kTile + r0);   // its tokens in the sequence
             // lane (n8, t4) reads the words of token pair t4, then the four
             // lanes of n8 exchange them, so that lane j has the four pairs (8
             // tokens) of the 32-channel span j
@@ -786,7 +778,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
                 for (int p = 0; p < 4; ++p) {
                   const uint2 y = vm[p * NG];
                   // tokens behind the sequence hold anything: their values are 0
-                  const int e = left - (8 * oct + 2 * p);
+                  const int e = left - (r0 + 8 * oct + 2 * p);
                   const unsigned keep = !good || e <= 0 ? 0u : (e == 1 ? 0x0000ffffu : kFull);
                   s[p] = bits_h2(y.x & keep);
                   z[p] = bits_h2(y.y & keep);
@@ -858,36 +850,37 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         ks ^= 1u;
         ph_k ^= ks == 0;
       };
-      while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
-        const int nt = it.k1 - it.k0;
-        const int slots = it.two || nt > 1 ? 2 : 1;
+      for (; ok && have; have = advance()) {
+        const int nt = walk.steps(tpt);
+        const bool two = walk.two(tpt);
+        const int slots = two || nt > 1 ? 2 : 1;
         // first scores of both slots: one key tile for two query tiles, or a
         // key tile each for one
         for (int i = 0; ok && i < slots; ++i) {
           ok = __all_sync(kFull, bar_wait(&B.q_full[i], ph_q[i], dead));
           ph_q[i] ^= 1u;
-          if (ok && (i == 0 || !it.two)) ok = keys();
+          if (ok && (i == 0 || !two)) ok = keys();
           if (!ok) break;
           fence_after();
           scores(i, ks);
-          if (!it.two || i + 1 == slots) keys_done();
+          if (!two || i + 1 == slots) keys_done();
         }
         for (int j = 0; ok && j < nt; ++j) {
           ok = __all_sync(kFull, bar_wait(&B.v_full[vs], ph_v, dead));
-          const bool last = it.two ? j + 1 == nt : j + 2 >= nt;
-          for (int i = it.two ? 0 : j & 1, n = it.two ? 2 : i + 1; ok && i < n; ++i) {
+          const bool last = two ? j + 1 == nt : j + 2 >= nt;
+          for (int i = two ? 0 : j & 1, n = two ? 2 : i + 1; ok && i < n; ++i) {
             ok = __all_sync(kFull, bar_wait(&B.p_full[i], ph_p[i], dead));
             ph_p[i] ^= 1u;
             if (!ok) break;
             fence_after();
-            outputs(i, vs, it.two ? j > 0 : j > 1);
+            outputs(i, vs, two ? j > 0 : j > 1);
             if (last) {
               mma_commit(&B.o_full[i]);
             } else {
-              if (i == 0 || !it.two) ok = keys();
+              if (i == 0 || !two) ok = keys();
               if (!ok) break;
               scores(i, ks);
-              if (!it.two || i == 1) keys_done();
+              if (!two || i == 1) keys_done();
             }
           }
           if (!ok) break;
@@ -907,14 +900,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     uint32_t raw = 0, ph_e = 1;
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
-    while (ok && walk.next(a, prefix, t.max_new, tpt, it)) {
-      const int nblk = (it.s.len + kBlk - 1) / kBlk;
-      for (int k4 = 2 * it.k0; ok && k4 < 2 * it.k1; ++k4) {
+    for (; ok && have; have = advance()) {
+      const int nblk = (walk.s.len + kBlk - 1) / kBlk, end = 2 * (walk.k + walk.steps(tpt));
+      for (int k4 = 2 * walk.k; ok && k4 < end; ++k4) {
         const int blk = 4 * k4 + lane;
         bool good = lane < 4 && blk < nblk;
         int p = -1;
         if (good) {
-          p = a.table[(int64_t)it.b * a.table_stride + (blk >> bpp)];
+          p = a.table[(int64_t)walk.b * a.table_stride + (blk >> bpp)];
           if ((unsigned)p >= (unsigned)a.n_pages) {
             atomicOr(a.status, kBadPage);
             good = false;
@@ -929,7 +922,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         }
         __syncwarp();
         if (good) {
-          const int64_t src = ((((int64_t)p * a.H_kv + it.h) << bpp) + (blk & ((1 << bpp) - 1)));
+          const int64_t src = ((((int64_t)p * a.H_kv + walk.h) << bpp) + (blk & ((1 << bpp) - 1)));
           bulk_g2s(sm + SM::RAW + ((kv * kRaw + raw) * 4 + lane) * SM::HALF,
                    a.pool + src * BLK + kv * SM::HALF, SM::HALF, &B.raw_full[kv][raw]);
         }
@@ -978,7 +971,7 @@ k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, long long *pr
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
   const long long u1 = cut.first(c + 1);
   Walk w;
-  w.seek(a, prefix, u1 - 1, u1, t.max_new, tpt);
+  w.seek(a, prefix, u1 - 1, 1, t.max_new, tpt);
   const Seq s = w.s;
   const int nk = tiles_of(s, w.pair, tpt), k = w.k, h = w.h, pair = w.pair;
   // the pair's first tile lies k tiles before unit u1 - 1
