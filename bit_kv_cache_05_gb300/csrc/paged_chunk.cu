@@ -13,20 +13,17 @@
 // its softmax: the two query tiles of a pair, or, where the second would be
 // empty, the even and the odd key tiles of one query tile (joined at the
 // end).  Its warps:
-//   0-7, 8-15  softmax of slot 0 and 1, two threads a row, 64 of its columns
-//              each: scores from tensor memory, online softmax in fp32 (their
-//              maxima compared through shared memory), weights back
-//              to tensor memory in fp16 (the A operand of the second
-//              product), the output read out at the end.  Rounding a weight
-//              to fp16 moves it by 2^-12 of itself at most, as one rounding
-//              of a 16-bit output does.
-//   16-19      rebuild k_hat (fp16 by definition) from the codes into two
-//   20-23      128-byte-swizzled stages, and v_hat likewise
-//   24         issues the products: S = Q k_hat^T, then O += P v_hat
-//   25, 26     copy the key and the value halves of the blocks (one bulk copy
+//   0-3, 4-7   softmax of slot 0 and 1, one row a thread: scores from tensor
+//              memory, online softmax in fp32, weights back to tensor memory
+//              in fp16 (the A operand of the second product), the output
+//              read out at the end.  Rounding a weight to fp16 moves it by
+//              2^-12 of itself at most, as one rounding of a 16-bit output
+//              does.
+//   8-11       rebuild k_hat (fp16 by definition) from the codes into two
+//   12-15      128-byte-swizzled stages, and v_hat likewise
+//   16         issues the products: S = Q k_hat^T, then O += P v_hat
+//   17, 18     copy the key and the value halves of the blocks (one bulk copy
 //              each), 64 tokens a stage
-// A slot's chain is scores, softmax, output, scores of the next tile; two
-// threads a row halve its longest part.
 // The running maximum of a row is a whole number (base 2) and is raised only
 // when a score passes it by more than 15: a weight stays below 2^15, which
 // fp16 holds, one pass over a tile's scores is enough, and what was weighed
@@ -43,7 +40,7 @@
 namespace vqk {
 namespace chunk {
 
-constexpr int kThreads = 864;
+constexpr int kThreads = 640;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
@@ -75,6 +72,32 @@ __device__ __forceinline__ __half2 field(uint32_t w) {
   return bits_h2(d);
 }
 
+// the (scale, zero) words of a token pair, all groups
+template <int NG>
+__device__ __forceinline__ void load_meta(const unsigned char *p, uint2 (&m)[NG]) {
+  if constexpr (NG == 1) {
+    m[0] = *reinterpret_cast<const uint2 *>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) {
+      const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
+      m[2 * i] = make_uint2(x.x, x.y);
+      m[2 * i + 1] = make_uint2(x.z, x.w);
+    }
+  }
+}
+
+template <int I>
+__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[I]) {
+  if constexpr (I == 4) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x; w[1] = x.y;
+  }
+}
+
 // ---- barriers ----------------------------------------------------------------
 
 __device__ __forceinline__ void bar_init(uint64_t *b, int count) {
@@ -83,18 +106,11 @@ __device__ __forceinline__ void bar_init(uint64_t *b, int count) {
 __device__ __forceinline__ void bar_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
 }
-// bounded (about half a second), given up at once when another role has
+// given up by its own limit, or soon after another role has
 __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *dead) {
-  if (mbar_try_wait(b, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(b, parity)) {
-    if (*dead) return false;
-    if (global_ns() - t0 > 500000000ull) {
-      *dead = 1;
-      return false;
-    }
-  }
-  return true;
+  if (bounded_wait(b, parity, dead)) return true;
+  *dead = 1;
+  return false;
 }
 
 // ---- tcgen05 -----------------------------------------------------------------
@@ -166,6 +182,33 @@ __device__ __forceinline__ void tm_ld16(uint32_t t, uint32_t (&v)[16]) {
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
       "tcgen05.wait::ld.sync.aligned;\n"
       : VQK_R8(v, 0), VQK_R8(v, 8)
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld8(uint32_t t, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : VQK_R8(v, 0)
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(t),
+      VQK_S8(v, 0)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld64(uint32_t t, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : VQK_R8(v, 0), VQK_R8(v, 8), VQK_R8(v, 16), VQK_R8(v, 24), VQK_R8(v, 32),
+        VQK_R8(v, 40), VQK_R8(v, 48), VQK_R8(v, 56)
       : "r"(t)
       : "memory");
 }
@@ -321,9 +364,7 @@ struct Smem {
   static constexpr int BLK = 16 * D + 128 * NG, HALF = BLK / 2;   // keys, values
   static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, RAW = 6 * OP;
   static constexpr int BAR = RAW + kRaw * 4 * BLK;
-  static constexpr int SWAP = BAR + 384;           // what a row's two threads exchange
-  static constexpr int EXP = SWAP + 2048;
-  static constexpr int PREFIX = EXP + 512;
+  static constexpr int PREFIX = BAR + 384;
   static constexpr int ALLOC = PREFIX + 8 * (kNear + 1) + 8 + 1024;   // room to align the base
 };
 
@@ -334,7 +375,6 @@ struct Bars {
   uint64_t raw_full[2][kRaw], raw_empty[2][kRaw];   // keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  uint64_t pair[2][4];      // the two warps of a slot's 32 rows
   uint64_t x_full, drain;
   uint32_t good[2][kRaw];   // which of a stage's 4 blocks arrived
   uint32_t tmem;
@@ -362,13 +402,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       bar_init(&B.v_full[i], 4);
       bar_init(&B.k_empty[i], 1);
       bar_init(&B.v_empty[i], 1);
-      bar_init(&B.q_full[i], 8);
+      bar_init(&B.q_full[i], 4);
       bar_init(&B.s_full[i], 1);
-      bar_init(&B.p_full[i], 8);
+      bar_init(&B.p_full[i], 4);
       bar_init(&B.o_full[i], 1);
-      for (int j = 0; j < 4; ++j) bar_init(&B.pair[i][j], 2);
     }
-    bar_init(&B.x_full, 8);
+    bar_init(&B.x_full, 4);
     bar_init(&B.drain, 1);
     B.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -400,30 +439,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
   }
   auto advance = [&]() { return walk.advance(a, prefix, t.max_new, tpt); };
 
-  if (warp < 16) {
+  // of the launch's 640 x 96 registers: 256 x 144 + 384 x 64 = 61440
+  if (warp < 8) {
     // ---- softmax ----
-    const int wg = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int wg = warp >> 2, row = tid & 127;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    // this thread's 64 columns of the scores, its D / 2 of the output
-    const uint32_t ts = tl + 128 * wg + 64 * half, to = tl + 256 + 128 * wg + half * (D / 2);
-    uint32_t ph_s = 0, ph_o = 0, ph_x = 0, ph_2 = 0;
-    // a value of the row's other thread, for one of its own
-    float *mine = reinterpret_cast<float *>(sm + SM::SWAP) + wg * 256 + half * 128 + row;
-    const float *other = reinterpret_cast<float *>(sm + SM::SWAP) + wg * 256 +
-                         (half ^ 1) * 128 + row;
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) bar_arrive(&B.pair[wg][warp & 3]);
-      const bool r = bar_wait(&B.pair[wg][warp & 3], ph_2, dead);
-      ph_2 ^= 1u;
-      return __all_sync(kFull, r);
-    };
-    auto exchange = [&](float x, float &y) {
-      *mine = x;
-      const bool r = meet();
-      y = *other;
-      return r;
-    };
+    const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
+    uint32_t ph_s = 0, ph_o = 0, ph_x = 0;
     float sl2 = 0.f;
     // query row of this thread, of the slot's query tile
     auto token = [&]() {
@@ -435,56 +458,48 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       const bool valid = row < tpt * GQ && tok < walk.s.n;
       const T *q = static_cast<const T *>(t.q) + (int64_t)(walk.s.first + tok) * t.q_token +
                    (int64_t)(walk.h * GQ + row % GQ) * t.q_head;
-      uint4 r[D / 16];
+      uint4 r[D / 8];
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < D / 8; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
       if (valid) {
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          r[c] = reinterpret_cast<const uint4 *>(q)[half * (D / 16) + c];
+        for (int c = 0; c < D / 8; ++c) r[c] = reinterpret_cast<const uint4 *>(q)[c];
       }
       sl2 = t.scale;
-      bool met = true;
+      float up = 1.f;
       if constexpr (!std::is_same<T, __half>::value) {
         // a bf16 row as fp16: scaled by a power of two to a maximum near 2^14
         uint32_t m = 0u;               // largest magnitude, as bits
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < D / 8; ++c) {
           const uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             m = max(m, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
         }
-        uint8_t *ex = sm + SM::EXP + wg * 256 + row;
-        ex[half * 128] = (uint8_t)(m >> 23);
-        met = meet();
-        const int e = max((int)(m >> 23), (int)ex[(half ^ 1) * 128]);
+        const int e = (int)(m >> 23);
         int f = e > 0 ? 14 - (e - 127) : 0;
         f = f > 126 ? 126 : (f < -100 ? -100 : f);
-        const float up = __uint_as_float((uint32_t)(127 + f) << 23);
+        up = __uint_as_float((uint32_t)(127 + f) << 23);
         sl2 *= __uint_as_float((uint32_t)(127 - f) << 23);
+      }
+      unsigned char *dst = sm + SM::Q + wg * SM::OP;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
+        if constexpr (!std::is_same<T, __half>::value) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             w[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * up,
                                              __uint_as_float(w[i] & 0xffff0000u) * up));
-          r[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
-      unsigned char *dst = sm + SM::Q + wg * SM::OP;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int c = half * (D / 16) + i;
         *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + sw(row, c & 7)) =
-            make_uint4(__byte_perm(r[i].x, r[i].z, 0x5410), __byte_perm(r[i].x, r[i].z, 0x7632),
-                       __byte_perm(r[i].y, r[i].w, 0x5410), __byte_perm(r[i].y, r[i].w, 0x7632));
+            make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
+                       __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(&B.q_full[wg]);
-      return met;
     };
     // past the pairs that this slot has no part in
     auto settle = [&]() {
@@ -492,7 +507,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     };
     bool ok = true;
     settle();
-    if (have) ok = load_q();
+    if (have) load_q();
     while (have && ok) {
       const int tok = token();
       const bool valid = row < tpt * GQ && tok < walk.s.n;
@@ -505,7 +520,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       float m = -INFINITY, l = 0.f;
       // columns up to vis are seen
       int vis = (valid ? walk.s.len - walk.s.n + tok : 0x3fffffff) -
-                (walk.k + (two ? 0 : wg)) * kTile - 64 * half;
+                (walk.k + (two ? 0 : wg)) * kTile;
       const int ahead = two ? kTile : 2 * kTile;
       for (int j = two ? 0 : wg; j < steps; j += two ? 1 : 2, vis -= ahead) {
         ok = bar_wait(&B.s_full[wg], ph_s, dead);
@@ -518,114 +533,95 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           if (lane == 0) bar_arrive(&B.p_full[wg]);
           continue;
         }
-        const bool all = __all_sync(kFull, vis >= kTile / 2 - 1);
-        // `mo`: the maximum that this thread's weights of the tile stand on
-        float mo = m;
-        float2 sum = make_float2(0.f, 0.f);
-        // the weights of this tile so far (16 columns of pairs a time), times f
-        auto rescale_weights = [&](int columns, float f) {
-          const __half2 f2 = __float2half2_rn(f);
-          tm_wait_st();
-#pragma unroll 1
-          for (int c = 0; c < columns; c += 16) {
-            uint32_t p[16];
-            tm_ld16(ts + c, p);
+        const bool all = __all_sync(kFull, vis >= kTile - 1);
+        float mo = m;       // the maximum that the tile's weights stand on
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = h2_bits(__hmul2(bits_h2(p[j]), f2));
-            tm_st16(ts + c, p);
-          }
-        };
-#pragma unroll
-        for (int c = 0; c < kTile / 2; c += 32) {
-          uint32_t v[32];
-          tm_ld32(ts + c, v);
+        for (int c = 0; c < kTile; c += 64) {
+          uint32_t v[64];
+          tm_ld64(ts + c, v);
           if (!all) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 64; ++j)
               if (c + j > vis) v[j] = __float_as_uint(-INFINITY);
           }
-          float mx = -INFINITY;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-          mx *= scale;
-          if (__any_sync(kFull, mx > mo + kLazy)) {
-            const float mn = mx > mo + kLazy ? ceilf(mx) : mo;
+          for (int j = 0; j < 64; j += 2)
+            mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+          const float top = scale * fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          if (__any_sync(kFull, top > mo + kLazy)) {
+            const float mn = top > mo + kLazy ? ceilf(top) : mo;
             const float f = mn > mo ? pow2(mo - mn) : 1.f;
             l *= f;
-            sum.x *= f;
-            sum.y *= f;
-            if (c > 0) rescale_weights(c / 2, f);
+            if (c > 0) {
+              // the weights of this tile so far
+              sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
+              const __half2 f2 = __float2half2_rn(f);
+              tm_wait_st();
+#pragma unroll 1
+              for (int d = 0; d < c / 2; d += 8) {
+                uint32_t p[8];
+                tm_ld8(ts + d, p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = h2_bits(__hmul2(bits_h2(p[j]), f2));
+                tm_st8(ts + d, p);
+              }
+            }
             mo = mn;
           }
           const float base = mo == -INFINITY ? 0.f : -mo;
-          uint32_t p[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = __ffma2_rn(
-                make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                make_float2(scale, scale), make_float2(base, base));
-            const float2 y = make_float2(ex2(x.x), ex2(x.y));
-            sum = __fadd2_rn(sum, y);
-            p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
+          for (int d = 0; d < 64; d += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[d + 2 * j]),
+                                                      __uint_as_float(v[d + 2 * j + 1])),
+                                          make_float2(scale, scale), make_float2(base, base));
+              const float2 y = make_float2(ex2(x.x), ex2(x.y));
+              sum[j & 1] = __fadd2_rn(sum[j & 1], y);
+              p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
+            }
+            // the weights of 32 columns take 16, all behind what is read
+            tm_st16(ts + (c + d) / 2, p);
           }
-          // the weights of these 32 columns take 16, all behind what this
-          // thread reads and none of the other thread's
-          tm_st16(ts + c / 2, p);
         }
-        l += sum.x + sum.y;
-        // both threads of a row, and O, go to the larger maximum
-        float my;
-        ok = exchange(mo, my);
-        if (!ok) break;
-        my = fmaxf(mo, my);
-        if (__any_sync(kFull, my > mo)) {
-          const float f = my > mo ? pow2(mo - my) : 1.f;
-          l *= f;
-          rescale_weights(kTile / 4, f);
-        }
-        if (j >= (two ? 1 : 2) && __any_sync(kFull, my > m)) {
-          const float f = my > m ? pow2(m - my) : 1.f;
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        // O goes to the new maximum
+        if (j >= (two ? 1 : 2) && __any_sync(kFull, mo > m)) {
+          const float f = mo > m ? pow2(m - mo) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
+          for (int c = 0; c < D; c += 16) {
             uint32_t v[16];
             tm_ld16(to + c, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
             tm_st16(to + c, v);
           }
         }
-        m = my;
+        m = mo;
         tm_wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&B.p_full[wg]);
       }
       if (!ok) break;
-      // before the next queries are announced, so that this value is read before
-      // the next tile's maximum takes its place
-      if (!idle) {
-        float ly;
-        ok = exchange(l, ly);
-        if (!ok) break;
-        l = half ? ly + l : l + ly;
-      }
       // slot 1 of a single query tile hands its sums to slot 0
       const bool halves = !two && steps > 1;
       const bool give = halves && wg == 1;
       const bool whole = walk.k == 0 && steps == walk.tiles(tpt);
-      const int c0 = half * (D / 2);
       float *xr = swap + (blockIdx.x * kTile + row) * (D + 4);
       float *pr = give ? xr
                        : part + ((2 * blockIdx.x + (walk.k > 0 ? 0 : 1)) * 2 * kTile +
                                  (two ? wg * kTile : 0) + row) * (D + 4);
       T *orow = static_cast<T *>(t.out) +
-                ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D + c0;
+                ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D;
       // the next queries: this slot's last scores have been read
       have = advance();
       settle();
-      if (have) ok = load_q();
-      ok = ok && bar_wait(&B.o_full[wg], ph_o, dead);
+      if (have) load_q();
+      ok = bar_wait(&B.o_full[wg], ph_o, dead);
       ph_o ^= 1u;
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
@@ -647,14 +643,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (!idle) {
 #pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
+        for (int c = 0; c < D; c += 32) {
           uint32_t v[32];
           __syncwarp();
           tm_ld32(to + c, v);
           if (halves && wg == 0 && valid) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 x = *reinterpret_cast<const float4 *>(xr + c0 + c + j);
+              const float4 x = *reinterpret_cast<const float4 *>(xr + c + j);
               v[j] = __float_as_uint(__uint_as_float(v[j]) * f0 + x.x * f1);
               v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f0 + x.y * f1);
               v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f0 + x.z * f1);
@@ -672,19 +668,20 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           } else if (valid) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4 *>(pr + c0 + c + j) =
+              *reinterpret_cast<uint4 *>(pr + c + j) =
                   make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
         }
-        if (valid && !half && (give || !whole)) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
+        if (valid && (give || !whole)) *reinterpret_cast<float2 *>(pr + D) = make_float2(m, l);
       }
       __syncwarp();
       if (give && lane == 0) bar_arrive(&B.x_full);
       fence_before();
     }
-  } else if (warp < 24) {
-    // ---- k_hat (warps 16-19) and v_hat (20-23) ----
-    const int kv = (warp - 16) >> 2, w = warp & 3, n8 = lane >> 2, t4 = lane & 3;
+  } else if (warp < 16) {
+    // ---- k_hat (warps 8-11) and v_hat (12-15) ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int kv = (warp - 8) >> 2, w = warp & 3, n8 = lane >> 2, t4 = lane & 3;
     uint64_t *full = kv ? B.v_full : B.k_full, *empty = kv ? B.v_empty : B.k_empty;
     uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
     bool ok = true;
@@ -705,30 +702,31 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
           const bool good = (B.good[kv][raw] >> w) & 1u;
           const int r0 = 64 * hf + 16 * w;             // its first key in the tile
           if (!kv) {
+            // the 8 lanes of a 16-byte store hold rows r and r + 4, whose
+            // swizzled chunks meet 8 different bank groups
+            const int nr = (n8 >> 1) | ((n8 & 1) << 2);
+            uint32_t kw[2][I];
+            uint2 km[2][NG];
 #pragma unroll
             for (int oct = 0; oct < 2; ++oct) {
-              const int tk = 8 * oct + n8, r = r0 + tk;
-              uint32_t kw[I];
-              if constexpr (I == 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(blk + tk * (D / 2) + t4 * 16);
-                kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
-              } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(blk + tk * (D / 2) + t4 * 8);
-                kw[0] = x.x; kw[1] = x.y;
-              }
-              const uint2 *km = reinterpret_cast<const uint2 *>(blk + off_km(D)) + (tk >> 1) * NG;
-              const unsigned sel = !good ? 0x4444u : (tk & 1) ? 0x3232u : 0x1010u;
-              // neighbouring rows store the two halves of a 128-byte row in
-              // turn, so that 8 lanes' 16-byte stores meet 8 bank groups
-              const int odd = n8 & 1;
+              const int tk = 8 * oct + nr;
+              load_words<I>(blk + tk * (D / 2) + t4 * (4 * I), kw[oct]);
+              load_meta<NG>(blk + off_km(D) + (tk >> 1) * (8 * NG), km[oct]);
+            }
+            const unsigned sel = !good ? 0x4444u : (nr & 1) ? 0x3232u : 0x1010u;
+            unsigned char *row = dst + (r0 + nr) * 128;
+            // chunk t4 of the row's lower half; the upper half is chunk t4 + 4
+            const int lower = (t4 ^ nr) << 4, upper = lower ^ 64;
 #pragma unroll
-              for (int i2 = 0; i2 < I; ++i2) {
-                const int i = i2 ^ odd;
-                uint32_t x = odd ? kw[i2 ^ 1] : kw[i2];
-                const uint2 y = km[32 * i / G];
-                const __half2 s = bits_h2(__byte_perm(y.x, 0u, sel)),
-                              z = bits_h2(__byte_perm(y.y, 0u, sel));
-                uint32_t o[4];
+            for (int oct = 0; oct < 2; ++oct) {
+              __half2 s, z;
+#pragma unroll
+              for (int i = 0; i < I; ++i) {
+                if ((32 * i) % G == 0) {
+                  s = bits_h2(__byte_perm(km[oct][32 * i / G].x, 0u, sel));
+                  z = bits_h2(__byte_perm(km[oct][32 * i / G].y, 0u, sel));
+                }
+                uint32_t x = kw[oct][i], o[4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   const __half2 c0 = __hsub2(field<0x000f000fu>(x), k1024);
@@ -737,7 +735,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
                   o[2 * j + 1] = h2_bits(__hfma2(c1, s, z));
                   x >>= 8;
                 }
-                *reinterpret_cast<uint4 *>(dst + (i >> 1) * 16384 + sw(r, 4 * (i & 1) + t4)) =
+                *reinterpret_cast<uint4 *>(row + oct * 1024 + (i >> 1) * 16384 +
+                                           ((i & 1) ? upper : lower)) =
                     make_uint4(o[0], o[1], o[2], o[3]);
               }
             }
@@ -813,7 +812,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         ph_e ^= st == 0;
       }
     }
-  } else if (warp == 24) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  }
+  if (warp == 16) {
     // ---- the products ----
     {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
@@ -836,7 +838,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
         const uint64_t v = dv + stage * (SM::OP >> 4);
 #pragma unroll
         for (int e = 0; e < kTile / 16; ++e)
-          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 64 * (e >> 2) + 8 * (e & 3),
+          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * e,
                  v + (e >> 2) * (D * 8) + 2 * (e & 3), id_o, more || e > 0);
       };
       // waits for the keys of the next tile, and gives them back
@@ -894,38 +896,44 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
       int never = 0;
       bar_wait(&B.drain, 0, &never);
     }
-  } else {
-    // ---- copies: keys (25) and values (26) ----
-    const int kv = warp - 25, bpp = a.page_log2 - 4;
+  } else if (warp == 17 || warp == 18) {
+    // ---- copies: keys (17) and values (18) ----
+    const int kv = warp - 17, bpp = a.page_log2 - 4;
     uint32_t raw = 0, ph_e = 1;
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
     for (; ok && have; have = advance()) {
       const int nblk = (walk.s.len + kBlk - 1) / kBlk, end = 2 * (walk.k + walk.steps(tpt));
-      for (int k4 = 2 * walk.k; ok && k4 < end; ++k4) {
-        const int blk = 4 * k4 + lane;
-        bool good = lane < 4 && blk < nblk;
-        int p = -1;
-        if (good) {
-          p = a.table[(int64_t)walk.b * a.table_stride + (blk >> bpp)];
-          if ((unsigned)p >= (unsigned)a.n_pages) {
-            atomicOr(a.status, kBadPage);
-            good = false;
+      // lane j looks up block 4 k4 + j of the next 8 stages at once, so that
+      // a table's latency is met once in 512 tokens
+      const uint8_t *src = nullptr;
+      unsigned there = 0u;
+      for (int k4 = 2 * walk.k, i = 0; ok && k4 < end; ++k4, i = (i + 1) & 7) {
+        if (i == 0) {
+          const int blk = 4 * k4 + lane;
+          bool good = blk < nblk && blk < 4 * end;
+          if (good) {
+            const int p = a.table[(int64_t)walk.b * a.table_stride + (blk >> bpp)];
+            if ((unsigned)p >= (unsigned)a.n_pages) {
+              atomicOr(a.status, kBadPage);
+              good = false;
+            }
+            src = a.pool + ((((int64_t)p * a.H_kv + walk.h) << bpp) + (blk & ((1 << bpp) - 1))) *
+                               BLK + kv * SM::HALF;
           }
+          there = __ballot_sync(kFull, good);
         }
         ok = bar_wait(&B.raw_empty[kv][raw], ph_e, dead);
         if (!__all_sync(kFull, ok)) { ok = false; break; }
-        const unsigned mask = __ballot_sync(kFull, good);
+        const unsigned mask = (there >> (4 * i)) & 15u;
         if (lane == 0) {
           B.good[kv][raw] = mask;
           mbar_expect_tx(&B.raw_full[kv][raw], __popc(mask) * SM::HALF);
         }
         __syncwarp();
-        if (good) {
-          const int64_t src = ((((int64_t)p * a.H_kv + walk.h) << bpp) + (blk & ((1 << bpp) - 1)));
-          bulk_g2s(sm + SM::RAW + ((kv * kRaw + raw) * 4 + lane) * SM::HALF,
-                   a.pool + src * BLK + kv * SM::HALF, SM::HALF, &B.raw_full[kv][raw]);
-        }
+        if (lane >> 2 == i && (there >> lane & 1u))
+          bulk_g2s(sm + SM::RAW + ((kv * kRaw + raw) * 4 + (lane & 3)) * SM::HALF, src, SM::HALF,
+                   &B.raw_full[kv][raw]);
         used |= 1u << raw;
         raw = raw + 1 == kRaw ? 0 : raw + 1;
         ph_e ^= raw == 0;

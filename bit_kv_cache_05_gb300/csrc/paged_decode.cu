@@ -375,7 +375,7 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
     for (; k < k_end; ++k) {
       const unsigned gd = (good >> (2 * s)) & 3u;
       if (gd) {
-        const bool ok = mbar_wait(&bar[s], (phases >> s) & 1u);
+        const bool ok = bounded_wait(&bar[s], (phases >> s) & 1u);
         phases ^= 1u << s;
         if (!__all_sync(kFull, ok)) {
           if (lane == 0) atomicOr(a.status, kGaveUp);
@@ -533,7 +533,7 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
   if (dead) {
     // let the copies in flight land before the CTA's memory is given up
     for (int i = 0; i < ST; ++i)
-      if ((good >> (2 * i)) & 3u) mbar_wait(&bar[i], (phases >> i) & 1u);
+      if ((good >> (2 * i)) & 3u) bounded_wait(&bar[i], (phases >> i) & 1u);
   }
 }
 
