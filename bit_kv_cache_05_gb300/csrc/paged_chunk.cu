@@ -47,7 +47,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLazy = 15.f;
 constexpr int kNear = 64;            // sequences whose prefix fits in shared memory
 constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
-constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes
+constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes, one a warp
 
 __device__ __forceinline__ uint32_t saddr(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -355,6 +355,15 @@ struct Walk {
   }
 };
 
+// A pair whose keys were cut: left by the CTA that has its first tiles, read
+// by the merge.
+struct alignas(16) CutPair {
+  int first;   // row of the token tensors of its first token
+  int n;       // tokens from there on in the sequence (0: no cut pair)
+  int h;       // kv head
+  int last;    // CTA with its last tiles
+};
+
 // ---- shared memory --------------------------------------------------------------
 
 template <int D, int NG>
@@ -379,11 +388,13 @@ struct Bars {
   uint32_t good[2][kRaw];   // which of a stage's 4 blocks arrived
   uint32_t tmem;
   int dead;
+  CutPair cut;
 };
 
 template <typename T, int D, int NG>
 __global__ void __launch_bounds__(kThreads, 1)
-k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *prefixes) {
+k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cuts,
+              long long *prefixes) {
   using SM = Smem<D, NG>;
   constexpr int I = D / 32, G = D / NG, BLK = SM::BLK;
   extern __shared__ unsigned char smem_raw[];
@@ -410,6 +421,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
     bar_init(&B.x_full, 4);
     bar_init(&B.drain, 1);
     B.dead = 0;
+    B.cut.n = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -420,8 +432,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
   fence_before();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  // (the merge reads CTA 0's)
-  long long *prefix = a.B <= kNear && blockIdx.x > 0
+  long long *prefix = a.B <= kNear
                           ? reinterpret_cast<long long *>(sm + SM::PREFIX)
                           : prefixes + (long long)blockIdx.x * (a.B + 1);
   tile_prefix(a, t.max_new, tpt, prefix);
@@ -617,6 +628,15 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
                                  (two ? wg * kTile : 0) + row) * (D + 4);
       T *orow = static_cast<T *>(t.out) +
                 ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D;
+      if (tid == 0 && walk.k == 0 && !whole) {
+        // the pair goes on in the next CTAs' pieces
+        const Cut cut(units, ctas);
+        int last = blockIdx.x;
+        for (long long rest = walk.tiles(tpt) - steps; rest > 0; ++last)
+          rest -= cut.each + (last + 1 < cut.more ? 1 : 0);
+        const int tok0 = walk.pair * 2 * tpt;
+        B.cut = CutPair{walk.s.first + tok0, walk.s.n - tok0, walk.h, last};
+      }
       // the next queries: this slot's last scores have been read
       have = advance();
       settle();
@@ -952,7 +972,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (tid == 0 && B.dead) atomicOr(a.status, kGaveUp);
+  if (tid == 0) {
+    if (B.dead) atomicOr(a.status, kGaveUp);
+    cuts[blockIdx.x] = B.cut;
+  }
   if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -960,64 +983,47 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, long long *p
 }
 
 // Merge of a pair whose keys were cut: CTA (slice, c) merges 16 rows of the
-// pair that ends CTA c's piece of the line, when that pair starts in it and
-// goes on.  One warp per row, lanes over channels.
+// pair that CTA c of the attention began and did not end.  One warp per row,
+// lanes over channels.
 template <typename T, int D>
-__global__ void __launch_bounds__(128)
-k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, long long *prefixes,
-                    int grid) {
-  const int c = blockIdx.y, slice = blockIdx.x;
+__global__ void __launch_bounds__(32 * kSliceRows)
+k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, const CutPair *cuts) {
   constexpr int CPL = D / 32, ROW = D + 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the attention's CTA 0 has left the prefix
-  const long long *prefix = prefixes;
-  const long long units = prefix[a.B];
-  if (units == 0) return;
-  const int ctas = ctas_used(units, grid);
-  if (c + 1 >= ctas) return;
-  const Cut cut(units, ctas);
+  const int c = blockIdx.y, lane = threadIdx.x & 31,
+            r = blockIdx.x * kSliceRows + (threadIdx.x >> 5);
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
-  const long long u1 = cut.first(c + 1);
-  Walk w;
-  w.seek(a, prefix, u1 - 1, 1, t.max_new, tpt);
-  const Seq s = w.s;
-  const int nk = tiles_of(s, w.pair, tpt), k = w.k, h = w.h, pair = w.pair;
-  // the pair's first tile lies k tiles before unit u1 - 1
-  if (k + 1 >= nk || u1 - 1 - k < cut.first(c)) return;
-  const long long ulast = u1 - 1 - k + nk - 1;
-  int cl = c + 1;
-  while (cl + 1 < ctas && cut.first(cl + 1) <= ulast) ++cl;
-  const int lane = threadIdx.x & 31;
-  for (int r = slice * kSliceRows + (threadIdx.x >> 5); r < (slice + 1) * kSliceRows; r += 4) {
-    const int wg = r >> 7, row = r & 127, tok = pair * 2 * tpt + wg * tpt + row / GQ;
-    if (row >= tpt * GQ || tok >= s.n) continue;
-    auto at = [&](int i) {
-      return part + ((int64_t)(i == c ? 2 * c + 1 : 2 * i) * 2 * kTile + r) * ROW;
-    };
-    float M = -INFINITY;
-    for (int i = c + lane; i <= cl; i += 32) M = fmaxf(M, at(i)[D]);
+  const int row = r & 127, tok = (r >> 7) * tpt + row / GQ;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 q = *reinterpret_cast<const int4 *>(&cuts[c]);
+  const CutPair cut{q.x, q.y, q.z, q.w};
+  if (row >= tpt * GQ || tok >= cut.n) return;
+  auto at = [&](int i) {
+    return part + ((int64_t)(i == c ? 2 * c + 1 : 2 * i) * 2 * kTile + r) * ROW;
+  };
+  float M = -INFINITY;
+  for (int i = c + lane; i <= cut.last; i += 32) M = fmaxf(M, at(i)[D]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float L = 0.f, acc[CPL];
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  float L = 0.f, acc[CPL];
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+  for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int i = c; i <= cl; ++i) {
-      const float *p = at(i);
-      const float2 ml = *reinterpret_cast<const float2 *>(p + D);
-      const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
-      L = fmaf(f, ml.y, L);
+  for (int i = c; i <= cut.last; ++i) {
+    const float *p = at(i);
+    const float2 ml = *reinterpret_cast<const float2 *>(p + D);
+    // a part without a seen token weighs nothing (NaN sums stay)
+    const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+    L = fmaf(f, ml.y, L);
 #pragma unroll
-      for (int e = 0; e < CPL; ++e) acc[e] = fmaf(f, p[32 * e + lane], acc[e]);
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    T *o = static_cast<T *>(t.out) +
-           ((int64_t)(s.first + tok) * a.H_q + h * GQ + row % GQ) * D;
+    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(f, p[32 * e + lane], acc[e]);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  T *o = static_cast<T *>(t.out) +
+         ((int64_t)(cut.first + tok) * a.H_q + cut.h * GQ + row % GQ) * D;
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) {
-      if constexpr (std::is_same<T, __half>::value) o[32 * e + lane] = __float2half_rn(acc[e] * inv);
-      else o[32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
-    }
+  for (int e = 0; e < CPL; ++e) {
+    if constexpr (std::is_same<T, __half>::value) o[32 * e + lane] = __float2half_rn(acc[e] * inv);
+    else o[32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
   }
 }
 
@@ -1033,17 +1039,18 @@ cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cud
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SM::ALLOC);
   if (e != cudaSuccess) return e;
   float *part = t.ws, *swap = part + part_floats(D, sm_count);
-  long long *prefixes = reinterpret_cast<long long *>(swap + swap_floats(D, sm_count));
+  CutPair *cuts = reinterpret_cast<CutPair *>(swap + swap_floats(D, sm_count));
+  long long *prefixes = reinterpret_cast<long long *>(cuts + sm_count);
   e = launch_pdl(k_paged_chunk<T, D, NG>, dim3(sm_count), dim3(kThreads), SM::ALLOC, st, a, t,
-                 part, swap, prefixes);
+                 part, swap, cuts, prefixes);
   count_launch();
   if (e != cudaSuccess) return e;
   // rows of a pair that can hold queries: one tile's, or both tiles'
   const int GQ = a.H_q / a.H_kv;
   const int slices = t.max_new <= kTile / GQ ? (t.max_new * GQ + kSliceRows - 1) / kSliceRows
                                              : 2 * kTile / kSliceRows;
-  e = launch_pdl(k_paged_chunk_merge<T, D>, dim3(slices, sm_count), dim3(128), 0, st, a, t,
-                 (const float *)part, prefixes, sm_count);
+  e = launch_pdl(k_paged_chunk_merge<T, D>, dim3(slices, sm_count), dim3(32 * kSliceRows), 0,
+                 st, a, t, (const float *)part, (const CutPair *)cuts);
   count_launch();
   return e;
 }
@@ -1064,6 +1071,7 @@ cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_cou
 
 size_t paged_chunk_ws(int B, int, int D, int sm_count) {
   return (chunk::part_floats(D, sm_count) + chunk::swap_floats(D, sm_count)) * sizeof(float) +
+         sm_count * sizeof(chunk::CutPair) +
          (size_t)sm_count * (B + 1) * sizeof(long long);
 }
 

@@ -147,13 +147,17 @@ __device__ __forceinline__ int warps_used(int units, int warps_max) {
   const int w = (units + kMinSteps - 1) / kMinSteps;
   return w < warps_max ? w : warps_max;
 }
-__device__ __forceinline__ int first_unit(int units, int warps, int w) {
-  return (int)((int64_t)units * w / warps);
-}
-// the warp that owns step u
-__device__ __forceinline__ int owner(int units, int warps, int u) {
-  return (int)((((int64_t)u + 1) * warps - 1) / units);
-}
+// (pieces differ by one step at most)
+struct Cut {
+  int each, more;
+  __device__ Cut(int units, int warps) : each(units / warps), more(units % warps) {}
+  __device__ int first(int w) const { return each * w + min(w, more); }
+  // the warp that owns step u
+  __device__ int owner(int u) const {
+    const int big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
+  }
+};
 
 template <int D>
 struct Part {   // a partial: rows x (D outputs, maximum, sum, padding)
@@ -201,7 +205,7 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)
 
 template <typename T, int D, int NG>
 __global__ void __launch_bounds__(kThreads, DecSmem<D, NG>::CTAS)
-k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
+k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
   using SM = DecSmem<D, NG>;
   constexpr int I = D / 32, BLK = SM::BLK, STEP = SM::STEP, ST = SM::STAGES, G = D / NG;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -218,13 +222,16 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max) {
   asm volatile("griddepcontrol.launch_dependents;");
   step_prefix(a, t.max_new, prefix, wsum);
 
+  if (blockIdx.x == 0)   // for the merge
+    for (int i = threadIdx.x; i <= a.B; i += kThreads) prefixes[i] = prefix[i];
   const int units = prefix[a.B];
   const int warps = warps_used(units, warps_max);
   // neighbouring pieces of the line go to different SMs
   const int w = warp * gridDim.x + blockIdx.x;
   if (w >= warps) return;
-  int u = first_unit(units, warps, w);
-  const int u_end = first_unit(units, warps, w + 1);
+  const Cut cut(units, warps);
+  int u = cut.first(w);
+  const int u_end = cut.first(w + 1);
   const int H = a.H_kv, GQ = a.H_q / a.H_kv;
 
   auto find = [&](int uu) {   // the sequence of step uu
@@ -543,30 +550,26 @@ constexpr int kMergeWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-k_paged_merge(PagedArgs a, PagedAttend t, int warps_max) {
+k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix) {
   constexpr int CPL = D / 32;
   __shared__ float red[kMergeWarps][D];
   __shared__ float rl[kMergeWarps], rm[kMergeWarps];
-  extern __shared__ int prefix[];
-  __shared__ int wsum[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  step_prefix(a, t.max_new, prefix, wsum);
   const int H = a.H_kv, GQ = a.H_q / H, R = t.max_new * GQ;
   const int row = blockIdx.x % R, seg = blockIdx.x / R, b = seg / H, h = seg % H;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Lengths L = lengths_of(a, b, t.max_new);
+  const int units = prefix[a.B], p0 = prefix[b], nb = (prefix[b + 1] - p0) / H;
   if (row >= L.n * GQ) return;
   const int64_t tokrow = (a.cu ? a.cu[b] : b) + row / GQ;
   T *out = static_cast<T *>(t.out) + (tokrow * a.H_q + h * GQ + row % GQ) * D;
-  const int units = prefix[a.B], nb = (prefix[b + 1] - prefix[b]) / H;
   float acc[CPL];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
   float lsum = 0.f, mw = -INFINITY;
   if (nb > 0) {
-    const int warps = warps_used(units, warps_max);
-    const int u0 = prefix[b] + h * nb;
-    const int w0 = owner(units, warps, u0), w1 = owner(units, warps, u0 + nb - 1);
+    const Cut cut(units, warps_used(units, warps_max));
+    const int u0 = p0 + h * nb, w0 = cut.owner(u0), w1 = cut.owner(u0 + nb - 1);
     // this warp's partials: the maximum first, then the weighted sums
     const float *base = t.ws + ((int64_t)(w0 + seg) * R + row) * Part<D>::ROW;
     const int64_t step = (int64_t)R * Part<D>::ROW;
@@ -621,6 +624,11 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max) {
 // CTAs of one wave
 int decode_ctas(int D, int sm_count) { return (D == 128 ? 3 : 4) * sm_count; }
 
+// a partial per warp and per (sequence, kv head)
+size_t part_floats(int B, int H_kv, int D, int rows, int sm_count) {
+  return ((size_t)decode_ctas(D, sm_count) * kWarps + (size_t)B * H_kv) * rows * (D + 4);
+}
+
 template <typename T, int D, int NG>
 cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
                        cudaStream_t st) {
@@ -630,13 +638,14 @@ cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int ctas = decode_ctas(D, sm_count), warps_max = ctas * kWarps;
+  const int rows = t.max_new * (a.H_q / a.H_kv);
+  int *prefixes = reinterpret_cast<int *>(t.ws + part_floats(a.B, a.H_kv, D, rows, sm_count));
   e = launch_pdl(k_paged_decode<T, D, NG>, dim3(ctas), dim3(kThreads), smem, st, a, t,
-                 warps_max);
+                 warps_max, prefixes);
   count_launch();
   if (e != cudaSuccess) return e;
-  const int rows = t.max_new * (a.H_q / a.H_kv);
-  e = launch_pdl(k_paged_merge<T, D>, dim3(a.B * a.H_kv * rows), dim3(32 * kMergeWarps),
-                 sizeof(int) * (a.B + 1), st, a, t, warps_max);
+  e = launch_pdl(k_paged_merge<T, D>, dim3(a.B * a.H_kv * rows), dim3(32 * kMergeWarps), 0, st,
+                 a, t, warps_max, (const int *)prefixes);
   count_launch();
   return e;
 }
@@ -656,8 +665,7 @@ cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_cou
 }  // namespace
 
 size_t paged_decode_ws(int B, int H_kv, int D, int rows, int sm_count) {
-  return ((size_t)decode_ctas(D, sm_count) * kWarps + (size_t)B * H_kv) * rows * (D + 4) *
-         sizeof(float);
+  return part_floats(B, H_kv, D, rows, sm_count) * sizeof(float) + (B + 1) * sizeof(int);
 }
 
 cudaError_t launch_paged_decode(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
