@@ -628,15 +628,6 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
                                  (two ? wg * kTile : 0) + row) * (D + 4);
       T *orow = static_cast<T *>(t.out) +
                 ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D;
-      if (tid == 0 && walk.k == 0 && !whole) {
-        // the pair goes on in the next CTAs' pieces
-        const Cut cut(units, ctas);
-        int last = blockIdx.x;
-        for (long long rest = walk.tiles(tpt) - steps; rest > 0; ++last)
-          rest -= cut.each + (last + 1 < cut.more ? 1 : 0);
-        const int tok0 = walk.pair * 2 * tpt;
-        B.cut = CutPair{walk.s.first + tok0, walk.s.n - tok0, walk.h, last};
-      }
       // the next queries: this slot's last scores have been read
       have = advance();
       settle();
@@ -923,6 +914,15 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
     for (; ok && have; have = advance()) {
+      if (kv && lane == 0 && walk.k == 0 && walk.steps(tpt) < walk.tiles(tpt)) {
+        // the pair goes on in the next CTAs' pieces
+        const Cut cut(units, ctas);
+        int last = blockIdx.x;
+        for (long long rest = walk.tiles(tpt) - walk.steps(tpt); rest > 0; ++last)
+          rest -= cut.each + (last + 1 < cut.more ? 1 : 0);
+        const int tok0 = walk.pair * 2 * tpt;
+        B.cut = CutPair{walk.s.first + tok0, walk.s.n - tok0, walk.h, last};
+      }
       const int nblk = (walk.s.len + kBlk - 1) / kBlk, end = 2 * (walk.k + walk.steps(tpt));
       // lane j looks up block 4 k4 + j of the next 8 stages at once, so that
       // a table's latency is met once in 512 tokens
