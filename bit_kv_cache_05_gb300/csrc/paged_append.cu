@@ -27,6 +27,51 @@ __device__ __forceinline__ __half to_half_sat(float x) {
   return __float2half_rn(x != x ? x : y);
 }
 
+__device__ __forceinline__ void store_half8(__half *p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __halves2half2(to_half_sat(v[2 * i]), to_half_sat(v[2 * i + 1]));
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Code of 16 channels x of a group from lo in steps of `scale`, 4 bits each,
+// the first lowest: rint((x - lo) / scale) with the quotient rounded to fp32.
+// The product with the reciprocal is off by less than 2^-21 of a quotient of
+// at most 15; only where it comes within 2^-12 of a tie (|t - rint(t)| near
+// 1/2) can the two round to different codes, and there the division decides.
+__device__ __forceinline__ void codes16(const float (&x)[16], float lo, float scale,
+                                        uint32_t (&w)[2]) {
+  constexpr float kMagic = 12582912.f;      // 1.5 * 2^23: its sum's low bits are rint
+  const float inv = __fdividef(1.f, scale);
+  float off = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t acc = 0u;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {
+      const float t = (x[8 * h + e] - lo) * inv;
+      const float r = t + kMagic;
+      off = fmaxf(off, fabsf(t - (r - kMagic)));
+      acc = acc * 16u + __float_as_uint(r);
+    }
+    // 0x4B400000 (kMagic's bits) times 1 + 16 + ... + 16^7, modulo 2^32
+    w[h] = acc - 0x3f400000u;
+  }
+  if (off > 0.5f - 0.000244140625f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t acc = 0u;
+#pragma unroll
+      for (int e = 7; e >= 0; --e)
+        acc = acc * 16u + (uint32_t)(int)rintf((x[8 * h + e] - lo) / scale);
+      w[h] = acc;
+    }
+  }
+}
+
 // One row's 16 neighbouring channels x per lane, quantized and stored in the
 // block `blk` (nullptr: not stored) at token tl.  `poison`: the token's key or
 // value row holds a NaN.  A key row then gets NaN zeros, so that the scores
@@ -50,13 +95,7 @@ __device__ __forceinline__ void quantize_row(const float (&x)[16], int g, int l,
   lo += 0.f;                                  // -0 to +0
   const float scale = (hi - lo) / 15.f;
   uint32_t w[2] = {0u, 0u};
-  if (scale > 0.f && !poison) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float t = fminf(fmaxf(rintf((x[e] - lo) / scale), 0.f), 15.f);
-      w[e >> 3] |= (uint32_t)(int)t << (4 * (e & 7));
-    }
-  }
+  if (scale > 0.f && !poison) codes16(x, lo, scale, w);
   __half s = __float2half_rn(scale), z = __float2half_rn(lo);
   // code 15 must stay inside fp16's range (it rounds to infinity from 65520)
   if (fmaf(15.f, __half2float(s), lo) >= 65520.f)
@@ -88,8 +127,12 @@ __device__ __forceinline__ void quantize_row(const float (&x)[16], int g, int l,
   }
 }
 
+// A warp serves a token (with few tokens `parts` warps do), 32 / LPR rows at a
+// time: first the query rows, then the key and value rows of as many kv
+// heads.  The next rows' loads are in flight while these are worked on, and
+// the first ones while the token's place is looked up.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
                bool rotate_by_place, float eps, int parts) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;
@@ -99,10 +142,32 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
   const int64_t t = w / parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t >= a.tokens) return;
-  const Place at = find_place(a, t);
-  if (at.pos < 0) return;
   int p0, p1;
   chunk_places(r, l, p0, p1);
+  const int gq = (q.heads + RPW - 1) / RPW, gk = (a.H_kv + RPW - 1) / RPW;
+  uint4 xa[1] = {}, xb[1] = {}, va[1] = {}, vb[1] = {};
+  auto fetch = [&](int gi) {
+    const bool isk = gi >= gq;
+    const HeadRows &h = isk ? k : q;
+    const int row = (isk ? gi - gq : gi) * RPW + sub;
+    if (gi < gq + gk && row < h.heads) {
+      const T *x = static_cast<const T *>(h.x) + t * h.x_token + row * h.x_head;
+      load8<T>(x + p0, xa);
+      load8<T>(x + p1, xb);
+      if (isk) {
+        const T *y = static_cast<const T *>(v.x) + t * v.x_token + row * v.x_head + 16 * l;
+        load8<T>(y, va);
+        load8<T>(y + 8, vb);
+      }
+    }
+  };
+  int gi = (int)(w % parts);
+  fetch(gi);
+  const Place at = find_place(a, t);
+  if (at.pos < 0) return;
+  // the token's page, looked up while the rows arrive
+  const bool stores = gi + (gq + gk - 1 - gi) / parts * parts >= gq;
+  const int page = stores ? a.table[(int64_t)at.b * a.table_stride + (at.pos >> a.page_log2)] : 0;
   float c[8], s[8];
   rope_angles<LPR>(r, [&](int ax) -> long long {
     if (rotate_by_place) return at.pos;
@@ -110,44 +175,37 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
     return r.pos64 ? static_cast<const long long *>(r.pos)[i]
                    : (long long)static_cast<const int *>(r.pos)[i];
   }, lane, c, s);
+  const bool good = (unsigned)page < (unsigned)a.n_pages;
+  if (!good && lane == 0) atomicOr(a.status, kBadPage);
 
-  const int gq = (q.heads + RPW - 1) / RPW, gk = (a.H_kv + RPW - 1) / RPW;
-  for (int gi = (int)(w % parts); gi < gq + gk; gi += parts) {
+  const void *held = nullptr;
+  uint4 wa[1] = {}, wb[1] = {};
+  for (; gi < gq + gk; gi += parts) {
     const bool isk = gi >= gq;
     const HeadRows &h = isk ? k : q;
     const int row = (isk ? gi - gq : gi) * RPW + sub;
     const bool valid = row < h.heads;
-    uint4 na[1] = {}, nb[1] = {};
-    float x0[8], x1[8];
-    if (valid) {
-      const T *x = static_cast<const T *>(h.x) + t * h.x_token + row * h.x_head;
-      load8<T>(x + p0, na);
-      load8<T>(x + p1, nb);
-    }
-    unpack8<T>(na, x0);
-    unpack8<T>(nb, x1);
-    float y[16];
+    float x0[8], x1[8], y[16];
+    unpack8<T>(xa, x0);
+    unpack8<T>(xb, x1);
     if (isk) {
-      uint4 va[1] = {}, vb[1] = {};
-      if (valid) {
-        const T *x = static_cast<const T *>(v.x) + t * v.x_token + row * v.x_head + 16 * l;
-        load8<T>(x, va);
-        load8<T>(x + 8, vb);
-      }
       float y0[8], y1[8];
       unpack8<T>(va, y0);
       unpack8<T>(vb, y1);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        y[e] = __half2float(to_half_sat(y0[e]));
-        y[8 + e] = __half2float(to_half_sat(y1[e]));
+        y[e] = y0[e];
+        y[8 + e] = y1[e];
       }
     }
+    fetch(gi + parts);
     if (h.weight) {
-      uint4 wa[1], wb[1];
+      if (held != h.weight) {
+        held = h.weight;
+        load8<T>(static_cast<const T *>(h.weight) + p0, wa);
+        load8<T>(static_cast<const T *>(h.weight) + p1, wb);
+      }
       float w0[8], w1[8];
-      load8<T>(static_cast<const T *>(h.weight) + p0, wa);
-      load8<T>(static_cast<const T *>(h.weight) + p1, wb);
       unpack8<T>(wa, w0);
       unpack8<T>(wb, w1);
       norm_row<LPR>(x0, x1, w0, w1, D, eps);
@@ -162,14 +220,9 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
       continue;
     }
     // the key row's lanes change from rotated pairs to neighbouring channels
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x0[e] = __half2float(to_half_sat(x0[e]));
-      x1[e] = __half2float(to_half_sat(x1[e]));
-    }
     __syncwarp();
-    store8<__half>(&rows[warp][sub][p0], x0);
-    store8<__half>(&rows[warp][sub][p1], x1);
+    store_half8(&rows[warp][sub][p0], x0);
+    store_half8(&rows[warp][sub][p1], x1);
     __syncwarp();
     uint4 ka[1], kb[1];
     load8<__half>(&rows[warp][sub][16 * l], ka);
@@ -177,16 +230,25 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
     unpack8<__half>(ka, x0);
     unpack8<__half>(kb, x1);
     float x[16];
-    bool nan = false;
+    float sum = 0.f;                       // NaN where any of them is
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       x[e] = x0[e];
       x[8 + e] = x1[e];
-      nan = nan || x0[e] != x0[e] || x1[e] != x1[e] || y[e] != y[e] || y[8 + e] != y[8 + e];
+      sum += 0.f * (x0[e] + x1[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      y[e] = __half2float(to_half_sat(y[e]));
+      sum += 0.f * y[e];
     }
     const unsigned mask = ((1u << LPR) - 1u) << (sub * LPR);
-    const bool poison = (__ballot_sync(kFull, nan) & mask) != 0u;
-    uint8_t *blk = valid ? find_block(a, at.b, at.pos, row, paged_block_bytes(D, a.g)) : nullptr;
+    const bool poison = (__ballot_sync(kFull, sum != sum) & mask) != 0u;
+    uint8_t *blk = nullptr;
+    if (valid && good)
+      blk = a.pool + ((((int64_t)page * a.H_kv + row) << (a.page_log2 - 4)) +
+                      ((at.pos & ((1 << a.page_log2) - 1)) >> 4)) *
+                         paged_block_bytes(D, a.g);
     quantize_row<D, false>(x, a.g, l, poison, blk, at.pos & 15);
     quantize_row<D, true>(y, a.g, l, poison, blk, at.pos & 15);
   }
