@@ -20,42 +20,77 @@ namespace {
 constexpr int kThreads = 128;
 constexpr unsigned kFull = 0xffffffffu;
 
-// fp16 of x; values beyond the type's range (infinities too) become its
-// largest, NaN stays NaN
-__device__ __forceinline__ __half to_half_sat(float x) {
-  const float y = fminf(fmaxf(x, -65504.f), 65504.f);
-  return __float2half_rn(x != x ? x : y);
+// two fp16 of two fp32; values beyond the type's range (infinities too) become
+// its largest, NaN stays NaN
+__device__ __forceinline__ uint32_t half2_sat(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
-__device__ __forceinline__ void store_half8(__half *p, const float (&v)[8]) {
-  uint32_t w[4];
+__device__ __forceinline__ __half2 as_half2(uint32_t u) {
+  return *reinterpret_cast<const __half2 *>(&u);
+}
+
+// 8 channels as stored in fp16, saturated as above
+template <typename T>
+__device__ __forceinline__ void to_half8(const uint4 &r, uint32_t (&h)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __halves2half2(to_half_sat(v[2 * i]), to_half_sat(v[2 * i + 1]));
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    if constexpr (std::is_same<T, __half>::value) {
+      const __half2 top = as_half2(0x7bff7bffu), low = as_half2(0xfbfffbffu);
+      const __half2 x = __hmax2_nan(__hmin2_nan(as_half2(w[i]), top), low);
+      h[i] = *reinterpret_cast<const uint32_t *>(&x);
+    } else {
+      h[i] = half2_sat(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
   }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Code of 16 channels x of a group from lo in steps of `scale`, 4 bits each,
+// smallest and largest of a group, whose 16-channel pieces lie in g / 16
+// neighbouring lanes; NaN where one of its values is
+__device__ __forceinline__ __half2 group_range(const uint32_t (&h)[8], int g) {
+  __half2 lo = as_half2(h[0]), hi = lo;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    lo = __hmin2_nan(lo, as_half2(h[e]));
+    hi = __hmax2_nan(hi, as_half2(h[e]));
+  }
+  __half l = __hmin_nan(__low2half(lo), __high2half(lo));
+  __half u = __hmax_nan(__low2half(hi), __high2half(hi));
+  for (int o = 1; o < (g >> 4); o <<= 1) {
+    const __half2 x = __shfl_xor_sync(kFull, __halves2half2(l, u), o);
+    l = __hmin_nan(l, __low2half(x));
+    u = __hmax_nan(u, __high2half(x));
+  }
+  return __halves2half2(l, u);
+}
+
+// Codes of 16 channels of a group from lo in steps of `scale`, 4 bits each,
 // the first lowest: rint((x - lo) / scale) with the quotient rounded to fp32.
 // The product with the reciprocal is off by less than 2^-21 of a quotient of
 // at most 15; only where it comes within 2^-12 of a tie (|t - rint(t)| near
 // 1/2) can the two round to different codes, and there the division decides.
-__device__ __forceinline__ void codes16(const float (&x)[16], float lo, float scale,
+__device__ __forceinline__ void codes16(const uint32_t (&x)[8], float lo, float scale,
                                         uint32_t (&w)[2]) {
   constexpr float kMagic = 12582912.f;      // 1.5 * 2^23: its sum's low bits are rint
   const float inv = __fdividef(1.f, scale);
+  const float2 lo2 = make_float2(-lo, -lo), inv2 = make_float2(inv, inv);
+  const float2 up2 = make_float2(kMagic, kMagic), down2 = make_float2(-kMagic, -kMagic);
   float off = 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t acc = 0u;
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-      const float t = (x[8 * h + e] - lo) * inv;
-      const float r = t + kMagic;
-      off = fmaxf(off, fabsf(t - (r - kMagic)));
-      acc = acc * 16u + __float_as_uint(r);
+    for (int e = 3; e >= 0; --e) {
+      const float2 d = __fadd2_rn(__half22float2(as_half2(x[4 * h + e])), lo2);
+      const float2 t = __fmul2_rn(d, inv2);
+      const float2 r = __fadd2_rn(t, up2);
+      const float2 i = __fadd2_rn(r, down2);
+      off = fmaxf(off, fmaxf(fabsf(t.x - i.x), fabsf(t.y - i.y)));
+      acc = acc * 16u + __float_as_uint(r.y);
+      acc = acc * 16u + __float_as_uint(r.x);
     }
     // 0x4B400000 (kMagic's bits) times 1 + 16 + ... + 16^7, modulo 2^32
     w[h] = acc - 0x3f400000u;
@@ -65,35 +100,27 @@ __device__ __forceinline__ void codes16(const float (&x)[16], float lo, float sc
     for (int h = 0; h < 2; ++h) {
       uint32_t acc = 0u;
 #pragma unroll
-      for (int e = 7; e >= 0; --e)
-        acc = acc * 16u + (uint32_t)(int)rintf((x[8 * h + e] - lo) / scale);
+      for (int e = 3; e >= 0; --e) {
+        const float2 v = __half22float2(as_half2(x[4 * h + e]));
+        acc = acc * 16u + (uint32_t)(int)rintf((v.y - lo) / scale);
+        acc = acc * 16u + (uint32_t)(int)rintf((v.x - lo) / scale);
+      }
       w[h] = acc;
     }
   }
 }
 
 // One row's 16 neighbouring channels x per lane, quantized and stored in the
-// block `blk` (nullptr: not stored) at token tl.  `poison`: the token's key or
+// block `blk` at token tl.  `poison`: the token's key or
 // value row holds a NaN.  A key row then gets NaN zeros, so that the scores
 // of every query that sees the token are NaN; a value row is stored as
 // zeros, because a masked token's weight of 0 times NaN would reach rows
 // that do not see it.
 template <int D, bool VALUES>
-__device__ __forceinline__ void quantize_row(const float (&x)[16], int g, int l, bool poison,
-                                             uint8_t *blk, int tl) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int e = 1; e < 16; ++e) {
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-  }
-  for (int o = 1; o < (g >> 4); o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-  }
-  if (!blk) return;
-  lo += 0.f;                                  // -0 to +0
-  const float scale = (hi - lo) / 15.f;
+__device__ __forceinline__ void quantize_row(const uint32_t (&x)[8], __half2 range, int g, int l,
+                                             bool poison, uint8_t *blk, int tl) {
+  const float lo = __low2float(range) + 0.f;            // -0 to +0
+  const float scale = (__high2float(range) - lo) / 15.f;
   uint32_t w[2] = {0u, 0u};
   if (scale > 0.f && !poison) codes16(x, lo, scale, w);
   __half s = __float2half_rn(scale), z = __float2half_rn(lo);
@@ -185,17 +212,18 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
     const HeadRows &h = isk ? k : q;
     const int row = (isk ? gi - gq : gi) * RPW + sub;
     const bool valid = row < h.heads;
-    float x0[8], x1[8], y[16];
+    float x0[8], x1[8];
     unpack8<T>(xa, x0);
     unpack8<T>(xb, x1);
+    uint32_t y[8];
     if (isk) {
-      float y0[8], y1[8];
-      unpack8<T>(va, y0);
-      unpack8<T>(vb, y1);
+      uint32_t y0[4], y1[4];
+      to_half8<T>(va[0], y0);
+      to_half8<T>(vb[0], y1);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         y[e] = y0[e];
-        y[8 + e] = y1[e];
+        y[4 + e] = y1[e];
       }
     }
     fetch(gi + parts);
@@ -221,36 +249,29 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
     }
     // the key row's lanes change from rotated pairs to neighbouring channels
     __syncwarp();
-    store_half8(&rows[warp][sub][p0], x0);
-    store_half8(&rows[warp][sub][p1], x1);
+    *reinterpret_cast<uint4 *>(&rows[warp][sub][p0]) =
+        make_uint4(half2_sat(x0[0], x0[1]), half2_sat(x0[2], x0[3]), half2_sat(x0[4], x0[5]),
+                   half2_sat(x0[6], x0[7]));
+    *reinterpret_cast<uint4 *>(&rows[warp][sub][p1]) =
+        make_uint4(half2_sat(x1[0], x1[1]), half2_sat(x1[2], x1[3]), half2_sat(x1[4], x1[5]),
+                   half2_sat(x1[6], x1[7]));
     __syncwarp();
-    uint4 ka[1], kb[1];
-    load8<__half>(&rows[warp][sub][16 * l], ka);
-    load8<__half>(&rows[warp][sub][16 * l + 8], kb);
-    unpack8<__half>(ka, x0);
-    unpack8<__half>(kb, x1);
-    float x[16];
-    float sum = 0.f;                       // NaN where any of them is
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = x0[e];
-      x[8 + e] = x1[e];
-      sum += 0.f * (x0[e] + x1[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      y[e] = __half2float(to_half_sat(y[e]));
-      sum += 0.f * y[e];
-    }
+    const uint4 k0 = *reinterpret_cast<const uint4 *>(&rows[warp][sub][16 * l]),
+                k1 = *reinterpret_cast<const uint4 *>(&rows[warp][sub][16 * l + 8]);
+    const uint32_t x[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+    const __half2 xr = group_range(x, a.g), yr = group_range(y, a.g);
+    // a NaN of any group of the token's key or value row
     const unsigned mask = ((1u << LPR) - 1u) << (sub * LPR);
-    const bool poison = (__ballot_sync(kFull, sum != sum) & mask) != 0u;
+    const bool poison =
+        (__ballot_sync(kFull, __hisnan(__low2half(xr)) || __hisnan(__low2half(yr))) & mask) != 0u;
     uint8_t *blk = nullptr;
     if (valid && good)
       blk = a.pool + ((((int64_t)page * a.H_kv + row) << (a.page_log2 - 4)) +
                       ((at.pos & ((1 << a.page_log2) - 1)) >> 4)) *
                          paged_block_bytes(D, a.g);
-    quantize_row<D, false>(x, a.g, l, poison, blk, at.pos & 15);
-    quantize_row<D, true>(y, a.g, l, poison, blk, at.pos & 15);
+    if (!blk) continue;
+    quantize_row<D, false>(x, xr, a.g, l, poison, blk, at.pos & 15);
+    quantize_row<D, true>(y, yr, a.g, l, poison, blk, at.pos & 15);
   }
 }
 
