@@ -146,7 +146,7 @@ struct PagedAttend {
   float *ws;                 // workspace
 };
 
-// few rows: up to 8 (new token, query head) pairs per kv head
+// few rows: up to 16 (new token, query head) pairs per kv head
 size_t paged_decode_ws(int B, int H_kv, int D, int rows, int sm_count);
 cudaError_t launch_paged_decode(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                 int sm_count, cudaStream_t st);

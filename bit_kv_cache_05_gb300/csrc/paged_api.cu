@@ -160,9 +160,9 @@ int check_batch(const vq_kivi_paged *p, const vq_kivi_paged_batch *s, PagedArgs 
   return VQ_OK;
 }
 
-// the few-row kernel serves up to 8 rows of a kv head
+// the split-KV kernel serves up to 16 rows of a kv head
 bool few_rows(const vq_kivi_paged *p, int max_new) {
-  return (int64_t)max_new * (p->H_q / p->H_kv) <= 8;
+  return (int64_t)max_new * (p->H_q / p->H_kv) <= 16;
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // Attention of few new tokens per sequence over the paged 4-bit cache: up to
-// 8 (new token, query head) pairs per kv head (vq_kivi_paged_attend).
+// 16 (new token, query head) pairs per kv head (vq_kivi_paged_attend).
 //
 //   out = sum_t softmax_t(scale q.k_hat_t) v_hat_t,  t <= the row's own token
 //
@@ -15,7 +15,10 @@
 // pair's scales are the halves of one word), B = up to 8 query rows; output:
 // A = weights, turned over by movmatrix, B = v_hat.  The weights enter as
 // fp16 hi (rows 0-7) plus the remainder lo (rows 8-15, free in a 16-row
-// product), so only the output is rounded to 16 bits.  Both operands that
+// product), so only the output is rounded to 16 bits.  With 9 to 16 rows
+// (drafts) the second 8 take those rows, and the weights of all are rounded to
+// fp16 once, as the tensor-memory kernel rounds them: 2^-12 of a weight at
+// most, no more than the output's own rounding.  Both operands that
 // change are made where the product reads them: no register is moved.  k_hat and
 // v_hat are fp16 by definition; a bf16 query row is scaled by a power of two
 // to a maximum near 2^14 and taken as fp16, which keeps every bit of values
@@ -164,13 +167,20 @@ struct Part {   // a partial: rows x (D outputs, maximum, sum, padding)
   static constexpr int ROW = D + 4;
 };
 
-template <int D, int NG>
+// CTAs of 4 warps on an SM: what the registers allow (64 accumulators a thread
+// at D = 128, the second 8 rows' queries and scores with 16 rows; 16 sequences
+// of about 6000 tokens, 16 rows: 53.6 us with two CTAs, 62 with three and
+// spills)
+__host__ __device__ constexpr int decode_ctas(int D, int rows) {
+  return D == 64 ? 4 : (rows > 8 ? 2 : 3);
+}
+
+template <int D, int NG, int ROWS>
 struct DecSmem {
   static constexpr int BLK = 16 * D + 128 * NG;
   static constexpr int STEP = 2 * BLK;
-  // 12 warps an SM at D = 128 (64 accumulators a thread), 16 at D = 64
-  static constexpr int CTAS = D == 128 ? 3 : 4;
-  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int CTAS = decode_ctas(D, ROWS);
+  static constexpr int STAGES = CTAS == 3 ? 3 : 4;
   static constexpr int PER_WARP = STAGES * STEP;         // a multiple of 128
   static constexpr int BAR = kWarps * PER_WARP;
   static constexpr int PREFIX = BAR + kWarps * STAGES * 8;
@@ -203,11 +213,13 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)
   }
 }
 
-template <typename T, int D, int NG>
-__global__ void __launch_bounds__(kThreads, DecSmem<D, NG>::CTAS)
+// ROWS: 8, or 16 for calls with more rows
+template <typename T, int D, int NG, int ROWS>
+__global__ void __launch_bounds__(kThreads, DecSmem<D, NG, ROWS>::CTAS)
 k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
-  using SM = DecSmem<D, NG>;
+  using SM = DecSmem<D, NG, ROWS>;
   constexpr int I = D / 32, BLK = SM::BLK, STEP = SM::STEP, ST = SM::STAGES, G = D / NG;
+  constexpr int NR = ROWS / 8;      // groups of 8 rows
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int wsum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, t4 = lane & 3;
@@ -311,38 +323,43 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
     enter(b, u, nb, h, k);
     const Lengths L = lengths_of(a, b, t.max_new);
     const int row0 = a.cu ? a.cu[b] : b, rows = L.n * GQ;
-    const int tok = n8 / GQ;
-    // the newest tokens that rows 2 t4 and 2 t4 + 1 see (rows without a
-    // query: none)
-    const int see0 = 2 * t4 < rows ? L.len - L.n + 2 * t4 / GQ : -1;
-    const int see1 = 2 * t4 + 1 < rows ? L.len - L.n + (2 * t4 + 1) / GQ : -1;
     const int all_see = L.len - L.n;      // tokens up to here are seen by all rows
-    uint32_t qa[I][4];
-    float sl2 = t.scale;
-    {
+    // of rows 8 g + 2 t4 and the next: the newest tokens they see (rows
+    // without a query: none), the scores' factors, maxima and sums
+    int2 see[NR];
+    float2 sc[NR], m[NR], l[NR];
+    uint32_t qa[NR][I][4];
+#pragma unroll
+    for (int g = 0; g < NR; ++g) {
+      const int r0 = 8 * g + 2 * t4, row = 8 * g + n8;
+      see[g] = make_int2(r0 < rows ? L.len - L.n + r0 / GQ : -1,
+                         r0 + 1 < rows ? L.len - L.n + (r0 + 1) / GQ : -1);
+      m[g] = make_float2(-INFINITY, -INFINITY);
+      l[g] = make_float2(0.f, 0.f);
+      float sl2 = t.scale;
       uint4 raw[I];
-      const T *q = static_cast<const T *>(t.q) + (row0 + tok) * t.q_token +
-                   (h * GQ + n8 % GQ) * t.q_head;
+      const T *q = static_cast<const T *>(t.q) + (int64_t)(row0 + row / GQ) * t.q_token +
+                   (int64_t)(h * GQ + row % GQ) * t.q_head;
 #pragma unroll
       for (int i = 0; i < I; ++i)
-        raw[i] = n8 < rows ? *reinterpret_cast<const uint4 *>(q + 32 * i + 8 * t4)
-                           : make_uint4(0u, 0u, 0u, 0u);
+        raw[i] = row < rows ? *reinterpret_cast<const uint4 *>(q + 32 * i + 8 * t4)
+                            : make_uint4(0u, 0u, 0u, 0u);
       if constexpr (!std::is_same<T, __half>::value) {
-        float m = 0.f;
+        float mq = 0.f;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
           const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            m = fmaxf(m, fabsf(__uint_as_float(x[e] << 16)));
-            m = fmaxf(m, fabsf(__uint_as_float(x[e] & 0xffff0000u)));
+            mq = fmaxf(mq, fabsf(__uint_as_float(x[e] << 16)));
+            mq = fmaxf(mq, fabsf(__uint_as_float(x[e] & 0xffff0000u)));
           }
         }
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+        mq = fmaxf(mq, __shfl_xor_sync(kFull, mq, 1));
+        mq = fmaxf(mq, __shfl_xor_sync(kFull, mq, 2));
         // factor 2^f, f = 14 - exponent, within what fp32 can hold
-        int f = 14 - ((int)(__float_as_uint(m) >> 23) - 127);
-        f = m > 0.f ? (f > 126 ? 126 : f) : 0;
+        int f = 14 - ((int)(__float_as_uint(mq) >> 23) - 127);
+        f = mq > 0.f ? (f > 126 ? 126 : f) : 0;
         f = f < -100 ? -100 : f;
         const float up = __uint_as_float((uint32_t)(127 + f) << 23);
         sl2 *= __uint_as_float((uint32_t)(127 - f) << 23);
@@ -359,16 +376,13 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         // pairs (r, r + 4) of the 8 channels, as the codes' words give them
-        qa[i][0] = __byte_perm(raw[i].x, raw[i].z, 0x5410);
-        qa[i][1] = __byte_perm(raw[i].x, raw[i].z, 0x7632);
-        qa[i][2] = __byte_perm(raw[i].y, raw[i].w, 0x5410);
-        qa[i][3] = __byte_perm(raw[i].y, raw[i].w, 0x7632);
+        qa[g][i][0] = __byte_perm(raw[i].x, raw[i].z, 0x5410);
+        qa[g][i][1] = __byte_perm(raw[i].x, raw[i].z, 0x7632);
+        qa[g][i][2] = __byte_perm(raw[i].y, raw[i].w, 0x5410);
+        qa[g][i][3] = __byte_perm(raw[i].y, raw[i].w, 0x7632);
       }
+      sc[g] = make_float2(__shfl_sync(kFull, sl2, 8 * t4), __shfl_sync(kFull, sl2, 8 * t4 + 4));
     }
-    // of rows 2 t4 and 2 t4 + 1
-    const float2 sc = make_float2(__shfl_sync(kFull, sl2, 8 * t4),
-                                  __shfl_sync(kFull, sl2, 8 * t4 + 4));
-    float2 m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
     float o[I][4][4];
 #pragma unroll
     for (int i = 0; i < I; ++i)
@@ -391,8 +405,9 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
         }
         const unsigned char *st = stage + s * STEP;
         const int t0 = k * kStep;
-        // raw scores of rows 2 t4, 2 t4 + 1: tokens 16 bk + 2 n8 and the next
-        float x[2][4];
+        // raw scores of rows 8 g + 2 t4 and the next: tokens 16 bk + 2 n8 and
+        // the next
+        float x[NR][2][4];
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
           const unsigned char *blk = st + bk * BLK;
@@ -402,74 +417,105 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
           load_words<I>(blk + (2 * n8 + 1) * (D / 2) + t4 * (4 * I), k1);
           load_meta<NG>(blk + off_km(D) + n8 * (8 * NG), km);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[bk][e] = 0.f;
+          for (int g = 0; g < NR; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[g][bk][e] = 0.f;
 #pragma unroll
           for (int i = 0; i < I; ++i) {
             const __half2 s2 = bits_h2(km[32 * i / G].x), z2 = bits_h2(km[32 * i / G].y);
             uint32_t v0[4], v1[4];
             word_values(k0[i], __low2half2(s2), __low2half2(z2), v0);
             word_values(k1[i], __high2half2(s2), __high2half2(z2), v1);
-            mma16816(x[bk], v0[0], v1[0], v0[1], v1[1], qa[i][0], qa[i][1]);
-            mma16816(x[bk], v0[2], v1[2], v0[3], v1[3], qa[i][2], qa[i][3]);
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+              mma16816(x[g][bk], v0[0], v1[0], v0[1], v1[1], qa[g][i][0], qa[g][i][1]);
+              mma16816(x[g][bk], v0[2], v1[2], v0[3], v1[3], qa[g][i][2], qa[g][i][3]);
+            }
           }
         }
         const bool special = t0 + kStep - 1 > all_see || gd != 3u;
         if (special) {
 #pragma unroll
-          for (int bk = 0; bk < 2; ++bk)
+          for (int g = 0; g < NR; ++g)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (t0 + 16 * bk + 2 * n8 + (e >> 1) > ((e & 1) ? see1 : see0) ||
-                  !((gd >> bk) & 1u))
-                x[bk][e] = -INFINITY;
+            for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (t0 + 16 * bk + 2 * n8 + (e >> 1) > ((e & 1) ? see[g].y : see[g].x) ||
+                    !((gd >> bk) & 1u))
+                  x[g][bk][e] = -INFINITY;
         }
-        const float mx0 = sc.x * fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        const float mx1 = sc.y * fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-        if (__any_sync(kFull, mx0 > m.x + kLazy || mx1 > m.y + kLazy)) {
-          float2 mn = make_float2(mx0, mx1);
+        float2 mx[NR];
+        bool raise = false;
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            mn.x = fmaxf(mn.x, __shfl_xor_sync(kFull, mn.x, d));
-            mn.y = fmaxf(mn.y, __shfl_xor_sync(kFull, mn.y, d));
+        for (int g = 0; g < NR; ++g) {
+          mx[g].x = sc[g].x * fmaxf(fmaxf(x[g][0][0], x[g][0][2]), fmaxf(x[g][1][0], x[g][1][2]));
+          mx[g].y = sc[g].y * fmaxf(fmaxf(x[g][0][1], x[g][0][3]), fmaxf(x[g][1][1], x[g][1][3]));
+          raise = raise || mx[g].x > m[g].x + kLazy || mx[g].y > m[g].y + kLazy;
+        }
+        if (__any_sync(kFull, raise)) {
+#pragma unroll
+          for (int g = 0; g < NR; ++g) {
+            float2 mn = mx[g];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              mn.x = fmaxf(mn.x, __shfl_xor_sync(kFull, mn.x, d));
+              mn.y = fmaxf(mn.y, __shfl_xor_sync(kFull, mn.y, d));
+            }
+            mn.x = fmaxf(m[g].x, mn.x);
+            mn.y = fmaxf(m[g].y, mn.y);
+            const float f0 = m[g].x == -INFINITY ? 0.f : ex2(m[g].x - mn.x);
+            const float f1 = m[g].y == -INFINITY ? 0.f : ex2(m[g].y - mn.y);
+            m[g] = mn;
+            l[g].x *= f0;
+            l[g].y *= f1;
+            // row 8 g + n8's factor; with 8 rows, of both its parts
+            const float g0 = __shfl_sync(kFull, f0, n8 >> 1),
+                        g1 = __shfl_sync(kFull, f1, n8 >> 1);
+            const float f = (n8 & 1) ? g1 : g0;
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                if (NR == 1 || g == 0) {
+                  o[i][r][0] *= f;
+                  o[i][r][1] *= f;
+                }
+                if (NR == 1 || g == 1) {
+                  o[i][r][2] *= f;
+                  o[i][r][3] *= f;
+                }
+              }
           }
-          mn.x = fmaxf(m.x, mn.x);
-          mn.y = fmaxf(m.y, mn.y);
-          const float f0 = m.x == -INFINITY ? 0.f : ex2(m.x - mn.x);
-          const float f1 = m.y == -INFINITY ? 0.f : ex2(m.y - mn.y);
-          m = mn;
-          l.x *= f0;
-          l.y *= f1;
-          // row n8's factor
-          const float g0 = __shfl_sync(kFull, f0, n8 >> 1), g1 = __shfl_sync(kFull, f1, n8 >> 1);
-          const float f = (n8 & 1) ? g1 : g0;
-#pragma unroll
-          for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[i][r][e] *= f;
         }
-        const float2 base = make_float2(m.x == -INFINITY ? 0.f : -m.x,
-                                        m.y == -INFINITY ? 0.f : -m.y);
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
-          // weights as fp16 hi + lo of the even (0) and the odd (1) tokens
-          uint32_t hi[2], lo[2];
+          // weights of the even (0) and the odd (1) tokens: of the 8 rows as
+          // fp16 hi + lo, or of both groups of rows
+          uint32_t wt[2][2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 y = __ffma2_rn(make_float2(x[bk][2 * e], x[bk][2 * e + 1]), sc, base);
-            const float2 p = make_float2(ex2(y.x), ex2(y.y));
-            l = __fadd2_rn(l, p);
-            const __half2 hh = __floats2half2_rn(p.x, p.y);
-            const float2 hf = __half22float2(hh);
-            hi[e] = turn(h2_bits(hh));
-            lo[e] = turn(h2_bits(__floats2half2_rn(p.x - hf.x, p.y - hf.y)));
+          for (int g = 0; g < NR; ++g) {
+            const float2 base = make_float2(m[g].x == -INFINITY ? 0.f : -m[g].x,
+                                            m[g].y == -INFINITY ? 0.f : -m[g].y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 y = __ffma2_rn(make_float2(x[g][bk][2 * e], x[g][bk][2 * e + 1]),
+                                          sc[g], base);
+              const float2 p = make_float2(ex2(y.x), ex2(y.y));
+              l[g] = __fadd2_rn(l[g], p);
+              const __half2 hh = __floats2half2_rn(p.x, p.y);
+              wt[g][e] = turn(h2_bits(hh));
+              if constexpr (NR == 1) {
+                const float2 hf = __half22float2(hh);
+                wt[1][e] = turn(h2_bits(__floats2half2_rn(p.x - hf.x, p.y - hf.y)));
+              }
+            }
           }
-          // row n8's weights of token pairs 2 t4 and 2 t4 + 1
-          const uint32_t a0 = __byte_perm(hi[0], hi[1], 0x5410),
-                         a1 = __byte_perm(lo[0], lo[1], 0x5410),
-                         a2 = __byte_perm(hi[0], hi[1], 0x7632),
-                         a3 = __byte_perm(lo[0], lo[1], 0x7632);
+          // row n8's (and 8 + n8's) weights of token pairs 2 t4 and 2 t4 + 1
+          const uint32_t a0 = __byte_perm(wt[0][0], wt[0][1], 0x5410),
+                         a1 = __byte_perm(wt[1][0], wt[1][1], 0x5410),
+                         a2 = __byte_perm(wt[0][0], wt[0][1], 0x7632),
+                         a3 = __byte_perm(wt[1][0], wt[1][1], 0x7632);
           const unsigned char *blk = st + bk * BLK;
           uint32_t vw[2][I];
           uint2 vm[2][NG];
@@ -509,27 +555,35 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
       if (iu < u_end) issue(s);
       s = s + 1 == ST ? 0 : s + 1;
     }
-    // the partial of this (sequence, kv head): row n8's channels 32 i + 8 t4 ...
-#pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-      l.x += __shfl_xor_sync(kFull, l.x, d);
-      l.y += __shfl_xor_sync(kFull, l.y, d);
-    }
+    // the partial of this (sequence, kv head): channels 32 i + 8 t4 ... of row
+    // n8 (and 8 + n8)
     float *first = t.ws + (int64_t)(w + b * H + h) * (t.max_new * GQ) * Part<D>::ROW;
-    if (n8 < 2 && 2 * t4 + n8 < rows)
-      *reinterpret_cast<float2 *>(first + (2 * t4 + n8) * Part<D>::ROW + D) =
-          n8 ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
-    if (n8 < rows) {
-      float *part = first + n8 * Part<D>::ROW;
 #pragma unroll
-      for (int i = 0; i < I; ++i) {
-        float4 c0, c1;
-        c0 = make_float4(o[i][0][0] + o[i][0][2], o[i][1][0] + o[i][1][2],
-                         o[i][2][0] + o[i][2][2], o[i][3][0] + o[i][3][2]);
-        c1 = make_float4(o[i][0][1] + o[i][0][3], o[i][1][1] + o[i][1][3],
-                         o[i][2][1] + o[i][2][3], o[i][3][1] + o[i][3][3]);
-        reinterpret_cast<float4 *>(part + 32 * i + 8 * t4)[0] = c0;
-        reinterpret_cast<float4 *>(part + 32 * i + 8 * t4)[1] = c1;
+    for (int g = 0; g < NR; ++g) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l[g].x += __shfl_xor_sync(kFull, l[g].x, d);
+        l[g].y += __shfl_xor_sync(kFull, l[g].y, d);
+      }
+      const int r0 = 8 * g + 2 * t4 + n8;
+      if (n8 < 2 && r0 < rows)
+        *reinterpret_cast<float2 *>(first + r0 * Part<D>::ROW + D) =
+            n8 ? make_float2(m[g].y, l[g].y) : make_float2(m[g].x, l[g].x);
+      if (8 * g + n8 < rows) {
+        float *part = first + (8 * g + n8) * Part<D>::ROW;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float4 y;
+            if constexpr (NR == 1)
+              y = make_float4(o[i][0][c] + o[i][0][2 + c], o[i][1][c] + o[i][1][2 + c],
+                              o[i][2][c] + o[i][2][2 + c], o[i][3][c] + o[i][3][2 + c]);
+            else
+              y = make_float4(o[i][0][2 * g + c], o[i][1][2 * g + c], o[i][2][2 * g + c],
+                              o[i][3][2 * g + c]);
+            reinterpret_cast<float4 *>(part + 32 * i + 8 * t4)[c] = y;
+          }
       }
     }
     // the next head or sequence with steps
@@ -621,26 +675,23 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix) {
   }
 }
 
-// CTAs of one wave
-int decode_ctas(int D, int sm_count) { return (D == 128 ? 3 : 4) * sm_count; }
-
 // a partial per warp and per (sequence, kv head)
 size_t part_floats(int B, int H_kv, int D, int rows, int sm_count) {
-  return ((size_t)decode_ctas(D, sm_count) * kWarps + (size_t)B * H_kv) * rows * (D + 4);
+  return ((size_t)decode_ctas(D, rows) * sm_count * kWarps + (size_t)B * H_kv) * rows * (D + 4);
 }
 
-template <typename T, int D, int NG>
+template <typename T, int D, int NG, int ROWS>
 cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
                        cudaStream_t st) {
-  using SM = DecSmem<D, NG>;
+  using SM = DecSmem<D, NG, ROWS>;
   const size_t smem = SM::PREFIX + sizeof(int) * (a.B + 1);
-  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<T, D, NG>,
+  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<T, D, NG, ROWS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int ctas = decode_ctas(D, sm_count), warps_max = ctas * kWarps;
+  const int ctas = SM::CTAS * sm_count, warps_max = ctas * kWarps;
   const int rows = t.max_new * (a.H_q / a.H_kv);
   int *prefixes = reinterpret_cast<int *>(t.ws + part_floats(a.B, a.H_kv, D, rows, sm_count));
-  e = launch_pdl(k_paged_decode<T, D, NG>, dim3(ctas), dim3(kThreads), smem, st, a, t,
+  e = launch_pdl(k_paged_decode<T, D, NG, ROWS>, dim3(ctas), dim3(kThreads), smem, st, a, t,
                  warps_max, prefixes);
   count_launch();
   if (e != cudaSuccess) return e;
@@ -650,16 +701,23 @@ cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
   return e;
 }
 
+template <typename T, int D, int NG>
+cudaError_t launch_rows(const PagedArgs &a, const PagedAttend &t, int sm_count,
+                        cudaStream_t st) {
+  return t.max_new * (a.H_q / a.H_kv) <= 8 ? launch_dec<T, D, NG, 8>(a, t, sm_count, st)
+                                           : launch_dec<T, D, NG, 16>(a, t, sm_count, st);
+}
+
 template <typename T>
 cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_count,
                      cudaStream_t st) {
   const int ng = D / a.g;
   if (D == 64)
-    return ng == 1 ? launch_dec<T, 64, 1>(a, t, sm_count, st)
-                   : launch_dec<T, 64, 2>(a, t, sm_count, st);
-  return ng == 1   ? launch_dec<T, 128, 1>(a, t, sm_count, st)
-         : ng == 2 ? launch_dec<T, 128, 2>(a, t, sm_count, st)
-                   : launch_dec<T, 128, 4>(a, t, sm_count, st);
+    return ng == 1 ? launch_rows<T, 64, 1>(a, t, sm_count, st)
+                   : launch_rows<T, 64, 2>(a, t, sm_count, st);
+  return ng == 1   ? launch_rows<T, 128, 1>(a, t, sm_count, st)
+         : ng == 2 ? launch_rows<T, 128, 2>(a, t, sm_count, st)
+                   : launch_rows<T, 128, 4>(a, t, sm_count, st);
 }
 
 }  // namespace

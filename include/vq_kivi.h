@@ -537,7 +537,7 @@ int vq_kivi_paged_append(const vq_kivi_paged *p,
  * prompt chunks with several.
  *   q              rows [tokens][H_q][D]; out contiguous, in q's type
  *   max_new        no sequence has more new tokens (1 without cu_new); up to
- *                  8 (token, query head) pairs per kv head are served by the
+ *                  16 (token, query head) pairs per kv head are served by the
  *                  split-KV kernel, more by the tensor-memory kernel
  *   softmax_scale  <= 0 selects 1/sqrt(D)
  *   workspace      device, 16-byte aligned */

@@ -8,8 +8,9 @@ import paged_ref as ref
 
 pytestmark = pytest.mark.gpu
 DT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
-# the few-row kernel keeps its weights in 32 bits (hi + lo), the tensor-memory
-# kernel rounds them to fp16 once (2^-11)
+# the split-KV kernel keeps the weights of up to 8 rows in 32 bits (hi + lo);
+# with more rows, and in the tensor-memory kernel, a weight is rounded to fp16
+# once (2^-11)
 FEW, MANY = 2.0 ** -21, 2.0 ** -11
 
 
@@ -268,9 +269,14 @@ def test_decode(dtype, lens, H_q, H_kv, D, g, page):
 
 
 CHUNK = [
-    # n, lens, H_q, H_kv, D, g, page: few rows, then many
+    # n, lens, H_q, H_kv, D, g, page: up to 8 rows of a kv head, up to 16, more
     ([2, 1, 0, 4], [2, 70, 33, 400], 2, 1, 128, 32, 16),
     ([3, 2], [300, 2], 4, 2, 64, 64, 32),
+    ([3, 2, 0], [300, 2, 9], 8, 2, 128, 32, 16),
+    ([4, 1, 2], [61, 800, 1], 4, 1, 64, 32, 64),
+    ([2, 2], [2049, 33], 16, 2, 128, 128, 32),
+    ([3, 2], [40, 1200], 5, 1, 128, 64, 16),
+    ([16, 9], [700, 31], 2, 2, 128, 64, 128),
     ([5, 3], [900, 131], 8, 2, 128, 32, 16),
     ([1, 200, 0, 17], [1, 200, 50, 150], 4, 2, 64, 32, 32),
     ([129, 64], [129, 700], 3, 3, 128, 64, 64),
