@@ -23,6 +23,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "bulk_pipe.cuh"
@@ -120,6 +121,19 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity,
     if (global_ns() - t0 > 500000000ull) return false;
   }
   return true;
+}
+
+// Dynamic shared memory of a kernel beyond 48 KB, allowed once per device
+template <typename F>
+inline cudaError_t allow_smem(F *fn, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // The operators wait for the stream's previous kernel before they read

@@ -1035,8 +1035,8 @@ size_t swap_floats(int D, int sm_count) { return (size_t)sm_count * kTile * (D +
 template <typename T, int D, int NG>
 cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cudaStream_t st) {
   using SM = Smem<D, NG>;
-  cudaError_t e = cudaFuncSetAttribute(k_paged_chunk<T, D, NG>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SM::ALLOC);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_paged_chunk<T, D, NG>, SM::ALLOC, done);
   if (e != cudaSuccess) return e;
   float *part = t.ws, *swap = part + part_floats(D, sm_count);
   CutPair *cuts = reinterpret_cast<CutPair *>(swap + swap_floats(D, sm_count));

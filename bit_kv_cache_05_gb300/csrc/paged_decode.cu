@@ -685,8 +685,9 @@ cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count,
                        cudaStream_t st) {
   using SM = DecSmem<D, NG, ROWS>;
   const size_t smem = SM::PREFIX + sizeof(int) * (a.B + 1);
-  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<T, D, NG, ROWS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_paged_decode<T, D, NG, ROWS>,
+                             SM::PREFIX + (int)sizeof(int) * (kMaxSeqs + 1), done);
   if (e != cudaSuccess) return e;
   const int ctas = SM::CTAS * sm_count, warps_max = ctas * kWarps;
   const int rows = t.max_new * (a.H_q / a.H_kv);
