@@ -313,8 +313,8 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream) {
     return fail(VQ_ERR_CUDA, "an attention kernel gave up waiting for its copies; its outputs "
                 "are not valid");
   if (flags & kBadPage)
-    return fail(VQ_ERR_ARG, "a block table names a page outside the pool; its tokens were left "
-                "out");
+    return fail(VQ_ERR_ARG, "a block table names a page outside the pool: its tokens were not "
+                "stored, and rows that see it are not valid");
   if (flags & kBadLength)
     return fail(VQ_ERR_ARG, "a sequence's length or its new tokens lie outside their ranges; "
                 "the sequence was left out");

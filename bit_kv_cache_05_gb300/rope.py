@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-from fractions import Fraction
 from typing import Optional, Sequence
 
 import torch
@@ -24,7 +23,18 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
         lambda i: torch.cuda.current_stream(i).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-_TWO_PI = Fraction("6.28318530717958647692528676655900576839433879875021164194988918")
+# 2^320 / (2 pi)
+_PER_RADIAN = 2 ** 320 * 10 ** 90 // int(
+    "6283185307179586476925286766559005768394338798750211641949889184615632812572417997256069650")
+
+
+def _turns(freq: float) -> int:
+    """Radians per position as turns, times 2^64, rounded, modulo 2^64."""
+    n, d = freq.as_integer_ratio()          # d is a power of two
+    shift = 256 + d.bit_length() - 1
+    return ((n * _PER_RADIAN + (1 << (shift - 1))) >> shift) % 2 ** 64
+
+
 DTYPES = {torch.float16: _lib.F16, torch.bfloat16: _lib.BF16, torch.float32: _lib.F32}
 
 
@@ -71,12 +81,15 @@ class Rope:
             if self.n_axes > 4:
                 raise ValueError("at most 4 axes")
         self.interleaved, self.scale = bool(interleaved), float(scale)
-        # turns per position in 64-bit fixed point, rounded once
-        turns = [round(Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in freq]
-        turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+        # turns per position in 64-bit fixed point, then the axes as bytes: one
+        # copy to the device
+        words = [_turns(f) for f in freq]
+        words += [int.from_bytes(bytes(axis[j:j + 8]), "little") for j in range(0, half, 8)]
+        words = [w - 2 ** 64 if w >= 2 ** 63 else w for w in words]
         device = torch.device("cuda" if device is None else device)
-        self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
-        self.axis = torch.tensor(axis, dtype=torch.uint8).to(device)
+        self._words = torch.tensor(words, dtype=torch.int64).to(device)
+        self.turns = self._words[:half]
+        self.axis = self._words[half:].view(torch.uint8)
         self.device = self.turns.device
         self.spec = _lib.RopeSpec(self.rot_dim, int(self.interleaved), self.n_axes, self.scale,
                                   self.turns.data_ptr(), self.axis.data_ptr())

@@ -495,9 +495,12 @@ typedef struct vq_kivi_paged {
  *   tokens   rows of the token tensors, at least cu_new[B]; rows behind
  *            cu_new[B] are neither read nor written
  * B <= 1024.  A new token at a negative position (lens[b] < n_b: padding) is
- * not in the cache: it is not stored and its attention row is zero.  A page
- * outside the pool or a length outside its range is left out and reported by
- * vq_kivi_paged_status.  No two new tokens of an append may share a place. */
+ * not in the cache: it is not stored and its attention row is zero.  A
+ * sequence whose length or new tokens lie outside their ranges is left out
+ * (its rows are not written); a token on a page outside the pool is not
+ * stored, and attention rows that see such a page are not valid.  Both are
+ * reported by vq_kivi_paged_status and touch no other sequence.  No two new
+ * tokens of an append may share a place. */
 typedef struct vq_kivi_paged_batch {
   int32_t B, max_pages;
   const int32_t *table;
@@ -535,7 +538,8 @@ int vq_kivi_paged_append(const vq_kivi_paged *p,
 /* Attention of the new tokens (already appended) over their sequences, each
  * seeing the positions up to its own: decode with one new token, drafts and
  * prompt chunks with several.
- *   q              rows [tokens][H_q][D]; out contiguous, in q's type
+ *   q              rows [tokens][H_q][D]; out contiguous, in q's type, not
+ *                  overlapping q
  *   max_new        no sequence has more new tokens (1 without cu_new); up to
  *                  16 (token, query head) pairs per kv head are served by the
  *                  split-KV kernel, more by the tensor-memory kernel

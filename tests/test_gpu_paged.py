@@ -516,6 +516,47 @@ def test_two_streams_and_repeatable():
         assert torch.equal(z, m) and torch.equal(w, m)
 
 
+@pytest.mark.parametrize("B,n", [(1024, 1), (300, 3), (130, 12)])
+def test_many_sequences(B, n):
+    """Batches up to the largest, many of them empty, all three kernels."""
+    D, g, page, H_q, H_kv = 64, 64, 16, 4, 2
+    lens = [(7 * b) % 53 for b in range(B)]
+    news = [min(n, s) if n > 1 else 1 for s in lens]
+    c, table, L = filled(lens, page, H_q, H_kv, D, g, seed=B)
+    q = randn(5, sum(news), H_q, D).half()
+    cu = None if n == 1 else offsets(news)
+    out = c.attend(q, table, L, cu, max_new=n)
+    c.status()
+    want, err = ref.attend64(q, c.pool, table, L, cu, D, g, H_kv,
+                             weight_step=FEW if 2 * n <= 8 else MANY)
+    ref.check_attend(out, want, err, q.dtype)
+
+
+def test_large_pages_and_few_heads_of_many():
+    c, table, L = filled([1500, 1024, 1], 1024, 8, 8, 128, 64)
+    for n in (1, 20):
+        q = randn(5, 3 * n, 8, 128).bfloat16()
+        cu = offsets([n, n, n])
+        out = c.attend(q, table, L, cu, max_new=n)
+        c.status()
+        want, err = ref.attend64(q, c.pool, table, L, cu, 128, 64, 8,
+                                 weight_step=FEW if n == 1 else MANY)
+        ref.check_attend(out, want, err, q.dtype)
+
+
+def test_bad_page_of_one_sequence_in_a_chunk():
+    from bit_kv_cache_05_gb300 import _lib
+    c, table, L = filled([200, 150], 16, 8, 2, 128, 32)
+    q = randn(5, 80, 8, 128).half()
+    want = c.attend(q, table, L, offsets([40, 40]), max_new=40)
+    bad = table.clone()
+    bad[0, 3] = 1 << 20
+    out = c.attend(q, bad, L, offsets([40, 40]), max_new=40)
+    with pytest.raises(_lib.VqError):
+        c.status()
+    assert torch.equal(out[40:], want[40:])
+
+
 def test_offsets_past_32_bits():
     """Pages whose bytes lie past 2^32 of the pool."""
     D, g, page, H = 128, 32, 128, 8
