@@ -831,7 +831,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
       const uint32_t sb = saddr(sm);
-      uint32_t ks = 0, ph_k = 0, vs = 0, ph_v = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+      uint32_t ks = 0, ph_k = 0, vs = 0, ph_v = 0, ph_q = 0, ph_p = 0;   // a bit a slot
       bool ok = true;
       // descriptors of the operands' starts; a step of 16 in K adds 32 bytes,
       // 64 in K the next block of 128-byte rows
@@ -870,8 +870,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
         // first scores of both slots: one key tile for two query tiles, or a
         // key tile each for one
         for (int i = 0; ok && i < slots; ++i) {
-          ok = __all_sync(kFull, bar_wait(&B.q_full[i], ph_q[i], dead));
-          ph_q[i] ^= 1u;
+          ok = __all_sync(kFull, bar_wait(&B.q_full[i], (ph_q >> i) & 1u, dead));
+          ph_q ^= 1u << i;
           if (ok && (i == 0 || !two)) ok = keys();
           if (!ok) break;
           fence_after();
@@ -882,8 +882,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           ok = __all_sync(kFull, bar_wait(&B.v_full[vs], ph_v, dead));
           const bool last = two ? j + 1 == nt : j + 2 >= nt;
           for (int i = two ? 0 : j & 1, n = two ? 2 : i + 1; ok && i < n; ++i) {
-            ok = __all_sync(kFull, bar_wait(&B.p_full[i], ph_p[i], dead));
-            ph_p[i] ^= 1u;
+            ok = __all_sync(kFull, bar_wait(&B.p_full[i], (ph_p >> i) & 1u, dead));
+            ph_p ^= 1u << i;
             if (!ok) break;
             fence_after();
             outputs(i, vs, two ? j > 0 : j > 1);
