@@ -126,23 +126,57 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // The issuing warp runs as a whole (its operands are then known to be uniform
-// and stay in uniform registers); one elected lane issues.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
+// and stay in uniform registers); one elected lane issues the products of a
+// tile, K in steps of 16.  One election a tile: one per product cost the warp
+// more than the products take.  A step adds 32 bytes to an operand's start,
+// 64 channels or tokens the next block of 128-byte rows.
+#define VQK_SS(e, off)                                                            \
+  " add.s64 x, %1, " #off ";\n add.s64 y, %2, " #off ";\n"                         \
+  " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, " e ";\n"
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n .reg .pred n, t, q;\n .reg .b64 x, y;\n setp.ne.b32 n, 0, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+        VQK_SS("n", 0) VQK_SS("t", 2) VQK_SS("t", 4) VQK_SS("t", 6)
+        VQK_SS("t", 1024) VQK_SS("t", 1026) VQK_SS("t", 1028) VQK_SS("t", 1030) "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred n, t, q;\n .reg .b64 x, y;\n setp.ne.b32 n, 0, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+        VQK_SS("n", 0) VQK_SS("t", 2) VQK_SS("t", 4) VQK_SS("t", 6) "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id)
+        : "memory");
 }
-// A from tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
+// A (the weights) from tensor memory, 8 columns a step; acc: add to what is
+// there
+#define VQK_TS(e, col, off)                                                       \
+  " add.u32 x, %1, " #col ";\n add.s64 y, %2, " off ";\n"                          \
+  " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, " e ";\n"
+template <int D>
+__device__ __forceinline__ void mma_outputs(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                            uint32_t acc) {
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n .reg .pred n, t, q;\n .reg .b32 x;\n .reg .b64 y;\n setp.ne.b32 n, %4, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+        VQK_TS("n", 0, "0") VQK_TS("t", 8, "2") VQK_TS("t", 16, "4") VQK_TS("t", 24, "6")
+        VQK_TS("t", 32, "1024") VQK_TS("t", 40, "1026") VQK_TS("t", 48, "1028")
+        VQK_TS("t", 56, "1030") "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred n, t, q;\n .reg .b32 x;\n .reg .b64 y;\n setp.ne.b32 n, %4, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+        VQK_TS("n", 0, "0") VQK_TS("t", 8, "2") VQK_TS("t", 16, "4") VQK_TS("t", 24, "6")
+        VQK_TS("t", 32, "512") VQK_TS("t", 40, "514") VQK_TS("t", 48, "516")
+        VQK_TS("t", 56, "518") "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile(
@@ -512,10 +546,21 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       __syncwarp();
       if (lane == 0) bar_arrive(&B.q_full[wg]);
     };
+    // key tiles before this pair, for the stages that they lie in
+    uint32_t ring = 0;
+    auto next = [&]() {
+      ring += walk.steps(tpt);
+      have = advance();
+    };
     // past the pairs that this slot has no part in
     auto settle = [&]() {
-      while (have && wg == 1 && !walk.two(tpt) && walk.steps(tpt) < 2) have = advance();
+      while (have && wg == 1 && !walk.two(tpt) && walk.steps(tpt) < 2) next();
     };
+    // The stages go back to the rebuilding warps from here: a commit of the
+    // tensor cores holds the next products up by more than 100 cycles, and
+    // the scores' own already says that the products before them are done.
+    // Slot 1 is the later user of a tile that both slots use.
+    const bool gives = (warp & 3) == 0 && lane == 0;
     bool ok = true;
     settle();
     if (have) load_q();
@@ -538,6 +583,11 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
         ph_s ^= 1u;
         if (!__all_sync(kFull, ok)) { ok = false; break; }
         fence_after();
+        if (gives && (!two || wg == 1)) {
+          bar_arrive(&B.k_empty[(ring + j) & 1]);
+          // the values of this slot's tile before
+          if (j >= (two ? 1 : 2)) bar_arrive(&B.v_empty[(ring + j - (two ? 1 : 2)) & 1]);
+        }
         if (idle) {
           fence_before();
           __syncwarp();
@@ -628,14 +678,17 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
                                  (two ? wg * kTile : 0) + row) * (D + 4);
       T *orow = static_cast<T *>(t.out) +
                 ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D;
+      // the stage of this slot's last tile
+      const uint32_t vlast = (ring + (two ? steps - 1 : steps - 1 - ((steps - 1 - wg) & 1))) & 1;
       // the next queries: this slot's last scores have been read
-      have = advance();
+      next();
       settle();
       if (have) load_q();
       ok = bar_wait(&B.o_full[wg], ph_o, dead);
       ph_o ^= 1u;
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
+      if (gives && (!two || wg == 1)) bar_arrive(&B.v_empty[vlast]);
       float f0 = 1.f, f1 = 0.f;
       if (halves && wg == 0) {
         ok = bar_wait(&B.x_full, ph_x, dead);
@@ -833,33 +886,23 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       const uint32_t sb = saddr(sm);
       uint32_t ks = 0, ph_k = 0, vs = 0, ph_v = 0, ph_q = 0, ph_p = 0;   // a bit a slot
       bool ok = true;
-      // descriptors of the operands' starts; a step of 16 in K adds 32 bytes,
-      // 64 in K the next block of 128-byte rows
       const uint64_t dq = desc128(sb + SM::Q), dk = desc128(sb + SM::K),
                      dv = desc128(sb + SM::V);
       auto scores = [&](int i, uint32_t stage) {
-        const uint64_t q = dq + i * (SM::OP >> 4), k = dk + stage * (SM::OP >> 4);
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e)
-          mma_ss(tmem + 128 * i, q + (e >> 2) * 1024 + 2 * (e & 3),
-                 k + (e >> 2) * 1024 + 2 * (e & 3), id_s, e > 0);
+        mma_scores<D>(tmem + 128 * i, dq + i * (SM::OP >> 4), dk + stage * (SM::OP >> 4), id_s);
         mma_commit(&B.s_full[i]);
       };
       auto outputs = [&](int i, uint32_t stage, bool more) {
-        const uint64_t v = dv + stage * (SM::OP >> 4);
-#pragma unroll
-        for (int e = 0; e < kTile / 16; ++e)
-          mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * e,
-                 v + (e >> 2) * (D * 8) + 2 * (e & 3), id_o, more || e > 0);
+        mma_outputs<D>(tmem + 256 + 128 * i, tmem + 128 * i, dv + stage * (SM::OP >> 4), id_o,
+                       more);
       };
-      // waits for the keys of the next tile, and gives them back
+      // waits for the keys of the next tile, and goes on from them
       auto keys = [&]() {
         const bool r = __all_sync(kFull, bar_wait(&B.k_full[ks], ph_k, dead));
         fence_after();
         return r;
       };
       auto keys_done = [&]() {
-        mma_commit(&B.k_empty[ks]);
         ks ^= 1u;
         ph_k ^= ks == 0;
       };
@@ -897,7 +940,6 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
             }
           }
           if (!ok) break;
-          mma_commit(&B.v_empty[vs]);
           vs ^= 1u;
           ph_v ^= vs == 0;
         }
