@@ -1042,30 +1042,57 @@ k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, const CutPair
   auto at = [&](int i) {
     return part + ((int64_t)(i == c ? 2 * c + 1 : 2 * i) * 2 * kTile + r) * ROW;
   };
-  float M = -INFINITY;
-  for (int i = c + lane; i <= cut.last; i += 32) M = fmaxf(M, at(i)[D]);
+  // the first two parts are there for every cut pair: on their way before the
+  // maximum is known
+  float v[2][CPL], m2[2], l2[2];
+  auto load = [&](int i, float (&x)[CPL], float &pm, float &pl) {
+    const float *p = at(i);
+    const float2 ml = *reinterpret_cast<const float2 *>(p + D);
+    pm = ml.x;
+    pl = ml.y;
+    if constexpr (CPL == 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(p + 4 * lane);
+      x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2 *>(p + 2 * lane);
+      x[0] = y.x; x[1] = y.y;
+    }
+  };
+  load(c, v[0], m2[0], l2[0]);
+  load(c + 1, v[1], m2[1], l2[1]);
+  float M = fmaxf(m2[0], m2[1]);
+  if (cut.last > c + 1) {
+    for (int i = c + 2 + lane; i <= cut.last; i += 32) M = fmaxf(M, at(i)[D]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  }
   float L = 0.f, acc[CPL];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = c; i <= cut.last; ++i) {
-    const float *p = at(i);
-    const float2 ml = *reinterpret_cast<const float2 *>(p + D);
+  auto add = [&](const float (&x)[CPL], float pm, float pl) {
     // a part without a seen token weighs nothing (NaN sums stay)
-    const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
-    L = fmaf(f, ml.y, L);
+    const float f = pm == -INFINITY ? (pl != pl ? pl : 0.f) : ex2(pm - M);
+    L = fmaf(f, pl, L);
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(f, p[32 * e + lane], acc[e]);
+    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(f, x[e], acc[e]);
+  };
+  add(v[0], m2[0], l2[0]);
+  add(v[1], m2[1], l2[1]);
+#pragma unroll 4
+  for (int i = c + 2; i <= cut.last; ++i) {
+    load(i, v[0], m2[0], l2[0]);
+    add(v[0], m2[0], l2[0]);
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   T *o = static_cast<T *>(t.out) +
-         ((int64_t)(cut.first + tok) * a.H_q + cut.h * GQ + row % GQ) * D;
+         ((int64_t)(cut.first + tok) * a.H_q + cut.h * GQ + row % GQ) * D + CPL * lane;
 #pragma unroll
-  for (int e = 0; e < CPL; ++e) {
-    if constexpr (std::is_same<T, __half>::value) o[32 * e + lane] = __float2half_rn(acc[e] * inv);
-    else o[32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
+  for (int e = 0; e < CPL; e += 2) {
+    if constexpr (std::is_same<T, __half>::value)
+      *reinterpret_cast<__half2 *>(o + e) = __floats2half2_rn(acc[e] * inv, acc[e + 1] * inv);
+    else
+      *reinterpret_cast<__nv_bfloat162 *>(o + e) =
+          __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
   }
 }
 
