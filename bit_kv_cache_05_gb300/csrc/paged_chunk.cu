@@ -749,6 +749,16 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     uint64_t *full = kv ? B.v_full : B.k_full, *empty = kv ? B.v_empty : B.k_empty;
     uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
     bool ok = true;
+    // values: where this lane's four stores of an octet go, and the shifts to
+    // the nibbles that they hold (the lanes of a store differ in the channel's
+    // low bits)
+    uint32_t to[4], shift[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = (q + t4) & 3;
+      to[q] = sw(32 * t4 + 4 * n8 + r, 2 * w);
+      shift[q] = 4 * r;
+    }
     const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
                   k64 = bits_h2(0xd400d400u);
     for (; ok && have; have = advance()) {
@@ -836,28 +846,29 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
               if (I == 4 || span < I) {
                 const uint2 *vm = reinterpret_cast<const uint2 *>(blk + 8 * D) + 4 * oct * NG +
                                   32 * span / G;
-                __half2 s[4], z[4];
+                uint2 m[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                  const uint2 y = vm[p * NG];
-                  // tokens behind the sequence hold anything: their values are 0
-                  const int e = left - (r0 + 8 * oct + 2 * p);
-                  const unsigned keep = !good || e <= 0 ? 0u : (e == 1 ? 0x0000ffffu : kFull);
-                  s[p] = bits_h2(y.x & keep);
-                  z[p] = bits_h2(y.y & keep);
+                for (int p = 0; p < 4; ++p) m[p] = vm[p * NG];
+                if (!good || left < r0 + 16) {
+                  // tokens behind the sequence hold anything: their values
+                  // become 0
+#pragma unroll
+                  for (int p = 0; p < 4; ++p) {
+                    const int e = left - (r0 + 8 * oct + 2 * p);
+                    const unsigned keep = !good || e <= 0 ? 0u : (e == 1 ? 0x0000ffffu : kFull);
+                    m[p].x &= keep;
+                    m[p].y &= keep;
+                  }
                 }
-                const int chunk = 2 * w + oct;         // octet within the 64 tokens
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                  // the lanes of a store differ in the channel's low bits
-                  const int r = (q + span) & 3, c = 32 * span + 4 * n8 + r;
                   uint32_t o[4];
 #pragma unroll
                   for (int p = 0; p < 4; ++p) {
-                    const __half2 cc = __hsub2(field<0x000f000fu>(x[p] >> (4 * r)), k1024);
-                    o[p] = h2_bits(__hfma2(cc, s[p], z[p]));
+                    const __half2 cc = __hsub2(field<0x000f000fu>(x[p] >> shift[q]), k1024);
+                    o[p] = h2_bits(__hfma2(cc, bits_h2(m[p].x), bits_h2(m[p].y)));
                   }
-                  *reinterpret_cast<uint4 *>(dst + hf * (D * 128) + sw(c, chunk)) =
+                  *reinterpret_cast<uint4 *>(dst + hf * (D * 128) + (to[q] ^ (oct << 4))) =
                       make_uint4(o[0], o[1], o[2], o[3]);
                 }
               }

@@ -516,6 +516,21 @@ def test_two_streams_and_repeatable():
         assert torch.equal(z, m) and torch.equal(w, m)
 
 
+@pytest.mark.parametrize("n,H_q", [(4, 2), (6, 4), (40, 4)])
+def test_rows_before_the_first_token_are_zero(n, H_q):
+    """Sequences shorter than their new tokens (padding in front): those rows
+    see nothing."""
+    c, table, L = filled([2, 13, 1], 16, H_q, 2, 64, 32)
+    q = randn(5, 3 * n, H_q, 64).half()
+    cu = offsets([n] * 3)
+    out = c.attend(q, table, L, cu, max_new=n)
+    c.status()
+    want, err = ref.attend64(q, c.pool, table, L, cu, 64, 32, 2, weight_step=MANY)
+    ref.check_attend(out, want, err, q.dtype)
+    for b, s in enumerate([2, 13, 1]):
+        assert (out[b * n:b * n + max(0, n - s)] == 0).all()
+
+
 @pytest.mark.parametrize("B,n", [(1024, 1), (300, 3), (130, 12)])
 def test_many_sequences(B, n):
     """Batches up to the largest, many of them empty, all three kernels."""
