@@ -13,8 +13,11 @@
 // fixed point (turns * 2^64), so position * frequency mod 1 is one 64-bit
 // integer product, exact for every position: the error of an angle is
 // position * 2^-65 turns, where position * inv_freq in fp32 loses the angle
-// at positions in the thousands (2^-24 relative).  The fraction's upper 32
-// bits go to sincospif, whose argument stays within one turn.
+// at positions in the thousands (2^-24 relative).  Cosine and sine of the
+// fraction are Taylor series on an eighth of a turn either side of a quarter,
+// summed so that little more than their last rounding is left: a key next to
+// an fp16 rounding border, or a code next to a tie, falls on its own side as
+// often as fp32 allows.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -114,6 +117,37 @@ __device__ __forceinline__ void chunk_places(const RopeArgs &r, int l, int &p0, 
   }
 }
 
+// cos and sin of a / 2^64 turns
+__device__ __forceinline__ void turn_cos_sin(unsigned long long a, float &c, float &s) {
+  // the nearest quarter, and what is left of it: r in [-1/8, 1/8) turns
+  const unsigned quarter = (unsigned)((a + (1ull << 61)) >> 62);
+  const long long r = (long long)(a - ((unsigned long long)quarter << 62));
+  // x = 2 pi r / 2^64 as xh + xl
+  const int top = (int)(r >> 32);
+  const float f = (float)top;
+  const float g = (float)(top - (int)f) + (float)(unsigned)r * 2.3283064365386963e-10f;
+  constexpr float kh = 1.4629180792671596e-09f;    // 2 pi / 2^32 in fp32
+  constexpr float kl = -4.0709404e-17f;            // and what is left of it
+  const float xh = f * kh;
+  const float xl = fmaf(f, kh, -xh) + fmaf(g, kh, f * kl);
+  const float z = xh * xh, zl = fmaf(xh, xh, -z) + 2.f * xh * xl;
+  float p = fmaf(z, -2.5052108e-8f, 2.7557319e-6f);          // -1/11!, 1/9!
+  p = fmaf(z, p, -1.9841270e-4f);                            // -1/7!
+  p = fmaf(z, p, 8.3333333e-3f);                             // 1/5!
+  p = fmaf(z, p, -1.6666667e-1f);                            // -1/3!
+  const float sx = xh + fmaf(xh * z, p, fmaf(xl, -0.5f * z, xl));
+  float q = fmaf(z, 2.0876757e-9f, -2.7557319e-7f);          // 1/12!, -1/10!
+  q = fmaf(z, q, 2.4801587e-5f);                             // 1/8!
+  q = fmaf(z, q, -1.3888889e-3f);                            // -1/6!
+  q = fmaf(z, q, 4.1666667e-2f);                             // 1/4!
+  const float w = fmaf(z, -0.5f, 1.f);
+  const float cx = w + fmaf(z * z, q, fmaf(zl, -0.5f, fmaf(z, -0.5f, 1.f - w)));
+  c = quarter & 1u ? sx : cx;
+  s = quarter & 1u ? cx : sx;
+  if (quarter == 1u || quarter == 2u) c = -c;
+  if (quarter & 2u) s = -s;
+}
+
 // cos and sin of the 8 pairs 8 l ... 8 l + 7 of a lane (1 and 0 behind the
 // rotated pairs).  The 32 / LPR rows of a warp share a token and so their
 // angles: each lane works out its share and the warp exchanges them.
@@ -130,10 +164,8 @@ __device__ __forceinline__ void rope_angles(const RopeArgs &r, At at, int lane, 
     mc[j] = 1.f;
     ms[j] = 0.f;
     if (f < r.half) {
-      const unsigned long long a =
-          (unsigned long long)at(r.axis ? (int)r.axis[f] : 0) * r.turns[f];
-      // the signed upper half counts 2^-32 turns: half turns are 2^-31
-      sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &ms[j], &mc[j]);
+      turn_cos_sin((unsigned long long)at(r.axis ? (int)r.axis[f] : 0) * r.turns[f], mc[j],
+                   ms[j]);
       mc[j] *= r.scale;
       ms[j] *= r.scale;
     }
