@@ -160,6 +160,16 @@ int check_batch(const vq_kivi_paged *p, const vq_kivi_paged_batch *s, PagedArgs 
   return VQ_OK;
 }
 
+// whether contiguous rows `out` lie within the range that rows `x` span: tiles
+// of queries are read while others' outputs are written
+bool overlap(const HeadRows &h, int64_t tokens, int D, int elem) {
+  const int64_t t = (tokens - 1) * h.x_token, e = (int64_t)(h.heads - 1) * h.x_head;
+  const int64_t lo = (t < 0 ? t : 0) + (e < 0 ? e : 0);
+  const int64_t hi = (t > 0 ? t : 0) + (e > 0 ? e : 0) + D;
+  const intptr_t x = reinterpret_cast<intptr_t>(h.x), o = reinterpret_cast<intptr_t>(h.out);
+  return o < x + hi * elem && x + lo * elem < o + tokens * h.heads * D * elem;
+}
+
 // the split-KV kernel serves up to 16 rows of a kv head
 bool few_rows(const vq_kivi_paged *p, int max_new) {
   return (int64_t)max_new * (p->H_q / p->H_kv) <= 16;
@@ -278,6 +288,8 @@ int vq_kivi_paged_attend(const vq_kivi_paged *p, const vq_kivi_paged_batch *batc
     return fail(VQ_ERR_ARG, "without cu_new max_new is 1, got %d", max_new);
   if (!std::isfinite(softmax_scale)) return fail(VQ_ERR_ARG, "softmax_scale is not finite");
   if (a.tokens == 0 || a.B == 0) return VQ_OK;
+  if (overlap(h, a.tokens, p->D, elem))
+    return fail(VQ_ERR_ARG, "the output overlaps the queries");
   if ((rc = sm_count(&sms))) return rc;
   const int GQ = p->H_q / p->H_kv;
   const bool few = few_rows(p, max_new);

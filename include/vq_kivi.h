@@ -434,6 +434,7 @@ typedef struct vq_kivi_rows {
 /* out = R(position) (x * rsqrt(mean x^2 + eps) * weight) for each token and
  * head of q and k, in fp32, rounded once; one kernel for both.
  *   dtype      VQ_F16, VQ_BF16 or VQ_F32 (rows and weights)
+ *   tokens     at most 2^24
  *   D          head dimension, a multiple of 16, at most 256
  *   k          NULL for queries alone
  *   rope       NULL for the norms alone (positions are then not read)
@@ -494,7 +495,7 @@ typedef struct vq_kivi_paged {
  *            sequence (row b; tokens = B)
  *   tokens   rows of the token tensors, at least cu_new[B]; rows behind
  *            cu_new[B] are neither read nor written
- * B <= 1024.  A new token at a negative position (lens[b] < n_b: padding) is
+ * B <= 1024, tokens <= 2^24.  A new token at a negative position (lens[b] < n_b: padding) is
  * not in the cache: it is not stored and its attention row is zero.  A
  * sequence whose length or new tokens lie outside their ranges is left out
  * (its rows are not written); a token on a page outside the pool is not
@@ -524,7 +525,7 @@ size_t vq_kivi_paged_workspace_bytes(const vq_kivi_paged *p, int32_t B,
 /* Append: the new tokens' keys are normed (k->weight, or NULL) and rotated
  * (rope, or NULL) in fp32 and quantized into their pages, the values
  * quantized; the queries (q, or NULL) are normed, rotated and written to
- * q->out in the same kernel.
+ * q->out (which may be q->x with the same strides) in the same kernel.
  *   dtype       VQ_F16 or VQ_BF16, of q, k, v and the weights
  *   positions   as vq_kivi_norm_rope, [n_axes][tokens]; NULL: a token's place
  *               in its sequence, on every axis */
@@ -538,8 +539,8 @@ int vq_kivi_paged_append(const vq_kivi_paged *p,
 /* Attention of the new tokens (already appended) over their sequences, each
  * seeing the positions up to its own: decode with one new token, drafts and
  * prompt chunks with several.
- *   q              rows [tokens][H_q][D]; out contiguous, in q's type, not
- *                  overlapping q
+ *   q              rows [tokens][H_q][D]; out contiguous, in q's type, outside
+ *                  the range that q's rows span
  *   max_new        no sequence has more new tokens (1 without cu_new); up to
  *                  16 (token, query head) pairs per kv head are served by the
  *                  split-KV kernel, more by the tensor-memory kernel

@@ -92,6 +92,20 @@ def test_attend_refusals(vqlib, q, dtype, max_new, scale, code):
                                       1 << 30, None) == code
 
 
+@pytest.mark.parametrize("q", [
+    dict(out=1 << 20), dict(out=(1 << 20) + 2048), dict(out=(1 << 20) - 4080),
+    dict(x_token=1 << 20, out=(1 << 21) + (1 << 20) + 2032),   # within the second token
+    dict(x_token=-(1 << 19), out=(1 << 20) - 4096),              # rows in falling order
+])
+def test_attend_output_over_its_queries(vqlib, q):
+    r = _rows(8)
+    for k, v in q.items():
+        setattr(r, k, v)
+    args = (0, r, 1, 0.0, 1 << 20, 1 << 30, None)
+    assert vqlib.vq_kivi_paged_attend(_paged(), _batch(), *args) == -1
+    assert b"overlaps" in vqlib.vq_kivi_last_error()
+
+
 @pytest.mark.parametrize("what,code", [
     ("k_null", -1), ("heads", -1), ("v_weight", -1), ("eps", -1), ("rot", -2), ("axes", -1),
     ("axis", -1), ("turns", -1), ("scale", -1), ("stride", -1), ("fp32", -2), ("q_out", -1),
