@@ -236,7 +236,7 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
       float w0[8], w1[8];
       unpack8<T>(wa, w0);
       unpack8<T>(wb, w1);
-      norm_row<LPR>(x0, x1, w0, w1, D, eps);
+      norm_row<T, LPR>(x0, x1, w0, w1, D, eps);
     }
     if (8 * l < r.half) rotate_row(r.interleaved, c, s, x0, x1);
     if (!isk) {

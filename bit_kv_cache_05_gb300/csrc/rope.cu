@@ -75,7 +75,7 @@ k_norm_rope(HeadRows q, HeadRows k, RopeArgs r, int D, int64_t tokens, float eps
         unpack8<T>(a, w0);
         unpack8<T>(b, w1);
       }
-      norm_row<LPR>(x0, x1, w0, w1, D, eps);
+      norm_row<T, LPR>(x0, x1, w0, w1, D, eps);
     }
     if (8 * l < r.half) rotate_row(r.interleaved, c, s, x0, x1);
     if (active && row < h.heads) {

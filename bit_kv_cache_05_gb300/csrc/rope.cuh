@@ -177,20 +177,33 @@ __device__ __forceinline__ void rope_angles(const RopeArgs &r, At at, int lane, 
   }
 }
 
-// RMS norm of a row held by LPR lanes (all lanes of the warp take part)
-template <int LPR>
+// RMS norm of a row held by LPR lanes (all lanes of the warp take part).  Of
+// fp16 rows the product with the weight is exact in fp32 (22 bits, no
+// overflow) and comes first; bf16 and fp32 rows could leave its range.
+template <typename T, int LPR>
 __device__ __forceinline__ void norm_row(float (&x0)[8], float (&x1)[8], const float (&w0)[8],
                                          const float (&w1)[8], int D, float eps) {
-  float ss = 0.f;
+  // four short sums, so that a square meets few roundings
+  float p[4] = {};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
+  for (int e = 0; e < 8; ++e) p[e & 3] = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], p[e & 3]));
+  float ss = (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float inv = rsqrtf(ss / (float)D + eps);
+  // one Newton step with its residual in two parts: the factor of a whole row
+  // is off by little more than its last rounding
+  const float m = ss / (float)D + eps, r = rsqrtf(m);
+  const float h = m * r, rest = fmaf(-h, r, 1.f) - fmaf(m, r, -h) * r;
+  const float inv = m > 0.f && r > 0.f ? fmaf(0.5f * r, rest, r) : r;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    x0[e] = x0[e] * inv * w0[e];
-    x1[e] = x1[e] * inv * w1[e];
+    if constexpr (std::is_same<T, __half>::value) {
+      x0[e] = x0[e] * w0[e] * inv;
+      x1[e] = x1[e] * w1[e] * inv;
+    } else {
+      x0[e] = x0[e] * inv * w0[e];
+      x1[e] = x1[e] * inv * w1[e];
+    }
   }
 }
 
