@@ -17,17 +17,20 @@
 //              memory, online softmax in fp32, weights back to tensor memory
 //              in fp16 (the A operand of the second product), the output
 //              read out at the end.  Rounding a weight to fp16 moves it by
-//              2^-12 of itself at most, as one rounding of a 16-bit output
-//              does.
+//              2^-11 of itself at most, as one rounding of an fp16 output
+//              does, or by 2^-25 where fp16 has no smaller steps: 2^-34 of
+//              the row's largest weight, which is 2^9 or more.
 //   8-11       rebuild k_hat (fp16 by definition) from the codes into two
 //   12-15      128-byte-swizzled stages, and v_hat likewise
 //   16         issues the products: S = Q k_hat^T, then O += P v_hat
 //   17, 18     copy the key and the value halves of the blocks (one bulk copy
 //              each), 64 tokens a stage
-// The running maximum of a row is a whole number (base 2) and is raised only
-// when a score passes it by more than 15: a weight stays below 2^15, which
-// fp16 holds, one pass over a tile's scores is enough, and what was weighed
-// with the old maximum is brought to a new one by an exact power of two.
+// The running maximum of a row is a whole number (base 2), its weight 2^10,
+// and it is raised only when a score passes it by more than 5: a weight stays
+// within 2^15, which fp16 holds, one pass over a tile's scores is enough, and
+// what was weighed with the old maximum is brought to a new one by an exact
+// power of two.  More of fp16's range for the small weights means more raises
+// (2 x 512 tokens at 33280: 464 us with 7 or 5 bits of headroom, 480 with 3).
 //
 // k_hat's channels lie in the order 0 4 1 5 2 6 3 7 within each 8, in which
 // a code word gives its fp16 pairs; the queries are laid out the same.
@@ -44,7 +47,7 @@ constexpr int kThreads = 640;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kLazy = 15.f;
+constexpr float kTop = 10.f, kLazy = 15.f - kTop;   // see above
 constexpr int kNear = 64;            // sequences whose prefix fits in shared memory
 constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
 constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes, one a warp
@@ -618,20 +621,23 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
             if (c > 0) {
               // the weights of this tile so far
               sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
-              const __half2 f2 = __float2half2_rn(f);
               tm_wait_st();
 #pragma unroll 1
               for (int d = 0; d < c / 2; d += 8) {
                 uint32_t p[8];
                 tm_ld8(ts + d, p);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = h2_bits(__hmul2(bits_h2(p[j]), f2));
+                for (int j = 0; j < 8; ++j) {
+                  // in fp32: the factor itself may be too small for fp16
+                  const float2 y = __half22float2(bits_h2(p[j]));
+                  p[j] = h2_bits(__floats2half2_rn(y.x * f, y.y * f));
+                }
                 tm_st8(ts + d, p);
               }
             }
             mo = mn;
           }
-          const float base = mo == -INFINITY ? 0.f : -mo;
+          const float base = mo == -INFINITY ? 0.f : kTop - mo;
 #pragma unroll
           for (int d = 0; d < 64; d += 32) {
             uint32_t p[16];

@@ -15,14 +15,22 @@
 // pair's scales are the halves of one word), B = up to 8 query rows; output:
 // A = weights, turned over by movmatrix, B = v_hat.  The weights enter as
 // fp16 hi (rows 0-7) plus the remainder lo (rows 8-15, free in a 16-row
-// product), so only the output is rounded to 16 bits.  With 9 to 16 rows
-// (drafts) the second 8 take those rows, and the weights of all are rounded to
-// fp16 once, as the tensor-memory kernel rounds them: 2^-12 of a weight at
-// most, no more than the output's own rounding.  Both operands that
-// change are made where the product reads them: no register is moved.  k_hat and
-// v_hat are fp16 by definition; a bf16 query row is scaled by a power of two
-// to a maximum near 2^14 and taken as fp16, which keeps every bit of values
-// down to 2^-28 of the row's largest.
+// product).  With 9 to 16 rows (drafts) the second 8 take those rows, and the
+// weights of all are rounded to fp16 once, as the tensor-memory kernel rounds
+// them.  Both operands that change are made where the product reads them: no
+// register is moved.  k_hat and v_hat are fp16 by definition; a bf16
+// query row is scaled by a power of two to a maximum near 2^14 and taken as
+// fp16, which keeps every bit of values down to 2^-28 of the row's largest.
+//
+// What a weight loses: below 2^-14 fp16 has steps of 2^-24, no longer small
+// beside the weight, while the weights' sum is kept in fp32; a long tail of
+// small weights behind a large one would be lost from the output alone.  So a
+// row's largest weight is 2^7 or 2^12 (Weights below), not 1, and may grow to
+// 2^15.  With hi + lo the remainder is taken times 2^12 (exact) into sums of
+// its own and is off by 2^-22 of the weight or 2^-37, which is 2^-44 of the
+// row's largest: only the output is rounded to 16 bits.  Rounded once (9 to
+// 16 rows) a weight is off by 2^-11 of itself, as an fp16 output, or by 2^-25,
+// which is 2^-37 of the row's largest.
 //
 // The bound is HBM: a block is read once (160 bytes per token and kv head at
 // D = 128, g = 32).
@@ -38,7 +46,15 @@ constexpr int kThreads = 32 * kWarps;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kStep = 32;          // tokens of a step: two blocks
 constexpr int kMinSteps = 1;       // steps a warp takes at least
-constexpr float kLazy = 8.f;       // a maximum is raised when it grows by more
+
+// A fresh maximum's weight is 2^top; a maximum is raised when it grows by
+// more than `lazy` bits, so that a weight stays within 2^15.  hi + lo need no
+// more range than 7 bits give; single fp16 weights get all but 3.
+template <int ROWS>
+struct Weights {
+  static constexpr float top = ROWS == 8 ? 7.f : 12.f, lazy = 15.f - top;
+};
+constexpr float kLo = 4096.f;      // the remainders' factor
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -218,6 +234,7 @@ template <typename T, int D, int NG, int ROWS>
 __global__ void __launch_bounds__(kThreads, DecSmem<D, NG, ROWS>::CTAS)
 k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
   using SM = DecSmem<D, NG, ROWS>;
+  using W = Weights<ROWS>;
   constexpr int I = D / 32, BLK = SM::BLK, STEP = SM::STEP, ST = SM::STAGES, G = D / NG;
   constexpr int NR = ROWS / 8;      // groups of 8 rows
   extern __shared__ __align__(128) unsigned char smem[];
@@ -451,7 +468,7 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
         for (int g = 0; g < NR; ++g) {
           mx[g].x = sc[g].x * fmaxf(fmaxf(x[g][0][0], x[g][0][2]), fmaxf(x[g][1][0], x[g][1][2]));
           mx[g].y = sc[g].y * fmaxf(fmaxf(x[g][0][1], x[g][0][3]), fmaxf(x[g][1][1], x[g][1][3]));
-          raise = raise || mx[g].x > m[g].x + kLazy || mx[g].y > m[g].y + kLazy;
+          raise = raise || mx[g].x > m[g].x + W::lazy || mx[g].y > m[g].y + W::lazy;
         }
         if (__any_sync(kFull, raise)) {
 #pragma unroll
@@ -495,8 +512,8 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
           uint32_t wt[2][2];
 #pragma unroll
           for (int g = 0; g < NR; ++g) {
-            const float2 base = make_float2(m[g].x == -INFINITY ? 0.f : -m[g].x,
-                                            m[g].y == -INFINITY ? 0.f : -m[g].y);
+            const float2 base = make_float2(m[g].x == -INFINITY ? 0.f : W::top - m[g].x,
+                                            m[g].y == -INFINITY ? 0.f : W::top - m[g].y);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float2 y = __ffma2_rn(make_float2(x[g][bk][2 * e], x[g][bk][2 * e + 1]),
@@ -507,7 +524,9 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
               wt[g][e] = turn(h2_bits(hh));
               if constexpr (NR == 1) {
                 const float2 hf = __half22float2(hh);
-                wt[1][e] = turn(h2_bits(__floats2half2_rn(p.x - hf.x, p.y - hf.y)));
+                const float2 lo = __fmul2_rn(make_float2(p.x - hf.x, p.y - hf.y),
+                                             make_float2(kLo, kLo));
+                wt[1][e] = turn(h2_bits(__floats2half2_rn(lo.x, lo.y)));
               }
             }
           }
@@ -577,8 +596,10 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
           for (int c = 0; c < 2; ++c) {
             float4 y;
             if constexpr (NR == 1)
-              y = make_float4(o[i][0][c] + o[i][0][2 + c], o[i][1][c] + o[i][1][2 + c],
-                              o[i][2][c] + o[i][2][2 + c], o[i][3][c] + o[i][3][2 + c]);
+              y = make_float4(fmaf(o[i][0][2 + c], 1.f / kLo, o[i][0][c]),
+                              fmaf(o[i][1][2 + c], 1.f / kLo, o[i][1][c]),
+                              fmaf(o[i][2][2 + c], 1.f / kLo, o[i][2][c]),
+                              fmaf(o[i][3][2 + c], 1.f / kLo, o[i][3][c]));
             else
               y = make_float4(o[i][0][2 * g + c], o[i][1][2 * g + c], o[i][2][2 * g + c],
                               o[i][3][2 * g + c]);

@@ -160,6 +160,22 @@ def attend64(q, pool, table, lens, cu, D, g, H_kv, scale=0.0, weight_step=2.0 **
     return out, err
 
 
+def attend64_rows(q, K, V, seen, scale, weight_step=2.0 ** -21, floor=0.0):
+    """As attend64 for rows q [R][D] over K, V [S][D] of one kv head, row r
+    seeing the first seen[r] >= 1 tokens; all float64 tensors of one device.
+    floor: what a weight is off by beside weight_step of itself, in units of
+    the row's largest weight (fp16 has no steps below 2^-24)."""
+    S, D = K.shape
+    hidden = torch.arange(S, device=q.device) >= torch.as_tensor(seen, device=q.device)[:, None]
+    s = (q @ K.T * scale).masked_fill(hidden, -math.inf)
+    p = torch.softmax(s, -1)
+    size = (q.abs() @ K.abs().T * scale).masked_fill(hidden, 0.0).amax(-1, keepdim=True)
+    rel = weight_step + 2.0 ** -20 + 2 * (D + 4) * 2.0 ** -23 * size + (S / 16 + 4) * 2.0 ** -23
+    sums = (~hidden).double() @ V.abs()
+    err = 2 * rel * (p @ V.abs()) + floor * p.amax(-1, keepdim=True) * sums
+    return (p @ V).cpu().numpy(), err.cpu().numpy()
+
+
 def check_attend(got, want, err, dtype):
     got = got.detach().cpu().double().numpy()
     tol = err + half_step(dtype) * (np.abs(want) + err) + sub_step(dtype)

@@ -588,3 +588,86 @@ def test_offsets_past_32_bits():
                                  weight_step=MANY)
         ref.check_attend(out, want, err, q.dtype)
     c.status()
+
+
+# ---- weights far apart, and walks of many steps -----------------------------------
+
+# a weight's error beside weight_step of itself, relative to the row's largest
+# weight: fp16's half step 2^-25 of weights whose largest is 2^9 or more,
+# twice (written, and brought to a new maximum); with hi + lo (up to 8 rows)
+# the half step of the remainders times 2^12
+FLOOR_FEW, FLOOR_MANY = 2.0 ** -43, 2.0 ** -33
+
+
+def levels_cache(levels, page, H_q, H_kv, D, g, seed):
+    """One sequence whose token t has the key levels[t] in every channel (so a
+    query of ones scores it D levels[t]) and values that are constant over a
+    group: 1 in the first group, but 0 for the token of the largest level;
+    some multiple of 1/8 in the others.  All exact in 4 bits."""
+    S = len(levels)
+    c = new_cache(-(-S // page) + 1, page, H_q, H_kv, D, g)
+    table = ref.make_table(1, [S], page, c.n_pages, "cuda", seed)
+    lv = torch.tensor(levels, dtype=torch.float64, device="cuda")
+    assert torch.equal(lv.half().double(), lv)
+    v = torch.randint(-16, 17, (S, D // g), generator=torch.Generator().manual_seed(seed)) / 8.0
+    v[:, 0] = 1.0
+    v[lv.argmax().item(), 0] = 0.0
+    K = lv[:, None].expand(S, D).contiguous()
+    V = v.double().cuda().repeat_interleave(g, -1)
+    rows = lambda x: x.half()[:, None].expand(S, H_kv, D)
+    c.append(rows(K), rows(V), table, i32([S]), offsets([S]))
+    c.status()
+    return c, table, K, V
+
+
+def _sink(S, at, gap):
+    x = [0.0] * S
+    x[at] = gap
+    return x
+
+
+def _stairs(S):
+    """Nothing for a tile, then half a tile 10.25 nats higher, then one token
+    17.75 nats up: what was weighed against the first maximum is brought far
+    down inside the tile."""
+    x = [0.0] * S
+    x[128:192] = [10.25] * 64
+    x[200] = 17.75
+    return x
+
+
+LEVELS = {
+    "sink 14": lambda S: _sink(S, 3, 14.0), "sink 16": lambda S: _sink(S, 0, 16.0),
+    "sink 17.5": lambda S: _sink(S, 70, 17.5), "sink 20": lambda S: _sink(S, 2001, 20.0),
+    "stairs": _stairs,
+    "rising": lambda S: [round(64 * 24 * t / S) / 64 for t in range(S)],
+}
+
+
+@pytest.mark.parametrize("name", list(LEVELS))
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("H_q,H_kv,n,D,g", [
+    (8, 8, 1, 128, 32), (32, 8, 1, 64, 64), (32, 8, 4, 128, 64), (16, 8, 8, 64, 32),
+    (8, 8, 33, 128, 32), (8, 8, 200, 64, 32), (32, 8, 50, 128, 128),
+])
+def test_one_large_weight_before_a_long_tail(name, dtype, H_q, H_kv, n, D, g):
+    """Weights far below a row's largest still count in sum (an attention sink
+    of value 0 before a flat tail; maxima that rise late).  As many sequences,
+    all of the same pages, as give every resident warp or CTA whole sequences
+    to walk."""
+    S = 4100
+    c, table, K, V = levels_cache(LEVELS[name](S), 64, H_q, H_kv, D, g, 3)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    few = n * (H_q // H_kv) <= 16
+    B = -(-sms * 16 // H_kv) + 1 if few else -(-2 * sms // H_kv)
+    q = torch.ones(B * n, H_q, D, dtype=DT[dtype], device="cuda")
+    cu = None if n == 1 else offsets([n] * B)
+    out = c.attend(q, table.repeat(B, 1), i32([S] * B), cu, max_new=n, scale=1.0 / D)
+    c.status()
+    hi_lo = n * (H_q // H_kv) <= 8
+    want, err = ref.attend64_rows(torch.ones(n, D, dtype=torch.float64, device="cuda"), K, V,
+                                  range(S - n + 1, S + 1), 1.0 / D, FEW if hi_lo else MANY,
+                                  FLOOR_FEW if hi_lo else FLOOR_MANY)
+    for b in range(0, B, max(B // 8, 1)):
+        for h in range(0, H_q, 3):
+            ref.check_attend(out[b * n:(b + 1) * n, h], want, err, q.dtype)
