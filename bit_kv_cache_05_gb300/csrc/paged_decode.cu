@@ -36,6 +36,7 @@
 // D = 128, g = 32).
 #include "bulk_pipe.cuh"
 #include "paged.cuh"
+#include "stage_ring.h"
 #include "vqk_internal.cuh"
 
 namespace vqk {
@@ -309,12 +310,12 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
     g1 = __ballot_sync(kFull, ok1);
   };
   prepare();
-  unsigned good = 0u;                                  // two bits a stage
+  StageRing ring;
   auto issue = [&](int s) {
     if (iu - ibase == 32) prepare();
     const int j = iu - ibase;
     const unsigned gd = ((g0 >> j) & 1u) | (((g1 >> j) & 1u) << 1);
-    good = (good & ~(3u << (2 * s))) | (gd << (2 * s));
+    ring.issued(s, gd);
     if (lane == j && gd) {
       unsigned char *dst = stage + s * STEP;
       mbar_expect_tx(&bar[s], gd == 3u ? STEP : BLK);
@@ -332,7 +333,6 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
     if (iu < u_end) issue(s);
 
   int s = 0;
-  unsigned phases = 0u;
   bool dead = false;
   while (u < u_end && !dead) {
     // one (sequence, kv head)
@@ -411,15 +411,15 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
     const int k_end = min(nb, k + (u_end - u));
     u += k_end - k;
     for (; k < k_end; ++k) {
-      const unsigned gd = (good >> (2 * s)) & 3u;
+      const unsigned gd = ring.blocks(s);
       if (gd) {
-        const bool ok = bounded_wait(&bar[s], (phases >> s) & 1u);
-        phases ^= 1u << s;
+        const bool ok = bounded_wait(&bar[s], ring.parity(s));
         if (!__all_sync(kFull, ok)) {
           if (lane == 0) atomicOr(a.status, kGaveUp);
           dead = true;
           break;
         }
+        ring.landed(s);
         const unsigned char *st = stage + s * STEP;
         const int t0 = k * kStep;
         // raw scores of rows 8 g + 2 t4 and the next: tokens 16 bk + 2 n8 and
@@ -615,7 +615,7 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
   if (dead) {
     // let the copies in flight land before the CTA's memory is given up
     for (int i = 0; i < ST; ++i)
-      if ((good >> (2 * i)) & 3u) bounded_wait(&bar[i], (phases >> i) & 1u);
+      if (ring.blocks(i)) bounded_wait(&bar[i], ring.parity(i));
   }
 }
 

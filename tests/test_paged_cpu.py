@@ -1,6 +1,9 @@
 """Refusals of the rotation and of the paged cache, and the facts behind their
 arithmetic, without a GPU."""
 import ctypes
+import os
+import shutil
+import subprocess
 from fractions import Fraction
 
 import numpy as np
@@ -247,3 +250,71 @@ def test_quantizer_reference_worked():
     assert (code[1] == 0).all() and s[1, 0] == 0 and z[1, 0] == 2.5
     top = np.float16(15 * float(s[2, 0]) + float(z[2, 0]))
     assert code[2, 1] == 15 and np.isfinite(top) and s[2, 0] == 8728
+
+
+RING = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "stage_ring.h"
+// A ring of ST stages under random copies, landings and one wait that gives
+// up; a barrier counts its completed phases, and a wait for parity p ends when
+// the phase under way has the other one.
+int main() {
+  srand(1);
+  for (int run = 0; run < 200000; ++run) {
+    const int ST = 3 + rand() % 2, steps = 1 + rand() % 12, fail = rand() % steps;
+    vqk::StageRing ring;
+    int done[4] = {}, copies[4] = {};        // completed phases; copies not landed
+    int issued = 0;
+    auto issue = [&](int s) {
+      const unsigned which = rand() % 4;
+      if (ring.blocks(s)) return false;
+      ring.issued(s, which);
+      copies[s] = which != 0;
+      ++issued;
+      return true;
+    };
+    auto land = [&](int s) { if (copies[s]) { copies[s] = 0; ++done[s]; } };
+    auto over = [&](int s) { return (unsigned)(done[s] & 1) != ring.parity(s); };
+    for (int s = 0; s < ST && issued < steps; ++s) if (!issue(s)) return 1;
+    bool dead = false;
+    for (int u = 0; u < steps && !dead; ++u) {
+      const int s = u % ST;
+      for (int i = 0; i < ST; ++i) if (rand() % 3 == 0 && !(u == fail && i == s)) land(i);
+      if (ring.blocks(s)) {
+        if (u == fail && copies[s]) { dead = true; break; }   // gives up
+        land(s);
+        if (!over(s)) return 2;
+        ring.landed(s);
+      }
+      if (issued < steps && !issue(s)) return 3;
+    }
+    // what is left: a wait for every stage with copies, ended by their landing
+    // and not before, and none for the others
+    for (int i = 0; i < ST; ++i) {
+      if (copies[i]) {
+        if (!ring.blocks(i) || over(i)) return 4;
+        land(i);
+      }
+      if (ring.blocks(i) && !over(i)) return 5;
+    }
+  }
+  return 0;
+}
+"""
+
+
+def test_a_warp_that_gives_up_waits_for_its_copies(tmp_path):
+    """The decode's bookkeeping of its shared-memory stages, run on the host:
+    after a wait that gave up, the copies under way, that one's among them, are
+    waited for, and no stage whose copies were used."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    import bit_kv_cache_05_gb300
+    src = tmp_path / "ring.cc"
+    src.write_text(RING)
+    inc = os.path.join(os.path.dirname(bit_kv_cache_05_gb300.__file__), "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-I", inc, str(src), "-o", str(tmp_path / "ring")],
+                   check=True)
+    assert subprocess.run([str(tmp_path / "ring")]).returncode == 0
