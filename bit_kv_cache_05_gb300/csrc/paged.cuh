@@ -107,6 +107,33 @@ __device__ __forceinline__ uint8_t *find_block(const PagedArgs &a, int b, int po
   return a.pool + ((((int64_t)p * a.H_kv + h) << (a.page_log2 - 4)) + in) * block_bytes;
 }
 
+// A bf16 query row enters the products as fp16, times the power of two that
+// brings its largest magnitude (`top`, the bits of an fp32) near 2^14; `back`
+// is the inverse.  Both are normal numbers for every top, infinity and NaN
+// among them.
+struct RowScale {
+  float up, back;
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  int f = top ? 14 - ((int)(top >> 23) - 127) : 0;     // -114 ... 141
+  f = f > 126 ? 126 : f;
+  return RowScale{__uint_as_float((uint32_t)(127 + f) << 23),
+                  __uint_as_float((uint32_t)(127 - f) << 23)};
+}
+
+// Far maxima.  A weight is 2^(score - maximum + top), a few bits above 1 for
+// the largest.  From 2^24 on fp32 has no room for those bits beside the
+// maximum, so that they are left out there (2^(score - maximum), which is
+// what a maximum larger by `top` gives); kFar leaves the nearer ones exact.
+constexpr float kFar = 8388608.f;
+__device__ __forceinline__ bool is_far(float m) {
+  return fabsf(m) > kFar && m != -INFINITY;
+}
+__device__ __forceinline__ float stand_in(float m, float top) {
+  return is_far(m) ? m + top : m;
+}
+
 // Waits for a barrier's phase; false after about half a second, or soon after
 // *dead (when given) is set.  Reading the clock between the tries is also the
 // pause that a waiting warp leaves the others: tries with none, with

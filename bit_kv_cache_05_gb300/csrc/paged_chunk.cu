@@ -47,7 +47,8 @@ constexpr int kThreads = 640;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
 constexpr int kRaw = 3;              // stages of 64 tokens as stored
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kTop = 10.f, kLazy = 15.f - kTop;   // see above
+// exponents of a fresh maximum's weight and of the largest one (see above)
+constexpr float kTop = 10.f, kMost = 15.f;
 constexpr int kNear = 64;            // sequences whose prefix fits in shared memory
 constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
 constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes, one a warp
@@ -496,6 +497,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
     uint32_t ph_s = 0, ph_o = 0, ph_x = 0;
     float sl2 = 0.f;
+    bool far_q = false;
     // query row of this thread, of the slot's query tile
     auto token = [&]() {
       return walk.pair * 2 * tpt + (walk.two(tpt) ? wg * tpt : 0) + row / GQ;
@@ -525,13 +527,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           for (int e = 0; e < 4; ++e)
             m = max(m, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
         }
-        const int e = (int)(m >> 23);
-        int f = e > 0 ? 14 - (e - 127) : 0;
-        f = f > 126 ? 126 : (f < -100 ? -100 : f);
-        up = __uint_as_float((uint32_t)(127 + f) << 23);
-        sl2 *= __uint_as_float((uint32_t)(127 - f) << 23);
+        const RowScale rs = row_scale(m);
+        up = rs.up;
+        sl2 *= rs.back;
       }
       unsigned char *dst = sm + SM::Q + wg * SM::OP;
+      __half2 size[2] = {bits_h2(0u), bits_h2(0u)};    // sum |q| / 256
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
@@ -541,6 +542,9 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
             w[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * up,
                                              __uint_as_float(w[i] & 0xffff0000u) * up));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          size[i & 1] = __hfma2(__habs2(bits_h2(w[i])), bits_h2(0x1c001c00u), size[i & 1]);
         *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + sw(row, c & 7)) =
             make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
                        __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
@@ -548,6 +552,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(&B.q_full[wg]);
+      // whether keys of fp16's size could take a row's scores beyond kFar (5 %
+      // and 1 / 64 cover the roundings of the sum; NaN counts as yes)
+      const float2 s2 = __half22float2(__hadd2(size[0], size[1]));
+      far_q = __any_sync(kFull, !(65504.f * sl2 * (269.f * (s2.x + s2.y) + 0.015625f) <= kFar));
     };
     // key tiles before this pair, for the stages that they lie in
     uint32_t ring = 0;
@@ -575,104 +583,126 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       const bool idle = !__any_sync(kFull, valid);
       const bool two = walk.two(tpt);
       const int steps = walk.steps(tpt);
-      const float scale = sl2;
+      const float raw = sl2;
       float m = -INFINITY, l = 0.f;
       // columns up to vis are seen
       int vis = (valid ? walk.s.len - walk.s.n + tok : 0x3fffffff) -
                 (walk.k + (two ? 0 : wg)) * kTile;
       const int ahead = two ? kTile : 2 * kTile;
-      for (int j = two ? 0 : wg; j < steps; j += two ? 1 : 2, vis -= ahead) {
-        ok = bar_wait(&B.s_full[wg], ph_s, dead);
-        ph_s ^= 1u;
-        if (!__all_sync(kFull, ok)) { ok = false; break; }
-        fence_after();
-        if (gives && (!two || wg == 1)) {
-          bar_arrive(&B.k_empty[(ring + j) & 1]);
-          // the values of this slot's tile before
-          if (j >= (two ? 1 : 2)) bar_arrive(&B.v_empty[(ring + j - (two ? 1 : 2)) & 1]);
-        }
-        if (idle) {
+      // In one fma with the maximum a weight's exponent is off by the
+      // maximum's own rounding, whole bits from 2^24 on: rows that may go
+      // that far get their scores scaled, and rounded, beforehand, in a loop
+      // of their own (a branch within the loop made all rows 3 to 5 % slower).
+      auto tiles = [&](auto scaled_before) {
+        constexpr bool before = decltype(scaled_before)::value;
+        const float scale = before ? 1.f : raw;
+        for (int j = two ? 0 : wg; j < steps; j += two ? 1 : 2, vis -= ahead) {
+          ok = bar_wait(&B.s_full[wg], ph_s, dead);
+          ph_s ^= 1u;
+          if (!__all_sync(kFull, ok)) { ok = false; break; }
+          fence_after();
+          if (gives && (!two || wg == 1)) {
+            bar_arrive(&B.k_empty[(ring + j) & 1]);
+            // the values of this slot's tile before
+            if (j >= (two ? 1 : 2)) bar_arrive(&B.v_empty[(ring + j - (two ? 1 : 2)) & 1]);
+          }
+          if (idle) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&B.p_full[wg]);
+            continue;
+          }
+          if constexpr (before) {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 16) {
+              uint32_t v[16];
+              tm_ld16(ts + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * raw);
+              tm_st16(ts + c, v);
+            }
+            tm_wait_st();
+          }
+          const bool all = __all_sync(kFull, vis >= kTile - 1);
+          float mo = m;       // the maximum that the tile's weights stand on
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < kTile; c += 64) {
+            uint32_t v[64];
+            tm_ld64(ts + c, v);
+            if (!all) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (c + j > vis) v[j] = __float_as_uint(-INFINITY);
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 64; j += 2)
+              mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            const float top = scale * fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+            if (__any_sync(kFull, top + (kTop - mo) > kMost)) {
+              const float mn = top + (kTop - mo) > kMost
+                                   ? fmaxf(mo, stand_in(ceilf(top), kTop)) : mo;
+              const float f = mn > mo ? pow2(mo - mn) : 1.f;
+              l *= f;
+              if (c > 0) {
+                // the weights of this tile so far
+                sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
+                tm_wait_st();
+#pragma unroll 1
+                for (int d = 0; d < c / 2; d += 8) {
+                  uint32_t p[8];
+                  tm_ld8(ts + d, p);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    // in fp32: the factor itself may be too small for fp16
+                    const float2 y = __half22float2(bits_h2(p[j]));
+                    p[j] = h2_bits(__floats2half2_rn(y.x * f, y.y * f));
+                  }
+                  tm_st8(ts + d, p);
+                }
+              }
+              mo = mn;
+            }
+            const float base = mo == -INFINITY ? 0.f : kTop - mo;
+#pragma unroll
+            for (int d = 0; d < 64; d += 32) {
+              uint32_t p[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[d + 2 * j]),
+                                                        __uint_as_float(v[d + 2 * j + 1])),
+                                            make_float2(scale, scale), make_float2(base, base));
+                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                sum[j & 1] = __fadd2_rn(sum[j & 1], y);
+                p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
+              }
+              // the weights of 32 columns take 16, all behind what is read
+              tm_st16(ts + (c + d) / 2, p);
+            }
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          // O goes to the new maximum
+          if (j >= (two ? 1 : 2) && __any_sync(kFull, mo > m)) {
+            const float f = mo > m ? pow2(m - mo) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t v[16];
+              tm_ld16(to + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tm_st16(to + c, v);
+            }
+          }
+          m = mo;
+          tm_wait_st();
           fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&B.p_full[wg]);
-          continue;
         }
-        const bool all = __all_sync(kFull, vis >= kTile - 1);
-        float mo = m;       // the maximum that the tile's weights stand on
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < kTile; c += 64) {
-          uint32_t v[64];
-          tm_ld64(ts + c, v);
-          if (!all) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (c + j > vis) v[j] = __float_as_uint(-INFINITY);
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 64; j += 2)
-            mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-          const float top = scale * fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          if (__any_sync(kFull, top > mo + kLazy)) {
-            const float mn = top > mo + kLazy ? ceilf(top) : mo;
-            const float f = mn > mo ? pow2(mo - mn) : 1.f;
-            l *= f;
-            if (c > 0) {
-              // the weights of this tile so far
-              sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
-              tm_wait_st();
-#pragma unroll 1
-              for (int d = 0; d < c / 2; d += 8) {
-                uint32_t p[8];
-                tm_ld8(ts + d, p);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  // in fp32: the factor itself may be too small for fp16
-                  const float2 y = __half22float2(bits_h2(p[j]));
-                  p[j] = h2_bits(__floats2half2_rn(y.x * f, y.y * f));
-                }
-                tm_st8(ts + d, p);
-              }
-            }
-            mo = mn;
-          }
-          const float base = mo == -INFINITY ? 0.f : kTop - mo;
-#pragma unroll
-          for (int d = 0; d < 64; d += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[d + 2 * j]),
-                                                      __uint_as_float(v[d + 2 * j + 1])),
-                                          make_float2(scale, scale), make_float2(base, base));
-              const float2 y = make_float2(ex2(x.x), ex2(x.y));
-              sum[j & 1] = __fadd2_rn(sum[j & 1], y);
-              p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
-            }
-            // the weights of 32 columns take 16, all behind what is read
-            tm_st16(ts + (c + d) / 2, p);
-          }
-        }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        // O goes to the new maximum
-        if (j >= (two ? 1 : 2) && __any_sync(kFull, mo > m)) {
-          const float f = mo > m ? pow2(m - mo) : 1.f;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t v[16];
-            tm_ld16(to + c, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tm_st16(to + c, v);
-          }
-        }
-        m = mo;
-        tm_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&B.p_full[wg]);
-      }
+      };
+      if (far_q) tiles(std::true_type{});
+      else tiles(std::false_type{});
       if (!ok) break;
       // slot 1 of a single query tile hands its sums to slot 0
       const bool halves = !two && steps > 1;

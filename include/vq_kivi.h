@@ -545,7 +545,9 @@ int vq_kivi_paged_append(const vq_kivi_paged *p,
  *                  16 (token, query head) pairs per kv head are served by the
  *                  split-KV kernel, more by the tensor-memory kernel
  *   softmax_scale  <= 0 selects 1/sqrt(D)
- *   workspace      device, 16-byte aligned */
+ *   workspace      device, 16-byte aligned
+ * Queries may be of any finite size; scores are fp32, so that a row is NaN
+ * where softmax_scale q.k passes fp32's range. */
 int vq_kivi_paged_attend(const vq_kivi_paged *p,
                          const vq_kivi_paged_batch *batch, int dtype,
                          const vq_kivi_rows *q, int32_t max_new,

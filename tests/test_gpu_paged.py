@@ -671,3 +671,42 @@ def test_one_large_weight_before_a_long_tail(name, dtype, H_q, H_kv, n, D, g):
     for b in range(0, B, max(B // 8, 1)):
         for h in range(0, H_q, 3):
             ref.check_attend(out[b * n:(b + 1) * n, h], want, err, q.dtype)
+
+
+@pytest.mark.parametrize("dtype,size,step", [("fp16", 2.0 ** 15, 32.0), ("bf16", 2.0 ** 120, 1.0),
+                                             ("bf16", -(2.0 ** 118), 1.0), ("fp16", -60000.0, 8.0),
+                                             ("bf16", 2.0 ** 15, 32.0)])
+@pytest.mark.parametrize("H_q,H_kv,n,D", [(4, 2, 1, 128), (8, 2, 4, 64), (2, 2, 33, 128),
+                                          (4, 2, 80, 64)])
+def test_finite_rows_of_any_size_give_finite_outputs(dtype, size, step, H_q, H_kv, n, D):
+    """Scores far beyond 2^24, whose fp32 steps are whole bits, and bf16 rows
+    near the type's largest values.  Keys are constant over the channels and
+    climb by `step` with the token, three equal ones in front: the softmax is
+    one token's, or the mean of the equal ones.  2^120 times 304 times 128
+    channels is no fp32 number by any way of adding up, so that the bf16 rows'
+    scale is 2^-16."""
+    S = 300
+    lv = torch.arange(S, dtype=torch.float64) * step - 2048 * step * (size == 2.0 ** 15)
+    lv[:3] = lv[-1] + 5 * step if size > 0 else lv[0] - 5 * step
+    assert torch.equal(lv.half().double(), lv)
+    c = new_cache(20, 16, H_q, H_kv, D, 32)
+    table = ref.make_table(1, [S], 16, 20, "cuda", 3)
+    v = (torch.randint(-16, 17, (S, D // 32), generator=torch.Generator().manual_seed(1)) / 8.0)
+    V = v.repeat_interleave(32, -1)
+    rows = lambda x: x.half().cuda()[:, None].expand(S, H_kv, D)
+    c.append(rows(lv[:, None].expand(S, D)), rows(V), table, i32([S]), offsets([S]))
+    q = torch.full((n, H_q, D), size, dtype=DT[dtype], device="cuda")
+    scale = 2.0 ** -16 if abs(size) > 1e30 else 0.0
+    out = c.attend(q, table, i32([S]), offsets([n]), max_new=n, scale=scale)
+    c.status()
+    want = V[:3].double().mean(0).numpy()
+    err = 4 * 2.0 ** -11 * V[:3].double().abs().mean(0).numpy()
+    ref.check_attend(out, np.broadcast_to(want, out.shape), np.broadcast_to(err, out.shape), q.dtype)
+    # and the climbing tokens alone: the newest that a row sees
+    if size > 0:
+        lv2 = lv.clone()
+        lv2[:3] = lv[3]
+        c.append(rows(lv2[:, None].expand(S, D)), rows(V), table, i32([S]), offsets([S]))
+        out = c.attend(q, table, i32([S]), offsets([n]), max_new=n, scale=scale)
+        want = np.repeat(V[S - n:].double().numpy()[:, None], H_q, 1)
+        ref.check_attend(out, want, 4 * 2.0 ** -11 * np.abs(want), q.dtype)
