@@ -109,17 +109,19 @@ __device__ __forceinline__ uint8_t *find_block(const PagedArgs &a, int b, int po
 
 // A bf16 query row enters the products as fp16, times the power of two that
 // brings its largest magnitude (`top`, the bits of an fp32) near 2^14; `back`
-// is the inverse.  Both are normal numbers for every top, infinity and NaN
-// among them.
+// is the scores' factor for it.  Both are normal numbers for every top,
+// infinity and NaN among them, and every scale: a factor of 0 or infinity would
+// make masked scores (-infinity), or scores of 0, NaN.
 struct RowScale {
   float up, back;
 };
 
-__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+__device__ __forceinline__ RowScale row_scale(uint32_t top, float scale) {
   int f = top ? 14 - ((int)(top >> 23) - 127) : 0;     // -114 ... 141
   f = f > 126 ? 126 : f;
+  const float back = scale * __uint_as_float((uint32_t)(127 - f) << 23);
   return RowScale{__uint_as_float((uint32_t)(127 + f) << 23),
-                  __uint_as_float((uint32_t)(127 - f) << 23)};
+                  fminf(fmaxf(back, 1.17549435e-38f), 3.40282347e+38f)};
 }
 
 // Far maxima.  A weight is 2^(score - maximum + top), a few bits above 1 for

@@ -287,6 +287,9 @@ int vq_kivi_paged_attend(const vq_kivi_paged *p, const vq_kivi_paged_batch *batc
   if (!batch->cu_new && max_new != 1)
     return fail(VQ_ERR_ARG, "without cu_new max_new is 1, got %d", max_new);
   if (!std::isfinite(softmax_scale)) return fail(VQ_ERR_ARG, "softmax_scale is not finite");
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p->D);
+  const float scale2 = scale * 1.4426950408889634f;      // base 2
+  if (!std::isfinite(scale2)) return fail(VQ_ERR_ARG, "softmax_scale=%g is too large", scale);
   if (a.tokens == 0 || a.B == 0) return VQ_OK;
   if (overlap(h, a.tokens, p->D, elem))
     return fail(VQ_ERR_ARG, "the output overlaps the queries");
@@ -302,8 +305,7 @@ int vq_kivi_paged_attend(const vq_kivi_paged *p, const vq_kivi_paged_batch *batc
   t.out = h.out;
   t.q_token = h.x_token;
   t.q_head = h.x_head;
-  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p->D);
-  t.scale = scale * 1.4426950408889634f;
+  t.scale = scale2;
   t.max_new = max_new;
   t.ws = static_cast<float *>(workspace);
   cudaError_t e = few ? launch_paged_decode(dtype, a, t, p->D, sms, (cudaStream_t)stream)

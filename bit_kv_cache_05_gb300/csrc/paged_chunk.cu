@@ -527,9 +527,9 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           for (int e = 0; e < 4; ++e)
             m = max(m, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
         }
-        const RowScale rs = row_scale(m);
+        const RowScale rs = row_scale(m, t.scale);
         up = rs.up;
-        sl2 *= rs.back;
+        sl2 = rs.back;
       }
       unsigned char *dst = sm + SM::Q + wg * SM::OP;
       __half2 size[2] = {bits_h2(0u), bits_h2(0u)};    // sum |q| / 256

@@ -374,9 +374,9 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
         }
         mq = fmaxf(mq, __shfl_xor_sync(kFull, mq, 1));
         mq = fmaxf(mq, __shfl_xor_sync(kFull, mq, 2));
-        const RowScale rs = row_scale(__float_as_uint(mq));
+        const RowScale rs = row_scale(__float_as_uint(mq), t.scale);
         const float up = rs.up;
-        sl2 *= rs.back;
+        sl2 = rs.back;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
           uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};

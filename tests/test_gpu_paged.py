@@ -710,3 +710,21 @@ def test_finite_rows_of_any_size_give_finite_outputs(dtype, size, step, H_q, H_k
         out = c.attend(q, table, i32([S]), offsets([n]), max_new=n, scale=scale)
         want = np.repeat(V[S - n:].double().numpy()[:, None], H_q, 1)
         ref.check_attend(out, want, 4 * 2.0 ** -11 * np.abs(want), q.dtype)
+
+
+@pytest.mark.parametrize("size,scale", [(2.0 ** -125, 1e-10), (2.0 ** -130, 1e-3), (1.0, 1e-42),
+                                        (2.0 ** 100, 1e20)])
+@pytest.mark.parametrize("H_q,H_kv,n", [(4, 2, 1), (8, 2, 4), (2, 2, 40)])
+def test_factors_at_the_ends_of_fp32(size, scale, H_q, H_kv, n):
+    """Tiny rows under a tiny scale, whose factors multiply to less than fp32
+    holds, and large ones whose factors pass it, over keys of 0: every seen
+    token weighs the same, masked ones (lengths inside a block) nothing."""
+    c, table, L = filled([45], 16, H_q, H_kv, 64, 32, gain=0.0 if size > 2 else 1.0)
+    q = torch.full((n, H_q, 64), size, dtype=torch.bfloat16, device="cuda")
+    out = c.attend(q, table, L, offsets([n]), max_new=n, scale=scale)
+    c.status()
+    V = c.dequantize(table, L, offsets([45]), n_tokens=45)[1].double().cpu()
+    for i in range(n):
+        v = V[:45 - n + i + 1].repeat_interleave(H_q // H_kv, 1)
+        ref.check_attend(out[i], v.mean(0).numpy(),
+                         (4 * 2.0 ** -11 * v.abs().mean(0)).numpy(), q.dtype)

@@ -318,3 +318,9 @@ def test_a_warp_that_gives_up_waits_for_its_copies(tmp_path):
     subprocess.run([cxx, "-std=c++17", "-O1", "-I", inc, str(src), "-o", str(tmp_path / "ring")],
                    check=True)
     assert subprocess.run([str(tmp_path / "ring")]).returncode == 0
+
+
+def test_attend_scale_beyond_fp32_in_base_two(vqlib):
+    args = (_paged(), _batch(), 0, _rows(8), 1)
+    assert vqlib.vq_kivi_paged_attend(*args, 3e38, 1 << 20, 1 << 30, None) == -1
+    assert b"softmax_scale" in vqlib.vq_kivi_last_error()
