@@ -160,6 +160,10 @@ int check_batch(const vq_kivi_paged *p, const vq_kivi_paged_batch *s, PagedArgs 
   return VQ_OK;
 }
 
+// Only the bits that were read: kernels of other streams may set others
+// meanwhile.  (A bit that one sets again before this is among those reported.)
+__global__ void k_clear_bits(unsigned *status, unsigned bits) { atomicAnd(status, ~bits); }
+
 // whether contiguous rows `out` lie within the range that rows `x` span: tiles
 // of queries are read while others' outputs are written
 bool overlap(const HeadRows &h, int64_t tokens, int D, int elem) {
@@ -321,18 +325,21 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaMemcpyAsync(&flags, p->status, sizeof flags, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess && flags) e = cudaMemsetAsync(p->status, 0, sizeof flags, st);
+  if (e == cudaSuccess && flags) {
+    k_clear_bits<<<1, 1, 0, st>>>(static_cast<unsigned *>(p->status), flags);
+    count_launch();
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
-  if (flags & kGaveUp)
-    return fail(VQ_ERR_CUDA, "an attention kernel gave up waiting for its copies; its outputs "
-                "are not valid");
-  if (flags & kBadPage)
-    return fail(VQ_ERR_ARG, "a block table names a page outside the pool: its tokens were not "
-                "stored, and rows that see it are not valid");
-  if (flags & kBadLength)
-    return fail(VQ_ERR_ARG, "a sequence's length or its new tokens lie outside their ranges; "
-                "the sequence was left out");
-  return VQ_OK;
+  if (!flags) return VQ_OK;
+  return fail(flags & kGaveUp ? VQ_ERR_CUDA : VQ_ERR_ARG, "%s%s%s",
+              flags & kGaveUp ? "an attention kernel gave up waiting for its copies; its outputs "
+                                "are not valid. " : "",
+              flags & kBadPage ? "a block table names a page outside the pool: its tokens were "
+                                 "not stored, and rows that see it are not valid. " : "",
+              flags & kBadLength ? "a sequence's length or its new tokens lie outside their "
+                                   "ranges; the sequence was left out." : "");
 }
 
 }  // extern "C"

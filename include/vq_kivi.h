@@ -563,7 +563,9 @@ int vq_kivi_paged_dequantize(const vq_kivi_paged *p,
 
 /* Synchronizes `stream` and reports what kernels found since the last check:
  * VQ_ERR_ARG for a page or a length outside its range, VQ_ERR_CUDA for a wait
- * that gave up (the word is then cleared). */
+ * that gave up; the message names all that was found.  What is reported is
+ * then cleared from the word, and nothing else: what a kernel of another
+ * stream finds meanwhile is left for the next check. */
 int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
 
 #ifdef __cplusplus

@@ -728,3 +728,35 @@ def test_factors_at_the_ends_of_fp32(size, scale, H_q, H_kv, n):
         v = V[:45 - n + i + 1].repeat_interleave(H_q // H_kv, 1)
         ref.check_attend(out[i], v.mean(0).numpy(),
                          (4 * 2.0 ** -11 * v.abs().mean(0)).numpy(), q.dtype)
+
+
+def test_status_keeps_what_another_stream_finds_meanwhile():
+    """A fault set by a kernel of another stream at any moment around a check
+    that has another fault to report is reported by this check or the next."""
+    from bit_kv_cache_05_gb300 import _lib
+    c = new_cache(2, 16, 1, 1, 64, 32)
+    k = randn(1, 1, 1, 64).half()
+    far, here = i32([7]).view(1, 1), i32([0]).view(1, 1)
+    one, long = i32([1]), i32([17])
+    other = torch.cuda.Stream()
+    c.append(k, k, here, one, stream=other)
+    torch.cuda.synchronize()
+
+    def found():
+        try:
+            c.status()
+        except _lib.VqError as e:
+            return str(e)
+        return ""
+
+    for i in range(600):
+        c.append(k, k, far, one)                      # a page outside the pool
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(400 * i)                # up to about 120 us
+            c.append(k, k, here, long)                # a length outside its range
+        first = found()
+        assert "page" in first
+        torch.cuda.synchronize()
+        assert "length" in first + found()
+        assert found() == ""
