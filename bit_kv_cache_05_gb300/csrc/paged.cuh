@@ -64,33 +64,64 @@ struct PagedArgs {
   int H_q, H_kv, g;
 };
 
+// What a call says of sequence b: tokens, new tokens, row of the first new one.
+struct Seq {
+  int len, n, first;
+};
+
+// One whose lengths lie outside their ranges counts as empty (and sets the
+// status bit).  max_new: no sequence has more new tokens.
+__device__ __forceinline__ Seq sequence_of(const PagedArgs &a, int b, int max_new) {
+  Seq s{a.lens[b], 1, b};
+  if (a.cu) {
+    s.first = a.cu[b];
+    s.n = a.cu[b + 1] - s.first;
+  }
+  if (s.len < 0 || s.len > ((int64_t)a.max_pages << a.page_log2) || s.n < 0 || s.n > max_new ||
+      s.first < 0 || (int64_t)s.first + s.n > a.tokens) {
+    atomicOr(a.status, kBadLength);
+    s.len = s.n = 0;
+  }
+  return s;
+}
+
 // sequence of new token i and its place in the sequence (-1: not in the
 // cache): the new tokens of a sequence are its last ones
 struct Place {
   int b, pos;
 };
 
-__device__ __forceinline__ Place find_place(const PagedArgs &a, int64_t i) {
-  if (!a.cu) {
-    const int len = a.lens[i];
-    if (len < 0 || len > ((int64_t)a.max_pages << a.page_log2)) {
-      atomicOr(a.status, kBadLength);
-      return Place{(int)i, -1};
+// As sequence_of, ranges are checked.  Sequences that no token leads to are
+// looked at as well, so that every operator reports the same of a batch: by
+// warps beyond those of the tokens, a lane a sequence (`look`, else -1), which
+// get no place.  (Looking in a branch of its own made the append of four
+// ragged chunks 71 us instead of 69.)
+__device__ __forceinline__ Place find_place(const PagedArgs &a, int64_t i, int64_t look) {
+  int lo = (int)i, end = (int)i + 1;
+  bool in = true;
+  if (look >= 0 && (!a.cu || look >= a.B)) return Place{-1, -1};
+  if (a.cu) {
+    int hi = a.B;
+    lo = 0;
+    if (look >= 0) {
+      lo = (int)look;
+      hi = lo + 1;
+    } else if (i < a.cu[0] || i >= a.cu[a.B]) {
+      return Place{-1, -1};
     }
-    return Place{(int)i, len - 1};
-  }
-  if (i < a.cu[0] || i >= a.cu[a.B]) return Place{-1, -1};
-  int lo = 0, hi = a.B;   // cu[lo] <= i < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= i) lo = mid; else hi = mid;
+    while (hi - lo > 1) {   // cu[lo] <= i < cu[hi]
+      const int mid = (lo + hi) >> 1;
+      if (a.cu[mid] <= i) lo = mid; else hi = mid;
+    }
+    end = a.cu[hi];
+    in = a.cu[lo] >= 0 && end >= a.cu[lo] && end <= a.tokens;
   }
   const int len = a.lens[lo];
-  if (len < 0 || len > ((int64_t)a.max_pages << a.page_log2)) {
+  if (!in || len < 0 || len > ((int64_t)a.max_pages << a.page_log2)) {
     atomicOr(a.status, kBadLength);
     return Place{lo, -1};
   }
-  const int pos = len - (a.cu[hi] - (int)i);
+  const int pos = look >= 0 ? -1 : len - (end - (int)i);
   return Place{lo, pos < 0 ? -1 : pos};
 }
 

@@ -168,7 +168,6 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
   const int64_t t = w / parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (t >= a.tokens) return;
   int p0, p1;
   chunk_places(r, l, p0, p1);
   const int gq = (q.heads + RPW - 1) / RPW, gk = (a.H_kv + RPW - 1) / RPW;
@@ -177,7 +176,7 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
     const bool isk = gi >= gq;
     const HeadRows &h = isk ? k : q;
     const int row = (isk ? gi - gq : gi) * RPW + sub;
-    if (gi < gq + gk && row < h.heads) {
+    if (t < a.tokens && gi < gq + gk && row < h.heads) {
       const T *x = static_cast<const T *>(h.x) + t * h.x_token + row * h.x_head;
       load8<T>(x + p0, xa);
       load8<T>(x + p1, xb);
@@ -190,7 +189,7 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
   };
   int gi = (int)(w % parts);
   fetch(gi);
-  const Place at = find_place(a, t);
+  const Place at = find_place(a, t, t < a.tokens ? -1 : 32 * (w - a.tokens * parts) + lane);
   if (at.pos < 0) return;
   // the token's page, looked up while the rows arrive
   const bool stores = gi + (gq + gk - 1 - gi) / parts * parts >= gq;
@@ -285,8 +284,7 @@ k_paged_dequantize(PagedArgs a, __half *K, __half *V, int parts) {
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (t >= a.tokens) return;
-  const Place at = find_place(a, t);
+  const Place at = find_place(a, t, t < a.tokens ? -1 : 32 * (w - a.tokens * parts) + lane);
   if (at.pos < 0) return;
   const int tl = at.pos & 15;
   for (int row = (int)(w % parts) * RPW + sub; row < a.H_kv; row += parts * RPW) {
@@ -334,6 +332,11 @@ int parts_for(int64_t tokens, int groups, int sm_count) {
   return (int)(p < 1 ? 1 : (p > groups ? groups : p));
 }
 
+// those and the ones that only look at sequences (find_place)
+int64_t warps_for(const PagedArgs &a, int parts) {
+  return a.tokens * parts + (a.cu ? (a.B + 31) / 32 : 0);
+}
+
 template <typename T, int D>
 cudaError_t launch_append(const PagedArgs &a, const HeadRows &q, const HeadRows &k,
                           const HeadRows &v, const RopeArgs &r, bool by_place, float eps,
@@ -343,7 +346,7 @@ cudaError_t launch_append(const PagedArgs &a, const HeadRows &q, const HeadRows 
   const int parts = parts_for(a.tokens, groups, sm_count);
   const int64_t wpc = kThreads / 32;
   cudaError_t e = launch_pdl(k_paged_append<T, D>,
-                             dim3((unsigned)((a.tokens * parts + wpc - 1) / wpc)),
+                             dim3((unsigned)((warps_for(a, parts) + wpc - 1) / wpc)),
                              dim3(kThreads), 0, st, a, q, k, v, r, by_place, eps, parts);
   count_launch();
   return e;
@@ -367,7 +370,7 @@ cudaError_t launch_paged_dequantize(const PagedArgs &a, __half *K, __half *V, in
                                     int sm_count, cudaStream_t st) {
   const int rpw = 512 / D, parts = parts_for(a.tokens, (a.H_kv + rpw - 1) / rpw, sm_count);
   const int64_t wpc = kThreads / 32;
-  const dim3 grid((unsigned)((a.tokens * parts + wpc - 1) / wpc));
+  const dim3 grid((unsigned)((warps_for(a, parts) + wpc - 1) / wpc));
   cudaError_t e = D == 64 ? launch_pdl(k_paged_dequantize<64>, grid, dim3(kThreads), 0, st, a,
                                        K, V, parts)
                           : launch_pdl(k_paged_dequantize<128>, grid, dim3(kThreads), 0, st, a,

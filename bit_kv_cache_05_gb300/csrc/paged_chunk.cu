@@ -272,24 +272,6 @@ __device__ __forceinline__ void tm_wait_st() {
 
 // ---- the work line -------------------------------------------------------------
 
-struct Seq {
-  int len, n, first;   // tokens, new tokens, row of the first new token
-};
-
-__device__ __forceinline__ Seq seq_of(const PagedArgs &a, int b, int max_new) {
-  Seq s{a.lens[b], 1, b};
-  if (a.cu) {
-    s.first = a.cu[b];
-    s.n = a.cu[b + 1] - s.first;
-  }
-  if (s.len < 0 || s.len > ((int64_t)a.max_pages << a.page_log2) || s.n < 0 || s.n > max_new ||
-      s.first < 0 || (int64_t)s.first + s.n > a.tokens) {
-    atomicOr(a.status, kBadLength);
-    s.len = s.n = 0;
-  }
-  return s;
-}
-
 __device__ __forceinline__ int pairs_of(const Seq &s, int tpt) {
   return (s.n + 2 * tpt - 1) / (2 * tpt);
 }
@@ -305,7 +287,7 @@ __device__ __forceinline__ int tiles_of(const Seq &s, int p, int tpt) {
 __device__ void tile_prefix(const PagedArgs &a, int max_new, int tpt, long long *prefix) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   for (int b = warp; b < a.B; b += nw) {
-    const Seq s = seq_of(a, b, max_new);
+    const Seq s = sequence_of(a, b, max_new);
     const int np = pairs_of(s, tpt);
     long long sum = 0;
     for (int p = lane; p < np; p += 32) sum += tiles_of(s, p, tpt);
@@ -364,7 +346,7 @@ struct Walk {
       if (prefix[mid] <= u) lo = mid; else hi = mid;
     }
     b = lo;
-    s = seq_of(a, b, max_new);
+    s = sequence_of(a, b, max_new);
     const long long per = (prefix[b + 1] - prefix[b]) / a.H_kv;
     long long v = u - prefix[b];
     h = (int)(v / per);
@@ -386,7 +368,7 @@ struct Walk {
       if (++h == a.H_kv) {
         h = 0;
         do { ++b; } while (prefix[b + 1] == prefix[b]);
-        s = seq_of(a, b, max_new);
+        s = sequence_of(a, b, max_new);
       }
     }
     return true;

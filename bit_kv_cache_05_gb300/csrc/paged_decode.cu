@@ -108,27 +108,7 @@ __device__ __forceinline__ void word_values(uint32_t w, __half2 s, __half2 z, ui
   }
 }
 
-// A sequence's lengths; faulty ones count as empty.
-struct Lengths {
-  int len, n;   // tokens, new tokens (rows)
-};
-
-__device__ __forceinline__ Lengths lengths_of(const PagedArgs &a, int b, int max_new) {
-  Lengths r{a.lens[b], 1};
-  int first = b;
-  if (a.cu) {
-    first = a.cu[b];
-    r.n = a.cu[b + 1] - first;
-  }
-  if (r.len < 0 || r.len > ((int64_t)a.max_pages << a.page_log2) || r.n < 0 || r.n > max_new ||
-      first < 0 || (int64_t)first + r.n > a.tokens) {
-    atomicOr(a.status, kBadLength);
-    r.len = r.n = 0;
-  }
-  return r;
-}
-
-__device__ __forceinline__ int steps_of(const Lengths &r) {
+__device__ __forceinline__ int steps_of(const Seq &r) {
   return r.n > 0 ? (r.len + kStep - 1) / kStep : 0;
 }
 
@@ -139,7 +119,7 @@ __device__ void step_prefix(const PagedArgs &a, int max_new, int *prefix, int *w
   int sum = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < a.B) sum += steps_of(lengths_of(a, b, max_new)) * a.H_kv;
+    if (b < a.B) sum += steps_of(sequence_of(a, b, max_new)) * a.H_kv;
   }
   int inc = sum;
 #pragma unroll
@@ -155,7 +135,7 @@ __device__ void step_prefix(const PagedArgs &a, int max_new, int *prefix, int *w
     const int b = tid * per + i;
     if (b < a.B) {
       prefix[b] = base;
-      base += steps_of(lengths_of(a, b, max_new)) * a.H_kv;
+      base += steps_of(sequence_of(a, b, max_new)) * a.H_kv;
       if (b == a.B - 1) prefix[a.B] = base;
     }
   }
@@ -338,8 +318,8 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
     // one (sequence, kv head)
     int nb, h, k;
     enter(b, u, nb, h, k);
-    const Lengths L = lengths_of(a, b, t.max_new);
-    const int row0 = a.cu ? a.cu[b] : b, rows = L.n * GQ;
+    const Seq L = sequence_of(a, b, t.max_new);
+    const int row0 = L.first, rows = L.n * GQ;
     const int all_see = L.len - L.n;      // tokens up to here are seen by all rows
     // of rows 8 g + 2 t4 and the next: the newest tokens they see (rows
     // without a query: none), the scores' factors, maxima and sums
@@ -641,10 +621,10 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix) {
   const int H = a.H_kv, GQ = a.H_q / H, R = t.max_new * GQ;
   const int row = blockIdx.x % R, seg = blockIdx.x / R, b = seg / H, h = seg % H;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Lengths L = lengths_of(a, b, t.max_new);
+  const Seq L = sequence_of(a, b, t.max_new);
   const int units = prefix[a.B], p0 = prefix[b], nb = (prefix[b + 1] - p0) / H;
   if (row >= L.n * GQ) return;
-  const int64_t tokrow = (a.cu ? a.cu[b] : b) + row / GQ;
+  const int64_t tokrow = L.first + row / GQ;
   T *out = static_cast<T *>(t.out) + (tokrow * a.H_q + h * GQ + row % GQ) * D;
   float acc[CPL];
 #pragma unroll

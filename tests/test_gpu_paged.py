@@ -760,3 +760,58 @@ def test_status_keeps_what_another_stream_finds_meanwhile():
         torch.cuda.synchronize()
         assert "length" in first + found()
         assert found() == ""
+
+
+@pytest.mark.parametrize("cu,lens,left", [
+    ([0, 3, 5, 11], [3, 20, 30], [2]),            # more new tokens than rows
+    ([0, 3, 1, 9], [3, 20, 30], [1]),             # falling
+    ([-2, 3, 5, 9], [30, 20, 30], [0]),           # a row before the first
+    ([0, 3, 3, 9], [3, 999, 30], [1]),            # too long, nothing new
+    ([0, 3, 3, 9], [3, -1, 30], [1]),
+    ([0, 3, 5, 9], [3, 999, 30], [1]),
+])
+def test_all_operators_leave_out_and_report_the_same_sequences(cu, lens, left):
+    """A sequence whose length or new tokens lie outside their ranges: append,
+    read-back and attention each report it, leave its pages and rows as they
+    were and serve the others."""
+    from bit_kv_cache_05_gb300 import _lib
+    H, D, T = 2, 64, 9
+    k, v, q = (randn(i, T, H, D).half() for i in (1, 2, 3))
+    table = i32([0, 1, 2, 3, 4, 5]).view(3, 2)
+    c = new_cache(6, 16, H, H, D, 32)
+    good = [b for b in range(3) if b not in left and cu[b + 1] > cu[b]]
+
+    def faulty(f):
+        r = f()
+        with pytest.raises(_lib.VqError, match="length"):
+            c.status()
+        c.status()
+        return r
+
+    qo = torch.full_like(q, 7.0)
+    faulty(lambda: c.append(k, v, table, i32(lens), i32(cu), q=q, q_out=qo))
+    out = (torch.full_like(k, 7.0), torch.full_like(v, 7.0))
+    faulty(lambda: c.dequantize(table, i32(lens), i32(cu), n_tokens=T, out=out))
+    n = [cu[b + 1] - cu[b] for b in range(3)]
+    for b in left:
+        assert (c.pool[table[b].long()] == 0xff).all()
+    mine = torch.zeros(T, dtype=torch.bool)
+    want = new_cache(6, 16, H, H, D, 32)
+    for b in good:
+        r = slice(cu[b], cu[b + 1])
+        mine[r] = True
+        want.append(k[r], v[r], table[b:b + 1], i32([lens[b]]), offsets([n[b]]))
+        K, V = want.dequantize(table[b:b + 1], i32([lens[b]]), offsets([n[b]]), n_tokens=n[b])
+        if cu != [0, 3, 1, 9]:                    # there rows belong to two sequences
+            assert torch.equal(c.pool[table[b].long()], want.pool[table[b].long()])
+            assert torch.equal(qo[r], q[r])
+            assert torch.equal(out[0][r].view(torch.int16), K.view(torch.int16))
+            assert torch.equal(out[1][r].view(torch.int16), V.view(torch.int16))
+    assert (qo[~mine] == 7).all() and (out[0][~mine] == 7).all() and (out[1][~mine] == 7).all()
+    # whole caches for the attention
+    c.pool.fill_(0)
+    for max_new in (4, 20):
+        o = torch.full_like(q, 7.0)
+        faulty(lambda: c.attend(q, table, i32(lens), i32(cu),
+                                max_new=max(max_new, max(n)), out=o))
+        assert (o[~mine] == 7).all() and (o[mine] == 0).all()
