@@ -80,7 +80,8 @@ int check_rope(const vq_kivi_rope *p, int D, int64_t tokens, const void *positio
     if (!positions && !places && tokens > 0) return fail(VQ_ERR_ARG, "positions is NULL");
     if (positions && !aligned(positions, pos_64 ? 8 : 4))
       return fail(VQ_ERR_ARG, "positions are misaligned");
-    if (positions && p->n_axes > 1 && pos_stride < tokens)
+    // stride 0: the same positions on every axis
+    if (positions && p->n_axes > 1 && pos_stride != 0 && pos_stride < tokens)
       return fail(VQ_ERR_ARG, "pos_stride=%lld < %lld tokens", (long long)pos_stride,
                   (long long)tokens);
   }

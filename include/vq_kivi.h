@@ -439,7 +439,8 @@ typedef struct vq_kivi_rows {
  *   k          NULL for queries alone
  *   rope       NULL for the norms alone (positions are then not read)
  *   positions  device int32 (positions_64 = 0) or int64 [n_axes][tokens],
- *              positions_stride elements between axes; any sign
+ *              positions_stride elements between axes (0: the same positions
+ *              on every axis); any sign
  * out may be x itself with the same strides; other overlaps are not
  * allowed. */
 int vq_kivi_norm_rope(int dtype, int64_t tokens, int D, const vq_kivi_rows *q,

@@ -815,3 +815,30 @@ def test_all_operators_leave_out_and_report_the_same_sequences(cu, lens, left):
         faulty(lambda: c.attend(q, table, i32(lens), i32(cu),
                                 max_new=max(max_new, max(n)), out=o))
         assert (o[~mine] == 7).all() and (o[mine] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.int64, torch.int32])
+def test_positions_broadcast_over_the_axes(dtype):
+    """One row of positions for all axes, as text has them: expanded, not
+    copied."""
+    from bit_kv_cache_05_gb300.rope import Rope, norm_rope
+    T, H, D = 37, 2, 64
+    rope = Rope(rot_dim=D, sections=[8, 12, 12])
+    q, k, v = (randn(i, T, H, D).half() for i in (1, 2, 3))
+    pos = torch.randint(0, 100000, (T,), generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    many = pos[None].expand(3, -1)
+    assert many.stride(0) == 0
+    a, b = norm_rope(q, k, many, rope), norm_rope(q, k, many.contiguous(), rope)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    inv = [1e4 ** (-2.0 * j / D) for j in range(D // 2)]
+    want, mag = ref.norm_rope64(q, None, many, inv, [0] * 8 + [1] * 12 + [2] * 12, False)
+    assert ((a[0].cpu().double() - want).abs()
+            <= ref.norm_rope_bound(want, mag, torch.float16, D)).all()
+    pools = []
+    for p in (many, many.contiguous()):
+        c = new_cache(3, 16, H, H, D, 32)
+        out = c.append(k, v, i32([0, 1, 2]).view(1, 3), i32([T]), offsets([T]), q=q, rope=rope,
+                       positions=p)
+        assert torch.equal(out, a[0])
+        pools.append(c.pool)
+    assert torch.equal(pools[0], pools[1])
