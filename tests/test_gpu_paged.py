@@ -842,3 +842,37 @@ def test_positions_broadcast_over_the_axes(dtype):
         assert torch.equal(out, a[0])
         pools.append(c.pool)
     assert torch.equal(pools[0], pools[1])
+
+
+def test_readme_sample():
+    """The README's paged sample as it stands: a prompt chunk, then one token
+    more per sequence, which must see the whole prompt."""
+    import os
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    code = [b.split("```")[0] for b in text.split("```python")[1:] if "PagedKiviCache(" in b]
+    assert len(code) == 1
+    n, B, H_q, H_kv, D, dt = [300, 128], 2, 32, 8, 128, torch.bfloat16
+    T = sum(n)
+    x = randn(1, T + B, H_q + 2 * H_kv, D).to(dt)
+    w = (1 + 0.1 * randn(2, D)).to(dt)
+    part = lambda r: (x[r, :H_q], x[r, H_q:H_q + H_kv], x[r, H_q + H_kv:])
+    q, k, v = part(slice(0, T))
+    q1, k1, v1 = part(slice(T, T + B))
+    env = dict(q=q, k=k, v=v, q1=q1, k1=k1, v1=v1, wk=w, wq=w, lens=i32(n), cu_new=offsets(n),
+               table=ref.make_table(B, [a + 1 for a in n], 64, 1024, "cuda", 3),
+               positions=torch.arange(T, device="cuda"))
+    exec(code[0], env)
+    c, table = env["cache"], env["table"]
+    lens = i32([a + 1 for a in n])
+    assert torch.equal(env["lens"], lens)
+    want, err = ref.attend64(env["q1"], c.pool, table, lens, None, D, 32, H_kv, weight_step=FEW)
+    ref.check_attend(env["out1"], want, err, dt)
+    # the prompt's tokens and the new ones as they would be stored at once
+    from bit_kv_cache_05_gb300.rope import Rope
+    one = new_cache(1024, 64, H_q, H_kv, D, 32)
+    order = list(range(300)) + [T] + list(range(300, T)) + [T + 1]
+    one.append(x[order, H_q:H_q + H_kv], x[order, H_q + H_kv:], table, lens, offsets([301, 129]),
+               rope=Rope(rot_dim=128, theta=5e5), k_weight=w)
+    a = c.dequantize(table, lens, offsets([301, 129]), n_tokens=T + B)
+    b = one.dequantize(table, lens, offsets([301, 129]), n_tokens=T + B)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
