@@ -20,6 +20,12 @@ from .rope import DTYPES, Rope, _current_device, _on, _positions, _raw_stream, _
 class PagedKiviCache:
     """A pool of `n_pages` pages of `page` tokens in 4 bits.
 
+    Keys and values are quantized per token, over `group` neighbouring
+    channels, so that a token is complete when it is appended and a page
+    stands by itself.  (``KiviCache`` quantizes keys per channel, over groups
+    of tokens.)  A key channel that stands out therefore widens the code steps
+    of its whole group: a smaller group keeps them to fewer channels.
+
     pool: an existing uint8 CUDA tensor of [n_pages][H_kv][page/16][block]
     (see `block_bytes`), else one is allocated (zeroed) on `device`.
 
