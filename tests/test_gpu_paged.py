@@ -876,3 +876,142 @@ def test_readme_sample():
     a = c.dequantize(table, lens, offsets([301, 129]), n_tokens=T + B)
     b = one.dequantize(table, lens, offsets([301, 129]), n_tokens=T + B)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# decode (one row, few rows, drafts), chunks of one query tile and of two,
+# mixed: heads, D, group, page, new tokens of a sequence
+LONG = [
+    (32, 8, 128, 32, 64, (1, 1)), (8, 8, 64, 64, 16, (1, 1)), (12, 4, 128, 64, 32, (1, 2)),
+    (32, 8, 128, 128, 128, (2, 4)), (16, 8, 64, 32, 16, (1, 8)),
+    (16, 4, 128, 64, 64, (17, 32)), (8, 4, 64, 32, 16, (20, 64)), (20, 4, 128, 32, 32, (4, 25)),
+    (8, 4, 128, 32, 64, (100, 300)), (16, 4, 64, 64, 32, (1, 150)),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("H_q,H_kv,D,g,page,new", LONG)
+def test_long_walks(dtype, H_q, H_kv, D, g, page, new):
+    """More work than resident warps and CTAs: 40 steps a warp, 10 key tiles a
+    CTA at least, so that every stage and barrier phase is used many times and
+    pieces of the work line end inside sequences and span whole ones.  The
+    sequences (empty and short ones among them) share a pool's pages in orders
+    of their own; keys grow with the page, so that maxima rise late, early or
+    at random."""
+    gen = torch.Generator().manual_seed(7)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    few = new[1] * (H_q // H_kv) <= 16
+    S = 8192
+    n_pages = S // page
+    c = new_cache(n_pages + 1, page, H_q, H_kv, D, g)
+    gain = (0.2 + 2.0 * torch.arange(S) / S).cuda()[:, None, None]
+    whole = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    c.append((randn(1, S, H_kv, D) * gain).half(), randn(2, S, H_kv, D).half(), whole, i32([S]),
+             offsets([S]))
+    # 32-token steps of 16 warps an SM, or 128-token tiles of a CTA an SM
+    need = 40 * 16 * sms * 32 if few else 12 * sms * 128
+    B = min(-(-need // (H_kv * 7000)) + 4, 200)
+    lens = [int(x) for x in torch.randint(6000, S + 1, (B,), generator=gen)]
+    lens[1], lens[B // 2], lens[B - 2] = 0, 1, 33
+    news = [int(x) for x in torch.randint(new[0], new[1] + 1, (B,), generator=gen)]
+    news[B // 3] = news[B // 3] if new == (1, 1) else 0
+    table = torch.stack([torch.arange(n_pages) if b % 3 == 0 else
+                         torch.arange(n_pages).flip(0) if b % 3 == 1 else
+                         torch.randperm(n_pages, generator=gen) for b in range(B)]).int().cuda()
+    T = sum(news)
+    q = (randn(3, T, H_q, D) * 2).to(DT[dtype])
+    cu = None if new == (1, 1) else offsets(news)
+    out = c.attend(q, table, i32(lens), cu, max_new=new[1])
+    c.status()
+    at = np.concatenate([[0], np.cumsum(news)])
+    hi_lo = new[1] * (H_q // H_kv) <= 8
+    for b in sorted({0, 1, 2, B // 3, B // 2, B - 2, B - 1, *range(4, B, max(1, B // 6))}):
+        rows = out[at[b]:at[b + 1]]
+        seen = [lens[b] - news[b] + i + 1 for i in range(news[b])]
+        off = sum(s <= 0 for s in seen)
+        assert (rows[:off] == 0).all()
+        if off == news[b]:
+            continue
+        K, V = c.dequantize(table[b:b + 1], i32(lens[b:b + 1]), offsets([lens[b]]),
+                            n_tokens=lens[b])
+        for h in {0, b % H_kv, H_kv - 1}:
+            for hq in (h * (H_q // H_kv), (h + 1) * (H_q // H_kv) - 1):
+                want, err = ref.attend64_rows(q[at[b] + off:at[b + 1], hq].double(),
+                                              K[:, h].double(), V[:, h].double(), seen[off:],
+                                              D ** -0.5, FEW if hi_lo else MANY,
+                                              FLOOR_FEW if hi_lo else FLOOR_MANY)
+                ref.check_attend(rows[off:, hq], want, err, q.dtype)
+
+
+@pytest.mark.parametrize("dtype,D,g,rot,inter,scale,axes,H_kv", [
+    ("fp16", 128, 32, 128, True, 1.0, 1, 3), ("bf16", 128, 64, 64, False, 1.25, 3, 2),
+    ("fp16", 128, 128, 96, True, 0.75, 2, 1), ("bf16", 64, 32, 64, False, 1.0, 1, 5),
+    ("fp16", 64, 64, 64, True, 1.0, 3, 2), ("bf16", 64, 32, 32, False, 2.0, 1, 8),
+    ("fp16", 64, 64, 16, True, 1.0, 1, 1), ("fp16", 128, 64, 128, False, 1.0, 4, 4),
+])
+def test_append_of_every_rotation(dtype, D, g, rot, inter, scale, axes, H_kv):
+    """Interleaved pairs, a partial rotation, a factor, D = 64 and groups
+    longer than a lane's channels: the stored keys' scales, zeros and codes are
+    those of the 64-bit rotation, up to its roundings."""
+    from bit_kv_cache_05_gb300.rope import Rope
+    dt, n, H_q = DT[dtype], [5, 40, 1], 2 * H_kv
+    T = sum(n)
+    x = (randn(7, T, H_q + 2 * H_kv, D) * 2).to(dt)
+    q, k, v = x[:, :H_q], x[:, H_q:H_q + H_kv], x[:, H_q + H_kv:]
+    w = (1 + 0.1 * randn(9, D)).to(dt)
+    axis = [j % axes for j in range(rot // 2)]
+    inv = [1e4 ** (-2.0 * j / rot) for j in range(rot // 2)]
+    rope = Rope(inv, axis=axis, interleaved=inter, scale=scale)
+    pos = torch.randint(0, 50000, (axes, T), generator=torch.Generator().manual_seed(4))
+    table = ref.make_table(3, n, 16, 8, "cuda", 3)
+    c = new_cache(8, 16, H_q, H_kv, D, g)
+    got = c.append(k, v, table, i32(n), offsets(n), q=q, rope=rope, q_weight=w, k_weight=w,
+                   positions=pos.cuda())
+    c.status()
+    want, mag = ref.norm_rope64(q, w, pos, inv, axis, inter, scale)
+    assert ((got.cpu().double() - want).abs() <= ref.norm_rope_bound(want, mag, dt, D)).all()
+    # the keys: norm and rotation of fp32 rows, rounded to fp16 as the append does
+    want, mag = ref.norm_rope64(k, w, pos, inv, axis, inter, scale)
+    err = ref.norm_rope_bound(want, mag, torch.float32, D)
+    tab, at = table.cpu().numpy(), 0
+    for b, m in enumerate(n):
+        for h in range(H_kv):
+            code, s, z = ref.cache_parts(c.pool, tab[b], m, h, D, g)["k"]
+            for i in range(m):
+                y, e = want[at + i, h].numpy(), err[at + i, h].numpy()
+                lo = y.reshape(-1, g).min(-1).repeat(g)
+                span = y.reshape(-1, g).max(-1).repeat(g) - lo
+                # an fp16 rounding (half a step) of the row's values on top of
+                # their fp32 errors, for the group's ends and the value itself
+                d = (e + 2.0 ** -11 * np.abs(y) + 2.0 ** -25).reshape(-1, g).max(-1).repeat(g)
+                zz, ss = z[i].astype(np.float64), s[i].astype(np.float64)
+                assert (np.abs(zz - lo) <= d).all()
+                assert (np.abs(ss - span / 15) <= 2 * d / 15 + 2.0 ** -11 * (span + 2 * d) / 15
+                        + 2.0 ** -25).all()
+                # the value's place between the ends, in steps of the scale:
+                # half a step, and the errors of both ends
+                step = np.maximum(span / 15, 1e-30)
+                place = (y - lo) / step
+                assert (np.abs(code[i] - place) <= 0.5 + 4 * d / step + 2.0 ** -20).all()
+        at += m
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_one_sequence_of_131089_tokens(n):
+    """A table of 1025 pages, each of the pool's 64 many times."""
+    H_q, H_kv, D, g, page, S = 8, 2, 128, 64, 128, 131072 + 17
+    c = new_cache(64, page, H_q, H_kv, D, g)
+    whole = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    c.append(randn(1, 8192, H_kv, D).half(), randn(2, 8192, H_kv, D).half(), whole, i32([8192]),
+             offsets([8192]))
+    gen = torch.Generator().manual_seed(5)
+    table = torch.randint(0, 64, (1, 1025), generator=gen).int().cuda()
+    q = (randn(3, n, H_q, D) * 2).bfloat16()
+    out = c.attend(q, table, i32([S]), offsets([n]), max_new=n)
+    c.status()
+    K, V = c.dequantize(table, i32([S]), offsets([S]), n_tokens=S)
+    for hq in (0, 3, 4, 7):
+        want, err = ref.attend64_rows(q[:, hq].double(), K[:, hq // 4].double(),
+                                      V[:, hq // 4].double(), range(S - n + 1, S + 1), D ** -0.5,
+                                      FEW if n == 1 else MANY,
+                                      FLOOR_FEW if n == 1 else FLOOR_MANY)
+        ref.check_attend(out[:, hq], want, err, q.dtype)
