@@ -175,7 +175,17 @@ bool overlap(const HeadRows &h, int64_t tokens, int D, int elem) {
   return o < x + hi * elem && x + lo * elem < o + tokens * h.heads * D * elem;
 }
 
-// the split-KV kernel serves up to 16 rows of a kv head
+// The split-KV kernel serves up to 16 rows of a kv head, which is all that its
+// products take; there it is the faster one at both head sizes.  Replayed
+// graphs, 8 kv heads, cold caches, split-KV against tensor-memory kernel, us:
+//   D = 128     1 x 1024     1 x 32768    16 x 8192     64 x 2048
+//   8 rows     15.5 / 23.7   33.9 / 49.3   56.5 / 118   62.6 / 148
+//   16 rows    19.6 / 23.7   35.9 / 51.4   65.7 / 117   75.9 / 150
+//   20, 32        23.7, 25      53, 56      120, 120     151, 153
+//   D = 64
+//   8 rows     15.5 / 19.6   25.8 / 44.1   40.1 / 108   44.2 / 128
+//   16 rows    17.5 / 21.6   29.8 / 44.2   46.2 / 108   56.4 / 128
+//   20, 32        21.6, 22      46, 46      107, 109     128, 129
 bool few_rows(const vq_kivi_paged *p, int max_new) {
   return (int64_t)max_new * (p->H_q / p->H_kv) <= 16;
 }

@@ -38,6 +38,7 @@
 // frees its tensor memory.
 #include "bulk_pipe.cuh"
 #include "paged.cuh"
+#include "paged_words.cuh"
 #include "vqk_internal.cuh"
 
 namespace vqk {
@@ -53,62 +54,13 @@ constexpr int kNear = 64;            // sequences whose prefix fits in shared me
 constexpr int kMinTiles = 2;         // key tiles a CTA takes at least
 constexpr int kSliceRows = 16;       // rows that a CTA of the merge takes, one a warp
 
-__device__ __forceinline__ uint32_t saddr(const void *p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) {
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ __half2 bits_h2(uint32_t u) {
-  return *reinterpret_cast<const __half2 *>(&u);
-}
-
-// (w & mask) | 0x64006400 in one instruction: 0x6400 | c is 1024 + c
-template <uint32_t mask>
-__device__ __forceinline__ __half2 field(uint32_t w) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(mask), "r"(0x64006400u));
-  return bits_h2(d);
-}
-
-// the (scale, zero) words of a token pair, all groups
-template <int NG>
-__device__ __forceinline__ void load_meta(const unsigned char *p, uint2 (&m)[NG]) {
-  if constexpr (NG == 1) {
-    m[0] = *reinterpret_cast<const uint2 *>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NG / 2; ++i) {
-      const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
-      m[2 * i] = make_uint2(x.x, x.y);
-      m[2 * i + 1] = make_uint2(x.z, x.w);
-    }
-  }
-}
-
-template <int I>
-__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[I]) {
-  if constexpr (I == 4) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-  } else {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    w[0] = x.x; w[1] = x.y;
-  }
-}
-
 // ---- barriers ----------------------------------------------------------------
 
 __device__ __forceinline__ void bar_init(uint64_t *b, int count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count));
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t *b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
 }
 // given up by its own limit, or soon after another role has
 __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *dead) {
@@ -186,7 +138,7 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          saddr(bar))
+          smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void fence_before() {
@@ -418,7 +370,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
   using SM = Smem<D, NG>;
   constexpr int I = D / 32, G = D / NG, BLK = SM::BLK;
   extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+  unsigned char *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Bars &B = *reinterpret_cast<Bars *>(sm + SM::BAR);
   static_assert(sizeof(Bars) <= 384, "barriers fit");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -446,7 +398,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-        saddr(&B.tmem)));
+        smem_addr(&B.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
@@ -912,7 +864,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     // ---- the products ----
     {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
-      const uint32_t sb = saddr(sm);
+      const uint32_t sb = smem_addr(sm);
       uint32_t ks = 0, ph_k = 0, vs = 0, ph_v = 0, ph_q = 0, ph_p = 0;   // a bit a slot
       bool ok = true;
       const uint64_t dq = desc128(sb + SM::Q), dk = desc128(sb + SM::K),

@@ -36,6 +36,7 @@
 // D = 128, g = 32).
 #include "bulk_pipe.cuh"
 #include "paged.cuh"
+#include "paged_words.cuh"
 #include "stage_ring.h"
 #include "vqk_internal.cuh"
 
@@ -57,12 +58,6 @@ struct Weights {
 };
 constexpr float kLo = 4096.f;      // the remainders' factor
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -78,21 +73,6 @@ __device__ __forceinline__ uint32_t turn(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) {
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ __half2 bits_h2(uint32_t u) {
-  return *reinterpret_cast<const __half2 *>(&u);
-}
-
-// (w & mask) | 0x64006400 in one instruction: 0x6400 | c is 1024 + c
-template <uint32_t mask>
-__device__ __forceinline__ __half2 field(uint32_t w, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(mask), "r"(magic));
-  return bits_h2(d);
-}
-
 // the four fp16 pairs of a word: nibbles r of its two halves, times s plus z
 __device__ __forceinline__ void word_values(uint32_t w, __half2 s, __half2 z, uint32_t (&v)[4]) {
   const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
@@ -100,8 +80,8 @@ __device__ __forceinline__ void word_values(uint32_t w, __half2 s, __half2 z, ui
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     // 1024 + c and 1024 + 16 c: both steps to c are exact
-    const __half2 c0 = __hsub2(field<0x000f000fu>(w, 0x64006400u), k1024);
-    const __half2 c1 = __hfma2(field<0x00f000f0u>(w, 0x64006400u), k16, k64);
+    const __half2 c0 = __hsub2(field<0x000f000fu>(w), k1024);
+    const __half2 c1 = __hfma2(field<0x00f000f0u>(w), k16, k64);
     v[2 * j] = h2_bits(__hfma2(c0, s, z));
     v[2 * j + 1] = h2_bits(__hfma2(c1, s, z));
     w >>= 8;
@@ -183,32 +163,6 @@ struct DecSmem {
   static constexpr int PREFIX = BAR + kWarps * STAGES * 8;
   static_assert(BLK % 128 == 0, "stages stay 128-byte aligned");
 };
-
-// the (scale, zero) words of a token pair, all groups
-template <int NG>
-__device__ __forceinline__ void load_meta(const unsigned char *p, uint2 (&m)[NG]) {
-  if constexpr (NG == 1) {
-    m[0] = *reinterpret_cast<const uint2 *>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NG / 2; ++i) {
-      const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
-      m[2 * i] = make_uint2(x.x, x.y);
-      m[2 * i + 1] = make_uint2(x.z, x.w);
-    }
-  }
-}
-
-template <int I>
-__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[I]) {
-  if constexpr (I == 4) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-  } else {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    w[0] = x.x; w[1] = x.y;
-  }
-}
 
 // ROWS: 8, or 16 for calls with more rows
 template <typename T, int D, int NG, int ROWS>
