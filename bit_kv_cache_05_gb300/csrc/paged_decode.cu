@@ -396,7 +396,7 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes) {
         // The scaled scores are rounded before a maximum is taken from them,
         // so that a score's distance from it is exact: in one fma with the
         // maximum it would be off by the maximum's own rounding, whole bits
-        // from 2^24 on (the fma takes 77.8 us, this 79.0: 65536 tokens, 32 kv
+        // from 2^24 on (the fma takes 77.7 us, this 78.8: 65536 tokens, 32 kv
         // heads).
         float2 mx[NR];
         bool raise = false;
@@ -578,7 +578,7 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix) {
   const Seq L = sequence_of(a, b, t.max_new);
   const int units = prefix[a.B], p0 = prefix[b], nb = (prefix[b + 1] - p0) / H;
   if (row >= L.n * GQ) return;
-  const int64_t tokrow = L.first + row / GQ;
+  const int64_t tokrow = (a.cu ? a.cu[b] : b) + row / GQ;
   T *out = static_cast<T *>(t.out) + (tokrow * a.H_q + h * GQ + row % GQ) * D;
   float acc[CPL];
 #pragma unroll
