@@ -562,7 +562,8 @@ def _verify_plain(s):
         bad = child & ~good
         if draft is not None:
             c = torch.where(good, 0.0, torch.where(bad, (c + mass).float().double(), c))
-            mass = torch.where(good, 1.0, torch.where(bad, residual().sum(-1) / UNIT, mass))
+            left = residual().sum(-1).double() / UNIT
+            mass = torch.where(good, 1.0, torch.where(bad, left, mass))
         else:
             less = torch.round(w.clamp(max=1.0) * UNIT) / UNIT
             mass = torch.where(good, 1.0, torch.where(bad, (mass - less).clamp(min=0), mass))
