@@ -34,7 +34,11 @@ EXPORTS = ("vq_kivi_quantize", "vq_kivi_quantize_ex", "vq_kivi_append",
            "vq_kivi_debug_fail_chunk", "vq_kivi_norm_rope",
            "vq_kivi_paged_pool_bytes", "vq_kivi_paged_workspace_bytes",
            "vq_kivi_paged_append", "vq_kivi_paged_attend",
-           "vq_kivi_paged_dequantize", "vq_kivi_paged_status")
+           "vq_kivi_paged_dequantize", "vq_kivi_paged_status",
+           "vq_kivi_paged_attend_tree", "vq_kivi_paged_attend_weights",
+           "vq_kivi_paged_weights_workspace_bytes", "vq_kivi_paged_keep",
+           "vq_kivi_paged_evict", "vq_kivi_paged_evict_workspace_bytes",
+           "vq_kivi_verify_drafts")
 
 F16, BF16, F32 = 0, 1, 2
 
@@ -93,6 +97,20 @@ class PagedBatch(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
                 ("lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
                 ("tokens", ctypes.c_int64)]
+
+
+class Weights(ctypes.Structure):
+    _fields_ = [("at", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("capacity", ctypes.c_int64)]
+
+
+class Drafts(ctypes.Structure):
+    _fields_ = [("target", ctypes.c_void_p), ("draft", ctypes.c_void_p),
+                ("target_row", ctypes.c_int64), ("draft_row", ctypes.c_int64),
+                ("token", ctypes.c_void_p), ("parent", ctypes.c_void_p),
+                ("uniforms", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("B", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("token_64", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -157,6 +175,16 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.vq_kivi_paged_attend.argtypes = [PG, PB, cint, RW, i32, f32, P, ctypes.c_size_t, P]
         L.vq_kivi_paged_dequantize.argtypes = [PG, PB, P, P, P]
         L.vq_kivi_paged_status.argtypes = [PG, P]
+        WT, size = ctypes.POINTER(Weights), ctypes.c_size_t
+        L.vq_kivi_paged_attend_tree.argtypes = [PG, PB, cint, RW, P, i32, f32, P, size, P]
+        L.vq_kivi_paged_attend_weights.argtypes = [PG, PB, cint, RW, WT, i32, f32, P, size, P]
+        L.vq_kivi_paged_weights_workspace_bytes.restype = size
+        L.vq_kivi_paged_weights_workspace_bytes.argtypes = [PG, i32, i32, i32]
+        L.vq_kivi_paged_keep.argtypes = [PG, PB, P, P, P, P]
+        L.vq_kivi_paged_evict_workspace_bytes.restype = size
+        L.vq_kivi_paged_evict_workspace_bytes.argtypes = [PG, i32, i32, i32]
+        L.vq_kivi_paged_evict.argtypes = [PG, PB, WT, WT, i32, i32, i32, P, P, size, P]
+        L.vq_kivi_verify_drafts.argtypes = [ctypes.POINTER(Drafts), cint, P, P, P, P]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
         L.vq_kivi_plane_bytes.restype = ctypes.c_size_t

@@ -1,0 +1,278 @@
+// Verification of drafted tokens (vq_kivi_verify_drafts): a walk down each
+// sequence's tree, and a token drawn where the walk ends.
+//
+// With p the target's row of the node that the walk is at and q the draft's, a
+// rejected child leaves the residual max(p - q, 0), normed.  Rejections after
+// the first have the same q, so that the residual of k of them is
+//   w = max(p - c q, 0) / S,   S = sum w,   c' = c + S   (c = 0 and S = 1 first)
+// and nothing of a row is kept between two children: a row is read once per
+// rejection.  Without q the drafted tokens stand for themselves: a rejected one
+// is taken out of p, S falls by what it had.
+//
+// Sums are whole numbers of 2^-44 (each value rounded once; 2^63 of them in a
+// row of 2^19 values of 1), so no order of summation changes a decision or
+// a token; products are taken in 64 bits.
+//
+// Bound: two rows of V values a sequence from HBM, or with few sequences the
+// chain of loads (offsets, tokens, probabilities, row) and barriers.  A cluster
+// takes a sequence; each CTA walks (all of them the same way) and sums its
+// slice of the row, each warp a piece of it that is read with neighbouring
+// lanes on neighbouring values.
+#include "cluster.cuh"
+#include "paged.cuh"
+#include "rope.cuh"
+#include "vqk_internal.cuh"
+
+namespace vqk {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr double kUnit = 17592186044416.0;           // 2^44
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// whole numbers of 2^-44; NaN and what is not positive count as nothing
+__device__ __forceinline__ unsigned long long units_of(float w) {
+  return w > 0.f ? __float2ull_rn(fminf(w, 1.f) * 17592186044416.f) : 0ull;
+}
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+struct VerifySmem {
+  uint64_t totals[2][8];            // of the cluster's CTAs, of the last two sums
+  uint64_t warp[kWarps];            // of this CTA's warps, of the last sum
+  int64_t token[kMaxTree];
+  float p[kMaxTree], q[kMaxTree], u[kMaxTree];
+  int parent[kMaxTree];
+  int gone[kMaxTree];               // without q: the rejected tokens
+  int bad;
+};
+
+template <typename T, bool DRAFT>
+__global__ void __launch_bounds__(kThreads)
+k_verify(Drafts d) {
+  __shared__ VerifySmem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned rank = cluster_rank(), ctas = cluster_ctas();
+  const int b = blockIdx.x / ctas;
+  const T *target = static_cast<const T *>(d.target), *draft = static_cast<const T *>(d.draft);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int start = d.cu[b], n = d.cu[b + 1] - start;
+  const bool lead = rank == 0 && tid == 0;
+  auto put = [&](int64_t after, int count) {
+    d.counts[b] = count;
+    if (d.tokens64) static_cast<int64_t *>(d.after)[b] = after;
+    else static_cast<int32_t *>(d.after)[b] = (int)after;
+  };
+  if (n <= 0 || n > kMaxTree || start < 0 || (int64_t)start + n > d.rows) {
+    if (lead) put(-1, n == 0 ? 0 : -1);
+    return;
+  }
+  // nodes: their tokens, and what their parents' rows say of them
+  if (tid == 0) sm.bad = 0;
+  __syncthreads();
+  if (tid < kMaxTree) {
+    sm.parent[tid] = -1;
+    if (tid < n) {
+      const int64_t x = d.tokens64 ? static_cast<const int64_t *>(d.tokens)[start + tid]
+                                   : static_cast<const int32_t *>(d.tokens)[start + tid];
+      const int parent = d.parents ? d.parents[start + tid] : tid - 1;
+      sm.u[tid] = d.uniforms[start + tid];
+      if (tid > 0) {
+        if (parent < 0 || parent >= tid || x < 0 || x >= d.V) {
+          sm.bad = 1;
+        } else {
+          sm.parent[tid] = parent;
+          sm.token[tid] = x;
+          sm.p[tid] = as_float(target[(int64_t)(start + parent) * d.target_row + x]);
+          if (DRAFT) sm.q[tid] = as_float(draft[(int64_t)(start + parent) * d.draft_row + x]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (sm.bad) {
+    for (int i = tid; rank == 0 && i < n; i += kThreads) d.path[start + i] = -1;
+    if (lead) put(-1, -1);
+    return;
+  }
+  // this warp's piece of a row
+  const int pieces = (int)ctas * kWarps, each = ((d.V + pieces - 1) / pieces + 31) & ~31;
+  const int v0 = min(d.V, ((int)rank * kWarps + warp) * each), v1 = min(d.V, v0 + each);
+  int gone = 0;                     // rejected tokens of the node, without q
+  unsigned sums = 0;                // taken so far
+  // what is left of value v
+  auto left = [&](const T *pr, const T *qr, float c, int v) {
+    const float p = as_float(pr[v]);
+    if (!DRAFT || c == 0.f) return p;
+    return __fmaf_rn(-c, as_float(qr[v]), p);
+  };
+  // the sum of what is left of node `node`'s row; kept per CTA and per warp
+  auto row_sum = [&](int node, float c) {
+    const T *pr = target + (int64_t)(start + node) * d.target_row;
+    const T *qr = DRAFT ? draft + (int64_t)(start + node) * d.draft_row : nullptr;
+    unsigned long long sum = 0ull;
+#pragma unroll 8
+    for (int v = v0 + lane; v < v1; v += 32) sum += units_of(left(pr, qr, c, v));
+    if (!DRAFT)
+      for (int i = lane; i < gone; i += 32) {
+        const int x = sm.gone[i];
+        if (x >= v0 && x < v1) sum -= units_of(as_float(pr[x]));
+      }
+    sum = warp_sum(sum);
+    __syncthreads();                // the last sum's warps have been read
+    if (lane == 0) sm.warp[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned long long all = warp_sum(lane < kWarps ? sm.warp[lane] : 0ull);
+      if (lane < (int)ctas) peer_store(&sm.totals[sums & 1][rank], lane, all);
+    }
+    cluster_sync();
+    unsigned long long total = 0ull;
+    for (unsigned r = 0; r < ctas; ++r) total += sm.totals[sums & 1][r];
+    ++sums;
+    return total;
+  };
+
+  // the walk, by every warp alike
+  int at = 0, count = 1;
+  float c = 0.f;
+  double mass = 1.0;
+  unsigned long long total = 0ull;  // of the node, once it has been summed
+  bool summed = false;
+  if (rank == 0)
+    for (int i = tid; i < n; i += kThreads)
+      if (i > 0) d.path[start + i] = -1;
+  __syncthreads();
+  if (lead) d.path[start] = 0;
+  for (bool down = true; down;) {
+    down = false;
+    unsigned long long kids = (unsigned long long)__ballot_sync(kFull, sm.parent[lane] == at) |
+                              (unsigned long long)__ballot_sync(kFull, sm.parent[lane + 32] == at)
+                                  << 32;
+    while (kids) {
+      const int i = __ffsll((long long)kids) - 1;
+      kids &= kids - 1;
+      const int x = (int)sm.token[i];
+      const double u = sm.u[i];
+      float w = sm.p[i];
+      bool good, taken = false;     // taken: rejected before, as another node
+      if (DRAFT) {
+        if (c != 0.f) w = __fmaf_rn(-c, sm.q[i], w);
+        good = mass > 0.0 && u * (double)sm.q[i] * mass < (double)w;
+      } else {
+        for (int j = lane; j < gone; j += 32) taken = taken || sm.gone[j] == x;
+        taken = __any_sync(kFull, taken);
+        if (taken) w = 0.f;
+        good = mass > 0.0 && u * mass < (double)w;
+      }
+      if (good) {
+        if (lead) d.path[start + count] = i;
+        ++count;
+        at = i;
+        c = 0.f;
+        mass = 1.0;
+        gone = 0;
+        summed = false;
+        down = true;
+        break;
+      }
+      if (DRAFT) {
+        if (mass > 0.0) {
+          c = (float)((double)c + mass);
+          total = row_sum(at, c);
+          mass = (double)total / kUnit;
+          summed = true;
+        }
+      } else if (!taken) {
+        mass = fmax(mass - (double)units_of(w) / kUnit, 0.0);
+        __syncthreads();            // every warp has looked for x
+        if (tid == 0) sm.gone[gone] = x;
+        ++gone;
+        __syncthreads();
+      }
+    }
+  }
+  if (!summed) total = row_sum(at, c);
+  if (total == 0ull && (c != 0.f || gone > 0)) {
+    // nothing left after rounding: from the target's row itself
+    c = 0.f;
+    gone = 0;
+    total = row_sum(at, 0.f);
+  }
+  // r of [0, total): the token is the first whose running sum passes it
+  const float u = sm.u[0];
+  const unsigned long long U = u > 0.f ? (unsigned long long)(fminf(u, 0.99999994f) * 2147483648.f)
+                                       : 0ull;
+  unsigned long long r = (__umul64hi(total, U) << 33) | ((total * U) >> 31);
+  if (total == 0ull) {
+    if (lead) put(-1, count);
+  } else {
+    for (unsigned k = 0; k < rank; ++k) {
+      const unsigned long long x = sm.totals[(sums - 1) & 1][k];
+      r = r < x ? ~0ull : r - x;    // in an earlier CTA's slice: in no warp's here
+      if (r == ~0ull) break;
+    }
+    if (r < sm.totals[(sums - 1) & 1][rank]) {
+      for (int k = 0; k < warp && r != ~0ull; ++k) r = r < sm.warp[k] ? ~0ull : r - sm.warp[k];
+      if (r < sm.warp[warp]) {
+        const T *pr = target + (int64_t)(start + at) * d.target_row;
+        const T *qr = DRAFT ? draft + (int64_t)(start + at) * d.draft_row : nullptr;
+        for (int base = v0; base < v1; base += 32) {
+          const int v = base + lane;
+          unsigned long long x = v < v1 ? units_of(left(pr, qr, c, v)) : 0ull;
+          if (!DRAFT)
+            for (int i = 0; i < gone; ++i)
+              if (sm.gone[i] == v) x = 0ull;
+          unsigned long long inc = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const unsigned hit = __ballot_sync(kFull, inc > r);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) put(v, count);
+            break;
+          }
+          r -= __shfl_sync(kFull, inc, 31);
+        }
+      }
+    }
+  }
+  cluster_sync();                   // no CTA ends while others write to its totals
+}
+
+// CTAs of a cluster: as many as keep the SMs busy
+int verify_cluster(int B, int sm_count) {
+  int c = 1;
+  while (c < 8 && B * c * 2 <= 2 * sm_count) c *= 2;
+  return c;
+}
+
+template <typename T>
+cudaError_t launch_t(const Drafts &d, int sm_count, cudaStream_t st) {
+  const int c = verify_cluster(d.B, sm_count);
+  cudaError_t e = d.draft ? launch_cluster(k_verify<T, true>, dim3(d.B * c), dim3(kThreads), c, 0,
+                                           st, d)
+                          : launch_cluster(k_verify<T, false>, dim3(d.B * c), dim3(kThreads), c,
+                                           0, st, d);
+  count_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_verify(int dtype, const Drafts &d, int sm_count, cudaStream_t st) {
+  return dtype == VQ_F32   ? launch_t<float>(d, sm_count, st)
+         : dtype == VQ_F16 ? launch_t<__half>(d, sm_count, st)
+                           : launch_t<__nv_bfloat16>(d, sm_count, st);
+}
+
+}  // namespace vqk

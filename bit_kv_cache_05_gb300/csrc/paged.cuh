@@ -34,11 +34,13 @@ namespace vqk {
 
 constexpr int kMaxSeqs = 1024;   // sequences of one paged call
 constexpr int kBlk = 16;         // tokens of a block
+constexpr int kMaxTree = 64;     // nodes of a tree of drafts: bits of a mask
 
 // status bits (device word)
 constexpr unsigned kBadPage = 1u;     // a block table entry outside the pool
 constexpr unsigned kBadLength = 2u;   // lens / cu_new outside their ranges
 constexpr unsigned kGaveUp = 4u;      // a bounded wait ran out
+constexpr unsigned kBadPath = 8u;     // a path of kept tokens outside its tree
 
 __host__ __device__ constexpr int paged_meta_bytes(int D, int g) { return 64 * (D / g); }
 __host__ __device__ constexpr int paged_block_bytes(int D, int g) {
@@ -123,6 +125,39 @@ __device__ __forceinline__ Place find_place(const PagedArgs &a, int64_t i, int64
   }
   const int pos = look >= 0 ? -1 : len - (end - (int)i);
   return Place{lo, pos < 0 ? -1 : pos};
+}
+
+// Which of the new tokens row `tok` of a sequence's tree sees: bits of new
+// tokens that the sequence does not have are left out.
+__device__ __forceinline__ unsigned long long tree_mask(const unsigned long long *tree,
+                                                        const Seq &s, int tok) {
+  const unsigned long long all = s.n >= kMaxTree ? ~0ull : (1ull << s.n) - 1ull;
+  return tree[s.first + tok] & all;
+}
+
+// The columns that a row sees of 64 whose first lies `at` behind the last token
+// before the new ones: a column before them is seen.
+__device__ __forceinline__ unsigned long long tree_columns(unsigned long long mask, int at) {
+  if (at >= 64) return 0ull;
+  if (at >= 0) return mask >> at;
+  if (at > -64) return (mask << -at) | ((1ull << -at) - 1ull);
+  return ~0ull;
+}
+
+// A row of a tree: its mask and where the new tokens begin.  own: the place of
+// the row's own token (negative: padding, or no row), which sees nothing.
+struct TreeRow {
+  unsigned long long mask;
+  int base;
+  __device__ __forceinline__ bool sees(int token) const {
+    const int j = token - base;
+    return j < 0 || (j < 64 && ((mask >> j) & 1ull));
+  }
+};
+__device__ __forceinline__ TreeRow tree_row(const unsigned long long *tree, const Seq &s, int tok,
+                                            int own) {
+  if (own < 0) return TreeRow{0ull, -0x3fffffff};
+  return TreeRow{tree_mask(tree, s, tok), s.len - s.n};
 }
 
 // the block of kv head h that holds position pos of sequence b, nullptr (and
@@ -218,15 +253,60 @@ struct PagedAttend {
   float scale;
   int max_new;               // no sequence has more new tokens
   float *ws;                 // workspace
+  const unsigned long long *tree = nullptr;   // mask of each new token
+};
+
+// accumulated weights: element (sequence, kv head, token) at at[b seq + h head + t]
+struct PagedWeights {
+  float *at;
+  int64_t seq, head;
 };
 
 // few rows: up to 16 (new token, query head) pairs per kv head
 size_t paged_decode_ws(int B, int H_kv, int D, int rows, int sm_count);
 cudaError_t launch_paged_decode(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                 int sm_count, cudaStream_t st);
+cudaError_t launch_paged_decode_tree(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
+                                     int sm_count, cudaStream_t st);
+// capacity: tokens that a sequence's table has room for
+size_t paged_weigh_ws(int B, int H_kv, int D, int rows, int64_t capacity, int sm_count);
+cudaError_t launch_paged_weigh(int dtype, const PagedArgs &a, const PagedAttend &t,
+                               const PagedWeights &w, int D, int sm_count, cudaStream_t st);
 // any number of new tokens
 size_t paged_chunk_ws(int B, int H_kv, int D, int sm_count);
 cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                int sm_count, cudaStream_t st);
+cudaError_t launch_paged_chunk_tree(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
+                                    int sm_count, cudaStream_t st);
+
+
+// tokens that stay move together: new tokens along a path (launch_paged_keep),
+// or those that weigh most, per kv head (launch_paged_evict)
+cudaError_t launch_paged_keep(const PagedArgs &a, const int32_t *path, const int32_t *counts,
+                              int32_t *lens_out, int D, cudaStream_t st);
+struct PagedEvict {
+  PagedWeights in, out;
+  int64_t capacity;          // tokens of a row of weights
+  int32_t *lens_out;
+  int budget, recent, first;
+  int2 *pairs;               // workspace: (place to fill, token that fills it)
+};
+size_t paged_evict_ws(int B, int H_kv, int budget, int recent);
+cudaError_t launch_paged_evict(const PagedArgs &a, const PagedEvict &e, int D, int sm_count,
+                               cudaStream_t st);
+
+// verification of drafted tokens (drafts.cu)
+struct Drafts {
+  const void *target, *draft;          // rows of V probabilities, of one type
+  int64_t target_row, draft_row;       // element strides
+  const void *tokens;
+  const int32_t *parents, *cu;
+  const float *uniforms;
+  int32_t *path, *counts;
+  void *after;
+  int64_t rows;                        // rows of the token arrays
+  int B, V, tokens64;
+};
+cudaError_t launch_verify(int dtype, const Drafts &d, int sm_count, cudaStream_t st);
 
 }  // namespace vqk

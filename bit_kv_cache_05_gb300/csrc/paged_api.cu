@@ -117,6 +117,11 @@ int check_pool(const vq_kivi_paged *p) {
   return VQ_OK;
 }
 
+// whether the work line of the attention counts more blocks than 31 bits hold
+bool too_many(const vq_kivi_paged *p, int B, int max_pages) {
+  return (int64_t)B * max_pages * (p->page / 16) * p->H_kv > 0x7fffffffLL;
+}
+
 int check_batch(const vq_kivi_paged *p, const vq_kivi_paged_batch *s, PagedArgs *to) {
   if (!s) return fail(VQ_ERR_ARG, "batch is NULL");
   if (s->B < 0 || s->tokens < 0 || s->max_pages < 0)
@@ -131,7 +136,7 @@ int check_batch(const vq_kivi_paged *p, const vq_kivi_paged_batch *s, PagedArgs 
   int lg = 4;
   while ((1 << lg) < p->page) ++lg;
   // the work line of the attention counts blocks in 31 bits
-  if ((int64_t)s->B * s->max_pages * (p->page / 16) * p->H_kv > 0x7fffffffLL)
+  if (too_many(p, s->B, s->max_pages))
     return fail(VQ_ERR_UNSUPPORTED, "B * max_pages * page * H_kv too large");
   if (s->B > 0) {
     if (!s->lens || !p->pool || !p->status || (s->max_pages > 0 && !s->table))
@@ -188,6 +193,111 @@ bool overlap(const HeadRows &h, int64_t tokens, int D, int elem) {
 //   20, 32        21.6, 22      46, 46      107, 109     128, 129
 bool few_rows(const vq_kivi_paged *p, int max_new) {
   return (int64_t)max_new * (p->H_q / p->H_kv) <= 16;
+}
+
+int check_weights(const vq_kivi_paged *p, const PagedArgs &a, const vq_kivi_weights *w,
+                  const char *name, PagedWeights *to) {
+  if (!w) return fail(VQ_ERR_ARG, "%s is NULL", name);
+  const int64_t room = (int64_t)a.max_pages << a.page_log2;
+  if (a.B > 0 && room > 0) {
+    if (!w->at || !aligned(w->at, 4)) return fail(VQ_ERR_ARG, "%s is NULL or misaligned", name);
+    if (w->capacity < room)
+      return fail(VQ_ERR_ARG, "%s has room for %lld tokens, the table for %lld", name,
+                  (long long)w->capacity, (long long)room);
+    // no two rows may share a place
+    const int64_t s = w->seq_stride, h = w->head_stride, H = p->H_kv, B = a.B;
+    const bool one_b = B == 1, one_h = H == 1;
+    if ((!one_b && s < room) || (!one_h && h < room) ||
+        (!one_b && !one_h && s < (H - 1) * h + room && h < (B - 1) * s + room))
+      return fail(VQ_ERR_ARG, "%s: rows overlap", name);
+  }
+  to->at = w->at;
+  to->seq = a.B == 1 ? 0 : w->seq_stride;
+  to->head = p->H_kv == 1 ? 0 : w->head_stride;
+  return VQ_OK;
+}
+
+// whether the ranges that two arrays of weights span meet
+bool weights_overlap(const PagedEvict &v, const PagedArgs &a) {
+  auto span = [&](const PagedWeights &w) {
+    return 4 * ((a.B - 1) * w.seq + (a.H_kv - 1) * w.head + v.capacity);
+  };
+  const intptr_t x = reinterpret_cast<intptr_t>(v.in.at), y = reinterpret_cast<intptr_t>(v.out.at);
+  return x < y + span(v.out) && y < x + span(v.in);
+}
+
+// what the three attentions share; tree: masks, weights: where weights are added
+int attend(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch, int dtype,
+           const vq_kivi_rows *q, const void *tree, const vq_kivi_weights *weights,
+           int32_t max_new, float softmax_scale, void *workspace, size_t workspace_bytes,
+           void *stream, bool with_tree = false) {
+  int elem, sms;
+  int rc = check_pool(p);
+  if (rc) return rc;
+  if ((rc = check_dtype(dtype, false, &elem))) return rc;
+  PagedArgs a;
+  if ((rc = check_batch(p, batch, &a))) return rc;
+  if (!q) return fail(VQ_ERR_ARG, "q is NULL");
+  HeadRows h;
+  if ((rc = check_rows(q, "q", elem, a.tokens, true, &h))) return rc;
+  if (h.heads != p->H_q) return fail(VQ_ERR_ARG, "q has %d heads, H_q=%d", h.heads, p->H_q);
+  if (h.weight) return fail(VQ_ERR_ARG, "attend does not norm its queries");
+  if (h.out_head != p->D || h.out_token != (int64_t)p->D * p->H_q)
+    return fail(VQ_ERR_ARG, "the output must be contiguous [tokens][H_q][D]");
+  if (max_new < 1) return fail(VQ_ERR_ARG, "max_new=%d < 1", max_new);
+  if (with_tree) {
+    if ((!tree && a.tokens > 0) || !aligned(tree, 8)) return fail(VQ_ERR_ARG, "tree is NULL or misaligned");
+    if (max_new > kMaxTree)
+      return fail(VQ_ERR_UNSUPPORTED, "a tree has at most %d nodes, max_new=%d", kMaxTree,
+                  max_new);
+  }
+  PagedWeights w;
+  if (weights) {
+    if ((rc = check_weights(p, a, weights, "weights", &w))) return rc;
+    if (!few_rows(p, max_new))
+      return fail(VQ_ERR_UNSUPPORTED, "weights: max_new=%d * H_q/H_kv=%d > 16", max_new,
+                  p->H_q / p->H_kv);
+  }
+  if (!batch->cu_new && max_new != 1)
+    return fail(VQ_ERR_ARG, "without cu_new max_new is 1, got %d", max_new);
+  if (!std::isfinite(softmax_scale)) return fail(VQ_ERR_ARG, "softmax_scale is not finite");
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p->D);
+  const float scale2 = scale * 1.4426950408889634f;      // base 2
+  if (!std::isfinite(scale2)) return fail(VQ_ERR_ARG, "softmax_scale=%g is too large", scale);
+  if (a.tokens == 0 || a.B == 0) return VQ_OK;
+  if (overlap(h, a.tokens, p->D, elem))
+    return fail(VQ_ERR_ARG, "the output overlaps the queries");
+  if ((rc = sm_count(&sms))) return rc;
+  const int GQ = p->H_q / p->H_kv;
+  const bool few = few_rows(p, max_new);
+  const size_t need =
+      weights ? paged_weigh_ws(a.B, p->H_kv, p->D, max_new * GQ,
+                               (int64_t)a.max_pages << a.page_log2, sms)
+      : few   ? paged_decode_ws(a.B, p->H_kv, p->D, max_new * GQ, sms)
+              : paged_chunk_ws(a.B, p->H_kv, p->D, sms);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+    return fail(VQ_ERR_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
+  PagedAttend t;
+  t.q = h.x;
+  t.out = h.out;
+  t.q_token = h.x_token;
+  t.q_head = h.x_head;
+  t.scale = scale2;
+  t.max_new = max_new;
+  t.ws = static_cast<float *>(workspace);
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+  if (with_tree) {
+    t.tree = static_cast<const unsigned long long *>(tree);
+    e = few ? launch_paged_decode_tree(dtype, a, t, p->D, sms, st)
+            : launch_paged_chunk_tree(dtype, a, t, p->D, sms, st);
+  } else if (weights) {
+    e = launch_paged_weigh(dtype, a, t, w, p->D, sms, st);
+  } else {
+    e = few ? launch_paged_decode(dtype, a, t, p->D, sms, st)
+            : launch_paged_chunk(dtype, a, t, p->D, sms, st);
+  }
+  return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged attend launch");
 }
 
 }  // namespace
@@ -282,50 +392,151 @@ int vq_kivi_paged_dequantize(const vq_kivi_paged *p, const vq_kivi_paged_batch *
   return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged dequantize launch");
 }
 
+size_t vq_kivi_paged_weights_workspace_bytes(const vq_kivi_paged *p, int32_t B, int32_t max_pages,
+                                             int32_t max_new) {
+  int sms;
+  if (check_pool(p) || B < 0 || max_pages < 0 || max_new < 1 || sm_count(&sms)) return 0;
+  if (!few_rows(p, max_new)) {
+    fail(VQ_ERR_UNSUPPORTED, "weights: max_new=%d * H_q/H_kv=%d > 16", max_new, p->H_q / p->H_kv);
+    return 0;
+  }
+  if (too_many(p, B, max_pages)) {
+    fail(VQ_ERR_UNSUPPORTED, "B * max_pages * page * H_kv too large");
+    return 0;
+  }
+  const size_t n = paged_weigh_ws(B, p->H_kv, p->D, max_new * (p->H_q / p->H_kv),
+                                  (int64_t)max_pages * p->page, sms);
+  return n < 256 ? 256 : n;
+}
+
 int vq_kivi_paged_attend(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch, int dtype,
                          const vq_kivi_rows *q, int32_t max_new, float softmax_scale,
                          void *workspace, size_t workspace_bytes, void *stream) {
-  int elem, sms;
+  return attend(p, batch, dtype, q, nullptr, nullptr, max_new, softmax_scale, workspace,
+                workspace_bytes, stream);
+}
+
+int vq_kivi_paged_attend_tree(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch, int dtype,
+                              const vq_kivi_rows *q, const void *tree, int32_t max_new,
+                              float softmax_scale, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  return attend(p, batch, dtype, q, tree, nullptr, max_new, softmax_scale, workspace,
+                workspace_bytes, stream, true);
+}
+
+int vq_kivi_paged_attend_weights(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
+                                 int dtype, const vq_kivi_rows *q, const vq_kivi_weights *weights,
+                                 int32_t max_new, float softmax_scale, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  if (!weights) return fail(VQ_ERR_ARG, "weights is NULL");
+  return attend(p, batch, dtype, q, nullptr, weights, max_new, softmax_scale, workspace,
+                workspace_bytes, stream);
+}
+
+int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
+                       const int32_t *path, const int32_t *counts, int32_t *lens_out,
+                       void *stream) {
   int rc = check_pool(p);
   if (rc) return rc;
-  if ((rc = check_dtype(dtype, false, &elem))) return rc;
   PagedArgs a;
   if ((rc = check_batch(p, batch, &a))) return rc;
-  if (!q) return fail(VQ_ERR_ARG, "q is NULL");
-  HeadRows h;
-  if ((rc = check_rows(q, "q", elem, a.tokens, true, &h))) return rc;
-  if (h.heads != p->H_q) return fail(VQ_ERR_ARG, "q has %d heads, H_q=%d", h.heads, p->H_q);
-  if (h.weight) return fail(VQ_ERR_ARG, "attend does not norm its queries");
-  if (h.out_head != p->D || h.out_token != (int64_t)p->D * p->H_q)
-    return fail(VQ_ERR_ARG, "the output must be contiguous [tokens][H_q][D]");
-  if (max_new < 1) return fail(VQ_ERR_ARG, "max_new=%d < 1", max_new);
-  if (!batch->cu_new && max_new != 1)
-    return fail(VQ_ERR_ARG, "without cu_new max_new is 1, got %d", max_new);
-  if (!std::isfinite(softmax_scale)) return fail(VQ_ERR_ARG, "softmax_scale is not finite");
-  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p->D);
-  const float scale2 = scale * 1.4426950408889634f;      // base 2
-  if (!std::isfinite(scale2)) return fail(VQ_ERR_ARG, "softmax_scale=%g is too large", scale);
-  if (a.tokens == 0 || a.B == 0) return VQ_OK;
-  if (overlap(h, a.tokens, p->D, elem))
-    return fail(VQ_ERR_ARG, "the output overlaps the queries");
-  if ((rc = sm_count(&sms))) return rc;
-  const int GQ = p->H_q / p->H_kv;
-  const bool few = few_rows(p, max_new);
-  const size_t need = few ? paged_decode_ws(a.B, p->H_kv, p->D, max_new * GQ, sms)
-                          : paged_chunk_ws(a.B, p->H_kv, p->D, sms);
+  if (a.B == 0) return VQ_OK;
+  if (!counts || !lens_out || (a.tokens > 0 && !path)) return fail(VQ_ERR_ARG, "NULL pointer");
+  if (!aligned(path, 4) || !aligned(counts, 4) || !aligned(lens_out, 4))
+    return fail(VQ_ERR_ARG, "int32 arrays must be 4-byte aligned");
+  cudaError_t e = launch_paged_keep(a, path, counts, lens_out, p->D, (cudaStream_t)stream);
+  return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged keep launch");
+}
+
+size_t vq_kivi_paged_evict_workspace_bytes(const vq_kivi_paged *p, int32_t B, int32_t budget,
+                                           int32_t recent) {
+  if (check_pool(p) || B < 0 || budget < 1 || recent < 0 || recent > budget) return 0;
+  const size_t n = paged_evict_ws(B, p->H_kv, budget, recent);
+  return n < 256 ? 256 : n;
+}
+
+int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
+                        const vq_kivi_weights *weights, const vq_kivi_weights *weights_out,
+                        int32_t budget, int32_t recent, int32_t first, int32_t *lens_out,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+  int sms;
+  int rc = check_pool(p);
+  if (rc) return rc;
+  PagedArgs a;
+  if ((rc = check_batch(p, batch, &a))) return rc;
+  if (batch->cu_new) return fail(VQ_ERR_ARG, "evict takes whole sequences: cu_new must be NULL");
+  if (budget < 1 || recent < 0 || first < 0 || (int64_t)recent + first > budget)
+    return fail(VQ_ERR_ARG, "budget=%d, recent=%d, first=%d: recent + first must be in [0, budget]",
+                budget, recent, first);
+  PagedEvict v;
+  if ((rc = check_weights(p, a, weights, "weights", &v.in))) return rc;
+  if ((rc = check_weights(p, a, weights_out, "weights_out", &v.out))) return rc;
+  v.capacity = (int64_t)a.max_pages << a.page_log2;
+  if (a.B == 0) return VQ_OK;
+  if (v.in.at == v.out.at ? v.in.seq != v.out.seq || v.in.head != v.out.head
+                          : weights_overlap(v, a))
+    return fail(VQ_ERR_ARG, "weights_out overlaps weights (it may be the same array)");
+  if (!lens_out || !aligned(lens_out, 4))
+    return fail(VQ_ERR_ARG, "lens_out is NULL or misaligned");
+  // heads read the lengths while another's sequence is done
+  const intptr_t l = reinterpret_cast<intptr_t>(a.lens), o = reinterpret_cast<intptr_t>(lens_out);
+  if (l < o + 4 * a.B && o < l + 4 * a.B) return fail(VQ_ERR_ARG, "lens_out overlaps lens");
+  const size_t need = paged_evict_ws(a.B, p->H_kv, budget, recent);
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return fail(VQ_ERR_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
-  PagedAttend t;
-  t.q = h.x;
-  t.out = h.out;
-  t.q_token = h.x_token;
-  t.q_head = h.x_head;
-  t.scale = scale2;
-  t.max_new = max_new;
-  t.ws = static_cast<float *>(workspace);
-  cudaError_t e = few ? launch_paged_decode(dtype, a, t, p->D, sms, (cudaStream_t)stream)
-                      : launch_paged_chunk(dtype, a, t, p->D, sms, (cudaStream_t)stream);
-  return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged attend launch");
+  if ((rc = sm_count(&sms))) return rc;
+  v.lens_out = lens_out;
+  v.budget = budget;
+  v.recent = recent;
+  v.first = first;
+  v.pairs = static_cast<int2 *>(workspace);
+  cudaError_t e = launch_paged_evict(a, v, p->D, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged evict launch");
+}
+
+int vq_kivi_verify_drafts(const vq_kivi_drafts *d, int dtype, int32_t *path, int32_t *counts,
+                          void *after, void *stream) {
+  int elem, sms;
+  int rc = check_dtype(dtype, true, &elem);
+  if (rc) return rc;
+  if (!d) return fail(VQ_ERR_ARG, "drafts is NULL");
+  if (d->B < 0 || d->tokens < 0 || d->V < 1)
+    return fail(VQ_ERR_ARG, "sizes: B=%d, tokens=%lld, V=%d", d->B, (long long)d->tokens, d->V);
+  if (d->B > kMaxSeqs) return fail(VQ_ERR_UNSUPPORTED, "B=%d > %d", d->B, kMaxSeqs);
+  if (d->V > (1 << 19)) return fail(VQ_ERR_UNSUPPORTED, "V=%d > 2^19", d->V);
+  if (d->tokens > (1 << 24))
+    return fail(VQ_ERR_UNSUPPORTED, "%lld new tokens > 2^24", (long long)d->tokens);
+  if (d->B == 0) return VQ_OK;
+  if (!d->cu_new || !counts || !after ||
+      (d->tokens > 0 && (!d->target || !d->token || !d->uniforms || !path)))
+    return fail(VQ_ERR_ARG, "NULL pointer");
+  if (d->tokens > 1 && (d->target_row < d->V || (d->draft && d->draft_row < d->V)))
+    return fail(VQ_ERR_ARG, "rows of probabilities overlap: strides %lld and %lld for V=%d",
+                (long long)d->target_row, (long long)d->draft_row, d->V);
+  const int wide = d->token_64 ? 8 : 4;
+  if (!aligned(d->target, elem) || !aligned(d->draft, elem) || !aligned(d->token, wide) ||
+      !aligned(after, wide) || !aligned(d->parent, 4) || !aligned(d->cu_new, 4) ||
+      !aligned(d->uniforms, 4) || !aligned(path, 4) || !aligned(counts, 4))
+    return fail(VQ_ERR_ARG, "misaligned pointer");
+  if ((rc = sm_count(&sms))) return rc;
+  Drafts x;
+  x.target = d->target;
+  x.draft = d->draft;
+  x.target_row = d->target_row;
+  x.draft_row = d->draft_row;
+  x.tokens = d->token;
+  x.parents = d->parent;
+  x.cu = d->cu_new;
+  x.uniforms = d->uniforms;
+  x.path = path;
+  x.counts = counts;
+  x.after = after;
+  x.rows = d->tokens;
+  x.B = d->B;
+  x.V = d->V;
+  x.tokens64 = d->token_64 ? 1 : 0;
+  cudaError_t e = launch_verify(dtype, x, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? VQ_OK : cuda_fail(e, "verify launch");
 }
 
 int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream) {
@@ -344,13 +555,15 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream) {
   }
   if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
   if (!flags) return VQ_OK;
-  return fail(flags & kGaveUp ? VQ_ERR_CUDA : VQ_ERR_ARG, "%s%s%s",
+  return fail(flags & kGaveUp ? VQ_ERR_CUDA : VQ_ERR_ARG, "%s%s%s%s",
               flags & kGaveUp ? "an attention kernel gave up waiting for its copies; its outputs "
                                 "are not valid. " : "",
               flags & kBadPage ? "a block table names a page outside the pool: its tokens were "
                                  "not stored, and rows that see it are not valid. " : "",
               flags & kBadLength ? "a sequence's length or its new tokens lie outside their "
-                                   "ranges; the sequence was left out." : "");
+                                   "ranges; the sequence was left out. " : "",
+              flags & kBadPath ? "a path of kept tokens does not rise within its tree; the "
+                                 "sequence was left as it was." : "");
 }
 
 }  // extern "C"

@@ -1,0 +1,434 @@
+// Tokens of the paged 4-bit cache that stay and move together, as codes: the
+// kept path of a tree of drafts (vq_kivi_paged_keep), and the tokens of the
+// largest accumulated weights (vq_kivi_paged_evict).
+#include "cluster.cuh"
+#include "paged.cuh"
+#include "vqk_internal.cuh"
+
+namespace vqk {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBatch = 8;         // tokens that a warp reads before it writes them
+
+// ---- one token's codes -----------------------------------------------------------
+//
+// A token is D / 2 + 4 D / g values of 16 bits in its block: key codes side by
+// side, value codes every second one (the other is its pair's other token),
+// (scale, min) likewise.  A lane takes every 32nd of them; value i of token tl
+// lies at a + (tl >> 3) x + (tl / 2 mod 4) y + (tl & 1) z.
+template <int D, int NG>
+struct TokenLanes {
+  static constexpr int I = D / 32, N = D / 2 + 4 * NG, PER = (N + 31) / 32;
+  int a[PER], x[PER], y[PER], z[PER];
+  __device__ __forceinline__ explicit TokenLanes(int lane) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      int e = lane + 32 * i;
+      a[i] = -1;
+      x[i] = y[i] = z[i] = 0;
+      if (e >= N) continue;
+      const bool value = e >= N / 2;
+      if (value) e -= N / 2;
+      const int half = value ? 4 * D + 32 * NG : 0;
+      if (e >= D / 4) {                                 // (scale, min) of a group
+        e -= D / 4;
+        a[i] = half + 4 * D + (e % NG) * 4 + 2 * (e / NG);
+        x[i] = 16 * NG;
+        y[i] = 4 * NG;
+        z[i] = 1;
+      } else if (value) {
+        a[i] = half + 2 * ((e / I) * 4 * I + e % I);
+        x[i] = 64 * I;
+        y[i] = 2 * I;
+        z[i] = 1;
+      } else {
+        a[i] = e;
+        x[i] = 2 * D;
+        y[i] = D / 2;
+        z[i] = D / 4;
+      }
+    }
+  }
+  __device__ __forceinline__ int at(int i, int tl) const {
+    return a[i] + (tl >> 3) * x[i] + ((tl >> 1) & 3) * y[i] + (tl & 1) * z[i];
+  }
+  __device__ __forceinline__ void load(const uint8_t *blk, int tl, uint16_t (&v)[PER]) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (a[i] >= 0) v[i] = reinterpret_cast<const uint16_t *>(blk)[at(i, tl)];
+  }
+  __device__ __forceinline__ void store(uint8_t *blk, int tl, const uint16_t (&v)[PER]) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (a[i] >= 0) reinterpret_cast<uint16_t *>(blk)[at(i, tl)] = v[i];
+  }
+};
+
+// The block of position pos in kv head 0, as a number; -1 (and the status bit)
+// where its page is not one of the pool.
+__device__ __forceinline__ int64_t block_of(const PagedArgs &a, int b, int pos) {
+  const int p = a.table[(int64_t)b * a.table_stride + (pos >> a.page_log2)];
+  if ((unsigned)p >= (unsigned)a.n_pages) {
+    atomicOr(a.status, kBadPage);
+    return -1;
+  }
+  return (((int64_t)p * a.H_kv) << (a.page_log2 - 4)) + ((pos & ((1 << a.page_log2) - 1)) >> 4);
+}
+
+// Up to kBatch tokens of a warp: lane j has the blocks and places of token j's
+// source and destination (source block -1: no token, or none to move).  All are
+// read before `between` is called and any is written.
+template <int D, int NG, typename F>
+__device__ __forceinline__ void move_batch(const PagedArgs &a, const TokenLanes<D, NG> &lanes,
+                                           int h, int n, int64_t from, int from_tl, int64_t to,
+                                           int to_tl, F between) {
+  constexpr int BLK = paged_block_bytes(D, D / NG);
+  const int64_t head = (int64_t)h << (a.page_log2 - 4);
+  uint16_t v[kBatch][TokenLanes<D, NG>::PER];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    if (j >= n) break;
+    const int64_t s = __shfl_sync(kFull, from, j);
+    const int tl = __shfl_sync(kFull, from_tl, j);
+    if (s >= 0) lanes.load(a.pool + (s + head) * BLK, tl, v[j]);
+  }
+  between();
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    if (j >= n) break;
+    const int64_t s = __shfl_sync(kFull, from, j), d = __shfl_sync(kFull, to, j);
+    const int tl = __shfl_sync(kFull, to_tl, j);
+    if (s >= 0) lanes.store(a.pool + (d + head) * BLK, tl, v[j]);
+  }
+}
+
+// ---- the kept path of a tree -----------------------------------------------------
+
+// One CTA a sequence, so that its length can be written where it was read; a
+// warp a kv head.  The path rises, so that a token moves to its own place or an
+// earlier one, and what a warp writes was read by it before: kBatch tokens at a
+// time, the earlier ones first.
+template <int D, int NG>
+__global__ void __launch_bounds__(1024)
+k_paged_keep(PagedArgs a, const int32_t *path, const int32_t *counts, int32_t *lens_out) {
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int raw = a.lens[b];
+  const Seq s = sequence_of(a, b, kMaxTree);
+  const int count = counts[b];
+  const int base = s.len - s.n, lead = base < 0 ? -base : 0;   // new tokens before the cache
+  const int start = base + lead;
+  const bool in = count >= 0 && count <= s.n - lead;
+  int node[2] = {0, 0};
+  bool rises = true;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    if (in && j < count) {
+      node[i] = path[s.first + j];
+      const int before = j > 0 ? path[s.first + j - 1] : lead - 1;
+      rises = rises && node[i] > before && node[i] < s.n;
+    }
+  }
+  const bool good = __all_sync(kFull, in && rises);
+  if (!good && threadIdx.x == 0) atomicOr(a.status, kBadPath);
+  __syncthreads();                      // every warp has read the length
+  if (threadIdx.x == 0) lens_out[b] = s.n == 0 || !good ? raw : start + count;
+  if (s.n == 0 || !good) return;
+  // blocks of this lane's two tokens
+  int64_t from[2] = {-1, -1}, to[2] = {-1, -1};
+  int from_tl[2] = {0, 0}, to_tl[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    if (j >= count || base + node[i] == start + j) continue;
+    from[i] = block_of(a, b, base + node[i]);
+    to[i] = block_of(a, b, start + j);
+    if (to[i] < 0) from[i] = -1;
+    from_tl[i] = (base + node[i]) & 15;
+    to_tl[i] = (start + j) & 15;
+  }
+  const TokenLanes<D, NG> lanes(lane);
+  for (int h = warp; h < a.H_kv; h += blockDim.x >> 5)
+    for (int j0 = 0; j0 < count; j0 += kBatch) {
+      const int src = (j0 & 31) + lane, i = j0 >> 5;
+      const int64_t f = __shfl_sync(kFull, i ? from[1] : from[0], src & 31),
+                    d = __shfl_sync(kFull, i ? to[1] : to[0], src & 31);
+      const int ft = __shfl_sync(kFull, i ? from_tl[1] : from_tl[0], src & 31),
+                dt = __shfl_sync(kFull, i ? to_tl[1] : to_tl[0], src & 31);
+      move_batch<D, NG>(a, lanes, h, min(kBatch, count - j0), f, ft, d, dt,
+                        [] { __syncwarp(); });
+      __syncwarp();
+    }
+}
+
+// ---- eviction ----------------------------------------------------------------------
+
+// Weights in an order of whole numbers: NaN lowest, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float w) {
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+constexpr int kEvictThreads = 1024;
+
+struct EvictSmem {
+  uint32_t hist[2][256];
+  uint32_t counts[4];       // weights above the threshold, at it, and of those before K
+  uint32_t warp[32];
+  uint32_t digit[2];        // the digit found, and how many of its weights stay
+};
+
+// One cluster a (sequence, kv head).  K = budget - recent places in front hold
+// the first tokens and the heaviest of the others, the newest tokens follow in
+// their order.
+//   1  the threshold: the weight of rank K - first, found 8 bits at a time from
+//      counts per digit
+//   2  the tokens before K that go are places to fill, the tokens behind K that
+//      stay fill them: both lists in rising order, written by ranks from counts
+//   3  the places are filled; the newest tokens move down
+// Nothing else moves: sources of 3 lie at K or behind, places before K, so no
+// token is overwritten before it is read.
+template <int D, int NG>
+__global__ void __launch_bounds__(kEvictThreads, 1)
+k_paged_evict(PagedArgs a, PagedEvict e) {
+  __shared__ EvictSmem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nw = kEvictThreads / 32;
+  const unsigned rank = cluster_rank(), ctas = cluster_ctas();
+  const int row = blockIdx.x / ctas, b = row / a.H_kv, h = row - b * a.H_kv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int len = a.lens[b];
+  const bool ok = len >= 0 && len <= ((int64_t)a.max_pages << a.page_log2);
+  const float *in = e.in.at + b * e.in.seq + h * e.in.head;
+  float *out = e.out.at + b * e.out.seq + h * e.out.head;
+  const bool same = e.in.at == e.out.at;
+  if (h == 0 && rank == 0 && tid == 0) {
+    if (!ok) atomicOr(a.status, kBadLength);
+    e.lens_out[b] = ok && len > e.budget ? e.budget : len;
+  }
+  const int64_t step = (int64_t)ctas * kEvictThreads, me = (int64_t)rank * kEvictThreads + tid;
+  if (!ok) return;
+  if (len <= e.budget) {
+    for (int64_t p = (same ? len : 0) + me; p < e.capacity; p += step)
+      out[p] = p < len ? in[p] : 0.f;
+    return;
+  }
+  const int K = e.budget - e.recent, lo = e.first, hi = len - e.recent;
+  const int per = (hi - lo + (int)ctas - 1) / (int)ctas;
+  const int p0 = min(lo + (int)rank * per, hi), p1 = min(p0 + per, hi);
+
+  // ---- 1: the threshold ----
+  uint32_t found = 0u, mask = 0u;
+  int need = K - lo;                  // how many of the weights at the threshold stay
+  if (need > 0) {
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      uint32_t *hist = sm.hist[pass & 1];
+      if (tid < 256) hist[tid] = 0u;
+      __syncthreads();
+      for (int p = p0 + tid; p < p1; p += kEvictThreads) {
+        const uint32_t u = order_of(in[p]);
+        if (((u ^ found) & mask) == 0u) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+      }
+      cluster_sync();
+      uint32_t mine = 0u;             // digit 255 - tid, over the cluster
+      if (tid < 256) {
+        for (unsigned r = 0; r < ctas; ++r) mine += peer_load(&hist[255 - tid], r);
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_up_sync(kFull, inc, o);
+          if (lane >= o) inc += v;
+        }
+        if (lane == 31) sm.warp[warp] = inc;
+        mine = inc - mine;            // of this warp's digits above this one
+      }
+      __syncthreads();
+      if (tid < 256) {
+        uint32_t above = mine;
+        for (int w = 0; w < warp; ++w) above += sm.warp[w];
+        uint32_t here = 0u;
+        for (unsigned r = 0; r < ctas; ++r) here += peer_load(&hist[255 - tid], r);
+        if (above < (uint32_t)need && (uint32_t)need <= above + here) {
+          sm.digit[0] = 255 - tid;
+          sm.digit[1] = need - above;
+        }
+      }
+      __syncthreads();
+      found |= sm.digit[0] << shift;
+      need = (int)sm.digit[1];
+      mask |= 255u << shift;
+    }
+  } else {
+    found = kFull;                    // none stays
+  }
+
+  // ---- 2: places to fill and tokens that fill them ----
+  if (tid < 4) sm.counts[tid] = 0u;
+  __syncthreads();
+  {
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+    for (int p = p0 + tid; p < p1; p += kEvictThreads) {
+      const uint32_t u = order_of(in[p]);
+      c[0] += u > found;
+      c[1] += u == found;
+      c[2] += p < K && u > found;
+      c[3] += p < K && u == found;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = __reduce_add_sync(kFull, c[i]);
+      if (lane == 0) atomicAdd(&sm.counts[i], c[i]);
+    }
+  }
+  cluster_sync();
+  int above = 0, equal = 0, above_k = 0, equal_k = 0;
+  for (unsigned r = 0; r < ctas; ++r) {
+    const int x = (int)peer_load(&sm.counts[0], r), y = (int)peer_load(&sm.counts[1], r);
+    if (r < rank) {
+      above += x;
+      equal += y;
+    }
+    above_k += (int)peer_load(&sm.counts[2], r);
+    equal_k += (int)peer_load(&sm.counts[3], r);
+  }
+  // of the weights at the threshold the first ones stay
+  const int kept_k = above_k + min(equal_k, need), holes = K - lo - kept_k;
+  int2 *pairs = e.pairs + (int64_t)row * K;
+  for (int q0 = p0; q0 < p1; q0 += kEvictThreads) {
+    const int p = q0 + tid;
+    const float w = p < p1 ? in[p] : 0.f;
+    const uint32_t u = order_of(w);
+    const bool gt = p < p1 && u > found, eq = p < p1 && u == found;
+    const unsigned bg = __ballot_sync(kFull, gt), be = __ballot_sync(kFull, eq);
+    const unsigned before = (1u << lane) - 1u;
+    __syncthreads();                  // the last tile's counts have been read
+    if (lane == 0) sm.warp[warp] = __popc(bg) | (__popc(be) << 16);
+    __syncthreads();
+    uint32_t inc = sm.warp[lane];
+    const uint32_t own = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t total = __shfl_sync(kFull, inc, 31),
+                   ahead = __shfl_sync(kFull, inc - own, warp);
+    const int g = above + (int)(ahead & 0xffffu) + __popc(bg & before),
+              q = equal + (int)(ahead >> 16) + __popc(be & before);
+    const bool stays = gt || (eq && q < need);
+    const int kept = g + min(q, need);           // tokens before this one that stay
+    if (p < p1) {
+      if (p < K) {
+        if (!stays) pairs[p - lo - kept].x = p;
+        else if (!same) out[p] = w;
+      } else if (stays) {
+        pairs[kept - kept_k].y = p;
+      }
+    }
+    above += (int)(total & 0xffffu);
+    equal += (int)(total >> 16);
+  }
+  if (!same) {
+    for (int64_t p = me; p < lo; p += step) out[p] = in[p];
+    for (int64_t p = e.budget + me; p < e.capacity; p += step) out[p] = 0.f;
+  }
+  cluster_sync();
+
+  // ---- 3: the places are filled ----
+  const TokenLanes<D, NG> lanes(lane);
+  const int gw = (int)rank * nw + warp, stride = (int)ctas * nw * kBatch;
+  for (int i0 = gw * kBatch; i0 < holes; i0 += stride) {
+    const int n = min(kBatch, holes - i0);
+    int64_t from = -1, to = -1;
+    int2 pr = make_int2(0, 0);
+    if (lane < n) {
+      pr = pairs[i0 + lane];
+      from = block_of(a, b, pr.y);
+      to = block_of(a, b, pr.x);
+      if (to < 0) from = -1;
+      out[pr.x] = in[pr.y];
+    }
+    move_batch<D, NG>(a, lanes, h, n, from, pr.y & 15, to, pr.x & 15, [] {});
+  }
+  // the newest tokens move down by hi - K places, the front ones first: all CTAs
+  // have read a round (and, in the first, what fills places) before any writes
+  for (int r0 = 0; r0 < e.recent; r0 += stride) {
+    const int i0 = r0 + gw * kBatch, n = max(0, min(kBatch, e.recent - i0));
+    int64_t from = -1, to = -1;
+    int src = 0, dst = 0;
+    float w = 0.f;
+    if (lane < n) {
+      src = hi + i0 + lane;
+      dst = K + i0 + lane;
+      from = block_of(a, b, src);
+      to = block_of(a, b, dst);
+      if (to < 0) from = -1;
+      w = in[src];
+    }
+    move_batch<D, NG>(a, lanes, h, n, from, src & 15, to, dst & 15, [] { cluster_sync(); });
+    if (lane < n) out[dst] = w;
+  }
+  if (same) {
+    cluster_sync();
+    for (int64_t p = e.budget + me; p < e.capacity; p += step) out[p] = 0.f;
+  }
+}
+
+// CTAs of a cluster: as many as keep all SMs busy
+int evict_cluster(int rows, int sm_count) {
+  int c = 1;
+  while (c < 8 && rows * c * 2 <= sm_count) c *= 2;
+  return c;
+}
+
+template <int D, int NG>
+cudaError_t keep_d(const PagedArgs &a, const int32_t *path, const int32_t *counts,
+                   int32_t *lens_out, cudaStream_t st) {
+  const int warps = a.H_kv < 32 ? a.H_kv : 32;
+  cudaError_t e = launch_pdl(k_paged_keep<D, NG>, dim3(a.B), dim3(32 * warps), 0, st, a, path,
+                             counts, lens_out);
+  count_launch();
+  return e;
+}
+
+template <int D, int NG>
+cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
+  const int rows = a.B * a.H_kv, c = evict_cluster(rows, sm_count);
+  cudaError_t e = launch_cluster(k_paged_evict<D, NG>, dim3(rows * c), dim3(kEvictThreads), c, 0,
+                                 st, a, v);
+  count_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_keep(const PagedArgs &a, const int32_t *path, const int32_t *counts,
+                              int32_t *lens_out, int D, cudaStream_t st) {
+  const int ng = D / a.g;
+  if (D == 64)
+    return ng == 1 ? keep_d<64, 1>(a, path, counts, lens_out, st)
+                   : keep_d<64, 2>(a, path, counts, lens_out, st);
+  return ng == 1   ? keep_d<128, 1>(a, path, counts, lens_out, st)
+         : ng == 2 ? keep_d<128, 2>(a, path, counts, lens_out, st)
+                   : keep_d<128, 4>(a, path, counts, lens_out, st);
+}
+
+size_t paged_evict_ws(int B, int H_kv, int budget, int recent) {
+  return (size_t)B * H_kv * (budget - recent) * sizeof(int2);
+}
+
+cudaError_t launch_paged_evict(const PagedArgs &a, const PagedEvict &e, int D, int sm_count,
+                               cudaStream_t st) {
+  const int ng = D / a.g;
+  if (D == 64)
+    return ng == 1 ? evict_d<64, 1>(a, e, sm_count, st) : evict_d<64, 2>(a, e, sm_count, st);
+  return ng == 1   ? evict_d<128, 1>(a, e, sm_count, st)
+         : ng == 2 ? evict_d<128, 2>(a, e, sm_count, st)
+                   : evict_d<128, 4>(a, e, sm_count, st);
+}
+
+}  // namespace vqk

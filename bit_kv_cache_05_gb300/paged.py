@@ -101,6 +101,24 @@ class PagedKiviCache:
             raise ValueError(f"{name} must be fp16 or bf16, got {dt}")
         return DTYPES[dt]
 
+    def _weights(self, t: torch.Tensor, batch: _lib.PagedBatch, name: str) -> _lib.Weights:
+        shape, st = t.shape, t.stride()
+        if t.dtype is not torch.float32 or t.device != self.device or len(shape) != 3 or \
+                shape[0] != batch.B or shape[1] != self.H_kv or (shape[2] > 1 and st[2] != 1):
+            raise ValueError(f"{name} must be fp32 [{batch.B}][{self.H_kv}][places] with "
+                             f"contiguous rows on {self.device}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient: the cache's operators have none")
+        return _lib.Weights(t.data_ptr() or None, st[0], st[1], shape[2])
+
+    def _lens_out(self, t: Optional[torch.Tensor], B: int) -> torch.Tensor:
+        if t is None:
+            return torch.empty(B, dtype=torch.int32, device=self.device)
+        if t.dtype is not torch.int32 or t.device != self.device or t.shape != (B,) or \
+                not t.is_contiguous():
+            raise ValueError(f"lens_out must be a contiguous int32 [{B}] on {self.device}")
+        return t
+
     def _elsewhere(self, stream) -> bool:
         return stream is not None or self._index != _current_device()
 
@@ -158,15 +176,26 @@ class PagedKiviCache:
 
     def attend(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                cu_new: Optional[torch.Tensor] = None, *, max_new: Optional[int] = None,
+               tree: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
                scale: float = 0.0, out: Optional[torch.Tensor] = None,
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Attention of the new tokens' queries q [tokens][H_q][D] over their
         sequences, each seeing the positions up to its own -> [tokens][H_q][D]
         in q's type.  max_new: no sequence has more new tokens (default: 1
-        without cu_new, else the rows of q)."""
+        without cu_new, else the rows of q, with a tree 64 at most).
+
+        tree: int64 [tokens] masks.  A new token then sees the tokens before
+        the new ones, and new token j of its sequence where bit j of its mask
+        is set (its own bit among them); at most 64 new tokens a sequence.
+
+        weights: fp32 [B][H_kv][>= max_pages * page] (rows may be strided):
+        each stored token's softmax weights, summed over the new tokens and the
+        query heads of its kv head, are added to its place.  At most 16 (new
+        token, query head) pairs per kv head; not with a tree."""
         if self._elsewhere(stream):
             with _on(self.device, stream):
-                return self.attend(q, table, lens, cu_new, max_new=max_new, scale=scale, out=out)
+                return self.attend(q, table, lens, cu_new, max_new=max_new, tree=tree,
+                                   weights=weights, scale=scale, out=out)
         dt, shape = self._dtype(q, "q"), q.shape
         fresh = out is None
         if fresh:
@@ -178,19 +207,103 @@ class PagedKiviCache:
         batch = self._batch(table, lens, cu_new, shape[0])
         if max_new is None:
             max_new = 1 if cu_new is None else max(shape[0], 1)
-        key = (batch.B, max_new)
+            if tree is not None:
+                max_new = min(max_new, 64)
+        w = None
+        if tree is not None:
+            if weights is not None:
+                raise ValueError("weights are not added over a tree")
+            if tree.dtype is not torch.int64 or tree.device != self.device or \
+                    tree.shape != shape[:1] or not tree.is_contiguous():
+                raise ValueError(f"tree must be a contiguous int64 [{shape[0]}] on {self.device}")
+        elif weights is not None:
+            w = self._weights(weights, batch, "weights")
+        key = (batch.B, max_new) if w is None else (batch.B, max_new, batch.max_pages)
         nbytes = self._ws.get(key)
         if nbytes is None:
-            nbytes = self._lib.vq_kivi_paged_workspace_bytes(self._spec, batch.B, int(max_new))
+            L, mn = self._lib, int(max_new)
+            nbytes = L.vq_kivi_paged_workspace_bytes(self._spec, batch.B, mn) if w is None else \
+                L.vq_kivi_paged_weights_workspace_bytes(self._spec, batch.B, batch.max_pages, mn)
             if nbytes and len(self._ws) < 4096:
                 self._ws[key] = nbytes
         ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        rc = self._lib.vq_kivi_paged_attend(
-            self._spec, batch, dt, rq, int(max_new), scale, ws.data_ptr(), nbytes,
-            _raw_stream(self._index))
+        tail = (int(max_new), scale, ws.data_ptr(), nbytes, _raw_stream(self._index))
+        if tree is not None:
+            rc = self._lib.vq_kivi_paged_attend_tree(self._spec, batch, dt, rq,
+                                                     tree.data_ptr() or None, *tail)
+        elif w is not None:
+            rc = self._lib.vq_kivi_paged_attend_weights(self._spec, batch, dt, rq, w, *tail)
+        else:
+            rc = self._lib.vq_kivi_paged_attend(self._spec, batch, dt, rq, *tail)
         if rc:
             _lib.check(rc)
         return out
+
+    def keep(self, table: torch.Tensor, lens: torch.Tensor, cu_new: torch.Tensor,
+             path: torch.Tensor, counts: torch.Tensor, *,
+             lens_out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Of the new tokens of sequence b (64 at most) those stay that the
+        first counts[b] entries of path (int32 [tokens], from row cu_new[b] on)
+        name, in rising order: their codes move to the places of the first new
+        tokens.  Returns the lengths without the others (lens_out, int32 [B];
+        it may be lens).  path and counts are what verify_drafts gives."""
+        if self._elsewhere(stream):
+            with _on(self.device, stream):
+                return self.keep(table, lens, cu_new, path, counts, lens_out=lens_out)
+        if cu_new is None:
+            raise ValueError("cu_new is needed")
+        for t, name in ((path, "path"), (counts, "counts")):
+            if t.dtype is not torch.int32 or t.device != self.device or t.dim() != 1 or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 vector on {self.device}")
+        batch = self._batch(table, lens, cu_new, path.shape[0])
+        if counts.shape[0] != batch.B:
+            raise ValueError(f"counts must be [{batch.B}], got {tuple(counts.shape)}")
+        lens_out = self._lens_out(lens_out, batch.B)
+        rc = self._lib.vq_kivi_paged_keep(self._spec, batch, path.data_ptr() or None,
+                                          counts.data_ptr() or None, lens_out.data_ptr() or None,
+                                          _raw_stream(self._index))
+        if rc:
+            _lib.check(rc)
+        return lens_out
+
+    def evict(self, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, budget: int,
+              *, recent: int, first: int = 0, lens_out: Optional[torch.Tensor] = None,
+              weights_out: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None):
+        """Bring every sequence of more than `budget` tokens down to `budget`,
+        each kv head by its own weights (what attend adds up): the `first`
+        tokens in front and the `recent` newest stay, and of the others those
+        of the largest weights.  Kept tokens in front of the newest stay in
+        their places or fill those of the evicted ones, the newest follow in
+        their order; places say no longer a token's position, so later appends
+        give theirs.  Pages behind the budget are the caller's again.
+
+        Returns (lens_out, weights_out): the lengths (not lens itself) and the
+        weights, moved with their tokens and zero behind (weights_out may be
+        weights itself)."""
+        if self._elsewhere(stream):
+            with _on(self.device, stream):
+                return self.evict(table, lens, weights, budget, recent=recent, first=first,
+                                  lens_out=lens_out, weights_out=weights_out)
+        batch = self._batch(table, lens, None, lens.shape[0])
+        w = self._weights(weights, batch, "weights")
+        if weights_out is None:
+            weights_out = torch.empty_like(weights)
+        elif weights_out.shape != weights.shape:
+            raise ValueError(f"weights_out must be {tuple(weights.shape)}")
+        wo = self._weights(weights_out, batch, "weights_out")
+        lens_out = self._lens_out(lens_out, batch.B)
+        budget, recent, first = int(budget), int(recent), int(first)
+        nbytes = self._lib.vq_kivi_paged_evict_workspace_bytes(self._spec, batch.B, budget, recent)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        rc = self._lib.vq_kivi_paged_evict(self._spec, batch, w, wo, budget, recent, first,
+                                           lens_out.data_ptr() or None, ws.data_ptr() or None,
+                                           nbytes, _raw_stream(self._index))
+        if rc:
+            _lib.check(rc)
+        return lens_out, weights_out
 
     def dequantize(self, table: torch.Tensor, lens: torch.Tensor,
                    cu_new: Optional[torch.Tensor] = None, *, n_tokens: Optional[int] = None,

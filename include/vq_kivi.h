@@ -562,12 +562,141 @@ int vq_kivi_paged_dequantize(const vq_kivi_paged *p,
                              const vq_kivi_paged_batch *batch, void *K_hat,
                              void *V_hat, void *stream);
 
+/* The same for a tree of drafted tokens: new token i of a sequence sees the
+ * tokens before the new ones, and new token j of its sequence where bit j of
+ * its mask is set (its own bit among them; nothing is implied).  Append the
+ * nodes with their depths' positions, attend, keep what is accepted.
+ *   tree           device uint64 [tokens], 8-byte aligned; bits of tokens that
+ *                  the sequence does not have are ignored.  A row that sees
+ *                  nothing is zero.
+ *   max_new        at most 64
+ * The workspace is vq_kivi_paged_workspace_bytes'. */
+int vq_kivi_paged_attend_tree(const vq_kivi_paged *p,
+                              const vq_kivi_paged_batch *batch, int dtype,
+                              const vq_kivi_rows *q, const void *tree,
+                              int32_t max_new, float softmax_scale,
+                              void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* Weights per stored token: element (sequence, kv head, place) at at[sequence *
+ * seq_stride + head * head_stride + place], fp32.
+ *   capacity       places of a row, at least max_pages * page */
+typedef struct vq_kivi_weights {
+  float *at;
+  int64_t seq_stride, head_stride, capacity;
+} vq_kivi_weights;
+
+/* vq_kivi_paged_attend, and each stored token's softmax weights, summed over
+ * the new tokens and the query heads of its kv head, are added to its place in
+ * `weights` (fp32, in a fixed order).  Places behind a sequence are not
+ * touched.  At most 16 (new token, query head) pairs per kv head. */
+int vq_kivi_paged_attend_weights(const vq_kivi_paged *p,
+                                 const vq_kivi_paged_batch *batch, int dtype,
+                                 const vq_kivi_rows *q,
+                                 const vq_kivi_weights *weights,
+                                 int32_t max_new, float softmax_scale,
+                                 void *workspace, size_t workspace_bytes,
+                                 void *stream);
+/* Its workspace (0 on an error). */
+size_t vq_kivi_paged_weights_workspace_bytes(const vq_kivi_paged *p, int32_t B,
+                                             int32_t max_pages,
+                                             int32_t max_new);
+
+/* The new tokens that stay: of sequence b the first counts[b] entries of path
+ * from row cu_new[b] on, numbers of new tokens (0 ... n_b - 1) in rising order.
+ * Their codes move to the places of the first new tokens, and lens_out[b] =
+ * lens[b] - n_b + counts[b].  (New tokens that are not in the cache may not be
+ * among them; the others then begin at place 0.)
+ *   path           device int32 [tokens]
+ *   counts         device int32 [B]
+ *   lens_out       device int32 [B], may be lens
+ * At most 64 new tokens per sequence.  A sequence whose path does not rise
+ * within its new tokens, or whose count is outside its range (a count of -1
+ * among them), is left as it was, and reported by vq_kivi_paged_status. */
+int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
+                       const int32_t *path, const int32_t *counts,
+                       int32_t *lens_out, void *stream);
+
+/* Eviction: each sequence of more than `budget` tokens goes down to `budget`,
+ * each kv head by its own weights.  The `first` tokens in front and the
+ * `recent` newest stay; of the others those of the largest weights (of equal
+ * ones the first; NaN counts as the lowest).  Afterwards the places before
+ * budget - recent hold the tokens that stay, those that were there before in
+ * their places and the others, in their order, in the places of the evicted
+ * ones; the newest follow in their order.  Weights move with their tokens, and
+ * the places behind, up to max_pages * page, are zero.  Pages behind the budget are the caller's again.
+ * A token's place no longer says its position: later appends give theirs.
+ *   batch          cu_new NULL, tokens = B; lens: all tokens
+ *   weights_out    as weights; the same array (in place) or one that does not
+ *                  overlap it
+ *   lens_out       device int32 [B], not lens
+ *   workspace      device, 16-byte aligned */
+int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
+                        const vq_kivi_weights *weights,
+                        const vq_kivi_weights *weights_out, int32_t budget,
+                        int32_t recent, int32_t first, int32_t *lens_out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+size_t vq_kivi_paged_evict_workspace_bytes(const vq_kivi_paged *p, int32_t B,
+                                           int32_t budget, int32_t recent);
+
 /* Synchronizes `stream` and reports what kernels found since the last check:
  * VQ_ERR_ARG for a page or a length outside its range, VQ_ERR_CUDA for a wait
  * that gave up; the message names all that was found.  What is reported is
  * then cleared from the word, and nothing else: what a kernel of another
  * stream finds meanwhile is left for the next check. */
 int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
+
+/* ---- verification of drafted tokens --------------------------------------- */
+
+/* Which of a sequence's drafted tokens stay, and the token that follows them.
+ * Row cu_new[b] + i of the arrays is node i of sequence b's tree: node 0 is the
+ * last token that is known, the others are drafts.
+ *   target      [tokens][V] in fp16, bf16 or fp32: row of node i = the target's
+ *               probabilities of the token behind it
+ *   draft       likewise the distribution that the children of node i were
+ *               drawn from, one by one; rows of nodes without children are not
+ *               read.  NULL: the drafts stand for themselves (the draft's best
+ *               tokens, say), whatever their probabilities were
+ *   token       int32 or (token_64) int64 [tokens]: tokens of the nodes (node
+ *               0's is not read), in [0, V)
+ *   parent      int32 [tokens]: a node's parent, below it (node 0's is not
+ *               read); NULL: chains, node i behind node i - 1
+ *   uniforms    fp32 [tokens] in [0, 1): node i's decides on node i, node 0's
+ *               draws the last token
+ * From node 0 down, the children of the node reached are tried in their order.
+ * With p and q its rows, c = 0 and S = 1 at first, child i of token x is
+ * accepted if
+ *   uniforms[i] q(x) S < w(x),   w = max(p - c q, 0)      (fp32, one rounding)
+ * and otherwise c becomes c + S (rounded to fp32) and S the sum of w over all
+ * tokens: w / S is the distribution left after a rejection.  Without q a child
+ * is accepted if uniforms[i] S < p(x) and otherwise x is taken out of p and S
+ * falls by p(x).  Where no child is accepted the walk ends, and the token
+ * behind it is drawn from w (from p itself where w is nothing but 0): the first
+ * whose running sum passes uniforms[0] times the sum.  Sums are whole numbers
+ * of 2^-44 (each value rounded once, at most 1), and a uniform is cut to 31
+ * bits for the last draw: results do not depend on any order of summation.
+ * Tokens that follow the target's distribution follow, whatever the draft's is.
+ *
+ * path int32 [tokens]: from row cu_new[b] on the nodes that stay, node 0 first,
+ * -1 behind them; counts int32 [B]: how many (vq_kivi_paged_keep takes both);
+ * after [B], in the tokens' type: the last token, -1 where a row has no
+ * positive probability.  A sequence without nodes gets a count of 0 and -1; one
+ * whose offsets, parents or tokens lie outside their ranges, or with more than
+ * 64 nodes, a count of -1, -1, and -1 in its path where its rows are in range.
+ * B <= 1024, V <= 2^19. */
+typedef struct vq_kivi_drafts {
+  const void *target, *draft;
+  int64_t target_row, draft_row; /* elements from row to row, at least V */
+  const void *token;
+  const int32_t *parent;
+  const float *uniforms;
+  const int32_t *cu_new; /* device int32 [B + 1] */
+  int64_t tokens;        /* rows of the arrays */
+  int32_t B, V, token_64;
+} vq_kivi_drafts;
+
+int vq_kivi_verify_drafts(const vq_kivi_drafts *d, int dtype, int32_t *path,
+                          int32_t *counts, void *after, void *stream);
 
 #ifdef __cplusplus
 }
