@@ -16,8 +16,7 @@
 // Bound: two rows of V values a sequence from HBM, or with few sequences the
 // chain of loads (offsets, tokens, probabilities, row) and barriers.  A cluster
 // takes a sequence; each CTA walks (all of them the same way) and sums its
-// slice of the row, each warp a piece of it that is read with neighbouring
-// lanes on neighbouring values.
+// slice of the row, each warp a piece of it, 16 bytes a lane.
 #include "cluster.cuh"
 #include "paged.cuh"
 #include "rope.cuh"
@@ -34,15 +33,60 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// whole numbers of 2^-44; NaN and what is not positive count as nothing
+// What is left of a value: max(p - c q, 0), rounded once, at most 1; a NaN
+// counts as nothing.
+__device__ __forceinline__ float left_of(float p, float q, float c) {
+  float w;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(w) : "f"(-c), "f"(q), "f"(p));
+  return w;
+}
+
+// Whole numbers of 2^-44 in two halves of 22 bits, each the low bits of an fp32
+// next to 2^23: whole = floor(w 2^22), then the rest, rounded to the nearest.
+// (Conversions to 64-bit integers take 57 us where this takes 22: 64 sequences,
+// rows of 131072.)  The halves of up to 1023 values add up in 32 bits.
+struct Halves {
+  uint32_t hi = 0u, lo = 0u;
+  __device__ __forceinline__ void add(float w) {
+    const float t = __fmaf_rd(w, 4194304.f, 8388608.f);
+    const float rest = __fmaf_rn(w, 4194304.f, 8388608.f - t);
+    hi += __float_as_uint(t) - 0x4b000000u;
+    lo += __float_as_uint(__fmaf_rn(rest, 4194304.f, 8388608.f)) - 0x4b000000u;
+  }
+  __device__ __forceinline__ unsigned long long units() const {
+    return ((unsigned long long)hi << 22) + lo;
+  }
+};
 __device__ __forceinline__ unsigned long long units_of(float w) {
-  return w > 0.f ? __float2ull_rn(fminf(w, 1.f) * 17592186044416.f) : 0ull;
+  Halves h;
+  h.add(__saturatef(w));
+  return h.units();
 }
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
+
+// N neighbouring values of a row from v on, 16 bytes of it: at once where they
+// are all in the row and lie on a 16-byte boundary (`wide`), else one by one;
+// 0 outside.
+template <typename T>
+struct Values {
+  static constexpr int N = 16 / sizeof(T);
+  float x[N];
+  __device__ __forceinline__ void load(const T *row, int v, int V, bool wide) {
+    if (wide && v >= 0 && v + N <= V) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + v));
+      const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = as_float(e[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = v + i >= 0 && v + i < V ? as_float(row[v + i]) : 0.f;
+    }
+  }
+};
 
 struct VerifySmem {
   uint64_t totals[2][8];            // of the cluster's CTAs, of the last two sums
@@ -102,24 +146,50 @@ k_verify(Drafts d) {
     if (lead) put(-1, -1);
     return;
   }
-  // this warp's piece of a row
-  const int pieces = (int)ctas * kWarps, each = ((d.V + pieces - 1) / pieces + 31) & ~31;
-  const int v0 = min(d.V, ((int)rank * kWarps + warp) * each), v1 = min(d.V, v0 + each);
+  // A warp's piece of a row: `each` values from v0 on, counted from the
+  // 16-byte boundary at or before the row.
+  constexpr int N = Values<T>::N, STEP = 32 * N;
+  const int pieces = (int)ctas * kWarps,
+            each = (d.V + N - 1 + pieces * STEP - 1) / (pieces * STEP) * STEP,
+            first = ((int)rank * kWarps + warp) * each;
+  auto before = [&](const T *pr) {
+    return (int)(reinterpret_cast<uintptr_t>(pr) % 16 / sizeof(T));
+  };
   int gone = 0;                     // rejected tokens of the node, without q
   unsigned sums = 0;                // taken so far
-  // what is left of value v
-  auto left = [&](const T *pr, const T *qr, float c, int v) {
-    const float p = as_float(pr[v]);
-    if (!DRAFT || c == 0.f) return p;
-    return __fmaf_rn(-c, as_float(qr[v]), p);
-  };
   // the sum of what is left of node `node`'s row; kept per CTA and per warp
   auto row_sum = [&](int node, float c) {
     const T *pr = target + (int64_t)(start + node) * d.target_row;
     const T *qr = DRAFT ? draft + (int64_t)(start + node) * d.draft_row : nullptr;
+    const int v0 = first - before(pr), v1 = min(d.V, v0 + each);
+    const bool with_q = DRAFT && c != 0.f, wide = with_q && before(pr) == before(qr);
     unsigned long long sum = 0ull;
-#pragma unroll 8
-    for (int v = v0 + lane; v < v1; v += 32) sum += units_of(left(pr, qr, c, v));
+    if (with_q) {
+      for (int o = v0; o < v1; o += 16 * STEP) {
+        Halves h;
+#pragma unroll 4
+        for (int v = o + lane * N; v < min(v1, o + 16 * STEP); v += STEP) {
+          Values<T> p, q;
+          p.load(pr, v, d.V, true);
+          q.load(qr, v, d.V, wide);
+#pragma unroll
+          for (int i = 0; i < N; ++i) h.add(left_of(p.x[i], q.x[i], c));
+        }
+        sum += h.units();
+      }
+    } else {
+      for (int o = v0; o < v1; o += 16 * STEP) {
+        Halves h;
+#pragma unroll 4
+        for (int v = o + lane * N; v < min(v1, o + 16 * STEP); v += STEP) {
+          Values<T> p;
+          p.load(pr, v, d.V, true);
+#pragma unroll
+          for (int i = 0; i < N; ++i) h.add(__saturatef(p.x[i]));
+        }
+        sum += h.units();
+      }
+    }
     if (!DRAFT)
       for (int i = lane; i < gone; i += 32) {
         const int x = sm.gone[i];
@@ -224,13 +294,23 @@ k_verify(Drafts d) {
       if (r < sm.warp[warp]) {
         const T *pr = target + (int64_t)(start + at) * d.target_row;
         const T *qr = DRAFT ? draft + (int64_t)(start + at) * d.draft_row : nullptr;
-        for (int base = v0; base < v1; base += 32) {
-          const int v = base + lane;
-          unsigned long long x = v < v1 ? units_of(left(pr, qr, c, v)) : 0ull;
-          if (!DRAFT)
-            for (int i = 0; i < gone; ++i)
-              if (sm.gone[i] == v) x = 0ull;
-          unsigned long long inc = x;
+        const int v0 = first - before(pr), v1 = min(d.V, v0 + each);
+        const bool with_q = DRAFT && c != 0.f, wide = with_q && before(pr) == before(qr);
+        for (int base = v0; base < v1; base += STEP) {
+          const int v = base + lane * N;
+          Values<T> p, q;
+          p.load(pr, v, d.V, true);
+          if (with_q) q.load(qr, v, d.V, wide);
+          unsigned long long x[N], own = 0ull;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            x[i] = units_of(with_q ? left_of(p.x[i], q.x[i], c) : p.x[i]);
+            if (!DRAFT)
+              for (int k = 0; k < gone; ++k)
+                if (sm.gone[k] == v + i) x[i] = 0ull;
+            own += x[i];
+          }
+          unsigned long long inc = own;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const unsigned long long y = __shfl_up_sync(kFull, inc, o);
@@ -238,7 +318,12 @@ k_verify(Drafts d) {
           }
           const unsigned hit = __ballot_sync(kFull, inc > r);
           if (hit) {
-            if (lane == __ffs(hit) - 1) put(v, count);
+            if (lane == __ffs(hit) - 1) {
+              inc -= own;
+              int i = 0;
+              for (; i < N - 1 && inc + x[i] <= r; ++i) inc += x[i];
+              put(v + i, count);
+            }
             break;
           }
           r -= __shfl_sync(kFull, inc, 31);

@@ -171,13 +171,11 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-constexpr int kEvictThreads = 1024;
-
 struct EvictSmem {
   uint32_t hist[2][256];
   uint32_t counts[4];       // weights above the threshold, at it, and of those before K
   uint32_t warp[32];
-  uint32_t digit[2];        // the digit found, and how many of its weights stay
+  uint32_t digit[3];        // the digit found, how many of its weights stay, how many it has
 };
 
 // One cluster a (sequence, kv head).  K = budget - recent places in front hold
@@ -190,12 +188,12 @@ struct EvictSmem {
 //   3  the places are filled; the newest tokens move down
 // Nothing else moves: sources of 3 lie at K or behind, places before K, so no
 // token is overwritten before it is read.
-template <int D, int NG>
-__global__ void __launch_bounds__(kEvictThreads, 1)
+template <int D, int NG, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 k_paged_evict(PagedArgs a, PagedEvict e) {
   __shared__ EvictSmem sm;
+  constexpr int nw = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nw = kEvictThreads / 32;
   const unsigned rank = cluster_rank(), ctas = cluster_ctas();
   const int row = blockIdx.x / ctas, b = row / a.H_kv, h = row - b * a.H_kv;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -208,7 +206,7 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
     if (!ok) atomicOr(a.status, kBadLength);
     e.lens_out[b] = ok && len > e.budget ? e.budget : len;
   }
-  const int64_t step = (int64_t)ctas * kEvictThreads, me = (int64_t)rank * kEvictThreads + tid;
+  const int64_t step = (int64_t)ctas * THREADS, me = (int64_t)rank * THREADS + tid;
   if (!ok) return;
   if (len <= e.budget) {
     for (int64_t p = (same ? len : 0) + me; p < e.capacity; p += step)
@@ -218,66 +216,83 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   const int K = e.budget - e.recent, lo = e.first, hi = len - e.recent;
   const int per = (hi - lo + (int)ctas - 1) / (int)ctas;
   const int p0 = min(lo + (int)rank * per, hi), p1 = min(p0 + per, hi);
+  // this CTA's weights in an order of whole numbers, several on their way
+  auto each = [&](auto f) {
+    constexpr int U = 8;
+    for (int q = p0; q < p1; q += U * THREADS) {
+      float w[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int p = q + i * THREADS + tid;
+        w[i] = p < p1 ? in[p] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int p = q + i * THREADS + tid;
+        if (p < p1) f(p, order_of(w[i]));
+      }
+    }
+  };
 
   // ---- 1: the threshold ----
   uint32_t found = 0u, mask = 0u;
   int need = K - lo;                  // how many of the weights at the threshold stay
   if (need > 0) {
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      uint32_t *hist = sm.hist[pass & 1];
-      if (tid < 256) hist[tid] = 0u;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      uint32_t *hist = sm.hist[(shift >> 3) & 1];
+      for (int i = tid; i < 256; i += THREADS) hist[i] = 0u;
       __syncthreads();
-      for (int p = p0 + tid; p < p1; p += kEvictThreads) {
-        const uint32_t u = order_of(in[p]);
+      each([&](int, uint32_t u) {
         if (((u ^ found) & mask) == 0u) atomicAdd(&hist[(u >> shift) & 255u], 1u);
-      }
+      });
       cluster_sync();
-      uint32_t mine = 0u;             // digit 255 - tid, over the cluster
+      // thread t: digit 255 - t, over the cluster, and how many lie above it
+      uint32_t here = 0u, inc = 0u;
       if (tid < 256) {
-        for (unsigned r = 0; r < ctas; ++r) mine += peer_load(&hist[255 - tid], r);
-        uint32_t inc = mine;
+        for (unsigned r = 0; r < ctas; ++r) here += peer_load(&hist[255 - tid], r);
+        inc = here;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t v = __shfl_up_sync(kFull, inc, o);
           if (lane >= o) inc += v;
         }
         if (lane == 31) sm.warp[warp] = inc;
-        mine = inc - mine;            // of this warp's digits above this one
       }
       __syncthreads();
       if (tid < 256) {
-        uint32_t above = mine;
+        uint32_t above = inc - here;
         for (int w = 0; w < warp; ++w) above += sm.warp[w];
-        uint32_t here = 0u;
-        for (unsigned r = 0; r < ctas; ++r) here += peer_load(&hist[255 - tid], r);
         if (above < (uint32_t)need && (uint32_t)need <= above + here) {
           sm.digit[0] = 255 - tid;
           sm.digit[1] = need - above;
+          sm.digit[2] = here;
         }
       }
       __syncthreads();
       found |= sm.digit[0] << shift;
       need = (int)sm.digit[1];
       mask |= 255u << shift;
+      if (sm.digit[2] == (uint32_t)need) break;    // all of them stay: no need to tell them apart
     }
   } else {
-    found = kFull;                    // none stays
+    found = mask = kFull;             // none stays
   }
+  // the lower bits may be left open
+  auto is_above = [&](uint32_t u) { return (u & mask) > found; };
+  auto is_at = [&](uint32_t u) { return (u & mask) == found; };
 
   // ---- 2: places to fill and tokens that fill them ----
   if (tid < 4) sm.counts[tid] = 0u;
   __syncthreads();
   {
     uint32_t c[4] = {0u, 0u, 0u, 0u};
-    for (int p = p0 + tid; p < p1; p += kEvictThreads) {
-      const uint32_t u = order_of(in[p]);
-      c[0] += u > found;
-      c[1] += u == found;
-      c[2] += p < K && u > found;
-      c[3] += p < K && u == found;
-    }
+    each([&](int p, uint32_t u) {
+      c[0] += is_above(u);
+      c[1] += is_at(u);
+      c[2] += p < K && is_above(u);
+      c[3] += p < K && is_at(u);
+    });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       c[i] = __reduce_add_sync(kFull, c[i]);
@@ -298,33 +313,47 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   // of the weights at the threshold the first ones stay
   const int kept_k = above_k + min(equal_k, need), holes = K - lo - kept_k;
   int2 *pairs = e.pairs + (int64_t)row * K;
-  for (int q0 = p0; q0 < p1; q0 += kEvictThreads) {
-    const int p = q0 + tid;
-    const float w = p < p1 ? in[p] : 0.f;
-    const uint32_t u = order_of(w);
-    const bool gt = p < p1 && u > found, eq = p < p1 && u == found;
-    const unsigned bg = __ballot_sync(kFull, gt), be = __ballot_sync(kFull, eq);
-    const unsigned before = (1u << lane) - 1u;
-    __syncthreads();                  // the last tile's counts have been read
-    if (lane == 0) sm.warp[warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();
-    uint32_t inc = sm.warp[lane];
-    const uint32_t own = inc;
+  constexpr int V = 4;                // neighbouring weights of a thread
+  for (int q0 = p0; q0 < p1; q0 += V * THREADS) {
+    const int q = q0 + V * tid;
+    float w[V];
+    uint32_t gt = 0u, eq = 0u;        // a bit each
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = q + i < p1 ? in[q + i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t u = order_of(w[i]);
+      gt |= (q + i < p1 && is_above(u) ? 1u : 0u) << i;
+      eq |= (q + i < p1 && is_at(u) ? 1u : 0u) << i;
+    }
+    const uint32_t own = __popc(gt) | (__popc(eq) << 16);
+    uint32_t inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(kFull, inc, o);
       if (lane >= o) inc += v;
     }
-    const uint32_t total = __shfl_sync(kFull, inc, 31),
-                   ahead = __shfl_sync(kFull, inc - own, warp);
-    const int g = above + (int)(ahead & 0xffffu) + __popc(bg & before),
-              q = equal + (int)(ahead >> 16) + __popc(be & before);
-    const bool stays = gt || (eq && q < need);
-    const int kept = g + min(q, need);           // tokens before this one that stay
-    if (p < p1) {
+    __syncthreads();                  // the last tile's counts have been read
+    if (lane == 31) sm.warp[warp] = inc;
+    __syncthreads();
+    uint32_t ahead = 0u, total = 0u;
+#pragma unroll
+    for (int k = 0; k < nw; ++k) {
+      if (k < warp) ahead += sm.warp[k];
+      total += sm.warp[k];
+    }
+    ahead += inc - own;
+    const int g = above + (int)(ahead & 0xffffu), x = equal + (int)(ahead >> 16);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int p = q + i;
+      if (p >= p1) break;
+      const uint32_t below = (1u << i) - 1u;
+      const int n_eq = x + __popc(eq & below), kept = g + __popc(gt & below) + min(n_eq, need);
+      const bool stays = ((gt >> i) & 1u) || (((eq >> i) & 1u) && n_eq < need);
       if (p < K) {
         if (!stays) pairs[p - lo - kept].x = p;
-        else if (!same) out[p] = w;
+        else if (!same) out[p] = w[i];
       } else if (stays) {
         pairs[kept - kept_k].y = p;
       }
@@ -378,13 +407,6 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   }
 }
 
-// CTAs of a cluster: as many as keep all SMs busy
-int evict_cluster(int rows, int sm_count) {
-  int c = 1;
-  while (c < 8 && rows * c * 2 <= sm_count) c *= 2;
-  return c;
-}
-
 template <int D, int NG>
 cudaError_t keep_d(const PagedArgs &a, const int32_t *path, const int32_t *counts,
                    int32_t *lens_out, cudaStream_t st) {
@@ -395,13 +417,24 @@ cudaError_t keep_d(const PagedArgs &a, const int32_t *path, const int32_t *count
   return e;
 }
 
-template <int D, int NG>
-cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
-  const int rows = a.B * a.H_kv, c = evict_cluster(rows, sm_count);
-  cudaError_t e = launch_cluster(k_paged_evict<D, NG>, dim3(rows * c), dim3(kEvictThreads), c, 0,
-                                 st, a, v);
+template <int D, int NG, int THREADS>
+cudaError_t evict_t(const PagedArgs &a, const PagedEvict &v, int cluster, cudaStream_t st) {
+  cudaError_t e = launch_cluster(k_paged_evict<D, NG, THREADS>, dim3(a.B * a.H_kv * cluster),
+                                 dim3(THREADS), cluster, 0, st, a, v);
   count_launch();
   return e;
+}
+
+// Short rows take few threads, so that many are at work on an SM; of few long
+// rows each is shared by as many CTAs as there is room for.
+template <int D, int NG>
+cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.B * a.H_kv;
+  const bool few = v.capacity <= 2048 || rows >= 8 * sm_count;
+  const int threads = few ? 256 : 512;
+  int c = 1;
+  while (c < 8 && v.capacity > 2 * c * threads && rows * c * threads <= 512 * sm_count) c *= 2;
+  return few ? evict_t<D, NG, 256>(a, v, c, st) : evict_t<D, NG, 512>(a, v, c, st);
 }
 
 }  // namespace
