@@ -276,6 +276,8 @@ cudaError_t launch_paged_weigh(int dtype, const PagedArgs &a, const PagedAttend 
 size_t paged_chunk_ws(int B, int H_kv, int D, int sm_count);
 cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                int sm_count, cudaStream_t st);
+cudaError_t launch_paged_chunk_tree_small(int dtype, const PagedArgs &a, const PagedAttend &t,
+                                          int D, int sm_count, cudaStream_t st);
 cudaError_t launch_paged_chunk_tree(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                     int sm_count, cudaStream_t st);
 

@@ -11,7 +11,7 @@ size_t paged_chunk_ws(int B, int, int D, int sm_count) {
 
 cudaError_t launch_paged_chunk(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                int sm_count, cudaStream_t st) {
-  return chunk::launch_form<false>(dtype, a, t, D, sm_count, st);
+  return chunk::launch_form<false, false>(dtype, a, t, D, sm_count, st);
 }
 
 }  // namespace vqk

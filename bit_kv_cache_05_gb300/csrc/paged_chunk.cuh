@@ -49,9 +49,9 @@ namespace vqk {
 namespace chunk {
 namespace {
 
-constexpr int kThreads = 640;
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
-constexpr int kRaw = 3;              // stages of 64 tokens as stored
+constexpr int kRawMost = 6;          // stages as stored, of keys or of values
+constexpr int kSmallRows = 64;       // rows of a pair that the small form takes
 constexpr unsigned kFull = 0xffffffffu;
 // exponents of a fresh maximum's weight and of the largest one (see above)
 constexpr float kTop = 10.f, kMost = 15.f;
@@ -227,6 +227,23 @@ __device__ __forceinline__ void tm_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// the weights of `keys` keys from column t on (two a column), times f
+__device__ __forceinline__ void lower_weights(uint32_t t, int keys, float f) {
+  tm_wait_st();
+#pragma unroll 1
+  for (int d = 0; d < keys / 2; d += 8) {
+    uint32_t p[8];
+    tm_ld8(t + d, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // in fp32: the factor itself may be too small for fp16
+      const float2 y = __half22float2(bits_h2(p[j]));
+      p[j] = h2_bits(__floats2half2_rn(y.x * f, y.y * f));
+    }
+    tm_st8(t + d, p);
+  }
+}
+
 // ---- the work line -------------------------------------------------------------
 
 __device__ __forceinline__ int pairs_of(const Seq &s, int tpt) {
@@ -344,16 +361,35 @@ struct alignas(16) CutPair {
   int last;    // CTA with its last tiles
 };
 
-// ---- shared memory --------------------------------------------------------------
+// ---- roles and shared memory -------------------------------------------------------
 
-template <int D, int NG>
+// Warps of each role.  The small form serves pairs of at most 64 rows: two
+// softmax warps a slot (slot 0 on lanes 0-63 of the accumulators, slot 1 on
+// lanes 64-127, so that the four schedulers share them) instead of four; eight
+// warps that rebuild keys and values in turn, a whole tile at a time, instead
+// of four for either; one tile of queries for both slots, which leaves room for
+// larger stages; and registers enough for all.  With few rows the rebuild is what
+// the others wait for, and a warp that only waits takes issue slots from it.
+// The large form moves registers: 256 x 144 + 384 x 64 of the launch's 640 x 96.
+template <bool SMALL>
+struct Roles {
+  static constexpr int SOFT = SMALL ? 4 : 8;       // softmax warps
+  static constexpr int SLOT = SOFT / 2;            // of a slot
+  static constexpr int KEYS = 4, VALUES = SMALL ? 8 : 4;   // that rebuild keys, values
+  static constexpr int ISSUE = SOFT + KEYS + VALUES;       // the issuing warp; copies: + 1, + 2
+  static constexpr int THREADS = 32 * (ISSUE + 4);
+  // a stage as stored has a block for each warp that rebuilds it
+  static constexpr int ROOM = SMALL ? 24 : 12;     // blocks of keys, and of values
+};
+
+template <int D, int NG, bool SMALL>
 struct Smem {
   static constexpr int KB = D / 64;
   static constexpr int OP = KB * 16384;            // one 128 x D fp16 operand
   static constexpr int BLK = 16 * D + 128 * NG, HALF = BLK / 2;   // keys, values
-  static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, RAW = 6 * OP;
-  static constexpr int BAR = RAW + kRaw * 4 * BLK;
-  static constexpr int PREFIX = BAR + 384;
+  static constexpr int Q = 0, K = (SMALL ? 1 : 2) * OP, V = K + 2 * OP, RAW = V + 2 * OP;
+  static constexpr int BAR = RAW + Roles<SMALL>::ROOM * BLK;
+  static constexpr int PREFIX = BAR + 512;
   static constexpr int ALLOC = PREFIX + 8 * (kNear + 1) + 8 + 1024;   // room to align the base
 };
 
@@ -361,44 +397,45 @@ struct Smem {
 __device__ __forceinline__ int sw(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 struct Bars {
-  uint64_t raw_full[2][kRaw], raw_empty[2][kRaw];   // keys, values
+  uint64_t raw_full[2][kRawMost], raw_empty[2][kRawMost];   // keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t x_full, drain;
-  uint32_t good[2][kRaw];   // which of a stage's 4 blocks arrived
+  uint32_t good[2][kRawMost];   // which of a stage's blocks arrived
   uint32_t tmem;
   int dead;
   CutPair cut;
 };
 
-template <typename T, int D, int NG, bool TREE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int D, int NG, bool TREE, bool SMALL>
+__global__ void __launch_bounds__(Roles<SMALL>::THREADS, 1)
 k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cuts,
               long long *prefixes) {
-  using SM = Smem<D, NG>;
+  using SM = Smem<D, NG, SMALL>;
+  using R = Roles<SMALL>;
   constexpr int I = D / 32, G = D / NG, BLK = SM::BLK;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Bars &B = *reinterpret_cast<Bars *>(sm + SM::BAR);
-  static_assert(sizeof(Bars) <= 384, "barriers fit");
+  static_assert(sizeof(Bars) <= 512, "barriers fit");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
   if (tid == 0) {
-    for (int i = 0; i < 2 * kRaw; ++i) {
+    for (int i = 0; i < 2 * kRawMost; ++i) {
       bar_init(&B.raw_full[0][0] + i, 1);
-      bar_init(&B.raw_empty[0][0] + i, 4);
+      bar_init(&B.raw_empty[0][0] + i, i < kRawMost ? R::KEYS : R::VALUES);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&B.k_full[i], 4);
-      bar_init(&B.v_full[i], 4);
+      bar_init(&B.k_full[i], R::KEYS);
+      bar_init(&B.v_full[i], R::VALUES);
       bar_init(&B.k_empty[i], 1);
       bar_init(&B.v_empty[i], 1);
-      bar_init(&B.q_full[i], 4);
+      bar_init(&B.q_full[i], R::SLOT);
       bar_init(&B.s_full[i], 1);
-      bar_init(&B.p_full[i], 4);
+      bar_init(&B.p_full[i], R::SLOT);
       bar_init(&B.o_full[i], 1);
     }
-    bar_init(&B.x_full, 4);
+    bar_init(&B.x_full, R::SLOT);
     bar_init(&B.drain, 1);
     B.dead = 0;
     B.cut.n = 0;
@@ -430,11 +467,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
   }
   auto advance = [&]() { return walk.advance(a, prefix, t.max_new, tpt); };
 
-  // of the launch's 640 x 96 registers: 256 x 144 + 384 x 64 = 61440
-  if (warp < 8) {
+  if (warp < R::SOFT) {
     // ---- softmax ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-    const int wg = warp >> 2, row = tid & 127;
+    if constexpr (SMALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    // slot, lane of the accumulators, row of the query tile
+    const int wg = warp / R::SLOT, at_row = tid & 127, row = SMALL ? at_row & 63 : at_row;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
     uint32_t ph_s = 0, ph_o = 0, ph_x = 0;
@@ -473,7 +511,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
         up = rs.up;
         sl2 = rs.back;
       }
-      unsigned char *dst = sm + SM::Q + wg * SM::OP;
+      unsigned char *dst = sm + SM::Q + (SMALL ? 0 : wg * SM::OP);
       __half2 size[2] = {bits_h2(0u), bits_h2(0u)};    // sum |q| / 256
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -487,7 +525,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           size[i & 1] = __hfma2(__habs2(bits_h2(w[i])), bits_h2(0x1c001c00u), size[i & 1]);
-        *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + sw(row, c & 7)) =
+        *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + sw(at_row, c & 7)) =
             make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
                        __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
       }
@@ -513,7 +551,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     // tensor cores holds the next products up by more than 100 cycles, and
     // the scores' own already says that the products before them are done.
     // Slot 1 is the later user of a tile that both slots use.
-    const bool gives = (warp & 3) == 0 && lane == 0;
+    const bool gives = warp % R::SLOT == 0 && lane == 0;
     bool ok = true;
     settle();
     if (have) load_q();
@@ -609,19 +647,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
               if (c > 0) {
                 // the weights of this tile so far
                 sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
-                tm_wait_st();
-#pragma unroll 1
-                for (int d = 0; d < c / 2; d += 8) {
-                  uint32_t p[8];
-                  tm_ld8(ts + d, p);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    // in fp32: the factor itself may be too small for fp16
-                    const float2 y = __half22float2(bits_h2(p[j]));
-                    p[j] = h2_bits(__floats2half2_rn(y.x * f, y.y * f));
-                  }
-                  tm_st8(ts + d, p);
-                }
+                lower_weights(ts, c, f);
               }
               mo = mn;
             }
@@ -739,25 +765,29 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       if (give && lane == 0) bar_arrive(&B.x_full);
       fence_before();
     }
-  } else if (warp < 16) {
-    // ---- k_hat (warps 8-11) and v_hat (12-15) ----
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    const int kv = (warp - 8) >> 2, w = warp & 3, n8 = lane >> 2, t4 = lane & 3;
-    uint64_t *full = kv ? B.v_full : B.k_full, *empty = kv ? B.v_empty : B.k_empty;
-    uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
-    bool ok = true;
-    // values: where this lane's four stores of an octet go, and the shifts to
+  } else if (warp < R::ISSUE) {
+    // ---- k_hat, v_hat ----
+    if constexpr (SMALL) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // keys or values, block of a stage
+    const int kv = warp >= R::SOFT + R::KEYS ? 1 : 0, w = warp - R::SOFT - (kv ? R::KEYS : 0),
+              blocks = kv ? R::VALUES : R::KEYS, stages = R::ROOM / blocks, n8 = lane >> 2,
+              t4 = lane & 3;
+    // values: where this lane's four stores of 8 tokens go, and the shifts to
     // the nibbles that they hold (the lanes of a store differ in the channel's
     // low bits)
     uint32_t to[4], shift[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = (q + t4) & 3;
-      to[q] = sw(32 * t4 + 4 * n8 + r, 2 * w);
+      to[q] = sw(32 * t4 + 4 * n8 + r, 2 * (w & 3));
       shift[q] = 4 * r;
     }
     const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
                   k64 = bits_h2(0xd400d400u);
+    uint64_t *full = kv ? B.v_full : B.k_full, *empty = kv ? B.v_empty : B.k_empty;
+    uint32_t raw = 0, ph_raw = 0, st = 0, ph_e = 1;    // stages start empty
+    bool ok = true;
     for (; ok && have; have = advance()) {
       const int steps = walk.steps(tpt);
       // the sequence's tokens from this tile on
@@ -765,13 +795,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       for (int j = 0; ok && j < steps; ++j, left -= kTile) {
         ok = bar_wait(&empty[st], ph_e, dead);
         unsigned char *dst = sm + (kv ? SM::V : SM::K) + st * SM::OP;
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int k0 = 0; k0 < 8; k0 += blocks) {
           ok = ok && bar_wait(&B.raw_full[kv][raw], ph_raw, dead);
           if (!__all_sync(kFull, ok)) { ok = false; break; }
-          // warp w takes block w of the stage
-          const unsigned char *blk = sm + SM::RAW + ((kv * kRaw + raw) * 4 + w) * SM::HALF;
+          const unsigned char *blk =
+              sm + SM::RAW + (kv * R::ROOM + raw * blocks + w) * SM::HALF;
           const bool good = (B.good[kv][raw] >> w) & 1u;
-          const int r0 = 64 * hf + 16 * w;             // its first key in the tile
+          const int r0 = 16 * (k0 + w);                // its first key in the tile
           if (!kv) {
             // the 8 lanes of a 16-byte store hold rows r and r + 4, whose
             // swizzled chunks meet 8 different bank groups
@@ -812,32 +842,29 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
               }
             }
           } else {
-            // lane (n8, t4) reads the words of token pair t4, then the four
-            // lanes of n8 exchange them, so that lane j has the four pairs (8
-            // tokens) of the 32-channel span j
+            // Lane (n8, t4) has channels 4 n8 ... + 3 of the 32-channel span
+            // t4: a word of each of the four token pairs.  Lanes of different
+            // n8 read the pairs in different orders, so that they meet
+            // different banks, and turn theirs back by n8 / 2 (four loads and a
+            // turn: 1000 cycles a half stage; a wide load of one pair and an
+            // exchange between the lanes: 1500)
 #pragma unroll
             for (int oct = 0; oct < 2; ++oct) {
-              uint32_t x[4] = {0u, 0u, 0u, 0u};
-              const unsigned char *vp = blk + (32 * oct + lane) * (4 * I);
-              if constexpr (I == 4) {
-                const uint4 y = *reinterpret_cast<const uint4 *>(vp);
-                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2 *>(vp);
-                x[0] = y.x; x[1] = y.y;
-              }
-              // 4 x 4 transposition over the lanes t4 in two exchanges
+              uint32_t x[4];
+              const uint32_t *vp = reinterpret_cast<const uint32_t *>(blk) +
+                                   (8 * oct + n8) * (4 * I) + (I == 4 ? t4 : t4 & 1);
+              const int turn = n8 >> 1;
+#pragma unroll
+              for (int p = 0; p < 4; ++p) x[p] = vp[((p + turn) & 3) * I];
               {
-                const bool o1 = t4 & 1, o2 = t4 & 2;
-                uint32_t s0 = o1 ? x[0] : x[1], s1 = o1 ? x[2] : x[3];
-                s0 = __shfl_xor_sync(kFull, s0, 1);
-                s1 = __shfl_xor_sync(kFull, s1, 1);
-                if (o1) { x[0] = s0; x[2] = s1; } else { x[1] = s0; x[3] = s1; }
-                s0 = o2 ? x[0] : x[2];
-                s1 = o2 ? x[1] : x[3];
-                s0 = __shfl_xor_sync(kFull, s0, 2);
-                s1 = __shfl_xor_sync(kFull, s1, 2);
-                if (o2) { x[0] = s0; x[1] = s1; } else { x[2] = s0; x[3] = s1; }
+                // x[p] holds pair p + turn
+                const bool o1 = turn & 1, o2 = turn & 2;
+                const uint32_t y0 = o1 ? x[3] : x[0], y1 = o1 ? x[0] : x[1],
+                               y2 = o1 ? x[1] : x[2], y3 = o1 ? x[2] : x[3];
+                x[0] = o2 ? y2 : y0;
+                x[1] = o2 ? y3 : y1;
+                x[2] = o2 ? y0 : y2;
+                x[3] = o2 ? y1 : y3;
               }
               const int span = t4;
               if (I == 4 || span < I) {
@@ -865,7 +892,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
                     const __half2 cc = __hsub2(field<0x000f000fu>(x[p] >> shift[q]), k1024);
                     o[p] = h2_bits(__hfma2(cc, bits_h2(m[p].x), bits_h2(m[p].y)));
                   }
-                  *reinterpret_cast<uint4 *>(dst + hf * (D * 128) + (to[q] ^ (oct << 4))) =
+                  *reinterpret_cast<uint4 *>(dst + (r0 >> 6) * (D * 128) + (to[q] ^ (oct << 4))) =
                       make_uint4(o[0], o[1], o[2], o[3]);
                 }
               }
@@ -873,7 +900,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           }
           __syncwarp();
           if (lane == 0) bar_arrive(&B.raw_empty[kv][raw]);
-          raw = raw + 1 == kRaw ? 0 : raw + 1;
+          raw = (int)raw + 1 == stages ? 0 : raw + 1;
           ph_raw ^= raw == 0;
         }
         if (!ok) break;
@@ -887,7 +914,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   }
-  if (warp == 16) {
+  if (warp == R::ISSUE) {
     // ---- the products ----
     {
       const uint32_t id_s = idesc(kTile, kTile), id_o = idesc(kTile, D);
@@ -897,7 +924,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       const uint64_t dq = desc128(sb + SM::Q), dk = desc128(sb + SM::K),
                      dv = desc128(sb + SM::V);
       auto scores = [&](int i, uint32_t stage) {
-        mma_scores<D>(tmem + 128 * i, dq + i * (SM::OP >> 4), dk + stage * (SM::OP >> 4), id_s);
+        mma_scores<D>(tmem + 128 * i, dq + (SMALL ? 0 : i * (SM::OP >> 4)), dk + stage * (SM::OP >> 4), id_s);
         mma_commit(&B.s_full[i]);
       };
       auto outputs = [&](int i, uint32_t stage, bool more) {
@@ -957,9 +984,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       int never = 0;
       bar_wait(&B.drain, 0, &never);
     }
-  } else if (warp == 17 || warp == 18) {
-    // ---- copies: keys (17) and values (18) ----
-    const int kv = warp - 17, bpp = a.page_log2 - 4;
+  } else if (warp == R::ISSUE + 1 || warp == R::ISSUE + 2) {
+    // ---- copies of keys, of values ----
+    const int kv = warp - R::ISSUE - 1, bpp = a.page_log2 - 4,
+              blocks = kv ? R::VALUES : R::KEYS, stages = R::ROOM / blocks;
     uint32_t raw = 0, ph_e = 1;
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
@@ -973,15 +1001,15 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
         const int tok0 = walk.pair * 2 * tpt;
         B.cut = CutPair{walk.s.first + tok0, walk.s.n - tok0, walk.h, last};
       }
-      const int nblk = (walk.s.len + kBlk - 1) / kBlk, end = 2 * (walk.k + walk.steps(tpt));
-      // lane j looks up block 4 k4 + j of the next 8 stages at once, so that
-      // a table's latency is met once in 512 tokens
+      const int nblk = (walk.s.len + kBlk - 1) / kBlk, end = 8 * (walk.k + walk.steps(tpt));
+      // the lanes look up the next 32 blocks at once, so that a table's latency
+      // is met once in 512 tokens
       const uint8_t *src = nullptr;
       unsigned there = 0u;
-      for (int k4 = 2 * walk.k, i = 0; ok && k4 < end; ++k4, i = (i + 1) & 7) {
+      for (int k = 8 * walk.k, i = 0; ok && k < end; k += blocks, i = (i + blocks) & 31) {
         if (i == 0) {
-          const int blk = 4 * k4 + lane;
-          bool good = blk < nblk && blk < 4 * end;
+          const int blk = k + lane;
+          bool good = blk < nblk && blk < end;
           if (good) {
             const int p = a.table[(int64_t)walk.b * a.table_stride + (blk >> bpp)];
             if ((unsigned)p >= (unsigned)a.n_pages) {
@@ -995,24 +1023,24 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
         }
         ok = bar_wait(&B.raw_empty[kv][raw], ph_e, dead);
         if (!__all_sync(kFull, ok)) { ok = false; break; }
-        const unsigned mask = (there >> (4 * i)) & 15u;
+        const unsigned mask = (there >> i) & ((1u << blocks) - 1u);
         if (lane == 0) {
           B.good[kv][raw] = mask;
           mbar_expect_tx(&B.raw_full[kv][raw], __popc(mask) * SM::HALF);
         }
         __syncwarp();
-        if (lane >> 2 == i && (there >> lane & 1u))
-          bulk_g2s(sm + SM::RAW + ((kv * kRaw + raw) * 4 + (lane & 3)) * SM::HALF, src, SM::HALF,
-                   &B.raw_full[kv][raw]);
+        if (lane >= i && lane < i + blocks && (there >> lane & 1u))
+          bulk_g2s(sm + SM::RAW + (kv * R::ROOM + raw * blocks + lane - i) * SM::HALF, src,
+                   SM::HALF, &B.raw_full[kv][raw]);
         used |= 1u << raw;
-        raw = raw + 1 == kRaw ? 0 : raw + 1;
+        raw = (int)raw + 1 == stages ? 0 : raw + 1;
         ph_e ^= raw == 0;
       }
     }
     // copies in flight land before the shared memory is given up: the phase
     // of a stage's last copies is the one before its next turn's
     if (lane == 0) {
-      for (int i = 0; i < kRaw; ++i) {
+      for (int i = 0; i < stages; ++i) {
         int never = 0;
         const uint32_t turn = (uint32_t)i < raw ? ph_e ^ 1u : ph_e;   // parity of its last full
         if ((used >> i) & 1u) bar_wait(&B.raw_full[kv][i], turn, &never);
@@ -1109,16 +1137,16 @@ k_paged_chunk_merge(PagedArgs a, PagedAttend t, const float *part, const CutPair
 size_t part_floats(int D, int sm_count) { return (size_t)2 * sm_count * 2 * kTile * (D + 4); }
 size_t swap_floats(int D, int sm_count) { return (size_t)sm_count * kTile * (D + 4); }
 
-template <bool TREE, typename T, int D, int NG>
+template <bool TREE, bool SMALL, typename T, int D, int NG>
 cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cudaStream_t st) {
-  using SM = Smem<D, NG>;
+  using SM = Smem<D, NG, SMALL>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(k_paged_chunk<T, D, NG, TREE>, SM::ALLOC, done);
+  cudaError_t e = allow_smem(k_paged_chunk<T, D, NG, TREE, SMALL>, SM::ALLOC, done);
   if (e != cudaSuccess) return e;
   float *part = t.ws, *swap = part + part_floats(D, sm_count);
   CutPair *cuts = reinterpret_cast<CutPair *>(swap + swap_floats(D, sm_count));
   long long *prefixes = reinterpret_cast<long long *>(cuts + sm_count);
-  e = launch_pdl(k_paged_chunk<T, D, NG, TREE>, dim3(sm_count), dim3(kThreads), SM::ALLOC, st, a, t,
+  e = launch_pdl(k_paged_chunk<T, D, NG, TREE, SMALL>, dim3(sm_count), dim3(Roles<SMALL>::THREADS), SM::ALLOC, st, a, t,
                  part, swap, cuts, prefixes);
   count_launch();
   if (e != cudaSuccess) return e;
@@ -1132,23 +1160,23 @@ cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cud
   return e;
 }
 
-template <bool TREE, typename T>
+template <bool TREE, bool SMALL, typename T>
 cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_count,
                      cudaStream_t st) {
   const int ng = D / a.g;
   if (D == 64)
-    return ng == 1 ? launch_d<TREE, T, 64, 1>(a, t, sm_count, st)
-                   : launch_d<TREE, T, 64, 2>(a, t, sm_count, st);
-  return ng == 1   ? launch_d<TREE, T, 128, 1>(a, t, sm_count, st)
-         : ng == 2 ? launch_d<TREE, T, 128, 2>(a, t, sm_count, st)
-                   : launch_d<TREE, T, 128, 4>(a, t, sm_count, st);
+    return ng == 1 ? launch_d<TREE, SMALL, T, 64, 1>(a, t, sm_count, st)
+                   : launch_d<TREE, SMALL, T, 64, 2>(a, t, sm_count, st);
+  return ng == 1   ? launch_d<TREE, SMALL, T, 128, 1>(a, t, sm_count, st)
+         : ng == 2 ? launch_d<TREE, SMALL, T, 128, 2>(a, t, sm_count, st)
+                   : launch_d<TREE, SMALL, T, 128, 4>(a, t, sm_count, st);
 }
 
-template <bool TREE>
+template <bool TREE, bool SMALL>
 cudaError_t launch_form(int dtype, const PagedArgs &a, const PagedAttend &t, int D, int sm_count,
                         cudaStream_t st) {
-  return dtype == VQ_F16 ? launch_t<TREE, __half>(a, t, D, sm_count, st)
-                         : launch_t<TREE, __nv_bfloat16>(a, t, D, sm_count, st);
+  return dtype == VQ_F16 ? launch_t<TREE, SMALL, __half>(a, t, D, sm_count, st)
+                         : launch_t<TREE, SMALL, __nv_bfloat16>(a, t, D, sm_count, st);
 }
 
 }  // namespace

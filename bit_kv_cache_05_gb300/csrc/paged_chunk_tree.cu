@@ -6,7 +6,9 @@ namespace vqk {
 
 cudaError_t launch_paged_chunk_tree(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                     int sm_count, cudaStream_t st) {
-  return chunk::launch_form<true>(dtype, a, t, D, sm_count, st);
+  return t.max_new * (a.H_q / a.H_kv) <= chunk::kSmallRows
+             ? launch_paged_chunk_tree_small(dtype, a, t, D, sm_count, st)
+             : chunk::launch_form<true, false>(dtype, a, t, D, sm_count, st);
 }
 
 }  // namespace vqk
