@@ -76,29 +76,29 @@ __device__ __forceinline__ int64_t block_of(const PagedArgs &a, int b, int pos) 
   return (((int64_t)p * a.H_kv) << (a.page_log2 - 4)) + ((pos & ((1 << a.page_log2) - 1)) >> 4);
 }
 
-// Up to kBatch tokens of a warp: lane j has the blocks and places of token j's
-// source and destination (source block -1: no token, or none to move).  All are
-// read before `between` is called and any is written.
+// Up to kBatch tokens of a warp: lane j0 + j has the blocks and places of token
+// j's source and destination (source block -1: no token, or none to move).  All
+// are read before `between` is called and any is written.
 template <int D, int NG, typename F>
 __device__ __forceinline__ void move_batch(const PagedArgs &a, const TokenLanes<D, NG> &lanes,
-                                           int h, int n, int64_t from, int from_tl, int64_t to,
-                                           int to_tl, F between) {
+                                           int h, int j0, int n, int64_t from, int from_tl,
+                                           int64_t to, int to_tl, F between) {
   constexpr int BLK = paged_block_bytes(D, D / NG);
   const int64_t head = (int64_t)h << (a.page_log2 - 4);
   uint16_t v[kBatch][TokenLanes<D, NG>::PER];
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
     if (j >= n) break;
-    const int64_t s = __shfl_sync(kFull, from, j);
-    const int tl = __shfl_sync(kFull, from_tl, j);
+    const int64_t s = __shfl_sync(kFull, from, j0 + j);
+    const int tl = __shfl_sync(kFull, from_tl, j0 + j);
     if (s >= 0) lanes.load(a.pool + (s + head) * BLK, tl, v[j]);
   }
   between();
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
     if (j >= n) break;
-    const int64_t s = __shfl_sync(kFull, from, j), d = __shfl_sync(kFull, to, j);
-    const int tl = __shfl_sync(kFull, to_tl, j);
+    const int64_t s = __shfl_sync(kFull, from, j0 + j), d = __shfl_sync(kFull, to, j0 + j);
+    const int tl = __shfl_sync(kFull, to_tl, j0 + j);
     if (s >= 0) lanes.store(a.pool + (d + head) * BLK, tl, v[j]);
   }
 }
@@ -152,12 +152,9 @@ k_paged_keep(PagedArgs a, const int32_t *path, const int32_t *counts, int32_t *l
   const TokenLanes<D, NG> lanes(lane);
   for (int h = warp; h < a.H_kv; h += blockDim.x >> 5)
     for (int j0 = 0; j0 < count; j0 += kBatch) {
-      const int src = (j0 & 31) + lane, i = j0 >> 5;
-      const int64_t f = __shfl_sync(kFull, i ? from[1] : from[0], src & 31),
-                    d = __shfl_sync(kFull, i ? to[1] : to[0], src & 31);
-      const int ft = __shfl_sync(kFull, i ? from_tl[1] : from_tl[0], src & 31),
-                dt = __shfl_sync(kFull, i ? to_tl[1] : to_tl[0], src & 31);
-      move_batch<D, NG>(a, lanes, h, min(kBatch, count - j0), f, ft, d, dt,
+      const int i = j0 >> 5;
+      move_batch<D, NG>(a, lanes, h, j0 & 31, min(kBatch, count - j0), i ? from[1] : from[0],
+                        i ? from_tl[1] : from_tl[0], i ? to[1] : to[0], i ? to_tl[1] : to_tl[0],
                         [] { __syncwarp(); });
       __syncwarp();
     }
@@ -173,9 +170,10 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 
 struct EvictSmem {
   uint32_t hist[2][256];
-  uint32_t counts[4];       // weights above the threshold, at it, and of those before K
-  uint32_t warp[32];
+  uint32_t counts[2];       // this CTA's weights above the threshold, and at it
+  uint32_t warp[32], own[32];
   uint32_t digit[3];        // the digit found, how many of its weights stay, how many it has
+  uint32_t kept;            // tokens before K that stay (the CTA that has place K)
 };
 
 // One cluster a (sequence, kv head).  K = budget - recent places in front hold
@@ -188,14 +186,18 @@ struct EvictSmem {
 //   3  the places are filled; the newest tokens move down
 // Nothing else moves: sources of 3 lie at K or behind, places before K, so no
 // token is overwritten before it is read.
-template <int D, int NG, int THREADS>
+template <int D, int NG, int THREADS, bool ONE>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 k_paged_evict(PagedArgs a, PagedEvict e) {
   __shared__ EvictSmem sm;
   constexpr int nw = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const unsigned rank = cluster_rank(), ctas = cluster_ctas();
+  const unsigned rank = ONE ? 0u : cluster_rank(), ctas = ONE ? 1u : cluster_ctas();
   const int row = blockIdx.x / ctas, b = row / a.H_kv, h = row - b * a.H_kv;
+  auto all_sync = [] {                // of all threads of the row
+    if constexpr (ONE) __syncthreads();
+    else cluster_sync();
+  };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = a.lens[b];
   const bool ok = len >= 0 && len <= ((int64_t)a.max_pages << a.page_log2);
@@ -237,6 +239,7 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   // ---- 1: the threshold ----
   uint32_t found = 0u, mask = 0u;
   int need = K - lo;                  // how many of the weights at the threshold stay
+  uint32_t above_here = 0u, equal_here = 0u;
   if (need > 0) {
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
@@ -246,33 +249,55 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
       each([&](int, uint32_t u) {
         if (((u ^ found) & mask) == 0u) atomicAdd(&hist[(u >> shift) & 255u], 1u);
       });
-      cluster_sync();
-      // thread t: digit 255 - t, over the cluster, and how many lie above it
-      uint32_t here = 0u, inc = 0u;
+      all_sync();
+      // thread t: digit 255 - t, over the cluster and of this CTA, and how many
+      // lie above it
+      uint32_t here = 0u, inc = 0u, own = 0u, own_inc = 0u;
       if (tid < 256) {
-        for (unsigned r = 0; r < ctas; ++r) here += peer_load(&hist[255 - tid], r);
+        own = hist[255 - tid];
+        here = own;
+        if (!ONE) {
+          here = 0u;
+#pragma unroll
+          for (unsigned r = 0; r < 8; ++r)
+            if (r < ctas) here += peer_load(&hist[255 - tid], r);
+        }
         inc = here;
+        own_inc = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(kFull, inc, o);
-          if (lane >= o) inc += v;
+          const uint32_t v = __shfl_up_sync(kFull, inc, o), w = __shfl_up_sync(kFull, own_inc, o);
+          if (lane >= o) {
+            inc += v;
+            own_inc += w;
+          }
         }
-        if (lane == 31) sm.warp[warp] = inc;
+        if (lane == 31) {
+          sm.warp[warp] = inc;
+          sm.own[warp] = own_inc;
+        }
       }
       __syncthreads();
       if (tid < 256) {
-        uint32_t above = inc - here;
-        for (int w = 0; w < warp; ++w) above += sm.warp[w];
+        uint32_t above = inc - here, mine = own_inc - own;
+        for (int w = 0; w < warp; ++w) {
+          above += sm.warp[w];
+          mine += sm.own[w];
+        }
         if (above < (uint32_t)need && (uint32_t)need <= above + here) {
           sm.digit[0] = 255 - tid;
           sm.digit[1] = need - above;
           sm.digit[2] = here;
+          sm.counts[0] = mine;
+          sm.counts[1] = own;
         }
       }
       __syncthreads();
       found |= sm.digit[0] << shift;
       need = (int)sm.digit[1];
       mask |= 255u << shift;
+      above_here += sm.counts[0];
+      equal_here = sm.counts[1];
       if (sm.digit[2] == (uint32_t)need) break;    // all of them stay: no need to tell them apart
     }
   } else {
@@ -283,35 +308,22 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   auto is_at = [&](uint32_t u) { return (u & mask) == found; };
 
   // ---- 2: places to fill and tokens that fill them ----
-  if (tid < 4) sm.counts[tid] = 0u;
-  __syncthreads();
-  {
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
-    each([&](int p, uint32_t u) {
-      c[0] += is_above(u);
-      c[1] += is_at(u);
-      c[2] += p < K && is_above(u);
-      c[3] += p < K && is_at(u);
-    });
+  int above = 0, equal = 0;           // before this CTA's weights
+  if (!ONE) {
+    __syncthreads();                  // the last pass's counts have been read
+    if (tid == 0) {
+      sm.counts[0] = above_here;
+      sm.counts[1] = equal_here;
+    }
+    all_sync();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = __reduce_add_sync(kFull, c[i]);
-      if (lane == 0) atomicAdd(&sm.counts[i], c[i]);
-    }
+    for (unsigned r = 0; r < 8; ++r)
+      if (r < rank) {
+        above += (int)peer_load(&sm.counts[0], r);
+        equal += (int)peer_load(&sm.counts[1], r);
+      }
   }
-  cluster_sync();
-  int above = 0, equal = 0, above_k = 0, equal_k = 0;
-  for (unsigned r = 0; r < ctas; ++r) {
-    const int x = (int)peer_load(&sm.counts[0], r), y = (int)peer_load(&sm.counts[1], r);
-    if (r < rank) {
-      above += x;
-      equal += y;
-    }
-    above_k += (int)peer_load(&sm.counts[2], r);
-    equal_k += (int)peer_load(&sm.counts[3], r);
-  }
-  // of the weights at the threshold the first ones stay
-  const int kept_k = above_k + min(equal_k, need), holes = K - lo - kept_k;
+  // pairs: the n-th place to fill, and the n-th token that stays
   int2 *pairs = e.pairs + (int64_t)row * K;
   constexpr int V = 4;                // neighbouring weights of a thread
   for (int q0 = p0; q0 < p1; q0 += V * THREADS) {
@@ -349,13 +361,15 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
       const int p = q + i;
       if (p >= p1) break;
       const uint32_t below = (1u << i) - 1u;
+      // of the weights at the threshold the first ones stay
       const int n_eq = x + __popc(eq & below), kept = g + __popc(gt & below) + min(n_eq, need);
       const bool stays = ((gt >> i) & 1u) || (((eq >> i) & 1u) && n_eq < need);
+      if (p == K) sm.kept = (uint32_t)kept;
       if (p < K) {
         if (!stays) pairs[p - lo - kept].x = p;
         else if (!same) out[p] = w[i];
       } else if (stays) {
-        pairs[kept - kept_k].y = p;
+        pairs[kept].y = p;
       }
     }
     above += (int)(total & 0xffffu);
@@ -365,28 +379,39 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
     for (int64_t p = me; p < lo; p += step) out[p] = in[p];
     for (int64_t p = e.budget + me; p < e.capacity; p += step) out[p] = 0.f;
   }
-  cluster_sync();
+  all_sync();
 
   // ---- 3: the places are filled ----
+  // (K lies among the weights: more than K - first of them compete)
+  const unsigned at_k = (unsigned)((K - lo) / per);
+  const int kept_k = (int)(ONE ? sm.kept : peer_load(&sm.kept, at_k)), holes = K - lo - kept_k;
   const TokenLanes<D, NG> lanes(lane);
-  const int gw = (int)rank * nw + warp, stride = (int)ctas * nw * kBatch;
-  for (int i0 = gw * kBatch; i0 < holes; i0 += stride) {
-    const int n = min(kBatch, holes - i0);
+  const int gw = (int)rank * nw + warp;
+  // a lane looks up a pair, then the warp moves kBatch of them at a time
+  for (int i0 = 0; i0 < holes; i0 += (int)ctas * nw * 32) {
+    // the warps share what is left evenly
+    const int left = holes - i0, share = min(32, (left + (int)ctas * nw - 1) / ((int)ctas * nw)),
+              first = i0 + gw * share, n = min(share, holes - first);
     int64_t from = -1, to = -1;
-    int2 pr = make_int2(0, 0);
+    int src = 0, dst = 0;
     if (lane < n) {
-      pr = pairs[i0 + lane];
-      from = block_of(a, b, pr.y);
-      to = block_of(a, b, pr.x);
+      dst = pairs[first + lane].x;
+      src = pairs[kept_k + first + lane].y;
+      from = block_of(a, b, src);
+      to = block_of(a, b, dst);
       if (to < 0) from = -1;
-      out[pr.x] = in[pr.y];
+      out[dst] = in[src];
     }
-    move_batch<D, NG>(a, lanes, h, n, from, pr.y & 15, to, pr.x & 15, [] {});
+    for (int j = 0; j < n; j += kBatch)
+      move_batch<D, NG>(a, lanes, h, j, min(kBatch, n - j), from, src & 15, to, dst & 15, [] {});
   }
   // the newest tokens move down by hi - K places, the front ones first: all CTAs
   // have read a round (and, in the first, what fills places) before any writes
-  for (int r0 = 0; r0 < e.recent; r0 += stride) {
-    const int i0 = r0 + gw * kBatch, n = max(0, min(kBatch, e.recent - i0));
+  const int round = (int)ctas * nw * kBatch;
+  for (int r0 = 0; r0 < e.recent; r0 += round) {
+    const int left = e.recent - r0,
+              share = min(kBatch, (left + (int)ctas * nw - 1) / ((int)ctas * nw)),
+              i0 = r0 + gw * share, n = max(0, min(share, e.recent - i0));
     int64_t from = -1, to = -1;
     int src = 0, dst = 0;
     float w = 0.f;
@@ -398,13 +423,12 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
       if (to < 0) from = -1;
       w = in[src];
     }
-    move_batch<D, NG>(a, lanes, h, n, from, src & 15, to, dst & 15, [] { cluster_sync(); });
+    move_batch<D, NG>(a, lanes, h, 0, n, from, src & 15, to, dst & 15, all_sync);
     if (lane < n) out[dst] = w;
   }
-  if (same) {
-    cluster_sync();
+  if (same || !ONE) all_sync();       // (no CTA ends while others read its counts)
+  if (same)
     for (int64_t p = e.budget + me; p < e.capacity; p += step) out[p] = 0.f;
-  }
 }
 
 template <int D, int NG>
@@ -417,24 +441,26 @@ cudaError_t keep_d(const PagedArgs &a, const int32_t *path, const int32_t *count
   return e;
 }
 
-template <int D, int NG, int THREADS>
+template <int D, int NG, int THREADS, bool ONE>
 cudaError_t evict_t(const PagedArgs &a, const PagedEvict &v, int cluster, cudaStream_t st) {
-  cudaError_t e = launch_cluster(k_paged_evict<D, NG, THREADS>, dim3(a.B * a.H_kv * cluster),
-                                 dim3(THREADS), cluster, 0, st, a, v);
+  const dim3 grid(a.B * a.H_kv * cluster), block(THREADS);
+  cudaError_t e = ONE ? launch_pdl(k_paged_evict<D, NG, THREADS, ONE>, grid, block, 0, st, a, v)
+                      : launch_cluster(k_paged_evict<D, NG, THREADS, ONE>, grid, block, cluster,
+                                       0, st, a, v);
   count_launch();
   return e;
 }
 
-// Short rows take few threads, so that many are at work on an SM; of few long
-// rows each is shared by as many CTAs as there is room for.
+// Short rows take one CTA of few threads, so that many are at work on an SM; of
+// few long rows each is shared by as many CTAs as there is room for.
 template <int D, int NG>
 cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
   const int64_t rows = (int64_t)a.B * a.H_kv;
-  const bool few = v.capacity <= 2048 || rows >= 8 * sm_count;
-  const int threads = few ? 256 : 512;
+  if (v.capacity <= 2048 || rows >= 8 * sm_count) return evict_t<D, NG, 256, true>(a, v, 1, st);
   int c = 1;
-  while (c < 8 && v.capacity > 2 * c * threads && rows * c * threads <= 512 * sm_count) c *= 2;
-  return few ? evict_t<D, NG, 256>(a, v, c, st) : evict_t<D, NG, 512>(a, v, c, st);
+  while (c < 8 && v.capacity > 1024 * c && rows * c <= sm_count) c *= 2;
+  return c == 1 ? evict_t<D, NG, 512, true>(a, v, 1, st)
+                : evict_t<D, NG, 512, false>(a, v, c, st);
 }
 
 }  // namespace
