@@ -12,6 +12,7 @@
 // memory so that its lanes hold 16 neighbouring channels, as a value row's
 // do: a group is then g / 16 neighbouring lanes, whatever the rotation.
 #include "paged.cuh"
+#include "paged_words.cuh"
 #include "vqk_internal.cuh"
 
 namespace vqk {
@@ -274,54 +275,67 @@ k_paged_append(PagedArgs a, HeadRows q, HeadRows k, HeadRows v, RopeArgs r,
   }
 }
 
-// 8 codes in fp16 times s plus z, each rounded once; words of four
-// neighbouring nibbles per half (see paged.cuh)
-template <int D>
+// the 8 values of a word of codes, lowest nibble first: code * s + z, each
+// rounded once (1024 + code and 1024 + 16 code are one logic operation from the
+// word, both steps to the code are exact)
+__device__ __forceinline__ uint4 word_row(uint32_t w, __half2 s, __half2 z) {
+  const __half2 k1024 = bits_h2(0x64006400u), k16 = bits_h2(0x2c002c00u),
+                k64 = bits_h2(0xd400d400u);
+  uint32_t v[4];                      // values (r, r + 4)
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    v[2 * j] = h2_bits(__hfma2(__hsub2(field<0x000f000fu>(w), k1024), s, z));
+    v[2 * j + 1] = h2_bits(__hfma2(__hfma2(field<0x00f000f0u>(w), k16, k64), s, z));
+    w >>= 8;
+  }
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
+// Four lanes a token, eight tokens a warp: lane t4 has the words t4 of the key
+// row and, of the value words, the token's halves of two neighbouring quads of
+// channels, which together read as a key word does; so channels 32 i + 8 t4 ...
+// of both rows, 16 bytes a store.  Neighbouring tokens share the value words'
+// sectors.  Bound: HBM, four bytes out per byte in (16384 tokens of 8 kv
+// heads, D = 128, g = 64: 25.3 us with a token's halves loaded one by one).
+template <int D, int NG>
 __global__ void __launch_bounds__(kThreads)
 k_paged_dequantize(PagedArgs a, __half *K, __half *V, int parts) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR, I = D / 32;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+  constexpr int I = D / 32, G = D / NG, BLK = paged_block_bytes(D, G);
+  const int lane = threadIdx.x & 31, t4 = lane & 3;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = w / parts;
+  const int64_t groups = (a.tokens + 7) / 8, t = w / parts * 8 + (lane >> 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Place at = find_place(a, t, t < a.tokens ? -1 : 32 * (w - a.tokens * parts) + lane);
+  Place at{-1, -1};
+  if (w >= groups * parts) at = find_place(a, a.tokens, 32 * (w - groups * parts) + lane);
+  else if (t < a.tokens) at = find_place(a, t, -1);
   if (at.pos < 0) return;
+  const uint8_t *blk = find_block(a, at.b, at.pos, 0, BLK);
+  if (!blk) return;
   const int tl = at.pos & 15;
-  for (int row = (int)(w % parts) * RPW + sub; row < a.H_kv; row += parts * RPW) {
-    const uint8_t *blk = find_block(a, at.b, at.pos, row, paged_block_bytes(D, a.g));
-    if (!blk) continue;
+  const unsigned half = (tl & 1) ? 0x7632u : 0x5410u, twice = (tl & 1) ? 0x3232u : 0x1010u;
+  const int64_t head = (int64_t)BLK << (a.page_log2 - 4);
+#pragma unroll 2
+  for (int h = (int)(w % parts); h < a.H_kv; h += parts) {
+    const uint8_t *b = blk + h * head;
+    uint32_t k[I], v0[I], v1[I];
+    uint2 km[NG], vm[NG];
+    const uint8_t *vw = b + off_vc(D, G) +
+                        ((8 * (tl >> 3) + 2 * t4) * 4 + ((tl & 7) >> 1)) * (4 * I);
+    load_words<I>(b + tl * (D / 2) + t4 * (4 * I), k);
+    load_meta<NG>(b + off_km(D) + (tl >> 1) * (8 * NG), km);
+    load_words<I>(vw, v0);
+    load_words<I>(vw + 16 * I, v1);
+    load_meta<NG>(b + off_vm(D, G) + (tl >> 1) * (8 * NG), vm);
+    const int64_t row = (t * a.H_kv + h) * D + 8 * t4;
 #pragma unroll
-    for (int values = 0; values < 2; ++values) {
-      uint32_t x[2];
-      if (values) {
-        const uint8_t *p = blk + off_vc(D, a.g) + 2 * (tl & 1) +
-                           4 * (((8 * (tl >> 3) + 4 * (l & 1)) * 4 + ((tl & 7) >> 1)) * I +
-                                (l >> 1));
-        uint32_t u[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) u[n] = *reinterpret_cast<const uint16_t *>(p + 16 * I * n);
-        x[0] = u[0] | (u[1] << 16);
-        x[1] = u[2] | (u[3] << 16);
-      } else {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(blk + tl * (D / 2)) +
-                            2 * (l & 1) * I + (l >> 1);
-        x[0] = p[0];
-        x[1] = p[I];
-      }
-      const __half *m = reinterpret_cast<const __half *>(
-                            blk + (values ? off_vm(D, a.g) : off_km(D))) +
-                        ((tl >> 1) * (D / a.g) + 16 * l / a.g) * 4 + (tl & 1);
-      const __half s = m[0], z = m[2];
-      __half2 o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = x[e >> 2] >> (8 * (e & 3));
-        o[e] = __halves2half2(__hfma(__ushort2half_rn(u & 15u), s, z),
-                              __hfma(__ushort2half_rn((u >> 4) & 15u), s, z));
-      }
-      uint4 *dst = reinterpret_cast<uint4 *>((values ? V : K) + (t * a.H_kv + row) * D + 16 * l);
-      dst[0] = reinterpret_cast<const uint4 *>(o)[0];
-      dst[1] = reinterpret_cast<const uint4 *>(o)[1];
+    for (int i = 0; i < I; ++i) {
+      const uint2 m = km[32 * i / G], n = vm[32 * i / G];
+      *reinterpret_cast<uint4 *>(K + row + 32 * i) =
+          word_row(k[i], bits_h2(__byte_perm(m.x, 0u, twice)), bits_h2(__byte_perm(m.y, 0u, twice)));
+      *reinterpret_cast<uint4 *>(V + row + 32 * i) =
+          word_row(__byte_perm(v0[i], v1[i], half), bits_h2(__byte_perm(n.x, 0u, twice)),
+                   bits_h2(__byte_perm(n.y, 0u, twice)));
     }
   }
 }
@@ -366,17 +380,29 @@ cudaError_t launch_paged_append(int dtype, const PagedArgs &a, const HeadRows &q
              : launch_append<__nv_bfloat16, 128>(a, q, k, v, r, by_place, eps, sm_count, st);
 }
 
-cudaError_t launch_paged_dequantize(const PagedArgs &a, __half *K, __half *V, int D,
-                                    int sm_count, cudaStream_t st) {
-  const int rpw = 512 / D, parts = parts_for(a.tokens, (a.H_kv + rpw - 1) / rpw, sm_count);
-  const int64_t wpc = kThreads / 32;
-  const dim3 grid((unsigned)((warps_for(a, parts) + wpc - 1) / wpc));
-  cudaError_t e = D == 64 ? launch_pdl(k_paged_dequantize<64>, grid, dim3(kThreads), 0, st, a,
-                                       K, V, parts)
-                          : launch_pdl(k_paged_dequantize<128>, grid, dim3(kThreads), 0, st, a,
-                                       K, V, parts);
+template <int D, int NG>
+static cudaError_t dequantize_d(const PagedArgs &a, __half *K, __half *V, int sm_count,
+                                cudaStream_t st) {
+  const int64_t groups = (a.tokens + 7) / 8, wpc = kThreads / 32;
+  int64_t parts = (int64_t)sm_count * 32 / groups;
+  parts = parts < 1 ? 1 : (parts > a.H_kv ? a.H_kv : parts);
+  // and warps that only look at sequences (find_place)
+  const int64_t warps = groups * parts + (a.cu ? (a.B + 31) / 32 : 0);
+  cudaError_t e = launch_pdl(k_paged_dequantize<D, NG>, dim3((unsigned)((warps + wpc - 1) / wpc)),
+                             dim3(kThreads), 0, st, a, K, V, (int)parts);
   count_launch();
   return e;
+}
+
+cudaError_t launch_paged_dequantize(const PagedArgs &a, __half *K, __half *V, int D,
+                                    int sm_count, cudaStream_t st) {
+  const int ng = D / a.g;
+  if (D == 64)
+    return ng == 1 ? dequantize_d<64, 1>(a, K, V, sm_count, st)
+                   : dequantize_d<64, 2>(a, K, V, sm_count, st);
+  return ng == 1   ? dequantize_d<128, 1>(a, K, V, sm_count, st)
+         : ng == 2 ? dequantize_d<128, 2>(a, K, V, sm_count, st)
+                   : dequantize_d<128, 4>(a, K, V, sm_count, st);
 }
 
 }  // namespace vqk
