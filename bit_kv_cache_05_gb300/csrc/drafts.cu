@@ -92,9 +92,13 @@ struct VerifySmem {
   uint64_t totals[2][8];            // of the cluster's CTAs, of the last two sums
   uint64_t warp[kWarps];            // of this CTA's warps, of the last sum
   int64_t token[kMaxTree];
-  float p[kMaxTree], q[kMaxTree], u[kMaxTree];
+  double uq[kMaxTree];              // uniform times q, or the uniform
+  float p[kMaxTree], q[kMaxTree];
   int parent[kMaxTree];
+  int good[kMaxTree];               // accepted if it is the first that is tried
   int gone[kMaxTree];               // without q: the rejected tokens
+  uint64_t run[kWarps];             // of the last search: sums of runs of steps
+  float last;                       // the uniform of the last draw
   int bad;
 };
 
@@ -127,15 +131,24 @@ k_verify(Drafts d) {
       const int64_t x = d.tokens64 ? static_cast<const int64_t *>(d.tokens)[start + tid]
                                    : static_cast<const int32_t *>(d.tokens)[start + tid];
       const int parent = d.parents ? d.parents[start + tid] : tid - 1;
-      sm.u[tid] = d.uniforms[start + tid];
+      const float u = d.uniforms[start + tid];
+      if (tid == 0) sm.last = u;
       if (tid > 0) {
         if (parent < 0 || parent >= tid || x < 0 || x >= d.V) {
           sm.bad = 1;
         } else {
           sm.parent[tid] = parent;
           sm.token[tid] = x;
-          sm.p[tid] = as_float(target[(int64_t)(start + parent) * d.target_row + x]);
-          if (DRAFT) sm.q[tid] = as_float(draft[(int64_t)(start + parent) * d.draft_row + x]);
+          const float p = as_float(target[(int64_t)(start + parent) * d.target_row + x]);
+          double uq = u;
+          if (DRAFT) {
+            const float q = as_float(draft[(int64_t)(start + parent) * d.draft_row + x]);
+            sm.q[tid] = q;
+            uq *= (double)q;        // exact
+          }
+          sm.p[tid] = p;
+          sm.uq[tid] = uq;
+          sm.good[tid] = uq < (double)p;
         }
       }
     }
@@ -226,22 +239,25 @@ k_verify(Drafts d) {
     unsigned long long kids = (unsigned long long)__ballot_sync(kFull, sm.parent[lane] == at) |
                               (unsigned long long)__ballot_sync(kFull, sm.parent[lane + 32] == at)
                                   << 32;
+    bool first_child = true;
     while (kids) {
       const int i = __ffsll((long long)kids) - 1;
       kids &= kids - 1;
       const int x = (int)sm.token[i];
-      const double u = sm.u[i];
       float w = sm.p[i];
       bool good, taken = false;     // taken: rejected before, as another node
-      if (DRAFT) {
-        if (c != 0.f) w = __fmaf_rn(-c, sm.q[i], w);
-        good = mass > 0.0 && u * (double)sm.q[i] * mass < (double)w;
+      if (first_child) {
+        good = sm.good[i];          // (64-bit products are slow: done for all nodes at once)
+      } else if (DRAFT) {
+        w = __fmaf_rn(-c, sm.q[i], w);
+        good = mass > 0.0 && sm.uq[i] * mass < (double)w;
       } else {
         for (int j = lane; j < gone; j += 32) taken = taken || sm.gone[j] == x;
         taken = __any_sync(kFull, taken);
         if (taken) w = 0.f;
-        good = mass > 0.0 && u * mass < (double)w;
+        good = mass > 0.0 && sm.uq[i] * mass < (double)w;
       }
+      first_child = false;
       if (good) {
         if (lead) d.path[start + count] = i;
         ++count;
@@ -277,7 +293,7 @@ k_verify(Drafts d) {
     total = row_sum(at, 0.f);
   }
   // r of [0, total): the token is the first whose running sum passes it
-  const float u = sm.u[0];
+  const float u = sm.last;
   const unsigned long long U = u > 0.f ? (unsigned long long)(fminf(u, 0.99999994f) * 2147483648.f)
                                        : 0ull;
   unsigned long long r = (__umul64hi(total, U) << 33) | ((total * U) >> 31);
@@ -289,27 +305,45 @@ k_verify(Drafts d) {
       r = r < x ? ~0ull : r - x;    // in an earlier CTA's slice: in no warp's here
       if (r == ~0ull) break;
     }
-    if (r < sm.totals[(sums - 1) & 1][rank]) {
-      for (int k = 0; k < warp && r != ~0ull; ++k) r = r < sm.warp[k] ? ~0ull : r - sm.warp[k];
-      if (r < sm.warp[warp]) {
-        const T *pr = target + (int64_t)(start + at) * d.target_row;
-        const T *qr = DRAFT ? draft + (int64_t)(start + at) * d.draft_row : nullptr;
-        const int v0 = first - before(pr), v1 = min(d.V, v0 + each);
-        const bool with_q = DRAFT && c != 0.f, wide = with_q && before(pr) == before(qr);
-        for (int base = v0; base < v1; base += STEP) {
-          const int v = base + lane * N;
-          Values<T> p, q;
-          p.load(pr, v, d.V, true);
-          if (with_q) q.load(qr, v, d.V, wide);
-          unsigned long long x[N], own = 0ull;
+    if (r < sm.totals[(sums - 1) & 1][rank]) {      // the same for all of the CTA
+      int owner = 0;                // the warp whose piece it is in
+      while (owner < kWarps - 1 && r >= sm.warp[owner]) r -= sm.warp[owner++];
+      // All warps look at that piece, a run of its steps each: the sums of the
+      // runs first, then the steps of one run.
+      const T *pr = target + (int64_t)(start + at) * d.target_row;
+      const T *qr = DRAFT ? draft + (int64_t)(start + at) * d.draft_row : nullptr;
+      const int piece = ((int)rank * kWarps + owner) * each - before(pr),
+                run = (each / STEP + kWarps - 1) / kWarps * STEP,
+                v0 = piece + warp * run, v1 = min(min(d.V, piece + each), v0 + run);
+      const bool with_q = DRAFT && c != 0.f, wide = with_q && before(pr) == before(qr);
+      // this lane's values of the step from `base` on, in whole numbers
+      unsigned long long x[N];
+      auto step_of = [&](int base) {
+        const int v = base + lane * N;
+        Values<T> p, q;
+        p.load(pr, v, d.V, true);
+        if (with_q) q.load(qr, v, d.V, wide);
+        unsigned long long own = 0ull;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            x[i] = units_of(with_q ? left_of(p.x[i], q.x[i], c) : p.x[i]);
-            if (!DRAFT)
-              for (int k = 0; k < gone; ++k)
-                if (sm.gone[k] == v + i) x[i] = 0ull;
-            own += x[i];
-          }
+        for (int i = 0; i < N; ++i) {
+          x[i] = units_of(with_q ? left_of(p.x[i], q.x[i], c) : p.x[i]);
+          if (!DRAFT)
+            for (int k = 0; k < gone; ++k)
+              if (sm.gone[k] == v + i) x[i] = 0ull;
+          own += x[i];
+        }
+        return own;
+      };
+      unsigned long long sum = 0ull;
+      for (int base = v0; base < v1; base += STEP) sum += step_of(base);
+      sum = warp_sum(sum);
+      if (lane == 0) sm.run[warp] = sum;
+      __syncthreads();
+      int mine = 0;
+      while (mine < kWarps - 1 && r >= sm.run[mine]) r -= sm.run[mine++];
+      if (mine == warp)
+        for (int base = v0; base < v1; base += STEP) {
+          const unsigned long long own = step_of(base);
           unsigned long long inc = own;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -322,13 +356,12 @@ k_verify(Drafts d) {
               inc -= own;
               int i = 0;
               for (; i < N - 1 && inc + x[i] <= r; ++i) inc += x[i];
-              put(v + i, count);
+              put(base + lane * N + i, count);
             }
             break;
           }
           r -= __shfl_sync(kFull, inc, 31);
         }
-      }
     }
   }
   cluster_sync();                   // no CTA ends while others write to its totals
