@@ -363,18 +363,19 @@ struct alignas(16) CutPair {
 
 // ---- roles and shared memory -------------------------------------------------------
 
-// Warps of each role.  The small form serves pairs of at most 64 rows: two
-// softmax warps a slot (slot 0 on lanes 0-63 of the accumulators, slot 1 on
-// lanes 64-127, so that the four schedulers share them) instead of four; eight
-// warps that rebuild keys and values in turn, a whole tile at a time, instead
-// of four for either; one tile of queries for both slots, which leaves room for
-// larger stages; and registers enough for all.  With few rows the rebuild is what
-// the others wait for, and a warp that only waits takes issue slots from it.
-// The large form moves registers: 256 x 144 + 384 x 64 of the launch's 640 x 96.
+// Warps of each role.  The small form serves pairs of at most 64 rows, with
+// few of which a slot's chain (scores, softmax, outputs, the next scores) and
+// the rebuild are what the others wait for.  Each row lies on two lanes of the
+// accumulators, r and 64 + r: the first weighs the first 64 keys of every tile,
+// the second the others, as if each had half the sequence, and the two are
+// joined at the end.  So four warps share a tile's softmax, one output
+// accumulator serves all, and the scores of the next tile are there when a tile
+// is done.  One tile of queries and twice the warps for the values, which leaves
+// room for more stages.  setmaxnreg: 256 x 144 + 384 x 64, or 128 x 200 + 384 x
+// 72 + 128 x 64, of the launch's 640 x 96 registers.
 template <bool SMALL>
 struct Roles {
   static constexpr int SOFT = SMALL ? 4 : 8;       // softmax warps
-  static constexpr int SLOT = SOFT / 2;            // of a slot
   static constexpr int KEYS = 4, VALUES = SMALL ? 8 : 4;   // that rebuild keys, values
   static constexpr int ISSUE = SOFT + KEYS + VALUES;       // the issuing warp; copies: + 1, + 2
   static constexpr int THREADS = 32 * (ISSUE + 4);
@@ -430,12 +431,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       bar_init(&B.v_full[i], R::VALUES);
       bar_init(&B.k_empty[i], 1);
       bar_init(&B.v_empty[i], 1);
-      bar_init(&B.q_full[i], R::SLOT);
+      bar_init(&B.q_full[i], 4);
       bar_init(&B.s_full[i], 1);
-      bar_init(&B.p_full[i], R::SLOT);
+      bar_init(&B.p_full[i], 4);
       bar_init(&B.o_full[i], 1);
     }
-    bar_init(&B.x_full, R::SLOT);
+    bar_init(&B.x_full, R::SOFT / 2);
     bar_init(&B.drain, 1);
     B.dead = 0;
     B.cut.n = 0;
@@ -471,11 +472,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     // ---- softmax ----
     if constexpr (SMALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-    // slot, lane of the accumulators, row of the query tile
-    const int wg = warp / R::SLOT, at_row = tid & 127, row = SMALL ? at_row & 63 : at_row;
+    // slot (small: half of a tile's keys), lane of the accumulators, row of the
+    // query tile
+    const int wg = warp / (R::SOFT / 2), at_row = tid & 127, row = SMALL ? at_row & 63 : at_row;
+    constexpr int KEYS = SMALL ? 64 : kTile;         // of a tile that a thread weighs
+    const int c0 = SMALL ? 64 * wg : 0;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t ts = tl + 128 * wg, to = tl + 256 + 128 * wg;
-    uint32_t ph_s = 0, ph_o = 0, ph_x = 0;
+    const uint32_t to = tl + 256 + (SMALL ? 0 : 128 * wg);
+    uint32_t ph_s = 0, ph_o = 0, ph_o1 = 0, ph_x = 0;   // ph_s: a bit a buffer
     float sl2 = 0.f;
     bool far_q = false;
     // query row of this thread, of the slot's query tile
@@ -531,7 +535,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(&B.q_full[wg]);
+      if (lane == 0) bar_arrive(&B.q_full[SMALL ? 0 : wg]);
       // whether keys of fp16's size could take a row's scores beyond kFar (5 %
       // and 1 / 64 cover the roundings of the sum; NaN counts as yes)
       const float2 s2 = __half22float2(__hadd2(size[0], size[1]));
@@ -545,13 +549,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     };
     // past the pairs that this slot has no part in
     auto settle = [&]() {
-      while (have && wg == 1 && !walk.two(tpt) && walk.steps(tpt) < 2) next();
+      while (!SMALL && have && wg == 1 && !walk.two(tpt) && walk.steps(tpt) < 2) next();
     };
     // The stages go back to the rebuilding warps from here: a commit of the
     // tensor cores holds the next products up by more than 100 cycles, and
     // the scores' own already says that the products before them are done.
     // Slot 1 is the later user of a tile that both slots use.
-    const bool gives = warp % R::SLOT == 0 && lane == 0;
+    const bool gives = (warp & 3) == 0 && lane == 0;
     bool ok = true;
     settle();
     if (have) load_q();
@@ -561,14 +565,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       // warps without a row leave the weights as they are: their rows of the
       // output are not read.  Rows without a query see everything.
       const bool idle = !__any_sync(kFull, valid);
-      const bool two = walk.two(tpt);
+      const bool two = walk.two(tpt), every = SMALL || two;   // every: tile, not every second
       const int steps = walk.steps(tpt);
       const float raw = sl2;
       float m = -INFINITY, l = 0.f;
       // columns up to vis are seen; of a tree those before the new tokens, and
       // new token j where bit j of `tree` is set
       int vis = (valid ? walk.s.len - walk.s.n + tok : 0x3fffffff) -
-                (walk.k + (two ? 0 : wg)) * kTile;
+                (walk.k + (every ? 0 : wg)) * kTile;
       unsigned long long tree = 0ull;
       if constexpr (TREE) {
         if (valid && walk.s.len - walk.s.n + tok >= 0) {
@@ -578,7 +582,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           vis = -0x3fffffff;
         }
       }
-      const int ahead = two ? kTile : 2 * kTile;
+      const int ahead = every ? kTile : 2 * kTile;
       // In one fma with the maximum a weight's exponent is off by the
       // maximum's own rounding, whole bits from 2^24 on: rows that may go
       // that far get their scores scaled, and rounded, beforehand, in a loop
@@ -586,9 +590,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       auto tiles = [&](auto scaled_before) {
         constexpr bool before = decltype(scaled_before)::value;
         const float scale = before ? 1.f : raw;
-        for (int j = two ? 0 : wg; j < steps; j += two ? 1 : 2, vis -= ahead) {
-          ok = bar_wait(&B.s_full[wg], ph_s, dead);
-          ph_s ^= 1u;
+        for (int j = every ? 0 : wg; j < steps; j += every ? 1 : 2, vis -= ahead) {
+          // scores and weights: a buffer a slot, or (small) the tiles' in turn
+          const int buf = SMALL ? (ring + j) & 1 : wg;
+          const uint32_t ts = tl + 128 * buf;
+          ok = bar_wait(&B.s_full[buf], (ph_s >> buf) & 1u, dead);
+          ph_s ^= 1u << buf;
           if (!__all_sync(kFull, ok)) { ok = false; break; }
           fence_after();
           if (gives && (!two || wg == 1)) {
@@ -599,12 +606,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           if (idle) {
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&B.p_full[wg]);
+            if (lane == 0) bar_arrive(&B.p_full[buf]);
             continue;
           }
           if constexpr (before) {
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 16) {
+            for (int c = c0; c < c0 + KEYS; c += 16) {
               uint32_t v[16];
               tm_ld16(ts + c, v);
 #pragma unroll
@@ -617,12 +624,12 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           float mo = m;       // the maximum that the tile's weights stand on
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < kTile; c += 64) {
+          for (int c = 0; c < KEYS; c += 64) {
             uint32_t v[64];
-            tm_ld64(ts + c, v);
+            tm_ld64(ts + c0 + c, v);
             if (!all) {
               if constexpr (TREE) {
-                const unsigned long long seen = tree_columns(tree, c - 1 - vis);
+                const unsigned long long seen = tree_columns(tree, c0 + c - 1 - vis);
                 const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
@@ -631,7 +638,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
               } else {
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
-                  if (c + j > vis) v[j] = __float_as_uint(-INFINITY);
+                  if (c0 + c + j > vis) v[j] = __float_as_uint(-INFINITY);
               }
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -665,12 +672,29 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
                 p[j] = h2_bits(__floats2half2_rn(y.x, y.y));
               }
               // the weights of 32 columns take 16, all behind what is read
-              tm_st16(ts + (c + d) / 2, p);
+              tm_st16(ts + (c0 + c + d) / 2, p);
             }
+          }
+          if constexpr (SMALL) {
+            // this lane has no part in the other half's keys
+            uint32_t none[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) none[i] = 0u;
+            tm_st16(ts + (64 - c0) / 2, none);
+            tm_st16(ts + (64 - c0) / 2 + 16, none);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           // O goes to the new maximum
-          if (j >= (two ? 1 : 2) && __any_sync(kFull, mo > m)) {
+          if (j >= (every ? 1 : 2) && __any_sync(kFull, mo > m)) {
+            if constexpr (SMALL) {
+              // the outputs before this tile's: done when the next scores are,
+              // which were issued behind them, or have a barrier of their own
+              ok = __all_sync(kFull, j + 1 < steps
+                                         ? bar_wait(&B.s_full[buf ^ 1], (ph_s >> (buf ^ 1)) & 1u, dead)
+                                         : bar_wait(&B.o_full[1], ph_o1, dead));
+              if (!ok) break;
+              fence_after();
+            }
             const float f = mo > m ? pow2(m - mo) : 1.f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -685,14 +709,14 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           tm_wait_st();
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(&B.p_full[wg]);
+          if (lane == 0) bar_arrive(&B.p_full[buf]);
         }
       };
       if (far_q) tiles(std::true_type{});
       else tiles(std::false_type{});
       if (!ok) break;
       // slot 1 of a single query tile hands its sums to slot 0
-      const bool halves = !two && steps > 1;
+      const bool halves = SMALL || (!two && steps > 1);
       const bool give = halves && wg == 1;
       const bool whole = walk.k == 0 && steps == walk.tiles(tpt);
       float *xr = swap + (blockIdx.x * kTile + row) * (D + 4);
@@ -702,16 +726,18 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       T *orow = static_cast<T *>(t.out) +
                 ((int64_t)(walk.s.first + tok) * a.H_q + walk.h * GQ + row % GQ) * D;
       // the stage of this slot's last tile
-      const uint32_t vlast = (ring + (two ? steps - 1 : steps - 1 - ((steps - 1 - wg) & 1))) & 1;
+      const uint32_t vlast = (ring + (every ? steps - 1 : steps - 1 - ((steps - 1 - wg) & 1))) & 1;
+      if (SMALL && steps > 1) ph_o1 ^= 1u;
       // the next queries: this slot's last scores have been read
       next();
       settle();
       if (have) load_q();
-      ok = bar_wait(&B.o_full[wg], ph_o, dead);
+      ok = bar_wait(&B.o_full[SMALL ? 0 : wg], ph_o, dead);
       ph_o ^= 1u;
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
       if (gives && (!two || wg == 1)) bar_arrive(&B.v_empty[vlast]);
+      if (SMALL && gives && steps > 1) bar_arrive(&B.v_empty[vlast ^ 1]);
       float f0 = 1.f, f1 = 0.f;
       if (halves && wg == 0) {
         ok = bar_wait(&B.x_full, ph_x, dead);
@@ -924,12 +950,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       const uint64_t dq = desc128(sb + SM::Q), dk = desc128(sb + SM::K),
                      dv = desc128(sb + SM::V);
       auto scores = [&](int i, uint32_t stage) {
-        mma_scores<D>(tmem + 128 * i, dq + (SMALL ? 0 : i * (SM::OP >> 4)), dk + stage * (SM::OP >> 4), id_s);
+        mma_scores<D>(tmem + 128 * i, dq + (SMALL ? 0 : i * (SM::OP >> 4)),
+                      dk + stage * (SM::OP >> 4), id_s);
         mma_commit(&B.s_full[i]);
       };
       auto outputs = [&](int i, uint32_t stage, bool more) {
-        mma_outputs<D>(tmem + 256 + 128 * i, tmem + 128 * i, dv + stage * (SM::OP >> 4), id_o,
-                       more);
+        mma_outputs<D>(tmem + 256 + (SMALL ? 0 : 128 * i), tmem + 128 * i,
+                       dv + stage * (SM::OP >> 4), id_o, more);
       };
       // waits for the keys of the next tile, and goes on from them
       auto keys = [&]() {
@@ -944,6 +971,37 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       for (; ok && have; have = advance()) {
         const int nt = walk.steps(tpt);
         const bool two = walk.two(tpt);
+        if constexpr (SMALL) {
+          // a tile's buffer has the parity of its stages
+          ok = __all_sync(kFull, bar_wait(&B.q_full[0], ph_q, dead));
+          ph_q ^= 1u;
+          for (int i = 0; ok && i < (nt > 1 ? 2 : 1); ++i) {
+            ok = keys();
+            if (!ok) break;
+            scores(ks, ks);
+            keys_done();
+          }
+          for (int j = 0; ok && j < nt; ++j) {
+            ok = __all_sync(kFull, bar_wait(&B.v_full[vs], ph_v, dead)) &&
+                 __all_sync(kFull, bar_wait(&B.p_full[vs], (ph_p >> vs) & 1u, dead));
+            ph_p ^= 1u << vs;
+            if (!ok) break;
+            fence_after();
+            outputs(vs, vs, j > 0);
+            if (j + 2 < nt) {
+              ok = keys();
+              if (!ok) break;
+              scores(ks, ks);
+              keys_done();
+            } else {
+              // of the last tile but one, and of the last
+              mma_commit(&B.o_full[j + 2 == nt ? 1 : 0]);
+            }
+            vs ^= 1u;
+            ph_v ^= vs == 0;
+          }
+          continue;
+        }
         const int slots = two || nt > 1 ? 2 : 1;
         // first scores of both slots: one key tile for two query tiles, or a
         // key tile each for one
