@@ -871,9 +871,9 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
             // Lane (n8, t4) has channels 4 n8 ... + 3 of the 32-channel span
             // t4: a word of each of the four token pairs.  Lanes of different
             // n8 read the pairs in different orders, so that they meet
-            // different banks, and turn theirs back by n8 / 2 (four loads and a
-            // turn: 1000 cycles a half stage; a wide load of one pair and an
-            // exchange between the lanes: 1500)
+            // different banks, and turn theirs back by n8 / 2 (16 sequences, 64
+            // rows, in the large form: 101 us; with a wide load of one pair and
+            // an exchange between the lanes 109)
 #pragma unroll
             for (int oct = 0; oct < 2; ++oct) {
               uint32_t x[4];

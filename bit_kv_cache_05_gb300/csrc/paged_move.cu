@@ -451,12 +451,21 @@ cudaError_t evict_t(const PagedArgs &a, const PagedEvict &v, int cluster, cudaSt
   return e;
 }
 
-// Short rows take one CTA of few threads, so that many are at work on an SM; of
-// few long rows each is shared by as many CTAs as there is room for.
+// Short rows, and longer ones of which few tokens go, take one CTA of few
+// threads: no barriers of a cluster.  Others are shared by as many CTAs as there
+// is room for.  One CTA of 256 threads against clusters of up to 8 of 512, with
+// the read-back, us (8 kv heads of D = 128):
+//             1025 > 1024  1025 > 512  2049 > 2048  2049 > 1024  4097 > 4096  4097 > 2048
+//   8 rows    10.5 / 15.1  15.6 / 16.1  12.6 / 16.8  23.9 / 17.2  17.3 / 18.8  41.6 / 18.6
+//   64 rows   15.4 / 20.3  18.5 / 19.3  24.6 / 30.7  32.6 / 27.6  46.0 / 48.7  64.3 / 42.2
+//   256 rows  42.2 / 43.8  37.2 / 37.3  73.3 / 74.1  65.0 / 63.4   128 / 127    119 / 116
+// (at 8193 > 8192, 8 rows: 26.5 / 21.4)
 template <int D, int NG>
 cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
   const int64_t rows = (int64_t)a.B * a.H_kv;
-  if (v.capacity <= 2048 || rows >= 8 * sm_count) return evict_t<D, NG, 256, true>(a, v, 1, st);
+  const bool few_go = v.capacity - v.budget <= 128 && v.capacity <= 6144;
+  if (v.capacity <= 1536 || few_go || rows >= 8 * sm_count)
+    return evict_t<D, NG, 256, true>(a, v, 1, st);
   int c = 1;
   while (c < 8 && v.capacity > 1024 * c && rows * c <= sm_count) c *= 2;
   return c == 1 ? evict_t<D, NG, 512, true>(a, v, 1, st)
