@@ -182,7 +182,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.vq_kivi_paged_weights_workspace_bytes.argtypes = [PG, i32, i32, i32]
         L.vq_kivi_paged_keep.argtypes = [PG, PB, P, P, P, P]
         L.vq_kivi_paged_evict_workspace_bytes.restype = size
-        L.vq_kivi_paged_evict_workspace_bytes.argtypes = [PG, i32, i32, i32]
+        L.vq_kivi_paged_evict_workspace_bytes.argtypes = [PG, i32, i32, i32, i32]
         L.vq_kivi_paged_evict.argtypes = [PG, PB, WT, WT, i32, i32, i32, P, P, size, P]
         L.vq_kivi_verify_drafts.argtypes = [ctypes.POINTER(Drafts), cint, P, P, P, P]
         for name in EXPORTS:

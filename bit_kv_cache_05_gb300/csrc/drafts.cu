@@ -77,7 +77,7 @@ struct Values {
   float x[N];
   __device__ __forceinline__ void load(const T *row, int v, int V, bool wide) {
     if (wide && v >= 0 && v + N <= V) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + v));
+      const uint4 u = *reinterpret_cast<const uint4 *>(row + v);
       const T *e = reinterpret_cast<const T *>(&u);
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = as_float(e[i]);

@@ -117,6 +117,18 @@ int check_pool(const vq_kivi_paged *p) {
   return VQ_OK;
 }
 
+// whether two ranges of bytes meet
+bool meet(const void *a, int64_t na, const void *b, int64_t nb) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// workspace of an eviction: none where no sequence can pass the budget
+size_t evict_bytes(const vq_kivi_paged *p, int B, int max_pages, int budget, int recent) {
+  return (int64_t)max_pages * p->page <= budget ? 0
+                                                : paged_evict_ws(B, p->H_kv, budget, recent);
+}
+
 // whether the work line of the attention counts more blocks than 31 bits hold
 bool too_many(const vq_kivi_paged *p, int B, int max_pages) {
   return (int64_t)B * max_pages * (p->page / 16) * p->H_kv > 0x7fffffffLL;
@@ -222,8 +234,7 @@ bool weights_overlap(const PagedEvict &v, const PagedArgs &a) {
   auto span = [&](const PagedWeights &w) {
     return 4 * ((a.B - 1) * w.seq + (a.H_kv - 1) * w.head + v.capacity);
   };
-  const intptr_t x = reinterpret_cast<intptr_t>(v.in.at), y = reinterpret_cast<intptr_t>(v.out.at);
-  return x < y + span(v.out) && y < x + span(v.in);
+  return meet(v.in.at, span(v.in), v.out.at, span(v.out));
 }
 
 // what the three attentions share; tree: masks, weights: where weights are added
@@ -444,14 +455,18 @@ int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
   if (!counts || !lens_out || (a.tokens > 0 && !path)) return fail(VQ_ERR_ARG, "NULL pointer");
   if (!aligned(path, 4) || !aligned(counts, 4) || !aligned(lens_out, 4))
     return fail(VQ_ERR_ARG, "int32 arrays must be 4-byte aligned");
+  // (in place a sequence's length is read and written by one CTA)
+  if (lens_out != a.lens && meet(lens_out, 4 * (int64_t)a.B, a.lens, 4 * (int64_t)a.B))
+    return fail(VQ_ERR_ARG, "lens_out overlaps lens (it may be the same array)");
   cudaError_t e = launch_paged_keep(a, path, counts, lens_out, p->D, (cudaStream_t)stream);
   return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged keep launch");
 }
 
-size_t vq_kivi_paged_evict_workspace_bytes(const vq_kivi_paged *p, int32_t B, int32_t budget,
-                                           int32_t recent) {
-  if (check_pool(p) || B < 0 || budget < 1 || recent < 0 || recent > budget) return 0;
-  const size_t n = paged_evict_ws(B, p->H_kv, budget, recent);
+size_t vq_kivi_paged_evict_workspace_bytes(const vq_kivi_paged *p, int32_t B, int32_t max_pages,
+                                           int32_t budget, int32_t recent) {
+  if (check_pool(p) || B < 0 || max_pages < 0 || budget < 1 || recent < 0 || recent > budget)
+    return 0;
+  const size_t n = evict_bytes(p, B, max_pages, budget, recent);
   return n < 256 ? 256 : n;
 }
 
@@ -479,9 +494,9 @@ int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch
   if (!lens_out || !aligned(lens_out, 4))
     return fail(VQ_ERR_ARG, "lens_out is NULL or misaligned");
   // heads read the lengths while another's sequence is done
-  const intptr_t l = reinterpret_cast<intptr_t>(a.lens), o = reinterpret_cast<intptr_t>(lens_out);
-  if (l < o + 4 * a.B && o < l + 4 * a.B) return fail(VQ_ERR_ARG, "lens_out overlaps lens");
-  const size_t need = paged_evict_ws(a.B, p->H_kv, budget, recent);
+  if (meet(lens_out, 4 * (int64_t)a.B, a.lens, 4 * (int64_t)a.B))
+    return fail(VQ_ERR_ARG, "lens_out overlaps lens");
+  const size_t need = evict_bytes(p, a.B, a.max_pages, budget, recent);
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return fail(VQ_ERR_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
   if ((rc = sm_count(&sms))) return rc;
@@ -518,6 +533,15 @@ int vq_kivi_verify_drafts(const vq_kivi_drafts *d, int dtype, int32_t *path, int
       !aligned(after, wide) || !aligned(d->parent, 4) || !aligned(d->cu_new, 4) ||
       !aligned(d->uniforms, 4) || !aligned(path, 4) || !aligned(counts, 4))
     return fail(VQ_ERR_ARG, "misaligned pointer");
+  // the CTAs of a sequence read its nodes each for itself
+  const struct { const void *at; int64_t bytes; } outs[3] = {
+      {path, 4 * d->tokens}, {counts, 4 * (int64_t)d->B}, {after, wide * (int64_t)d->B}},
+      ins[4] = {{d->token, wide * d->tokens}, {d->parent, d->parent ? 4 * d->tokens : 0},
+                {d->uniforms, 4 * d->tokens}, {d->cu_new, 4 * ((int64_t)d->B + 1)}};
+  for (const auto &o : outs)
+    for (const auto &i : ins)
+      if (o.bytes > 0 && i.bytes > 0 && meet(o.at, o.bytes, i.at, i.bytes))
+        return fail(VQ_ERR_ARG, "an output overlaps an input");
   if ((rc = sm_count(&sms))) return rc;
   Drafts x;
   x.target = d->target;

@@ -278,7 +278,8 @@ class PagedKiviCache:
         of the largest weights.  Kept tokens in front of the newest stay in
         their places or fill those of the evicted ones, the newest follow in
         their order; places say no longer a token's position, so later appends
-        give theirs.  Pages behind the budget are the caller's again.
+        give theirs.  Pages behind the budget are the caller's again; no other
+        sequence may share the pages before it.
 
         Returns (lens_out, weights_out): the lengths (not lens itself) and the
         weights, moved with their tokens and zero behind (weights_out may be
@@ -296,7 +297,8 @@ class PagedKiviCache:
         wo = self._weights(weights_out, batch, "weights_out")
         lens_out = self._lens_out(lens_out, batch.B)
         budget, recent, first = int(budget), int(recent), int(first)
-        nbytes = self._lib.vq_kivi_paged_evict_workspace_bytes(self._spec, batch.B, budget, recent)
+        nbytes = self._lib.vq_kivi_paged_evict_workspace_bytes(self._spec, batch.B,
+                                                               batch.max_pages, budget, recent)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         rc = self._lib.vq_kivi_paged_evict(self._spec, batch, w, wo, budget, recent, first,
                                            lens_out.data_ptr() or None, ws.data_ptr() or None,

@@ -609,7 +609,7 @@ size_t vq_kivi_paged_weights_workspace_bytes(const vq_kivi_paged *p, int32_t B,
  * among them; the others then begin at place 0.)
  *   path           device int32 [tokens]
  *   counts         device int32 [B]
- *   lens_out       device int32 [B], may be lens
+ *   lens_out       device int32 [B], lens itself or apart from it
  * At most 64 new tokens per sequence.  A sequence whose path does not rise
  * within its new tokens, or whose count is outside its range (a count of -1
  * among them), is left as it was, and reported by vq_kivi_paged_status. */
@@ -626,6 +626,7 @@ int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
  * ones; the newest follow in their order.  Weights move with their tokens, and
  * the places behind, up to max_pages * page, are zero.  Pages behind the budget are the caller's again.
  * A token's place no longer says its position: later appends give theirs.
+ * Tokens move within their sequence's pages: no other sequence may share them.
  *   batch          cu_new NULL, tokens = B; lens: all tokens
  *   weights_out    as weights; the same array (in place) or one that does not
  *                  overlap it
@@ -637,7 +638,8 @@ int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch
                         int32_t recent, int32_t first, int32_t *lens_out,
                         void *workspace, size_t workspace_bytes, void *stream);
 size_t vq_kivi_paged_evict_workspace_bytes(const vq_kivi_paged *p, int32_t B,
-                                           int32_t budget, int32_t recent);
+                                           int32_t max_pages, int32_t budget,
+                                           int32_t recent);
 
 /* Synchronizes `stream` and reports what kernels found since the last check:
  * VQ_ERR_ARG for a page or a length outside its range, VQ_ERR_CUDA for a wait
@@ -680,7 +682,7 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
  * path int32 [tokens]: from row cu_new[b] on the nodes that stay, node 0 first,
  * -1 behind them; counts int32 [B]: how many (vq_kivi_paged_keep takes both);
  * after [B], in the tokens' type: the last token, -1 where a row has no
- * positive probability.  A sequence without nodes gets a count of 0 and -1; one
+ * positive probability.  Outputs may not overlap the nodes' arrays.  A sequence without nodes gets a count of 0 and -1; one
  * whose offsets, parents or tokens lie outside their ranges, or with more than
  * 64 nodes, a count of -1, -1, and -1 in its path where its rows are in range.
  * B <= 1024, V <= 2^19. */

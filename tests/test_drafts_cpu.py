@@ -70,6 +70,24 @@ def test_weights_refusals(vqlib, kw, max_new, code):
     assert vqlib.vq_kivi_paged_weights_workspace_bytes(_paged(), 1 << 20, 1 << 20, 1) == 0
 
 
+@pytest.mark.parametrize("path,counts,after", [
+    (P + 64, 2 * P, 3 * P), (2 * P, P, 3 * P), (2 * P, 3 * P, P + 56), (P - 28, 2 * P, 3 * P),
+])
+def test_verify_outputs_over_its_inputs(vqlib, path, counts, after):
+    """The CTAs of a sequence read its nodes each for itself: what they read may
+    not change under them."""
+    far = 1 << 24
+    d = _drafts(token=P, parent=P + 64, uniforms=P + 96, cu_new=P + 128, target=far, draft=far)
+    rc = vqlib.vq_kivi_verify_drafts(d, 2, path, counts, after, None)
+    assert rc == -1 and b"overlaps" in vqlib.vq_kivi_last_error()
+
+
+def test_keep_lengths_half_over(vqlib):
+    b = _batch(cu_new=P, tokens=8, lens=2 * P)
+    assert vqlib.vq_kivi_paged_keep(_paged(), b, P, P, 2 * P + 4, None) == -1
+    assert b"overlaps" in vqlib.vq_kivi_last_error()
+
+
 @pytest.mark.parametrize("which", ["path", "counts", "lens_out", "odd"])
 def test_keep_refusals(vqlib, which):
     b = _batch(cu_new=P, tokens=8)
@@ -106,8 +124,11 @@ def test_evict_refusals(vqlib, kw, code):
 
 def test_evict_workspace(vqlib):
     f = vqlib.vq_kivi_paged_evict_workspace_bytes
-    assert f(_paged(), 3, 100, 40) == 3 * 2 * 60 * 8
-    assert f(_paged(), 1, 1, 1) == 256 and f(_paged(), 1, 0, 0) == 0 and f(_paged(), 1, 5, 6) == 0
+    assert f(_paged(), 3, 4, 100, 40) == 3 * 2 * 60 * 8
+    assert f(_paged(), 3, 4, 256, 40) == 256                  # no sequence can pass it
+    assert f(_paged(), 3, 4, 2 ** 31 - 1, 0) == 256
+    assert f(_paged(), 1, 4, 1, 1) == 256 and f(_paged(), 1, 4, 0, 0) == 0
+    assert f(_paged(), 1, 4, 5, 6) == 0 and f(_paged(), 1, -1, 5, 1) == 0
 
 
 @pytest.mark.parametrize("kw,dtype,code", [
