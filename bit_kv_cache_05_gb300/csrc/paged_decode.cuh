@@ -621,6 +621,8 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix, floa
   const int H = a.H_kv, GQ = a.H_q / H, R = t.max_new * GQ;
   const int row = blockIdx.x % R, seg = blockIdx.x / R, b = seg / H, h = seg % H;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (k_paged_weigh reads nothing before its own wait)
+  if constexpr (WEIGH) asm volatile("griddepcontrol.launch_dependents;");
   const Seq L = sequence_of(a, b, t.max_new);
   const int units = prefix[a.B], p0 = prefix[b], nb = (prefix[b + 1] - p0) / H;
   if (row >= L.n * GQ) return;
