@@ -726,3 +726,170 @@ def test_empty_calls():
                             torch.zeros(0, device="cuda"), i32([0, 0]))
     assert k.tolist() == [0] and a.tolist() == [-1]
     c.status()
+
+
+def test_readme_samples_of_drafts_and_eviction():
+    """The README's two samples as they stand."""
+    import os
+    from bit_kv_cache_05_gb300 import verify_drafts
+    from bit_kv_cache_05_gb300.rope import Rope
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    code = [b.split("```")[0] for b in text.split("```python")[1:]]
+    trees = [b for b in code if "verify_drafts(" in b]
+    evict = [b for b in code if ".evict(" in b]
+    assert len(trees) == len(evict) == 1
+    B, H_q, H_kv, D, V, n, lens = 2, 8, 2, 128, 97, [9, 5], [700, 300]
+    c, table, L = filled([s + 9 for s in lens], 16, H_q, H_kv, D, 32, torch.bfloat16)
+    rng = random.Random(6)
+    p, dr, tokens, parents, u = draft_case(31, n, V, "fp32", False, True)
+    T = sum(n)
+    x = randn(1, T, H_q + 2 * H_kv, D).to(torch.bfloat16)
+    at = [0, n[0]]
+    trees_of = [parents[a:a + k] for a, k in zip(at, n)]
+    env = dict(cache=c, verify_drafts=verify_drafts, rope=Rope(rot_dim=D), table=table,
+               lens=i32(lens), full=i32([a + b for a, b in zip(lens, n)]), cu=offsets(n),
+               q=x[:, :H_q], k=x[:, H_q:H_q + H_kv], v=x[:, H_q + H_kv:], max_nodes=max(n),
+               seq=i64([0] * n[0] + [1] * n[1]),
+               depth=i32(d for t in trees_of for d in dref.depths_of(t)),
+               masks=i64(m for t in trees_of for m in dref.masks_of(t)), parents=i32(parents),
+               tokens=i64(tokens), uniforms=u.cuda(), target=p.cuda(), draft=dr.cuda())
+    exec(trees[0], env)
+    c.status()
+    want = [dref.verify(p[a:a + k].numpy(), dr[a:a + k].numpy(), tokens[a:a + k],
+                        parents[a:a + k], u[a:a + k].numpy()) for a, k in zip(at, n)]
+    assert env["after"].tolist() == [w[1] for w in want]
+    assert env["lens"].tolist() == [a + len(w[0]) for a, w in zip(lens, want)]
+    kept = env["lens"].tolist()
+    x = randn(2, B, H_q + 2 * H_kv, D).to(torch.bfloat16)
+    env.update(q=x[:, :H_q], k=x[:, H_q:H_q + H_kv], v=x[:, H_q + H_kv:], budget=512,
+               lens=i32([s + 1 for s in kept]), position=i32(kept),
+               weights=torch.zeros(B, H_kv, table.shape[1] * 16, device="cuda"))
+    exec(evict[0], env)
+    c.status()
+    assert env["lens"].tolist() == [512, kept[1] + 1]
+    assert abs(float(env["weights"][1].sum()) - H_q) < 1e-3
+
+
+def test_rows_behind_the_last_sequence_stay():
+    """Token tensors with more rows than the sequences have: the rows behind are
+    neither read nor written."""
+    from bit_kv_cache_05_gb300 import verify_drafts
+    for n, H_q in (([4, 3], 4), ([20, 9], 4), ([40, 30], 8)):
+        lens = [n[0] + 70, n[1] + 5]
+        c, table, L = filled(lens, 16, H_q, 1, 64, 32)
+        T, extra, cu = sum(n), 5, offsets(n)
+        q = randn(3, T + extra, H_q, 64).half()
+        q[T:] = float("nan")
+        rng = random.Random(2)
+        masks = [m for k in n for m in dref.masks_of(dref.random_tree(k, rng))]
+        out = torch.full_like(q, 7.0)
+        c.attend(q, table, L, cu, max_new=max(n), tree=i64(masks + [-1] * extra), out=out)
+        want = c.attend(q[:T], table, L, cu, max_new=max(n), tree=i64(masks))
+        assert torch.equal(out[:T], want) and (out[T:] == 7).all()
+        p, dr, tokens, parents, u = draft_case(5, n, 50, "fp32", False, True)
+        pad = lambda t, x: torch.cat((t, torch.full((extra, *t.shape[1:]), x, dtype=t.dtype)))
+        path = torch.full((T + extra,), 9, dtype=torch.int32, device="cuda")
+        verify_drafts(pad(p, 2.0).cuda(), pad(torch.tensor(tokens), -5).cuda(), pad(u, 3.0).cuda(),
+                      cu, parents=pad(torch.tensor(parents, dtype=torch.int32), 99).cuda(),
+                      draft=pad(dr, -1.0).cuda(), path=path)
+        ref_path, counts, _ = run_verify(p, dr, tokens, parents, u, n)
+        assert torch.equal(path[:T], ref_path) and (path[T:] == 9).all()
+        kept = c.keep(table, L, cu, path, counts)
+        assert kept.tolist() == [s - k + int(x) for s, k, x in zip(lens, n, counts)]
+        c.status()
+
+
+def test_offsets_past_32_bits_of_drafts_and_eviction():
+    """Pages whose bytes lie past 2^32 of the pool."""
+    D, g, page, H = 128, 32, 128, 8
+    n_pages = 2 ** 32 // (H * 8 * 2560) + 5
+    c = new_cache(n_pages, page, H, H, D, g, fill=0)
+    table = i32([n_pages - 1, 1, n_pages - 3]).view(1, 3)
+    S = 300
+    k, v = randn(1, S, H, D).half(), randn(2, S, H, D).half()
+    c.append(k, v, table, i32([S]), offsets([S]))
+    rng = random.Random(1)
+    for n in (4, 40):
+        masks = dref.masks_of(dref.random_tree(n, rng))
+        check_tree(c, table, [S], [n], masks, "fp16", H, H, D, g)
+    K, V = c.dequantize(table, i32([S]), offsets([S]), n_tokens=S)
+    path = [0, 3, 17, 31]
+    L = c.keep(table, i32([S]), offsets([40]), i32(path + [0] * 36), i32([4]))
+    order = list(range(260)) + [260 + x for x in path]
+    K1, V1 = c.dequantize(table, L, offsets([264]), n_tokens=264)
+    assert L.tolist() == [264] and torch.equal(K1, K[order]) and torch.equal(V1, V[order])
+    w = evict_weights([264], H, 384, "plain")
+    L2, w2 = c.evict(table, L, w, 150, recent=20, first=3)
+    K2, V2 = c.dequantize(table, L2, offsets([150]), n_tokens=150)
+    for h in range(H):
+        take = dref.evict_row(w[0, h].cpu(), 264, 150, 20, 3)
+        assert torch.equal(K2[:, h], K1[take, h]) and torch.equal(V2[:, h], V1[take, h])
+        assert torch.equal(w2[0, h, :150], w[0, h][take]) and (w2[0, h, 150:] == 0).all()
+    c.status()
+
+
+def test_most_sequences_of_a_call():
+    """1024 sequences, as many as a call takes."""
+    B, n = 1024, 3
+    lens = [3 + b % 30 for b in range(B)]
+    c, table, L = filled(lens, 16, 2, 1, 64, 32)
+    q = randn(4, B * n, 2, 64).half()
+    masks = [1, 3, 5] * B
+    out = c.attend(q, table, L, offsets([n] * B), max_new=n, tree=i64(masks))
+    big = c.attend(q, table, L, offsets([n] * B), max_new=40, tree=i64(masks))  # the other kernel
+    assert ((out.float() - big.float()).abs() <= 2.0 ** -9 * big.float().abs() + 2.0 ** -9).all()
+    acc = torch.zeros(B, 1, table.shape[1] * 16, device="cuda")
+    c.attend(q[:B], table, L, weights=acc)
+    assert ((acc.sum(-1) - 2).abs() < 1e-4).all()
+    p, dr, tokens, parents, u = draft_case(8, [n] * B, 20, "fp32", False, True)
+    path, counts, after = run_verify(p, dr, tokens, parents, u, [n] * B)
+    for b in (0, 511, 1023):
+        s = slice(n * b, n * b + n)
+        want, token = dref.verify(p[s].numpy(), dr[s].numpy(), tokens[s], parents[s], u[s].numpy())
+        assert path[s].tolist()[:len(want)] == want and int(after[b]) == token
+    before = c.pool.clone()
+    kept = c.keep(table, L, offsets([n] * B), path, counts)
+    moves = [(b, 0, lens[b] - n + j, lens[b] - n + x) for b in range(B)
+             for j, x in enumerate(path[n * b:n * b + int(counts[b])].tolist())]
+    assert torch.equal(c.pool.cpu(), dref.move_tokens(before, table, 64, 32, moves))
+    check_evict(c, table, kept.tolist(), acc, 12, 4, 1, 64, 32)
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side on two streams share nothing: each gives what
+    it gives alone."""
+    jobs = []
+    for seed in (1, 2):
+        c, table, L = filled([900, 500], 16, 8, 2, 128, 32, seed=10 * seed)
+        n = [24, 17]
+        rng = random.Random(seed)
+        masks = i64(m for k in n for m in dref.masks_of(dref.random_tree(k, rng)))
+        jobs.append((c, table, L, n, masks, randn(seed, 41, 8, 128).half(),
+                     torch.rand(2, 2, table.shape[1] * 16, device="cuda"),
+                     draft_case(seed, n, 5000, "fp32", False, True), c.pool.clone()))
+
+    def run(job, stream):
+        c, table, L, n, masks, q, w, d, pool = job
+        with torch.cuda.stream(stream):
+            c.pool.copy_(pool)
+            acc, got = w.clone(), []
+            for _ in range(5):
+                got.append(c.attend(q, table, L, offsets(n), max_new=24, tree=masks))
+                got.append(c.attend(q[:2], table, L, weights=acc))
+                got += run_verify(*d, n)
+                got += c.evict(table, L, acc, 400, recent=30)
+            return got + [acc, c.pool.clone()]
+
+    alone = []
+    for job in jobs:
+        alone.append(run(job, torch.cuda.current_stream()))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    both = [run(job, s) for job, s in zip(jobs, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+    for job in jobs:
+        job[0].status()
