@@ -554,8 +554,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     // The stages go back to the rebuilding warps from here: a commit of the
     // tensor cores holds the next products up by more than 100 cycles, and
     // the scores' own already says that the products before them are done.
-    // Slot 1 is the later user of a tile that both slots use.
-    const bool gives = (warp & 3) == 0 && lane == 0;
+    // Slot 1 is the later user of a tile that both slots use.  (The small form's
+    // warps see a tile's scores only when they are done with the tile before: a
+    // warp of its own gives the stages back.)
+    const bool gives = !SMALL && (warp & 3) == 0 && lane == 0;
     bool ok = true;
     settle();
     if (have) load_q();
@@ -737,7 +739,6 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       if (!__all_sync(kFull, ok)) { ok = false; break; }
       fence_after();
       if (gives && (!two || wg == 1)) bar_arrive(&B.v_empty[vlast]);
-      if (SMALL && gives && steps > 1) bar_arrive(&B.v_empty[vlast ^ 1]);
       float f0 = 1.f, f1 = 0.f;
       if (halves && wg == 0) {
         ok = bar_wait(&B.x_full, ph_x, dead);
@@ -1041,6 +1042,31 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       mma_commit(&B.drain);
       int never = 0;
       bar_wait(&B.drain, 0, &never);
+    }
+  } else if (SMALL && warp == R::ISSUE + 3) {
+    // ---- stages given back: a tile's keys when its scores are there, which
+    // also says that the products issued before them are done ----
+    uint32_t at = 0, ph_s = 0, ph_o = 0, ph_o1 = 0;    // tile; ph_s: a bit a buffer
+    bool ok = true;
+    for (; ok && have; have = advance()) {
+      const int nt = walk.steps(tpt);
+      for (int j = 0; ok && j < nt; ++j, ++at) {
+        const uint32_t buf = at & 1;
+        ok = __all_sync(kFull, bar_wait(&B.s_full[buf], (ph_s >> buf) & 1u, dead));
+        ph_s ^= 1u << buf;
+        if (ok && lane == 0) {
+          bar_arrive(&B.k_empty[buf]);
+          if (j >= 2) bar_arrive(&B.v_empty[buf]);
+        }
+      }
+      if (ok && nt > 1) {
+        ok = __all_sync(kFull, bar_wait(&B.o_full[1], ph_o1, dead));
+        ph_o1 ^= 1u;
+        if (ok && lane == 0) bar_arrive(&B.v_empty[at & 1]);
+      }
+      ok = ok && __all_sync(kFull, bar_wait(&B.o_full[0], ph_o, dead));
+      ph_o ^= 1u;
+      if (ok && lane == 0) bar_arrive(&B.v_empty[(at + 1) & 1]);
     }
   } else if (warp == R::ISSUE + 1 || warp == R::ISSUE + 2) {
     // ---- copies of keys, of values ----
