@@ -14,7 +14,7 @@
 // A CTA works in two slots, so that one is multiplied while the other is in
 // its softmax: the two query tiles of a pair, or, where the second would be
 // empty, the even and the odd key tiles of one query tile (joined at the
-// end).  Its warps:
+// end).  Its warps (the form for few rows has others: Roles):
 //   0-3, 4-7   softmax of slot 0 and 1, one row a thread: scores from tensor
 //              memory, online softmax in fp32, weights back to tensor memory
 //              in fp16 (the A operand of the second product), the output
@@ -50,7 +50,7 @@ namespace chunk {
 namespace {
 
 constexpr int kTile = 128;           // keys of a tile, rows of a query tile
-constexpr int kRawMost = 6;          // stages as stored, of keys or of values
+constexpr int kRaw = 3;              // stages as stored, of keys and of values
 constexpr int kSmallRows = 64;       // rows of a pair that the small form takes
 constexpr unsigned kFull = 0xffffffffu;
 // exponents of a fresh maximum's weight and of the largest one (see above)
@@ -370,17 +370,20 @@ struct alignas(16) CutPair {
 // the second the others, as if each had half the sequence, and the two are
 // joined at the end.  So four warps share a tile's softmax, one output
 // accumulator serves all, and the scores of the next tile are there when a tile
-// is done.  One tile of queries and twice the warps for the values, which leaves
-// room for more stages.  setmaxnreg: 256 x 144 + 384 x 64, or 128 x 200 + 384 x
-// 72 + 128 x 64, of the launch's 640 x 96 registers.
+// is done.  One tile of queries, which leaves room for larger stages; twice the
+// warps for keys and for values; and a warp that gives the stages back, since the
+// softmax warps see a tile's scores only when they are done with the one before.
+// 16 trees of 16 nodes and 4 heads at 4096 to 8192, us: two slots as in the large
+// form 81.4; halves of a tile 80.7; stages given back by a warp 79.9; eight warps
+// for the keys too 77.9.  setmaxnreg: 256 x 144 + 384 x 64, or 128 x 160 + 512 x
+// 64 + 128 x 64, of the launch's 640 x 96 or 768 x 80 registers.
 template <bool SMALL>
 struct Roles {
   static constexpr int SOFT = SMALL ? 4 : 8;       // softmax warps
-  static constexpr int KEYS = 4, VALUES = SMALL ? 8 : 4;   // that rebuild keys, values
-  static constexpr int ISSUE = SOFT + KEYS + VALUES;       // the issuing warp; copies: + 1, + 2
+  static constexpr int BUILD = SMALL ? 8 : 4;      // that rebuild keys, and values: a block
+                                                   // of a stage as stored each
+  static constexpr int ISSUE = SOFT + 2 * BUILD;   // the issuing warp; copies: + 1, + 2; + 3
   static constexpr int THREADS = 32 * (ISSUE + 4);
-  // a stage as stored has a block for each warp that rebuilds it
-  static constexpr int ROOM = SMALL ? 24 : 12;     // blocks of keys, and of values
 };
 
 template <int D, int NG, bool SMALL>
@@ -389,8 +392,8 @@ struct Smem {
   static constexpr int OP = KB * 16384;            // one 128 x D fp16 operand
   static constexpr int BLK = 16 * D + 128 * NG, HALF = BLK / 2;   // keys, values
   static constexpr int Q = 0, K = (SMALL ? 1 : 2) * OP, V = K + 2 * OP, RAW = V + 2 * OP;
-  static constexpr int BAR = RAW + Roles<SMALL>::ROOM * BLK;
-  static constexpr int PREFIX = BAR + 512;
+  static constexpr int BAR = RAW + kRaw * Roles<SMALL>::BUILD * BLK;
+  static constexpr int PREFIX = BAR + 384;
   static constexpr int ALLOC = PREFIX + 8 * (kNear + 1) + 8 + 1024;   // room to align the base
 };
 
@@ -398,11 +401,11 @@ struct Smem {
 __device__ __forceinline__ int sw(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 struct Bars {
-  uint64_t raw_full[2][kRawMost], raw_empty[2][kRawMost];   // keys, values
+  uint64_t raw_full[2][kRaw], raw_empty[2][kRaw];   // keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t x_full, drain;
-  uint32_t good[2][kRawMost];   // which of a stage's blocks arrived
+  uint32_t good[2][kRaw];   // which of a stage's blocks arrived
   uint32_t tmem;
   int dead;
   CutPair cut;
@@ -418,17 +421,17 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Bars &B = *reinterpret_cast<Bars *>(sm + SM::BAR);
-  static_assert(sizeof(Bars) <= 512, "barriers fit");
+  static_assert(sizeof(Bars) <= 384, "barriers fit");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int GQ = a.H_q / a.H_kv, tpt = kTile / GQ;
   if (tid == 0) {
-    for (int i = 0; i < 2 * kRawMost; ++i) {
+    for (int i = 0; i < 2 * kRaw; ++i) {
       bar_init(&B.raw_full[0][0] + i, 1);
-      bar_init(&B.raw_empty[0][0] + i, i < kRawMost ? R::KEYS : R::VALUES);
+      bar_init(&B.raw_empty[0][0] + i, R::BUILD);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&B.k_full[i], R::KEYS);
-      bar_init(&B.v_full[i], R::VALUES);
+      bar_init(&B.k_full[i], R::BUILD);
+      bar_init(&B.v_full[i], R::BUILD);
       bar_init(&B.k_empty[i], 1);
       bar_init(&B.v_empty[i], 1);
       bar_init(&B.q_full[i], 4);
@@ -470,12 +473,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
 
   if (warp < R::SOFT) {
     // ---- softmax ----
-    if constexpr (SMALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if constexpr (SMALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // slot (small: half of a tile's keys), lane of the accumulators, row of the
     // query tile
     const int wg = warp / (R::SOFT / 2), at_row = tid & 127, row = SMALL ? at_row & 63 : at_row;
-    constexpr int KEYS = SMALL ? 64 : kTile;         // of a tile that a thread weighs
+    // keys of a tile that a thread weighs, and that it holds at once
+    constexpr int KEYS = SMALL ? 64 : kTile, CH = SMALL ? 32 : 64;
     const int c0 = SMALL ? 64 * wg : 0;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t to = tl + 256 + (SMALL ? 0 : 128 * wg);
@@ -626,26 +630,27 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           float mo = m;       // the maximum that the tile's weights stand on
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < KEYS; c += 64) {
-            uint32_t v[64];
-            tm_ld64(ts + c0 + c, v);
+          for (int c = 0; c < KEYS; c += CH) {
+            uint32_t v[CH];
+            if constexpr (CH == 64) tm_ld64(ts + c0 + c, v);
+            else tm_ld32(ts + c0 + c, v);
             if (!all) {
               if constexpr (TREE) {
                 const unsigned long long seen = tree_columns(tree, c0 + c - 1 - vis);
                 const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
+                for (int j = 0; j < CH; ++j)
                   if (!((j < 32 ? lo >> j : hi >> (j - 32)) & 1u))
                     v[j] = __float_as_uint(-INFINITY);
               } else {
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
+                for (int j = 0; j < CH; ++j)
                   if (c0 + c + j > vis) v[j] = __float_as_uint(-INFINITY);
               }
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 64; j += 2)
+            for (int j = 0; j < CH; j += 2)
               mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
             const float top = scale * fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
             if (__any_sync(kFull, top + (kTop - mo) > kMost)) {
@@ -656,13 +661,13 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
               if (c > 0) {
                 // the weights of this tile so far
                 sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
-                lower_weights(ts, c, f);
+                lower_weights(ts + c0 / 2, c, f);
               }
               mo = mn;
             }
             const float base = mo == -INFINITY ? 0.f : kTop - mo;
 #pragma unroll
-            for (int d = 0; d < 64; d += 32) {
+            for (int d = 0; d < CH; d += 32) {
               uint32_t p[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
@@ -794,11 +799,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     }
   } else if (warp < R::ISSUE) {
     // ---- k_hat, v_hat ----
-    if constexpr (SMALL) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (SMALL) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // keys or values, block of a stage
-    const int kv = warp >= R::SOFT + R::KEYS ? 1 : 0, w = warp - R::SOFT - (kv ? R::KEYS : 0),
-              blocks = kv ? R::VALUES : R::KEYS, stages = R::ROOM / blocks, n8 = lane >> 2,
+    const int kv = (warp - R::SOFT) / R::BUILD, w = (warp - R::SOFT) % R::BUILD, n8 = lane >> 2,
               t4 = lane & 3;
     // values: where this lane's four stores of 8 tokens go, and the shifts to
     // the nibbles that they hold (the lanes of a store differ in the channel's
@@ -822,11 +826,11 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       for (int j = 0; ok && j < steps; ++j, left -= kTile) {
         ok = bar_wait(&empty[st], ph_e, dead);
         unsigned char *dst = sm + (kv ? SM::V : SM::K) + st * SM::OP;
-        for (int k0 = 0; k0 < 8; k0 += blocks) {
+        for (int k0 = 0; k0 < 8; k0 += R::BUILD) {
           ok = ok && bar_wait(&B.raw_full[kv][raw], ph_raw, dead);
           if (!__all_sync(kFull, ok)) { ok = false; break; }
           const unsigned char *blk =
-              sm + SM::RAW + (kv * R::ROOM + raw * blocks + w) * SM::HALF;
+              sm + SM::RAW + ((kv * kRaw + raw) * R::BUILD + w) * SM::HALF;
           const bool good = (B.good[kv][raw] >> w) & 1u;
           const int r0 = 16 * (k0 + w);                // its first key in the tile
           if (!kv) {
@@ -927,7 +931,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
           }
           __syncwarp();
           if (lane == 0) bar_arrive(&B.raw_empty[kv][raw]);
-          raw = (int)raw + 1 == stages ? 0 : raw + 1;
+          raw = raw + 1 == kRaw ? 0 : raw + 1;
           ph_raw ^= raw == 0;
         }
         if (!ok) break;
@@ -1070,8 +1074,8 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     }
   } else if (warp == R::ISSUE + 1 || warp == R::ISSUE + 2) {
     // ---- copies of keys, of values ----
-    const int kv = warp - R::ISSUE - 1, bpp = a.page_log2 - 4,
-              blocks = kv ? R::VALUES : R::KEYS, stages = R::ROOM / blocks;
+    constexpr int SB = R::BUILD;   // blocks of a stage
+    const int kv = warp - R::ISSUE - 1, bpp = a.page_log2 - 4;
     uint32_t raw = 0, ph_e = 1;
     uint32_t used = 0;             // stages with copies not known to have landed
     bool ok = true;
@@ -1090,7 +1094,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
       // is met once in 512 tokens
       const uint8_t *src = nullptr;
       unsigned there = 0u;
-      for (int k = 8 * walk.k, i = 0; ok && k < end; k += blocks, i = (i + blocks) & 31) {
+      for (int k = 8 * walk.k, i = 0; ok && k < end; k += SB, i = (i + SB) & 31) {
         if (i == 0) {
           const int blk = k + lane;
           bool good = blk < nblk && blk < end;
@@ -1107,24 +1111,24 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
         }
         ok = bar_wait(&B.raw_empty[kv][raw], ph_e, dead);
         if (!__all_sync(kFull, ok)) { ok = false; break; }
-        const unsigned mask = (there >> i) & ((1u << blocks) - 1u);
+        const unsigned mask = (there >> i) & ((1u << SB) - 1u);
         if (lane == 0) {
           B.good[kv][raw] = mask;
           mbar_expect_tx(&B.raw_full[kv][raw], __popc(mask) * SM::HALF);
         }
         __syncwarp();
-        if (lane >= i && lane < i + blocks && (there >> lane & 1u))
-          bulk_g2s(sm + SM::RAW + (kv * R::ROOM + raw * blocks + lane - i) * SM::HALF, src,
-                   SM::HALF, &B.raw_full[kv][raw]);
+        if (lane >= i && lane < i + SB && (there >> lane & 1u))
+          bulk_g2s(sm + SM::RAW + ((kv * kRaw + raw) * SB + lane - i) * SM::HALF, src, SM::HALF,
+                   &B.raw_full[kv][raw]);
         used |= 1u << raw;
-        raw = (int)raw + 1 == stages ? 0 : raw + 1;
+        raw = raw + 1 == kRaw ? 0 : raw + 1;
         ph_e ^= raw == 0;
       }
     }
     // copies in flight land before the shared memory is given up: the phase
     // of a stage's last copies is the one before its next turn's
     if (lane == 0) {
-      for (int i = 0; i < stages; ++i) {
+      for (int i = 0; i < kRaw; ++i) {
         int never = 0;
         const uint32_t turn = (uint32_t)i < raw ? ph_e ^ 1u : ph_e;   // parity of its last full
         if ((used >> i) & 1u) bar_wait(&B.raw_full[kv][i], turn, &never);
