@@ -259,7 +259,7 @@ struct PagedAttend {
 // accumulated weights: element (sequence, kv head, token) at at[b seq + h head + t]
 struct PagedWeights {
   float *at;
-  int64_t seq, head;
+  int64_t seq, head, capacity;   // capacity: places of a row
 };
 
 // few rows: up to 16 (new token, query head) pairs per kv head
@@ -288,7 +288,6 @@ cudaError_t launch_paged_keep(const PagedArgs &a, const int32_t *path, const int
                               int32_t *lens_out, int D, cudaStream_t st);
 struct PagedEvict {
   PagedWeights in, out;
-  int64_t capacity;          // tokens of a row of weights
   int32_t *lens_out;
   int budget, recent, first;
   int2 *pairs;               // workspace: (place to fill, token that fills it)

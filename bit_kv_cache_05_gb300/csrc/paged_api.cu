@@ -217,22 +217,23 @@ int check_weights(const vq_kivi_paged *p, const PagedArgs &a, const vq_kivi_weig
       return fail(VQ_ERR_ARG, "%s has room for %lld tokens, the table for %lld", name,
                   (long long)w->capacity, (long long)room);
     // no two rows may share a place
-    const int64_t s = w->seq_stride, h = w->head_stride, H = p->H_kv, B = a.B;
+    const int64_t s = w->seq_stride, h = w->head_stride, H = p->H_kv, B = a.B, n = w->capacity;
     const bool one_b = B == 1, one_h = H == 1;
-    if ((!one_b && s < room) || (!one_h && h < room) ||
-        (!one_b && !one_h && s < (H - 1) * h + room && h < (B - 1) * s + room))
+    if ((!one_b && s < n) || (!one_h && h < n) ||
+        (!one_b && !one_h && s < (H - 1) * h + n && h < (B - 1) * s + n))
       return fail(VQ_ERR_ARG, "%s: rows overlap", name);
   }
   to->at = w->at;
   to->seq = a.B == 1 ? 0 : w->seq_stride;
   to->head = p->H_kv == 1 ? 0 : w->head_stride;
+  to->capacity = w->capacity;
   return VQ_OK;
 }
 
 // whether the ranges that two arrays of weights span meet
 bool weights_overlap(const PagedEvict &v, const PagedArgs &a) {
   auto span = [&](const PagedWeights &w) {
-    return 4 * ((a.B - 1) * w.seq + (a.H_kv - 1) * w.head + v.capacity);
+    return 4 * ((a.B - 1) * w.seq + (a.H_kv - 1) * w.head + w.capacity);
   };
   return meet(v.in.at, span(v.in), v.out.at, span(v.out));
 }
@@ -257,7 +258,8 @@ int attend(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch, int dtype,
     return fail(VQ_ERR_ARG, "the output must be contiguous [tokens][H_q][D]");
   if (max_new < 1) return fail(VQ_ERR_ARG, "max_new=%d < 1", max_new);
   if (with_tree) {
-    if ((!tree && a.tokens > 0) || !aligned(tree, 8)) return fail(VQ_ERR_ARG, "tree is NULL or misaligned");
+    if ((!tree && a.tokens > 0) || !aligned(tree, 8))
+      return fail(VQ_ERR_ARG, "tree is NULL or misaligned");
     if (max_new > kMaxTree)
       return fail(VQ_ERR_UNSUPPORTED, "a tree has at most %d nodes, max_new=%d", kMaxTree,
                   max_new);
@@ -486,9 +488,9 @@ int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch
   PagedEvict v;
   if ((rc = check_weights(p, a, weights, "weights", &v.in))) return rc;
   if ((rc = check_weights(p, a, weights_out, "weights_out", &v.out))) return rc;
-  v.capacity = (int64_t)a.max_pages << a.page_log2;
   if (a.B == 0) return VQ_OK;
-  if (v.in.at == v.out.at ? v.in.seq != v.out.seq || v.in.head != v.out.head
+  if (v.in.at == v.out.at ? v.in.seq != v.out.seq || v.in.head != v.out.head ||
+                                v.in.capacity != v.out.capacity
                           : weights_overlap(v, a))
     return fail(VQ_ERR_ARG, "weights_out overlaps weights (it may be the same array)");
   if (!lens_out || !aligned(lens_out, 4))

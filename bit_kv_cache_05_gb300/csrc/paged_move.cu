@@ -211,7 +211,7 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   const int64_t step = (int64_t)ctas * THREADS, me = (int64_t)rank * THREADS + tid;
   if (!ok) return;
   if (len <= e.budget) {
-    for (int64_t p = (same ? len : 0) + me; p < e.capacity; p += step)
+    for (int64_t p = (same ? len : 0) + me; p < e.out.capacity; p += step)
       out[p] = p < len ? in[p] : 0.f;
     return;
   }
@@ -377,7 +377,7 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   }
   if (!same) {
     for (int64_t p = me; p < lo; p += step) out[p] = in[p];
-    for (int64_t p = e.budget + me; p < e.capacity; p += step) out[p] = 0.f;
+    for (int64_t p = e.budget + me; p < e.out.capacity; p += step) out[p] = 0.f;
   }
   all_sync();
 
@@ -428,7 +428,7 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   }
   if (same || !ONE) all_sync();       // (no CTA ends while others read its counts)
   if (same)
-    for (int64_t p = e.budget + me; p < e.capacity; p += step) out[p] = 0.f;
+    for (int64_t p = e.budget + me; p < e.out.capacity; p += step) out[p] = 0.f;
 }
 
 template <int D, int NG>
@@ -463,11 +463,12 @@ cudaError_t evict_t(const PagedArgs &a, const PagedEvict &v, int cluster, cudaSt
 template <int D, int NG>
 cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
   const int64_t rows = (int64_t)a.B * a.H_kv;
-  const bool few_go = v.capacity - v.budget <= 128 && v.capacity <= 6144;
-  if (v.capacity <= 1536 || few_go || rows >= 8 * sm_count)
+  const int64_t room = (int64_t)a.max_pages << a.page_log2;
+  const bool few_go = room - v.budget <= 128 && room <= 6144;
+  if (room <= 1536 || few_go || rows >= 8 * sm_count)
     return evict_t<D, NG, 256, true>(a, v, 1, st);
   int c = 1;
-  while (c < 8 && v.capacity > 1024 * c && rows * c <= sm_count) c *= 2;
+  while (c < 8 && room > 1024 * c && rows * c <= sm_count) c *= 2;
   return c == 1 ? evict_t<D, NG, 512, true>(a, v, 1, st)
                 : evict_t<D, NG, 512, false>(a, v, c, st);
 }

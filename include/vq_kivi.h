@@ -580,7 +580,8 @@ int vq_kivi_paged_attend_tree(const vq_kivi_paged *p,
 
 /* Weights per stored token: element (sequence, kv head, place) at at[sequence *
  * seq_stride + head * head_stride + place], fp32.
- *   capacity       places of a row, at least max_pages * page */
+ *   capacity       places of a row, at least max_pages * page; no two rows may
+ *                  share one */
 typedef struct vq_kivi_weights {
   float *at;
   int64_t seq_stride, head_stride, capacity;
@@ -624,7 +625,7 @@ int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
  * budget - recent hold the tokens that stay, those that were there before in
  * their places and the others, in their order, in the places of the evicted
  * ones; the newest follow in their order.  Weights move with their tokens, and
- * the places behind, up to max_pages * page, are zero.  Pages behind the budget are the caller's again.
+ * the places behind, up to weights_out's capacity, are zero.  Pages behind the budget are the caller's again.
  * A token's place no longer says its position: later appends give theirs.
  * Tokens move within their sequence's pages: no other sequence may share them.
  *   batch          cu_new NULL, tokens = B; lens: all tokens

@@ -515,6 +515,10 @@ def test_evict(kind, lens, budget, recent, first, H_kv, D, g, page):
     w = evict_weights(lens, H_kv, table.shape[1] * page, kind)
     check_evict(c, table, lens, w, budget, recent, first, D, g)
     c.pool.random_(0, 256)
+    # (more places than the tables have room for: zero as well)
+    w = torch.cat((w, torch.ones(len(lens), H_kv, 7, device="cuda")), -1)
+    check_evict(c, table, lens, w, budget, recent, first, D, g)
+    c.pool.random_(0, 256)
     check_evict(c, table, lens, w, budget, recent, first, D, g, in_place=True)
 
 
