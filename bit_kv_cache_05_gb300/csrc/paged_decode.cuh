@@ -49,8 +49,7 @@ namespace {
 
 // What a row sees and what is left beside the outputs: kCausal the tokens up to
 // its own; kTree those before the new tokens and the ones that its mask names;
-// kWeigh as kCausal, each score and each row's maximum and sum left for
-// k_paged_weigh.
+// kWeigh as kCausal, each score left for k_paged_merge_weigh.
 enum Form { kCausal, kTree, kWeigh };
 
 constexpr int kWarps = 4;
@@ -607,22 +606,23 @@ k_paged_decode(PagedArgs a, PagedAttend t, int warps_max, int *prefixes, float *
   }
 }
 
+// a partial's factor beside the maximum M; one without a seen token weighs
+// nothing (NaN sums stay)
+__device__ __forceinline__ float part_factor(float2 ml, float M) {
+  return ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+}
+
 // Merge of the partials of a (sequence, kv head): one CTA per output row;
 // each warp takes every WARPS-th partial, its lanes the channels.
-// WEIGH: what k_paged_weigh needs of the row is left in `stats`.
-template <typename T, int D, int WARPS, bool WEIGH>
-__global__ void __launch_bounds__(32 * WARPS)
-k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix, float2 *stats,
-              float top) {
+template <typename T, int D, int WARPS>
+__device__ __forceinline__ void merge_row(const PagedArgs &a, const PagedAttend &t, int warps_max,
+                                          const int *prefix) {
   constexpr int CPL = D / 32;
   __shared__ float red[WARPS][D];
   __shared__ float rl[WARPS], rm[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = a.H_kv, GQ = a.H_q / H, R = t.max_new * GQ;
   const int row = blockIdx.x % R, seg = blockIdx.x / R, b = seg / H, h = seg % H;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (k_paged_weigh reads nothing before its own wait)
-  if constexpr (WEIGH) asm volatile("griddepcontrol.launch_dependents;");
   const Seq L = sequence_of(a, b, t.max_new);
   const int units = prefix[a.B], p0 = prefix[b], nb = (prefix[b + 1] - p0) / H;
   if (row >= L.n * GQ) return;
@@ -647,7 +647,7 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix, floa
     for (int i = warp; i < count; i += WARPS) {
       const float *p = base + i * step;
       const float2 ml = *reinterpret_cast<const float2 *>(p + D);
-      const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - mw);
+      const float f = part_factor(ml, mw);
       float v[CPL];
       if constexpr (CPL == 4) {
         const float4 x = *reinterpret_cast<const float4 *>(p + 4 * lane);
@@ -681,12 +681,101 @@ k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix, floa
     }
     // no token seen: a row of zeros
     const float y = sum == 0.f ? 0.f : v / sum;
-    if constexpr (WEIGH)
-      if (threadIdx.x == 0)
-        stats[(int64_t)seg * R + row] =
-            make_float2(M == -INFINITY ? 0.f : top - M, sum == 0.f ? 0.f : 1.f / sum);
     if constexpr (std::is_same<T, __half>::value) out[threadIdx.x] = __float2half_rn(y);
     else out[threadIdx.x] = __float2bfloat16_rn(y);
+  }
+}
+
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
+k_paged_merge(PagedArgs a, PagedAttend t, int warps_max, const int *prefix) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  merge_row<T, D, WARPS>(a, t, warps_max, prefix);
+}
+
+// The merge, and beside it, in CTAs of their own behind those of the output's
+// rows, weights[token] += sum over the rows of 2^(score + top - maximum) / sum
+// from the scores that the attention left.  Such a CTA takes 8 WARPS steps of a
+// (sequence, kv head): it finds its rows' maxima and sums from the partials, as
+// the merge does, then eight lanes take a step, four tokens each.  A token is one
+// thread's, so that no two threads add to one place and the order of a sum is
+// fixed.
+//
+// The scores are kept (4 bytes a row and token, written and read) rather than
+// computed a second time: with 4 rows that is 32 bytes against the 80 of the
+// key's codes at D = 128, g = 32, and no product.  Bound: latency.  In a kernel
+// behind the merge, with the merge's maxima: 56.9 us a call where this takes
+// 53.2 (16 sequences of 8192, 8 kv heads, 4 rows).
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
+k_paged_merge_weigh(PagedArgs a, PagedAttend t, int warps_max, const int *prefix,
+                    const float *scores, PagedWeights w, float top, int out_rows, int chunks) {
+  constexpr int STEPS = 8 * WARPS;
+  __shared__ float2 stats[16];        // of each row: top - maximum, 1 / sum
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < out_rows) {
+    merge_row<T, D, WARPS>(a, t, warps_max, prefix);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = a.H_kv, R = t.max_new * (a.H_q / H);
+  const int at = blockIdx.x - out_rows, seg = at / chunks, k0 = (at - seg * chunks) * STEPS,
+            b = seg / H, h = seg - b * H;
+  const int units = prefix[a.B], p0 = prefix[b], nb = (prefix[b + 1] - p0) / H;
+  if (k0 >= nb) return;
+  const Seq L = sequence_of(a, b, t.max_new);
+  const int rows = L.n * (a.H_q / H), u0 = p0 + h * nb;
+  const Cut cut(units, warps_used(units, warps_max));
+  const int w0 = cut.owner(u0), count = cut.owner(u0 + nb - 1) - w0 + 1;
+  for (int r = warp; r < rows; r += WARPS) {
+    const float *ml = t.ws + ((int64_t)(w0 + seg) * R + r) * Part<D>::ROW + D;
+    const int64_t step = (int64_t)R * Part<D>::ROW;
+    float M = -INFINITY, sum = 0.f;
+    for (int i = lane; i < count; i += 32) M = fmaxf(M, ml[i * step]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    for (int i = lane; i < count; i += 32) {
+      const float2 x = *reinterpret_cast<const float2 *>(ml + i * step);
+      sum = fmaf(part_factor(x, M), x.y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0)
+      stats[r] = make_float2(M == -INFINITY ? 0.f : top - M, sum == 0.f ? 0.f : 1.f / sum);
+  }
+  __syncthreads();
+  for (int k = k0 + 4 * warp + (lane >> 3); k < min(nb, k0 + STEPS); k += 4 * WARPS) {
+    const int tok = k * kStep + 4 * (lane & 7);
+    const float4 *x = reinterpret_cast<const float4 *>(scores + (int64_t)(u0 + k) * (R * kStep)) +
+                      (lane & 7);
+    float *to = w.at + b * w.seq + h * w.head + tok;
+    const int n = min(4, L.len - tok);            // (none where the step ends behind the sequence)
+    const bool wide = n == 4 && reinterpret_cast<uintptr_t>(to) % 16 == 0;
+    float old[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+    if (wide) {
+      const float4 y = *reinterpret_cast<const float4 *>(to);
+      old[0] = y.x; old[1] = y.y; old[2] = y.z; old[3] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) old[i] = i < n ? to[i] : 0.f;
+    }
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const float4 y = x[r * (kStep / 4)];
+      const float2 f = stats[r];
+      const float s[4] = {y.x, y.y, y.z, y.w};
+      // a token that the row does not see gets nothing, whatever the others are
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += s[i] == -INFINITY ? 0.f : ex2(s[i] + f.x) * f.y;
+    }
+    if (wide) {
+      *reinterpret_cast<float4 *>(to) =
+          make_float4(old[0] + sum[0], old[1] + sum[1], old[2] + sum[2], old[3] + sum[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) to[i] = old[i] + sum[i];
+    }
   }
 }
 
@@ -695,21 +784,18 @@ size_t part_floats(int B, int H_kv, int D, int rows, int sm_count) {
   return ((size_t)decode_ctas(D, rows) * sm_count * kWarps + (size_t)B * H_kv) * rows * (D + 4);
 }
 
-// workspace: partials, the prefixes; for kWeigh the rows' maxima and sums and
-// the scores of all steps that the tables have room for
+// workspace: partials, the prefixes; for kWeigh the scores of all steps that the
+// tables have room for
 size_t prefix_at(int B, int H_kv, int D, int rows, int sm_count) {
   return part_floats(B, H_kv, D, rows, sm_count) * sizeof(float);
 }
-size_t stats_at(int B, int H_kv, int D, int rows, int sm_count) {
-  return (prefix_at(B, H_kv, D, rows, sm_count) + (B + 1) * sizeof(int) + 15) / 16 * 16;
-}
 size_t scores_at(int B, int H_kv, int D, int rows, int sm_count) {
-  return (stats_at(B, H_kv, D, rows, sm_count) + (size_t)B * H_kv * rows * sizeof(float2) + 127) /
-         128 * 128;
+  return (prefix_at(B, H_kv, D, rows, sm_count) + (B + 1) * sizeof(int) + 127) / 128 * 128;
 }
 
 template <int FORM, typename T, int D, int NG, int ROWS>
-cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count, cudaStream_t st) {
+cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, const PagedWeights *w,
+                       int sm_count, cudaStream_t st) {
   using SM = DecSmem<D, NG, ROWS>;
   const size_t smem = SM::PREFIX + sizeof(int) * (a.B + 1);
   static std::atomic<uint64_t> done{0};
@@ -720,51 +806,60 @@ cudaError_t launch_dec(const PagedArgs &a, const PagedAttend &t, int sm_count, c
   const int rows = t.max_new * (a.H_q / a.H_kv);
   char *ws = reinterpret_cast<char *>(t.ws);
   int *prefixes = reinterpret_cast<int *>(ws + prefix_at(a.B, a.H_kv, D, rows, sm_count));
-  float2 *stats = reinterpret_cast<float2 *>(ws + stats_at(a.B, a.H_kv, D, rows, sm_count));
   float *scores = reinterpret_cast<float *>(ws + scores_at(a.B, a.H_kv, D, rows, sm_count));
-  constexpr bool weigh = FORM == kWeigh;
   e = launch_pdl(k_paged_decode<T, D, NG, ROWS, FORM>, dim3(ctas), dim3(kThreads), smem, st, a,
-                 t, warps_max, prefixes, weigh ? scores : nullptr);
+                 t, warps_max, prefixes, FORM == kWeigh ? scores : nullptr);
   count_launch();
   if (e != cudaSuccess) return e;
   // many rows have few partials each (about warps_max over the number of
   // sequences and kv heads): 512 rows of 14, 4 warps 49.4 us a call, 16 warps
   // 51.4; 128 rows of 57, 8 warps 98.3 us, 16 warps 97.8
   const int out_rows = a.B * a.H_kv * rows;
-  const float top = Weights<ROWS>::top;
-  e = out_rows >= 2 * sm_count
-          ? launch_pdl(k_paged_merge<T, D, 4, weigh>, dim3(out_rows), dim3(128), 0, st, a, t,
-                       warps_max, (const int *)prefixes, stats, top)
-          : launch_pdl(k_paged_merge<T, D, 16, weigh>, dim3(out_rows), dim3(512), 0, st, a, t,
-                       warps_max, (const int *)prefixes, stats, top);
+  auto merge = [&](auto warps) {
+    constexpr int W = decltype(warps)::value;
+    if constexpr (FORM == kWeigh) {
+      const int64_t steps = (((int64_t)a.max_pages << a.page_log2) + kStep - 1) / kStep,
+                    chunks = (steps + 8 * W - 1) / (8 * W);
+      return launch_pdl(k_paged_merge_weigh<T, D, W>,
+                        dim3((unsigned)(out_rows + a.B * a.H_kv * chunks)), dim3(32 * W), 0, st,
+                        a, t, warps_max, (const int *)prefixes, (const float *)scores, *w,
+                        Weights<ROWS>::top, out_rows, (int)chunks);
+    } else {
+      return launch_pdl(k_paged_merge<T, D, W>, dim3(out_rows), dim3(32 * W), 0, st, a, t,
+                        warps_max, (const int *)prefixes);
+    }
+  };
+  e = out_rows >= 2 * sm_count ? merge(std::integral_constant<int, 4>{})
+                               : merge(std::integral_constant<int, 16>{});
   count_launch();
   return e;
 }
 
 template <int FORM, typename T, int D, int NG>
-cudaError_t launch_rows(const PagedArgs &a, const PagedAttend &t, int sm_count, cudaStream_t st) {
+cudaError_t launch_rows(const PagedArgs &a, const PagedAttend &t, const PagedWeights *w,
+                        int sm_count, cudaStream_t st) {
   return t.max_new * (a.H_q / a.H_kv) <= 8
-             ? launch_dec<FORM, T, D, NG, 8>(a, t, sm_count, st)
-             : launch_dec<FORM, T, D, NG, 16>(a, t, sm_count, st);
+             ? launch_dec<FORM, T, D, NG, 8>(a, t, w, sm_count, st)
+             : launch_dec<FORM, T, D, NG, 16>(a, t, w, sm_count, st);
 }
 
 template <int FORM, typename T>
-cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, int D, int sm_count,
-                     cudaStream_t st) {
+cudaError_t launch_t(const PagedArgs &a, const PagedAttend &t, const PagedWeights *w, int D,
+                     int sm_count, cudaStream_t st) {
   const int ng = D / a.g;
   if (D == 64)
-    return ng == 1 ? launch_rows<FORM, T, 64, 1>(a, t, sm_count, st)
-                   : launch_rows<FORM, T, 64, 2>(a, t, sm_count, st);
-  return ng == 1   ? launch_rows<FORM, T, 128, 1>(a, t, sm_count, st)
-         : ng == 2 ? launch_rows<FORM, T, 128, 2>(a, t, sm_count, st)
-                   : launch_rows<FORM, T, 128, 4>(a, t, sm_count, st);
+    return ng == 1 ? launch_rows<FORM, T, 64, 1>(a, t, w, sm_count, st)
+                   : launch_rows<FORM, T, 64, 2>(a, t, w, sm_count, st);
+  return ng == 1   ? launch_rows<FORM, T, 128, 1>(a, t, w, sm_count, st)
+         : ng == 2 ? launch_rows<FORM, T, 128, 2>(a, t, w, sm_count, st)
+                   : launch_rows<FORM, T, 128, 4>(a, t, w, sm_count, st);
 }
 
 template <int FORM>
-cudaError_t launch_form(int dtype, const PagedArgs &a, const PagedAttend &t, int D, int sm_count,
-                        cudaStream_t st) {
-  return dtype == VQ_F16 ? launch_t<FORM, __half>(a, t, D, sm_count, st)
-                         : launch_t<FORM, __nv_bfloat16>(a, t, D, sm_count, st);
+cudaError_t launch_form(int dtype, const PagedArgs &a, const PagedAttend &t,
+                        const PagedWeights *w, int D, int sm_count, cudaStream_t st) {
+  return dtype == VQ_F16 ? launch_t<FORM, __half>(a, t, w, D, sm_count, st)
+                         : launch_t<FORM, __nv_bfloat16>(a, t, w, D, sm_count, st);
 }
 
 }  // namespace

@@ -6,7 +6,7 @@ namespace vqk {
 
 cudaError_t launch_paged_decode_tree(int dtype, const PagedArgs &a, const PagedAttend &t, int D,
                                      int sm_count, cudaStream_t st) {
-  return launch_form<kTree>(dtype, a, t, D, sm_count, st);
+  return launch_form<kTree>(dtype, a, t, nullptr, D, sm_count, st);
 }
 
 }  // namespace vqk

@@ -75,6 +75,42 @@ def test_masks_of_every_form(H_q, n):
     assert (out[1] != 0).any()
 
 
+@pytest.mark.parametrize("dtype,gain", [("fp16", 6000.0), ("bf16", 1e30), ("bf16", 1e-30)])
+@pytest.mark.parametrize("H_q,n", [(2, 8), (4, 16), (8, 20)])
+def test_tree_scores_of_any_size(dtype, gain, H_q, n):
+    """Queries of any finite size, in each of the three kernels: a row far from
+    zero sees its largest score alone, one near it the mean; masks hold."""
+    lens = [300 + n, n + 5]
+    c, table, L = filled(lens, 16, H_q, 1, 64, 32)
+    rng = random.Random(4)
+    masks = [m for _ in lens for m in dref.masks_of(dref.random_tree(n, rng))]
+    q = (randn(7, 2 * n, H_q, 64) * gain).to(DT[dtype])
+    out = c.attend(q, table, L, offsets([n, n]), max_new=n, tree=i64(masks))
+    c.status()
+    assert torch.isfinite(out).all()
+    small = gain < 1
+    for b, S in enumerate(lens):
+        K, V = (torch.as_tensor(x).cuda() for x in
+                ref.cache_rows64(c.pool, table[b].cpu().numpy(), S, 0, 64, 32))
+        for i in range(n):
+            see = torch.as_tensor(dref.seen_by(masks[b * n + i], i, n, S)).cuda()
+            for j in range(H_q):
+                x = q[b * n + i, j].double()
+                s = torch.where(see, K @ x / 8, -math.inf)
+                top = torch.topk(s, 2).values
+                got = out[b * n + i, j].double()
+                if small:
+                    want = V[see].mean(0)
+                    tol = 2.0 ** -7 * want.abs() + 2.0 ** -7
+                else:
+                    # where no other token comes near the largest score
+                    if top[0] - top[1] < 60 + 2.0 ** -12 * top[0].abs():
+                        continue
+                    want = V[int(s.argmax())]
+                    tol = 2.0 ** -7 * want.abs() + 1e-6
+                assert ((got - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("H_q,n", [(2, 8), (8, 20)])
 def test_tree_padding_in_front(H_q, n):
     """New tokens before a sequence's first place see nothing and are seen by
