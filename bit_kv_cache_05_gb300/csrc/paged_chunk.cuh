@@ -696,10 +696,10 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
             if constexpr (SMALL) {
               // the outputs before this tile's: done when the next scores are,
               // which were issued behind them, or have a barrier of their own
-              ok = __all_sync(kFull, j + 1 < steps
-                                         ? bar_wait(&B.s_full[buf ^ 1], (ph_s >> (buf ^ 1)) & 1u, dead)
-                                         : bar_wait(&B.o_full[1], ph_o1, dead));
-              if (!ok) break;
+              const int nb = buf ^ 1;
+              ok = j + 1 < steps ? bar_wait(&B.s_full[nb], (ph_s >> nb) & 1u, dead)
+                                 : bar_wait(&B.o_full[1], ph_o1, dead);
+              if (!__all_sync(kFull, ok)) { ok = false; break; }
               fence_after();
             }
             const float f = mo > m ? pow2(m - mo) : 1.f;
@@ -1234,8 +1234,8 @@ cudaError_t launch_d(const PagedArgs &a, const PagedAttend &t, int sm_count, cud
   float *part = t.ws, *swap = part + part_floats(D, sm_count);
   CutPair *cuts = reinterpret_cast<CutPair *>(swap + swap_floats(D, sm_count));
   long long *prefixes = reinterpret_cast<long long *>(cuts + sm_count);
-  e = launch_pdl(k_paged_chunk<T, D, NG, TREE, SMALL>, dim3(sm_count), dim3(Roles<SMALL>::THREADS), SM::ALLOC, st, a, t,
-                 part, swap, cuts, prefixes);
+  e = launch_pdl(k_paged_chunk<T, D, NG, TREE, SMALL>, dim3(sm_count),
+                 dim3(Roles<SMALL>::THREADS), SM::ALLOC, st, a, t, part, swap, cuts, prefixes);
   count_launch();
   if (e != cudaSuccess) return e;
   // rows of a pair that can hold queries: one tile's, or both tiles'

@@ -57,7 +57,9 @@ class PagedKiviCache:
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._spec.pool, self._spec.status = pool.data_ptr(), self._status.data_ptr()
         self._lib, self._index = L, self.device.index
-        self._ws = {}      # workspace bytes by (B, max_new)
+        # workspace bytes by (B, max_new), with weights (B, max_new, max_pages), of
+        # evictions (B, max_pages, budget, recent)
+        self._ws = {}
 
     # -- arguments -------------------------------------------------------------
 
@@ -297,8 +299,12 @@ class PagedKiviCache:
         wo = self._weights(weights_out, batch, "weights_out")
         lens_out = self._lens_out(lens_out, batch.B)
         budget, recent, first = int(budget), int(recent), int(first)
-        nbytes = self._lib.vq_kivi_paged_evict_workspace_bytes(self._spec, batch.B,
-                                                               batch.max_pages, budget, recent)
+        key = (batch.B, batch.max_pages, budget, recent)
+        nbytes = self._ws.get(key)
+        if nbytes is None:
+            nbytes = self._lib.vq_kivi_paged_evict_workspace_bytes(self._spec, *key)
+            if nbytes and len(self._ws) < 4096:
+                self._ws[key] = nbytes
         ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         rc = self._lib.vq_kivi_paged_evict(self._spec, batch, w, wo, budget, recent, first,
                                            lens_out.data_ptr() or None, ws.data_ptr() or None,
