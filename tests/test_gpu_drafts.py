@@ -464,6 +464,40 @@ def test_weights(dtype, n, lens, H_q, H_kv, D, g, page):
     assert torch.equal(other, acc)
 
 
+@pytest.mark.parametrize("dtype,gain", [("fp16", 6000.0), ("bf16", 1e30), ("bf16", 1e-30)])
+@pytest.mark.parametrize("H_q,n", [(4, 1), (4, 2), (8, 2)])
+def test_weights_of_scores_of_any_size(dtype, gain, H_q, n):
+    """Queries of any finite size: the weights of a row still sum to one, all on
+    the largest score where no other comes near it, equal ones near zero."""
+    S = 700
+    c, table, L = filled([S], 16, H_q, 1, 64, 32)
+    q = (randn(3, n, H_q, 64) * gain).to(DT[dtype])
+    acc = torch.zeros(1, 1, table.shape[1] * 16, device="cuda")
+    c.attend(q, table, L, offsets([n]), max_new=n, weights=acc)
+    c.status()
+    # each weight is off by 2^-20 of itself, a row's sum by as much
+    assert abs(float(acc.double().sum()) - n * H_q) <= n * H_q * 2.0 ** -18
+    K = torch.as_tensor(ref.cache_rows64(c.pool, table[0].cpu().numpy(), S, 0, 64, 32)[0]).cuda()
+    want, open_rows = torch.zeros(S, dtype=torch.float64, device="cuda"), 0
+    for i in range(n):
+        seen = S - n + i + 1
+        for j in range(H_q):
+            s = (K @ q[i, j].double() / 8)[:seen]
+            if gain < 1:
+                want[:seen] += 1 / seen
+                continue
+            top = torch.topk(s, 2).values
+            if top[0] - top[1] < 60 + 2.0 ** -12 * top[0].abs():
+                open_rows += 1
+            else:
+                want[int(s.argmax())] += 1
+    off = (acc[0, 0, :S].double() - want).abs()
+    if gain < 1:
+        assert off.max() <= n * H_q * 2.0 ** -18 / (S - n)
+    else:
+        assert off.sum() <= 2 * open_rows + n * H_q * 2.0 ** -18
+
+
 def test_weights_of_nan_tokens_bad_pages_and_strides():
     from bit_kv_cache_05_gb300 import _lib
     lens = [40, 50]
