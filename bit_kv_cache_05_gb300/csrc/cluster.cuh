@@ -25,6 +25,15 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Another CTA's shared memory may be touched once that CTA is known to run:
+// every thread arrives where its kernel begins, and waits before the first peer
+// access, or where it leaves without one.
+__device__ __forceinline__ void cluster_began() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_runs() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // the address of `p`, a place in this CTA's shared memory, in CTA `rank`'s
 __device__ __forceinline__ uint32_t peer_addr(const void *p, unsigned rank) {
   uint32_t a;

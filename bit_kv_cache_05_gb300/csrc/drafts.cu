@@ -110,6 +110,7 @@ k_verify(Drafts d) {
   const unsigned rank = cluster_rank(), ctas = cluster_ctas();
   const int b = blockIdx.x / ctas;
   const T *target = static_cast<const T *>(d.target), *draft = static_cast<const T *>(d.draft);
+  cluster_began();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int start = d.cu[b], n = d.cu[b + 1] - start;
   const bool lead = rank == 0 && tid == 0;
@@ -120,6 +121,7 @@ k_verify(Drafts d) {
   };
   if (n <= 0 || n > kMaxTree || start < 0 || (int64_t)start + n > d.rows) {
     if (lead) put(-1, n == 0 ? 0 : -1);
+    cluster_runs();
     return;
   }
   // nodes: their tokens, and what their parents' rows say of them
@@ -154,6 +156,7 @@ k_verify(Drafts d) {
     }
   }
   __syncthreads();
+  cluster_runs();                   // row_sum writes to the other CTAs
   if (sm.bad) {
     for (int i = tid; rank == 0 && i < n; i += kThreads) d.path[start + i] = -1;
     if (lead) put(-1, -1);

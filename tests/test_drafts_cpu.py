@@ -1,7 +1,9 @@
 """Refusals of the tree attention, the weights, the kept paths, the eviction and
 the draft verification, and the facts behind their arithmetic, without a GPU."""
 import ctypes
+import os
 import random
+import re
 from fractions import Fraction
 
 import numpy as np
@@ -197,6 +199,23 @@ def test_whole_numbers_in_two_halves():
     assert (hi * 2 ** 22 + lo == dref.units(w)).all()
     # 1023 of the largest add up in 32 bits
     assert 1023 * 2 ** 22 < 2 ** 32
+
+
+@pytest.mark.parametrize("name", ["drafts.cu", "paged_move.cu"])
+def test_clusters_meet_before_they_touch_each_other(name):
+    """A CTA may touch another one's shared memory once that one is known to run:
+    in each kernel a barrier of the cluster stands before the first peer access,
+    as every path to it passes them in the order of the source."""
+    src = os.path.join(os.path.dirname(__file__), "..", "bit_kv_cache_05_gb300", "csrc", name)
+    text = re.sub(r"//[^\n]*", "", open(src).read())
+    kernels = re.split(r"(?=__global__)", text)[1:]
+    touching = [k for k in kernels if re.search(r"\bpeer_(load|store)\(", k)]
+    assert touching
+    for k in touching:
+        peer = re.search(r"\bpeer_(load|store)\(", k).start()
+        waits = [m.start() for m in re.finditer(r"^\s*(cluster_sync|cluster_runs|all_sync)\(\);", k,
+                                                re.M)]
+        assert waits and waits[0] < peer
 
 
 def test_masks_and_depths_of_a_tree():

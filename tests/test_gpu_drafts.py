@@ -323,6 +323,29 @@ def test_verify_bad_sequences_are_left_out():
     assert got[1].tolist()[0] == int(good[1][0])
 
 
+@pytest.mark.parametrize("B,V", [(5, 40000), (50, 9000), (100, 5000), (200, 300)])
+def test_verify_every_way_out_of_a_cluster(B, V):
+    """Clusters of eight, four, two and one CTAs, whose sequences walk, have no
+    nodes, too many of them, or a parent outside its range, side by side."""
+    n = [(6, 0, 4, 70, 1)[b % 5] for b in range(B)]
+    p, q, tokens, parents, u = draft_case(B, n, V, "fp32", False, True, 1.0, 3.0)
+    at = np.cumsum([0] + n)
+    bad = [b for b in range(B) if b % 10 == 2]
+    for b in bad:
+        parents[at[b] + 2] = 2
+    for _ in range(3):
+        path, counts, after = run_verify(p, q, tokens, parents, u, n)
+        for b, k in enumerate(n):
+            s = slice(at[b], at[b + 1])
+            if k == 0 or k > 64 or b in bad:
+                assert int(counts[b]) == (0 if k == 0 else -1) and int(after[b]) == -1
+                continue
+            want, token = dref.verify(p[s].numpy(), q[s].numpy(), tokens[s], parents[s],
+                                      u[s].numpy())
+            assert path[s].tolist() == want + [-1] * (k - len(want)), b
+            assert int(counts[b]) == len(want) and int(after[b]) == token, b
+
+
 @pytest.mark.parametrize("with_draft", [True, False])
 @pytest.mark.parametrize("kids", [1, 3])
 def test_verified_tokens_follow_the_target(with_draft, kids):
