@@ -120,6 +120,9 @@ k_verify(Drafts d) {
     else static_cast<int32_t *>(d.after)[b] = (int)after;
   };
   if (n <= 0 || n > kMaxTree || start < 0 || (int64_t)start + n > d.rows) {
+    // (more nodes than a tree has: their rows are there)
+    if (rank == 0 && start >= 0 && (int64_t)start + n <= d.rows)
+      for (int i = tid; i < n; i += kThreads) d.path[start + i] = -1;
     if (lead) put(-1, n == 0 ? 0 : -1);
     cluster_runs();
     return;

@@ -323,6 +323,25 @@ def test_verify_bad_sequences_are_left_out():
     assert got[1].tolist()[0] == int(good[1][0])
 
 
+def test_verify_too_many_nodes_clear_their_path():
+    """More nodes than a tree has, their rows in range: -1 in all of their path;
+    rows behind the last sequence stay as they were."""
+    n, V, extra = [3, 70, 2, 2000], 50, 4
+    p, q, tokens, parents, u = draft_case(3, n, V, "fp32", False, True)
+    T = sum(n)
+    pad = lambda t: torch.cat((t, torch.zeros(extra, *t.shape[1:], dtype=t.dtype)))
+    path = torch.full((T + extra,), 9, dtype=torch.int32, device="cuda")
+    got = run_verify(pad(p), pad(q), tokens + [0] * extra, parents + [0] * extra, pad(u), n,
+                     path=path)
+    assert got[0] is path and got[1].tolist()[1::2] == [-1, -1]
+    assert got[2].tolist()[1::2] == [-1, -1]
+    assert (path[3:73] == -1).all() and (path[75:T] == -1).all() and (path[T:] == 9).all()
+    # offsets behind the rows: nothing of them is written
+    path.fill_(9)
+    got = run_verify(p[:60], q[:60], tokens[:60], parents[:60], u[:60], [3, 70], path=path[:60])
+    assert got[1].tolist()[1] == -1 and (path[3:] == 9).all()
+
+
 @pytest.mark.parametrize("B,V", [(5, 40000), (50, 9000), (100, 5000), (200, 300)])
 def test_verify_every_way_out_of_a_cluster(B, V):
     """Clusters of eight, four, two and one CTAs, whose sequences walk, have no
