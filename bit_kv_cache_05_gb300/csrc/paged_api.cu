@@ -211,7 +211,10 @@ int check_weights(const vq_kivi_paged *p, const PagedArgs &a, const vq_kivi_weig
                   const char *name, PagedWeights *to) {
   if (!w) return fail(VQ_ERR_ARG, "%s is NULL", name);
   const int64_t room = (int64_t)a.max_pages << a.page_log2;
-  if (a.B > 0 && room > 0) {
+  if (w->capacity < 0)
+    return fail(VQ_ERR_ARG, "%s: capacity=%lld < 0", name, (long long)w->capacity);
+  // (an eviction clears all places, also of a table without pages)
+  if (a.B > 0 && (room > 0 || w->capacity > 0)) {
     if (!w->at || !aligned(w->at, 4)) return fail(VQ_ERR_ARG, "%s is NULL or misaligned", name);
     if (w->capacity < room)
       return fail(VQ_ERR_ARG, "%s has room for %lld tokens, the table for %lld", name,

@@ -72,6 +72,21 @@ def test_weights_refusals(vqlib, kw, max_new, code):
     assert vqlib.vq_kivi_paged_weights_workspace_bytes(_paged(), 1 << 20, 1 << 20, 1) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(at=None), dict(at=P + 2), dict(seq_stride=0),
+                                dict(head_stride=255), dict(capacity=-1), dict(at=None, capacity=-1)])
+@pytest.mark.parametrize("B,max_pages", [(2, 0), (0, 4)])
+def test_weights_without_room_in_the_table(vqlib, kw, B, max_pages):
+    """Tables without a page: the places are cleared all the same, so that they
+    are looked at; a call without sequences only looks at their number."""
+    b = _batch(B=B, tokens=B, max_pages=max_pages, cu_new=None)
+    w = _weights(**kw)
+    code = -1 if B or w.capacity < 0 else 0
+    assert vqlib.vq_kivi_paged_evict(_paged(), b, w, w, 4, 1, 0, 2 * P, 3 * P, 1 << 20,
+                                     None) == code
+    if code:
+        assert vqlib.vq_kivi_last_error().startswith(b"weights")
+
+
 @pytest.mark.parametrize("path,counts,after", [
     (P + 64, 2 * P, 3 * P), (2 * P, P, 3 * P), (2 * P, 3 * P, P + 56), (P - 28, 2 * P, 3 * P),
 ])
