@@ -35,6 +35,8 @@ namespace vqk {
 constexpr int kMaxSeqs = 1024;   // sequences of one paged call
 constexpr int kBlk = 16;         // tokens of a block
 constexpr int kMaxTree = 64;     // nodes of a tree of drafts: bits of a mask
+constexpr int kMaxLen = 0x7fff0000;   // tokens of a sequence: a place and what a
+                                      // kernel takes at once fit in 31 bits
 
 // status bits (device word)
 constexpr unsigned kBadPage = 1u;     // a block table entry outside the pool
@@ -64,6 +66,7 @@ struct PagedArgs {
   int64_t tokens;            // new tokens the token tensors have room for
   int n_pages, page_log2, max_pages, B;
   int H_q, H_kv, g;
+  int max_len;               // tokens that a table has room for, kMaxLen at most
 };
 
 // What a call says of sequence b: tokens, new tokens, row of the first new one.
@@ -79,7 +82,7 @@ __device__ __forceinline__ Seq sequence_of(const PagedArgs &a, int b, int max_ne
     s.first = a.cu[b];
     s.n = a.cu[b + 1] - s.first;
   }
-  if (s.len < 0 || s.len > ((int64_t)a.max_pages << a.page_log2) || s.n < 0 || s.n > max_new ||
+  if (s.len < 0 || s.len > a.max_len || s.n < 0 || s.n > max_new ||
       s.first < 0 || (int64_t)s.first + s.n > a.tokens) {
     atomicOr(a.status, kBadLength);
     s.len = s.n = 0;
@@ -119,7 +122,7 @@ __device__ __forceinline__ Place find_place(const PagedArgs &a, int64_t i, int64
     in = a.cu[lo] >= 0 && end >= a.cu[lo] && end <= a.tokens;
   }
   const int len = a.lens[lo];
-  if (!in || len < 0 || len > ((int64_t)a.max_pages << a.page_log2)) {
+  if (!in || len < 0 || len > a.max_len) {
     atomicOr(a.status, kBadLength);
     return Place{lo, -1};
   }

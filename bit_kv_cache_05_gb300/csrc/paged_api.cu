@@ -171,6 +171,8 @@ int check_batch(const vq_kivi_paged *p, const vq_kivi_paged_batch *s, PagedArgs 
   to->n_pages = p->n_pages;
   to->page_log2 = lg;
   to->max_pages = s->max_pages;
+  const int64_t room = (int64_t)s->max_pages << lg;
+  to->max_len = (int)(room < kMaxLen ? room : kMaxLen);
   to->B = s->B;
   to->H_q = p->H_q;
   to->H_kv = p->H_kv;

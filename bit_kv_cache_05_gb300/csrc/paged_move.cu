@@ -200,7 +200,7 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = a.lens[b];
-  const bool ok = len >= 0 && len <= ((int64_t)a.max_pages << a.page_log2);
+  const bool ok = len >= 0 && len <= a.max_len;
   const float *in = e.in.at + b * e.in.seq + h * e.in.head;
   float *out = e.out.at + b * e.out.seq + h * e.out.head;
   const bool same = e.in.at == e.out.at;

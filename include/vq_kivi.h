@@ -491,7 +491,7 @@ typedef struct vq_kivi_paged {
  *            positions page * j ... in entry j.  Entries behind a sequence's
  *            last page are not read.
  *   lens     device int32 [B]: tokens with the new ones, at most max_pages *
- *            page
+ *            page and 2^31 - 2^16
  *   cu_new   device int32 [B + 1], not decreasing, or NULL: one new token per
  *            sequence (row b; tokens = B)
  *   tokens   rows of the token tensors, at least cu_new[B]; rows behind

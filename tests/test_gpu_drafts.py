@@ -944,6 +944,54 @@ def test_offsets_past_32_bits_of_drafts_and_eviction():
     c.status()
 
 
+def test_lengths_at_the_end_of_31_bits():
+    """A table with room for 2^31 tokens: a length whose sums with a tile would
+    pass 31 bits is outside its range for every operator; the others of the call
+    are served."""
+    from bit_kv_cache_05_gb300 import _lib
+    page, S, n = 1024, 300, 3
+    c = new_cache(1, page, 2, 1, 64, 64)
+    table = torch.zeros(2, 2 ** 31 // page, dtype=torch.int32, device="cuda")
+    k, v = randn(1, S, 1, 64).half(), randn(2, S, 1, 64).half()
+    c.append(k, v, table[:1], i32([S]), offsets([S]))
+    c.status()
+    before, cu = c.pool.clone(), offsets([n, n])
+    kv, q = randn(3, 2 * n, 1, 64).half(), randn(4, 2 * n, 2, 64).half()
+
+    def reported():
+        with pytest.raises(_lib.VqError, match="length"):
+            c.status()
+
+    for far in (2 ** 31 - 1, 2 ** 31 - 2 ** 16 + 1):
+        L = i32([far, S])
+        out = torch.full_like(q, 7.0)
+        for a in (dict(), dict(tree=i64([1, 3, 7] * 2)), dict(max_new=40),
+                  dict(max_new=40, tree=i64([1, 3, 7] * 2)), dict(max_new=20, tree=i64([1, 3, 7] * 2))):
+            a.setdefault("max_new", n)
+            c.attend(q, table, L, cu, out=out, **a)
+            reported()
+            assert (out[:n] == 7).all() and (out[n:] != 7).any()
+        K = torch.full((2 * n, 1, 64), 7.0, dtype=torch.float16, device="cuda")
+        V = K.clone()
+        c.dequantize(table, L, cu, n_tokens=2 * n, out=(K, V))
+        reported()
+        assert (K[:n] == 7).all() and (V[:n] == 7).all() and (K[n:] != 7).any()
+        out = c.keep(table, L, cu, i32([2, -1, -1] * 2), i32([1, 1]))
+        reported()
+        assert out.tolist() == [far, S - 2]
+        c.pool.copy_(before)
+        # the append leaves the far sequence out
+        c.append(kv, kv, table[:1], L[:1], cu[:2])
+        reported()
+        assert torch.equal(c.pool, before)
+        w = torch.zeros(1, 1, 2 ** 31, device="cuda")
+        lens, _ = c.evict(table[:1], L[:1], w, 16, recent=4, weights_out=w)
+        reported()
+        assert lens.tolist() == [far] and torch.equal(c.pool, before)
+        del w
+    torch.cuda.empty_cache()
+
+
 def test_most_sequences_of_a_call():
     """1024 sequences, as many as a call takes."""
     B, n = 1024, 3
