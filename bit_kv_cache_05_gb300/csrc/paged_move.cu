@@ -209,10 +209,12 @@ k_paged_evict(PagedArgs a, PagedEvict e) {
     e.lens_out[b] = ok && len > e.budget ? e.budget : len;
   }
   const int64_t step = (int64_t)ctas * THREADS, me = (int64_t)rank * THREADS + tid;
-  if (!ok) return;
-  if (len <= e.budget) {
-    for (int64_t p = (same ? len : 0) + me; p < e.out.capacity; p += step)
-      out[p] = p < len ? in[p] : 0.f;
+  if (!ok || len <= e.budget) {
+    // as it was, and zero behind; a length outside its range says nothing of
+    // where that is
+    const int64_t n = ok ? len : e.in.capacity;
+    for (int64_t p = (same ? n : 0) + me; p < e.out.capacity; p += step)
+      out[p] = p < n ? in[p] : 0.f;
     return;
   }
   const int K = e.budget - e.recent, lo = e.first, hi = len - e.recent;

@@ -285,7 +285,8 @@ class PagedKiviCache:
 
         Returns (lens_out, weights_out): the lengths (not lens itself) and the
         weights, moved with their tokens and zero behind (weights_out may be
-        weights itself)."""
+        weights itself).  A sequence whose length is outside its range keeps
+        both (and is reported by status)."""
         if self._elsewhere(stream):
             with _on(self.device, stream):
                 return self.evict(table, lens, weights, budget, recent=recent, first=first,

@@ -625,7 +625,9 @@ int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
  * budget - recent hold the tokens that stay, those that were there before in
  * their places and the others, in their order, in the places of the evicted
  * ones; the newest follow in their order.  Weights move with their tokens, and
- * the places behind, up to weights_out's capacity, are zero.  Pages behind the budget are the caller's again.
+ * the places behind, up to weights_out's capacity, are zero.  A sequence whose
+ * length is outside its range is left out: its length and all its weights are
+ * what they were.  Pages behind the budget are the caller's again.
  * A token's place no longer says its position: later appends give theirs.
  * Tokens move within their sequence's pages: no other sequence may share them.
  *   batch          cu_new NULL, tokens = B; lens: all tokens

@@ -691,6 +691,30 @@ def test_evict_strides_bad_pages_and_lengths():
     assert torch.equal(c.pool.cpu(), dref.move_tokens(before, table, 64, 32, moves))
 
 
+@pytest.mark.parametrize("budget", [30, 64])
+def test_evict_keeps_the_weights_of_what_it_leaves_out(budget):
+    """Lengths outside their range: their weights come out as they went in, in
+    an array of its own and in place."""
+    from bit_kv_cache_05_gb300 import _lib
+    lens = [60] * 5
+    c, table, _ = filled(lens, 16, 2, 2, 64, 32)
+    w = evict_weights(lens, 2, 70, "wild")
+    L = i32([60, 65, -1, 20, 2 ** 31 - 1])
+    wo = torch.full_like(w, 9.0)
+    for out in (wo, None, w):
+        before, w0 = c.pool.clone(), w.clone()
+        lens_out, got = c.evict(table, L, w, budget, recent=8, first=2, weights_out=out)
+        with pytest.raises(_lib.VqError, match="length"):
+            c.status()
+        assert lens_out.tolist() == [min(60, budget), 65, -1, 20, 2 ** 31 - 1]
+        for b in (1, 2, 4):
+            assert same_floats(got[b], w0[b])
+        assert same_floats(got[3, :, :20], w0[3, :, :20]) and (got[3, :, 20:] == 0).all()
+        for b in (1, 2, 3, 4):
+            pages = table[b].long()
+            assert torch.equal(c.pool[pages], before[pages])
+
+
 # ---- together ---------------------------------------------------------------------------
 
 def test_speculative_steps_together():
