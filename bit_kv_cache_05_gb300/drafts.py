@@ -84,7 +84,8 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Te
     # what nearly every call passes, in few steps; anything else is looked at
     # one by one
     if not (dt in DTYPES and target.is_cuda and len(shape) == 2 and st[1] == 1 and
-            sd[1] == 1 and not target.requires_grad and
+            (draft is None or draft.shape == shape) and sd[1] == 1 and
+            not target.requires_grad and
             (tt is torch.int64 or tt is i32) and tokens.shape == rows and
             tokens.get_device() == index and tokens.is_contiguous() and
             uniforms.dtype is torch.float32 and uniforms.shape == rows and
@@ -93,8 +94,8 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Te
             cu_new.get_device() == index and cu_new.is_contiguous() and
             (parents is None or (parents.dtype is i32 and parents.shape == rows and
                                  parents.get_device() == index and parents.is_contiguous())) and
-            (draft is None or (draft.dtype is dt and draft.shape == shape and
-                               draft.get_device() == index and not draft.requires_grad)) and
+            (draft is None or (draft.dtype is dt and draft.get_device() == index and
+                               not draft.requires_grad)) and
             path is None and counts is None and after is None):
         _check(target, tokens, uniforms, cu_new, parents, draft, path, counts, after)
     T, V = shape

@@ -323,6 +323,23 @@ def test_verify_bad_sequences_are_left_out():
     assert got[1].tolist()[0] == int(good[1][0])
 
 
+def test_verify_arguments_of_other_shapes():
+    """Every tensor with a dimension less or more: the argument is named."""
+    from bit_kv_cache_05_gb300 import verify_drafts
+    V, n = 50, [3, 2]
+    p, q, tokens, parents, u = draft_case(3, n, V, "fp32", False, True)
+    good = dict(target=p.cuda(), tokens=i64(tokens), uniforms=u.cuda(), cu_new=offsets(n),
+                parents=i32(parents), draft=q.cuda(), path=i32([0] * 5), counts=i32([0, 0]),
+                after=i64([0, 0]))
+    verify_drafts(**good)
+    for name, t in good.items():
+        for bad in (t[0], t[:, 0] if t.dim() > 1 else t[:1], t[None], t.flatten()[0], t[:0]):
+            if bad.shape == t.shape:
+                continue
+            with pytest.raises(ValueError):
+                verify_drafts(**dict(good, **{name: bad}))
+
+
 def test_verify_too_many_nodes_clear_their_path():
     """More nodes than a tree has, their rows in range: -1 in all of their path;
     rows behind the last sequence stay as they were."""
