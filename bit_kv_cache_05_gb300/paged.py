@@ -291,7 +291,7 @@ class PagedKiviCache:
             with _on(self.device, stream):
                 return self.evict(table, lens, weights, budget, recent=recent, first=first,
                                   lens_out=lens_out, weights_out=weights_out)
-        batch = self._batch(table, lens, None, lens.shape[0])
+        batch = self._batch(table, lens, None, lens.numel())
         w = self._weights(weights, batch, "weights")
         if weights_out is None:
             weights_out = torch.empty_like(weights)

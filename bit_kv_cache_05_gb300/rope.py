@@ -111,7 +111,7 @@ def _check_rows(t, heads, D, dtype, device, name, weight, out):
             raise ValueError(f"{what} must be {dtype}, got {x.dtype}")
         if x.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{what} requires a gradient: the cache's operators have none")
-        if D > 1 and x.numel() and x.stride(-1) != 1:
+        if D > 1 and x.dim() and x.numel() and x.stride(-1) != 1:
             raise ValueError(f"{what}: the last dimension must be contiguous")
     if weight is not None and tuple(weight.shape) != (D,):
         raise ValueError(f"{name}_weight must be [{D}], got {tuple(weight.shape)}")

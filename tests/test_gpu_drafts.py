@@ -927,6 +927,44 @@ def test_readme_samples_of_drafts_and_eviction():
     assert abs(float(env["weights"][1].sum()) - H_q) < 1e-3
 
 
+def test_cache_arguments_of_other_shapes():
+    """Every tensor of the tree attention, the weights, the kept paths and the
+    eviction with a dimension less or more: the argument is named, and the cache
+    stays as it is."""
+    from bit_kv_cache_05_gb300 import _lib
+    lens, n = [40, 30], [3, 2]
+    c, table, L = filled(lens, 16, 4, 2, 64, 32)
+    cu, T = offsets(n), sum(n)
+    q, w = randn(1, T, 4, 64).half(), torch.zeros(2, 2, table.shape[1] * 16, device="cuda")
+    base = dict(table=table, lens=L, cu_new=cu)
+    calls = [(c.attend, dict(base, q=q, tree=i64([1, 3, 7, 1, 3]), out=torch.empty_like(q))),
+             (c.attend, dict(base, q=q, weights=w, max_new=3)),
+             (c.keep, dict(base, path=i32([0, 1, 2, 0, 1]), counts=i32([2, 1]),
+                           lens_out=L.clone())),
+             (c.evict, dict(table=table, lens=L, weights=w, budget=32, recent=4,
+                            lens_out=L.clone(), weights_out=w.clone()))]
+    before = c.pool.clone()
+    for call, good in calls:
+        for name, t in good.items():
+            if not torch.is_tensor(t):
+                continue
+            for bad in (t[0], t[:, 0] if t.dim() > 1 else t[:1], t[None], t.flatten()[0], t[:0]):
+                try:
+                    call(**dict(good, **{name: bad}))
+                except ValueError:
+                    continue
+                # fewer rows than the offsets say: found by the kernels
+                assert name in ("q", "path") and bad.dim() == t.dim()
+                if len(bad) or name == "path":
+                    with pytest.raises(_lib.VqError, match="length"):
+                        c.status()
+        assert torch.equal(c.pool, before) and (w == 0).all()
+    c.status()
+    for call, good in calls:
+        call(**good)
+    c.status()
+
+
 def test_rows_behind_the_last_sequence_stay():
     """Token tensors with more rows than the sequences have: the rows behind are
     neither read nor written."""
