@@ -17,6 +17,14 @@ from . import _lib
 from .rope import DTYPES, Rope, _current_device, _on, _positions, _raw_stream, _rows
 
 
+def _int32(x, name: str) -> int:
+    """A number that the library takes in 32 bits (the call would cut others)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}={x} does not fit in 32 bits")
+    return x
+
+
 class PagedKiviCache:
     """A pool of `n_pages` pages of `page` tokens in 4 bits.
 
@@ -211,6 +219,8 @@ class PagedKiviCache:
             max_new = 1 if cu_new is None else max(shape[0], 1)
             if tree is not None:
                 max_new = min(max_new, 64)
+        else:
+            max_new = _int32(max_new, "max_new")
         w = None
         if tree is not None:
             if weights is not None:
@@ -223,13 +233,14 @@ class PagedKiviCache:
         key = (batch.B, max_new) if w is None else (batch.B, max_new, batch.max_pages)
         nbytes = self._ws.get(key)
         if nbytes is None:
-            L, mn = self._lib, int(max_new)
-            nbytes = L.vq_kivi_paged_workspace_bytes(self._spec, batch.B, mn) if w is None else \
-                L.vq_kivi_paged_weights_workspace_bytes(self._spec, batch.B, batch.max_pages, mn)
+            L = self._lib
+            nbytes = L.vq_kivi_paged_workspace_bytes(self._spec, batch.B, max_new) if w is None \
+                else L.vq_kivi_paged_weights_workspace_bytes(self._spec, batch.B,
+                                                             batch.max_pages, max_new)
             if nbytes and len(self._ws) < 4096:
                 self._ws[key] = nbytes
         ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        tail = (int(max_new), scale, ws.data_ptr(), nbytes, _raw_stream(self._index))
+        tail = (max_new, scale, ws.data_ptr(), nbytes, _raw_stream(self._index))
         if tree is not None:
             rc = self._lib.vq_kivi_paged_attend_tree(self._spec, batch, dt, rq,
                                                      tree.data_ptr() or None, *tail)
@@ -299,7 +310,8 @@ class PagedKiviCache:
             raise ValueError(f"weights_out must be {tuple(weights.shape)}")
         wo = self._weights(weights_out, batch, "weights_out")
         lens_out = self._lens_out(lens_out, batch.B)
-        budget, recent, first = int(budget), int(recent), int(first)
+        budget, recent, first = (_int32(budget, "budget"), _int32(recent, "recent"),
+                                 _int32(first, "first"))
         key = (batch.B, batch.max_pages, budget, recent)
         nbytes = self._ws.get(key)
         if nbytes is None:

@@ -965,6 +965,27 @@ def test_cache_arguments_of_other_shapes():
     c.status()
 
 
+def test_numbers_beyond_32_bits():
+    """Refused, not cut to their low bits."""
+    c, table, L = filled([60], 16, 2, 2, 64, 32)
+    w = evict_weights([60], 2, 64, "plain")
+    q, before = randn(1, 1, 2, 64).half(), c.pool.clone()
+    for a in (dict(budget=2 ** 32 + 20, recent=2), dict(budget=20, recent=2 ** 32 + 2),
+              dict(budget=20, recent=2, first=2 ** 32), dict(budget=20 - 2 ** 32, recent=2),
+              dict(budget=2 ** 31, recent=2)):
+        with pytest.raises(ValueError, match="32 bits"):
+            c.evict(table, L, w, **a)
+    for n in (2 ** 32 + 1, 1 - 2 ** 32):
+        for a in (dict(), dict(tree=i64([1])), dict(weights=w)):
+            with pytest.raises(ValueError, match="32 bits"):
+                c.attend(q, table, L, max_new=n, **a)
+    assert torch.equal(c.pool, before)
+    # the largest number is a budget that no sequence passes
+    lens, _ = c.evict(table, L, w, 2 ** 31 - 1, recent=2)
+    c.status()
+    assert lens.tolist() == [60] and torch.equal(c.pool, before)
+
+
 def test_rows_behind_the_last_sequence_stay():
     """Token tensors with more rows than the sequences have: the rows behind are
     neither read nor written."""
