@@ -123,6 +123,14 @@ bool meet(const void *a, int64_t na, const void *b, int64_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// whether what is written at `o` meets the batch's table or offsets
+bool over_batch(const PagedArgs &a, const void *o, int64_t bytes) {
+  if (a.max_pages > 0 &&
+      meet(o, bytes, a.table, 4 * ((a.B - 1) * a.table_stride + a.max_pages)))
+    return true;
+  return a.cu && meet(o, bytes, a.cu, 4 * ((int64_t)a.B + 1));
+}
+
 // workspace of an eviction: none where no sequence can pass the budget
 size_t evict_bytes(const vq_kivi_paged *p, int B, int max_pages, int budget, int recent) {
   return (int64_t)max_pages * p->page <= budget ? 0
@@ -235,12 +243,9 @@ int check_weights(const vq_kivi_paged *p, const PagedArgs &a, const vq_kivi_weig
   return VQ_OK;
 }
 
-// whether the ranges that two arrays of weights span meet
-bool weights_overlap(const PagedEvict &v, const PagedArgs &a) {
-  auto span = [&](const PagedWeights &w) {
-    return 4 * ((a.B - 1) * w.seq + (a.H_kv - 1) * w.head + w.capacity);
-  };
-  return meet(v.in.at, span(v.in), v.out.at, span(v.out));
+// bytes that an array of weights spans
+int64_t span(const PagedWeights &w, const PagedArgs &a) {
+  return 4 * ((a.B - 1) * w.seq + (a.H_kv - 1) * w.head + w.capacity);
 }
 
 // what the three attentions share; tree: masks, weights: where weights are added
@@ -463,8 +468,14 @@ int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
   if (!aligned(path, 4) || !aligned(counts, 4) || !aligned(lens_out, 4))
     return fail(VQ_ERR_ARG, "int32 arrays must be 4-byte aligned");
   // (in place a sequence's length is read and written by one CTA)
-  if (lens_out != a.lens && meet(lens_out, 4 * (int64_t)a.B, a.lens, 4 * (int64_t)a.B))
+  const int64_t bytes = 4 * (int64_t)a.B;
+  if (lens_out != a.lens && meet(lens_out, bytes, a.lens, bytes))
     return fail(VQ_ERR_ARG, "lens_out overlaps lens (it may be the same array)");
+  // (so are the counts)
+  if ((lens_out != counts && meet(lens_out, bytes, counts, bytes)) ||
+      (a.tokens > 0 && meet(lens_out, bytes, path, 4 * a.tokens)) ||
+      over_batch(a, lens_out, bytes))
+    return fail(VQ_ERR_ARG, "lens_out overlaps what other sequences' CTAs read");
   cudaError_t e = launch_paged_keep(a, path, counts, lens_out, p->D, (cudaStream_t)stream);
   return e == cudaSuccess ? VQ_OK : cuda_fail(e, "paged keep launch");
 }
@@ -496,13 +507,21 @@ int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch
   if (a.B == 0) return VQ_OK;
   if (v.in.at == v.out.at ? v.in.seq != v.out.seq || v.in.head != v.out.head ||
                                 v.in.capacity != v.out.capacity
-                          : weights_overlap(v, a))
+                          : meet(v.in.at, span(v.in, a), v.out.at, span(v.out, a)))
     return fail(VQ_ERR_ARG, "weights_out overlaps weights (it may be the same array)");
   if (!lens_out || !aligned(lens_out, 4))
     return fail(VQ_ERR_ARG, "lens_out is NULL or misaligned");
   // heads read the lengths while another's sequence is done
-  if (meet(lens_out, 4 * (int64_t)a.B, a.lens, 4 * (int64_t)a.B))
+  const int64_t bytes = 4 * (int64_t)a.B;
+  if (meet(lens_out, bytes, a.lens, bytes))
     return fail(VQ_ERR_ARG, "lens_out overlaps lens");
+  // (weights in place, too, change while other heads' CTAs read the batch)
+  const int64_t n = span(v.out, a);
+  if (over_batch(a, lens_out, bytes) || meet(lens_out, bytes, v.in.at, span(v.in, a)) ||
+      meet(lens_out, bytes, v.out.at, n))
+    return fail(VQ_ERR_ARG, "lens_out overlaps another array of the call");
+  if (over_batch(a, v.out.at, n) || meet(v.out.at, n, a.lens, bytes))
+    return fail(VQ_ERR_ARG, "weights_out overlaps the batch's arrays");
   const size_t need = evict_bytes(p, a.B, a.max_pages, budget, recent);
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return fail(VQ_ERR_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
@@ -540,15 +559,24 @@ int vq_kivi_verify_drafts(const vq_kivi_drafts *d, int dtype, int32_t *path, int
       !aligned(after, wide) || !aligned(d->parent, 4) || !aligned(d->cu_new, 4) ||
       !aligned(d->uniforms, 4) || !aligned(path, 4) || !aligned(counts, 4))
     return fail(VQ_ERR_ARG, "misaligned pointer");
-  // the CTAs of a sequence read its nodes each for itself
+  // the CTAs of a sequence read its nodes and rows each for itself
+  auto rows = [&](const void *p, int64_t row) {
+    return p && d->tokens > 0 ? elem * ((d->tokens - 1) * row + d->V) : (int64_t)0;
+  };
   const struct { const void *at; int64_t bytes; } outs[3] = {
       {path, 4 * d->tokens}, {counts, 4 * (int64_t)d->B}, {after, wide * (int64_t)d->B}},
-      ins[4] = {{d->token, wide * d->tokens}, {d->parent, d->parent ? 4 * d->tokens : 0},
-                {d->uniforms, 4 * d->tokens}, {d->cu_new, 4 * ((int64_t)d->B + 1)}};
-  for (const auto &o : outs)
+      ins[6] = {{d->token, wide * d->tokens}, {d->parent, d->parent ? 4 * d->tokens : 0},
+                {d->uniforms, 4 * d->tokens}, {d->cu_new, 4 * ((int64_t)d->B + 1)},
+                {d->target, rows(d->target, d->target_row)},
+                {d->draft, rows(d->draft, d->draft_row)}};
+  for (const auto &o : outs) {
     for (const auto &i : ins)
       if (o.bytes > 0 && i.bytes > 0 && meet(o.at, o.bytes, i.at, i.bytes))
         return fail(VQ_ERR_ARG, "an output overlaps an input");
+    for (const auto &x : outs)
+      if (&x != &o && o.bytes > 0 && x.bytes > 0 && meet(o.at, o.bytes, x.at, x.bytes))
+        return fail(VQ_ERR_ARG, "two outputs overlap");
+  }
   if ((rc = sm_count(&sms))) return rc;
   Drafts x;
   x.target = d->target;

@@ -610,7 +610,8 @@ size_t vq_kivi_paged_weights_workspace_bytes(const vq_kivi_paged *p, int32_t B,
  * among them; the others then begin at place 0.)
  *   path           device int32 [tokens]
  *   counts         device int32 [B]
- *   lens_out       device int32 [B], lens itself or apart from it
+ *   lens_out       device int32 [B], lens itself (or counts) or apart from the
+ *                  other arrays of the call
  * At most 64 new tokens per sequence.  A sequence whose path does not rise
  * within its new tokens, or whose count is outside its range (a count of -1
  * among them), is left as it was, and reported by vq_kivi_paged_status. */
@@ -633,7 +634,7 @@ int vq_kivi_paged_keep(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
  *   batch          cu_new NULL, tokens = B; lens: all tokens
  *   weights_out    as weights; the same array (in place) or one that does not
  *                  overlap it
- *   lens_out       device int32 [B], not lens
+ *   lens_out       device int32 [B], apart from the other arrays of the call
  *   workspace      device, 16-byte aligned */
 int vq_kivi_paged_evict(const vq_kivi_paged *p, const vq_kivi_paged_batch *batch,
                         const vq_kivi_weights *weights,
@@ -685,9 +686,10 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
  * path int32 [tokens]: from row cu_new[b] on the nodes that stay, node 0 first,
  * -1 behind them; counts int32 [B]: how many (vq_kivi_paged_keep takes both);
  * after [B], in the tokens' type: the last token, -1 where a row has no
- * positive probability.  Outputs may not overlap the nodes' arrays.  A sequence without nodes gets a count of 0 and -1; one
- * whose offsets, parents or tokens lie outside their ranges, or with more than
- * 64 nodes, a count of -1, -1, and -1 in its path where its rows are in range.
+ * positive probability.  Outputs may overlap neither an input nor one another.
+ * A sequence without nodes gets a count of 0 and -1; one whose offsets, parents
+ * or tokens lie outside their ranges, or with more than 64 nodes, a count of
+ * -1, -1, and -1 in its path where its rows are in range.
  * B <= 1024, V <= 2^19. */
 typedef struct vq_kivi_drafts {
   const void *target, *draft;

@@ -105,6 +105,42 @@ def test_keep_lengths_half_over(vqlib):
     assert b"overlaps" in vqlib.vq_kivi_last_error()
 
 
+@pytest.mark.parametrize("lens_out", ["path", "path end", "half counts", "cu_new", "table"])
+def test_keep_lengths_over_what_others_read(vqlib, lens_out):
+    """A sequence's CTA writes its length while others read theirs."""
+    at = dict(path=4 * P, counts=5 * P, cu_new=6 * P, table=7 * P)
+    at.update({"path end": at["path"] + 28, "half counts": at["counts"] + 4})
+    b = _batch(cu_new=at["cu_new"], tokens=8, lens=2 * P, table=at["table"])
+    out = at[lens_out] + (24 if lens_out == "table" else 0)
+    assert vqlib.vq_kivi_paged_keep(_paged(), b, at["path"], at["counts"], out, None) == -1
+    assert b"overlaps" in vqlib.vq_kivi_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lens_out=7 * P + 24), dict(lens_out=P + 1024), dict(lens_out=4 * P),
+    dict(w_out=7 * P - 1000), dict(w_out=2 * P - 2048), dict(w_out=P, w=P, lens=P + 64),
+])
+def test_evict_outputs_over_the_batch(vqlib, kw):
+    """The CTAs of other heads and sequences read the table, the lengths and their
+    weights while one is done."""
+    a = dict(lens_out=3 * P, w=P, w_out=4 * P, lens=2 * P)
+    a.update(kw)
+    b = _batch(table=7 * P, lens=a["lens"])
+    rc = vqlib.vq_kivi_paged_evict(_paged(), b, _weights(at=a["w"]), _weights(at=a["w_out"]), 100, 8,
+                                   2, a["lens_out"], 9 * P, 1 << 30, None)
+    assert rc == -1 and b"overlaps" in vqlib.vq_kivi_last_error()
+
+
+@pytest.mark.parametrize("path,counts,after", [
+    (9 * P, 9 * P + 28, 4 * P), (9 * P, 4 * P, 9 * P + 24), (4 * P, 9 * P, 9 * P), # one another
+    (11 * P, 2 * P, 3 * P), (2 * P, 12 * P + 4 * 250, 3 * P), (2 * P, 3 * P, 11 * P + 4 * 799 - 4),
+])
+def test_verify_outputs_over_rows_and_one_another(vqlib, path, counts, after):
+    d = _drafts(token=P, parent=P + 64, uniforms=P + 96, cu_new=P + 128, target=11 * P, draft=12 * P)
+    rc = vqlib.vq_kivi_verify_drafts(d, 2, path, counts, after, None)
+    assert rc == -1 and (b"overlap" in vqlib.vq_kivi_last_error())
+
+
 @pytest.mark.parametrize("which", ["path", "counts", "lens_out", "odd"])
 def test_keep_refusals(vqlib, which):
     b = _batch(cu_new=P, tokens=8)

@@ -447,6 +447,23 @@ def test_keep(D, g, page, H_kv):
     assert torch.equal(c.pool.cpu(), dref.move_tokens(before, table, D, g, moves))
 
 
+def test_keep_lengths_into_the_counts():
+    """The counts' own array may take the lengths; neighbours of one buffer are
+    apart."""
+    c, table, L = filled([20, 30, 9], 16, 2, 2, 64, 32)
+    n, path, counts = [4, 6, 5], [0, 2, -1, -1, 0, 1, 5, -1, -1, -1, 0, 4, -1, -1, -1], [2, 3, 2]
+    before = c.pool.clone()
+    want = c.keep(table, L, offsets(n), i32(path), i32(counts))
+    pool = c.pool.clone()
+    buffer = torch.cat((L, i32([0] * 3), i32(counts), offsets(n), i32(path)))
+    lens, lens_out, k, cu, p = buffer.split([3, 3, 3, 4, 15])
+    for out in (lens_out, k):
+        c.pool.copy_(before)
+        assert torch.equal(c.keep(table, lens, cu, p, k, lens_out=out), want)
+        assert torch.equal(c.pool, pool)
+    c.status()
+
+
 @pytest.mark.parametrize("path,count", [
     ([0, 2, 2, 3], 4), ([0, 3, 1, 2], 3), ([0, 1, 2, 4], 4), ([-1, 0, 1, 2], 2), ([0, 1, 2, 3], 5),
     ([0, 1, 2, 3], -1),
