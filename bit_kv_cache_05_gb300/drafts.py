@@ -65,7 +65,9 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Te
     parents   int32 [rows]: a node's parent in its sequence, below it; None:
               chains
     draft     [rows][V], target's type: what the children of a node were drawn
-              from, one by one; None: the drafts stand for themselves
+              from, each independently of the others (torch.multinomial needs
+              replacement=True for it); None: the drafts stand for themselves
+              (the draft's best tokens, or tokens drawn without replacement)
 
     Returns (path, counts, after): int32 [rows] the nodes that stay, node 0
     first, -1 behind them; int32 [B] how many; [B] the token behind them in the

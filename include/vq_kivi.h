@@ -660,9 +660,11 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
  *   target      [tokens][V] in fp16, bf16 or fp32: row of node i = the target's
  *               probabilities of the token behind it
  *   draft       likewise the distribution that the children of node i were
- *               drawn from, one by one; rows of nodes without children are not
- *               read.  NULL: the drafts stand for themselves (the draft's best
- *               tokens, say), whatever their probabilities were
+ *               drawn from, each independently of the others (with
+ *               replacement: the same token may come twice); rows of nodes
+ *               without children are not read.  NULL: the drafts stand for
+ *               themselves (the draft's best tokens, say, or tokens drawn
+ *               without replacement), whatever their probabilities were
  *   token       int32 or (token_64) int64 [tokens]: tokens of the nodes (node
  *               0's is not read), in [0, V)
  *   parent      int32 [tokens]: a node's parent, below it (node 0's is not
@@ -681,7 +683,8 @@ int vq_kivi_paged_status(const vq_kivi_paged *p, void *stream);
  * whose running sum passes uniforms[0] times the sum.  Sums are whole numbers
  * of 2^-44 (each value rounded once, at most 1), and a uniform is cut to 31
  * bits for the last draw: results do not depend on any order of summation.
- * Tokens that follow the target's distribution follow, whatever the draft's is.
+ * Tokens that follow the target's distribution follow, whatever the draft's is;
+ * not, with a draft, where a child's draw depended on its siblings'.
  *
  * path int32 [tokens]: from row cu_new[b] on the nodes that stay, node 0 first,
  * -1 behind them; counts int32 [B]: how many (vq_kivi_paged_keep takes both);

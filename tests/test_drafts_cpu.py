@@ -232,6 +232,52 @@ def test_residuals_of_residuals_are_one_difference():
             assert r == [x / S for x in w]
 
 
+@pytest.mark.parametrize("kids", [1, 2, 3])
+def test_independent_children_follow_the_target(kids):
+    """The walk's rule over all draws of a root's children, in exact fractions:
+    children drawn independently leave the target's distribution, children drawn
+    without replacement do not (from the second on); without a draft any children
+    leave it."""
+    rng = random.Random(5)
+    V = 4
+    p, q = ([Fraction(rng.randrange(1, 30)) for _ in range(V)] for _ in range(2))
+    p, q = [x / sum(p) for x in p], [x / sum(q) for x in q]
+
+    def first(with_draft, replacement):
+        out = [Fraction(0)] * V
+
+        def walk(prob, k, drawn, c, S, gone):
+            w = [max(a - c * b, 0) if with_draft else 0 if x in gone else a
+                 for x, (a, b) in enumerate(zip(p, q))]
+            if k == kids or sum(w) == 0:
+                for x in range(V):
+                    out[x] += prob * w[x] / sum(w) if sum(w) else prob * p[x]
+                return
+            rest = 1 if replacement else 1 - sum(q[x] for x in drawn)
+            for x in range(V):
+                if not replacement and x in drawn:
+                    continue
+                pick = prob * q[x] / rest
+                # accepted if u q(x) S < w(x), or u S < w(x)
+                yes = min(1, w[x] / (q[x] * S if with_draft else S))
+                out[x] += pick * yes
+                if yes == 1:
+                    continue
+                if with_draft:
+                    c2 = c + S
+                    S2 = sum(max(a - c2 * b, 0) for a, b in zip(p, q))
+                    walk(pick * (1 - yes), k + 1, drawn | {x}, c2, S2, gone)
+                else:
+                    walk(pick * (1 - yes), k + 1, drawn | {x}, c, S - w[x], gone | {x})
+
+        walk(Fraction(1), 0, frozenset(), Fraction(0), Fraction(1), frozenset())
+        return out
+
+    assert first(True, True) == p
+    assert (first(True, False) == p) == (kids == 1)
+    assert first(False, True) == p and first(False, False) == p
+
+
 def test_whole_numbers_in_two_halves():
     """The kernel's way to a whole number of 2^-44, in steps of fp32: floor(w
     2^22) beside 2^23, then the rest rounded to 2^-22 of it, is the value
