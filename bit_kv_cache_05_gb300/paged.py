@@ -201,7 +201,10 @@ class PagedKiviCache:
         weights: fp32 [B][H_kv][>= max_pages * page] (rows may be strided):
         each stored token's softmax weights, summed over the new tokens and the
         query heads of its kv head, are added to its place.  At most 16 (new
-        token, query head) pairs per kv head; not with a tree."""
+        token, query head) pairs per kv head; not with a tree.  Such a call
+        allocates 4 bytes for each of these pairs and each place that the tables
+        have room for (64 sequences, 8 kv heads, 4 query heads each, tables of
+        131072 places: 1 GiB), so cut the table to the pages in use."""
         if self._elsewhere(stream):
             with _on(self.device, stream):
                 return self.attend(q, table, lens, cu_new, max_new=max_new, tree=tree,
@@ -360,6 +363,7 @@ class PagedKiviCache:
 
     def status(self):
         """Raise if a kernel since the last check found a page or a length
-        outside its range, or gave up a wait (synchronizes)."""
+        outside its range, or a path of kept tokens outside its tree, or gave up
+        a wait (synchronizes)."""
         with torch.cuda.device(self.device):
             _lib.check(self._lib.vq_kivi_paged_status(self._spec, _raw_stream(self._index)))

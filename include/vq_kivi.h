@@ -598,7 +598,10 @@ int vq_kivi_paged_attend_weights(const vq_kivi_paged *p,
                                  int32_t max_new, float softmax_scale,
                                  void *workspace, size_t workspace_bytes,
                                  void *stream);
-/* Its workspace (0 on an error). */
+/* Its workspace (0 on an error): the scores of every place that the tables have
+ * room for are kept from the attention to the sums, B * H_kv * max_pages * page
+ * * max_new * H_q / H_kv * 4 bytes, whatever the lengths; cut the tables to the
+ * pages in use.  (vq_kivi_paged_attend's depends on B and max_new alone.) */
 size_t vq_kivi_paged_weights_workspace_bytes(const vq_kivi_paged *p, int32_t B,
                                              int32_t max_pages,
                                              int32_t max_new);
@@ -646,7 +649,8 @@ size_t vq_kivi_paged_evict_workspace_bytes(const vq_kivi_paged *p, int32_t B,
                                            int32_t recent);
 
 /* Synchronizes `stream` and reports what kernels found since the last check:
- * VQ_ERR_ARG for a page or a length outside its range, VQ_ERR_CUDA for a wait
+ * VQ_ERR_ARG for a page or a length outside its range or a path of kept tokens
+ * outside its tree, VQ_ERR_CUDA for a wait
  * that gave up; the message names all that was found.  What is reported is
  * then cleared from the word, and nothing else: what a kernel of another
  * stream finds meanwhile is left for the next check. */
