@@ -799,8 +799,7 @@ k_paged_chunk(PagedArgs a, PagedAttend t, float *part, float *swap, CutPair *cut
     }
   } else if (warp < R::ISSUE) {
     // ---- k_hat, v_hat ----
-    if constexpr (SMALL) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // keys or values, block of a stage
     const int kv = (warp - R::SOFT) / R::BUILD, w = (warp - R::SOFT) % R::BUILD, n8 = lane >> 2,
               t4 = lane & 3;
