@@ -265,6 +265,48 @@ def test_verify_large_vocabulary_strided_rows(with_draft):
             assert int(got[2][b]) == token
 
 
+@pytest.mark.parametrize("dtype,B,n,V,with_draft,kids", [
+    ("fp32", 1, 2, 2 ** 19, True, 1), ("fp32", 1, 3, 2 ** 19 - 3, False, 2),
+    ("bf16", 1, 2, 2 ** 19, True, 1), ("fp16", 3, 3, 2 ** 19 - 5, True, 2),
+    ("fp32", 320, 2, 40001, True, 1), ("fp16", 320, 2, 70001, False, 1),
+])
+def test_verify_large_slices(dtype, B, n, V, with_draft, kids):
+    """Pieces of a warp of more than 16 steps (sums start anew there), and last
+    draws in the second step of a warp's run and behind: the largest vocabulary
+    over eight CTAs, and one CTA a sequence.  Rows start off a 16-byte boundary
+    where V is odd."""
+    from bit_kv_cache_05_gb300 import verify_drafts
+    dt, T = DT[dtype], B * n
+    p = torch.empty(T, V, dtype=dt, device="cuda")
+    q = torch.empty_like(p) if with_draft else None
+    for a in range(0, T, 64):
+        logits = 2 * randn(100 + a, min(64, T - a), V)
+        p[a:a + 64] = torch.softmax(logits, -1).to(dt)
+        if with_draft:
+            q[a:a + 64] = torch.softmax(logits + randn(900 + a, *logits.shape), -1).to(dt)
+    rng = random.Random(V)
+    parents = ([-1] + [0] * kids + [1])[:n] * B
+    tokens = [rng.randrange(V) for _ in range(T)]
+    u = torch.rand(T, generator=torch.Generator().manual_seed(V))
+    u[1::n] = 0.999 if with_draft else 0.5             # most first children are rejected
+    if B == 1:
+        uniforms = [0.0, 0.03, 0.31, 0.77, 0.99999994]
+    else:
+        uniforms = [None]
+    for u0 in uniforms:
+        if u0 is not None:
+            u[0] = u0
+        path, counts, after = verify_drafts(p, i64(tokens), u.cuda(), offsets([n] * B),
+                                            parents=i32(parents), draft=q)
+        for b in range(B):
+            s = slice(b * n, b * n + n)
+            want, token = dref.verify(p[s].float().cpu().numpy(),
+                                      q[s].float().cpu().numpy() if with_draft else None,
+                                      tokens[s], parents[s], u[s].numpy())
+            assert path[s].tolist() == want + [-1] * (n - len(want)), b
+            assert int(counts[b]) == len(want) and int(after[b]) == token, b
+
+
 def test_verify_rows_without_mass_and_odd_values():
     """Rows of zeros, NaN, infinities and values above one; drafts equal to the
     target (rejections leave nothing); uniforms at their ends."""
@@ -723,6 +765,97 @@ def test_evict_strides_bad_pages_and_lengths():
             take = dref.evict_row(w[b, h].cpu(), 60, 30, 8, 2)
             moves += [(b, h, i, t) for i, t in enumerate(take) if i != t and not (b == 1 and t >= 48)]
     assert torch.equal(c.pool.cpu(), dref.move_tokens(before, table, 64, 32, moves))
+
+
+def evict_by_sorting(w, lens, budget, recent, first):
+    """The token of each place of every row [B][H_kv][budget], by a stable sort
+    (dref.evict_row says the same; a test compares them)."""
+    K, t = budget - recent, torch.arange(w.shape[-1], device=w.device)
+    hi = (lens.long() - recent)[:, None, None]
+    candidate = (t >= first) & (t < hi)
+    # NaN lowest, below -infinity; behind both what does not compete
+    size = torch.where(torch.isnan(w), -math.inf, w.double() + 0.0)
+    one = torch.sort(size, dim=-1, descending=True, stable=True)[1]
+    group = torch.where(candidate, torch.isnan(w).long(), 2).gather(-1, one)
+    order = one.gather(-1, torch.sort(group, dim=-1, stable=True)[1])
+    rank = torch.empty_like(order).scatter_(-1, order, t.expand_as(order))
+    stays = candidate & (rank < K - first) | (t < first)
+    hole = ~stays & (t < K)
+    source = torch.sort((~(stays & (t >= K))).to(torch.uint8), dim=-1, stable=True)[1]
+    take = torch.where(hole, source.gather(-1, (hole.cumsum(-1) - 1).clamp(min=0)), t)
+    return torch.where(t < K, take, hi - K + t)[..., :budget]
+
+
+def test_evictions_of_the_references_agree():
+    for kind in ("plain", "ties", "equal", "wild"):
+        w = evict_weights([0, 0], 3, 90, kind)
+        lens = [90, 71]
+        got = evict_by_sorting(w, i32(lens), 50, 17, 3)
+        for b, S in enumerate(lens):
+            for h in range(3):
+                assert got[b, h].tolist() == dref.evict_row(w[b, h].cpu(), S, 50, 17, 3)
+
+
+# What a row is shared by: rows of up to 1536 places, and longer ones of at least
+# eight per SM or of which few tokens go, take one CTA of 256 threads; others a
+# cluster of at most eight CTAs of 512, as many as there are SMs for and 1024
+# places each.
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "wild"])
+@pytest.mark.parametrize("ctas,rows,S,budget,recent,first,D,g", [
+    (2, 4, 2000, 900, 100, 4, 128, 32), (4, 4, 4000, 1500, 300, 0, 128, 64),
+    (8, 2, 9000, 2500, 64, 4, 128, 32), (8, 2, 8100, 8000, 6000, 3, 128, 128),
+    (2, "3/4", 5000, 600, 0, 0, 128, 32), (4, "3/8", 5000, 600, 77, 2, 64, 64),
+    (1, "2", 1800, 500, 33, 1, 64, 32), (1, "9", 1700, 400, 20, 4, 64, 64),
+    (1, 3, 5000, 4993, 64, 4, 128, 32),
+])
+def test_evict_over_clusters(kind, ctas, rows, S, budget, recent, first, D, g):
+    """Clusters of two, four and eight and the forms of one CTA, at ties, equal
+    weights, NaN and infinities: the order of equal weights crosses CTAs."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H = 2
+    if isinstance(rows, str):                          # rows by the number of SMs
+        a, _, b = rows.partition("/")
+        rows = int(sms * int(a) / int(b or 1)) // H * H
+    B, page = rows // H if rows % H == 0 else rows, 128
+    H = rows // B
+    lens = [S - b % 7 for b in range(B)]
+    need = sum(-(-s // page) for s in lens)
+    c = new_cache(need + 2, page, H, H, D, g, 0)
+    c.pool.view(-1)[:] = torch.randint(0, 256, (c.pool.numel(),), dtype=torch.uint8, device="cuda",
+                                       generator=torch.Generator("cuda").manual_seed(S))
+    # (random bytes: scales may be NaN, so compare the rows' bits)
+    table, L = ref.make_table(B, lens, page, need + 2, "cuda", 1), i32(lens)
+    w = evict_weights(lens, H, table.shape[1] * page, kind)
+    before = c.pool.clone()
+
+    def rows_of(pool, place):
+        """The 16-bit parts of tokens place [B][H][n], in one order."""
+        ng, I, t = D // g, D // 32, torch.arange(16, device="cuda")[:, None]
+        x = torch.arange(D // 4, device="cuda")
+        m = torch.arange(2 * ng, device="cuda")
+        meta = 4 * D + (t // 2 * ng + m // 2) * 4 + 2 * (m % 2) + t % 2
+        value = 2 * (((8 * (t // 8) + x // I) * 4 + t % 8 // 2) * I + x % I) + t % 2
+        half = 4 * D + 32 * ng
+        parts = torch.cat((t * (D // 4) + x, meta, half + value, half + meta), 1)
+        b = torch.arange(B, device="cuda")[:, None, None]
+        h = torch.arange(H, device="cuda")[:, None]
+        blk = (table[b, place // page].long() * H + h) * (page // 16) + place % page // 16
+        at = blk[..., None] * (pool.shape[-1] // 2) + parts[place % 16]
+        return pool.view(torch.int16).view(-1)[at]
+
+    take = evict_by_sorting(w, L, budget, recent, first)
+    places = torch.arange(budget, device="cuda").expand_as(take)
+    want = rows_of(before, take)
+    for in_place in (False, True):
+        c.pool.copy_(before)
+        w0 = w.clone()
+        lens_out, wo = c.evict(table, L, w, budget, recent=recent, first=first,
+                               weights_out=w if in_place else None)
+        c.status()
+        assert (lens_out == budget).all()
+        assert torch.equal(rows_of(c.pool, places), want)
+        assert same_floats(wo[..., :budget], w0.gather(-1, take))
+        assert (wo[..., budget:] == 0).all()
 
 
 @pytest.mark.parametrize("budget", [30, 64])
