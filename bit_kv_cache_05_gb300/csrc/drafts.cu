@@ -374,8 +374,8 @@ k_verify(Drafts d) {
 }
 
 // CTAs of a cluster: as many as keep the SMs busy.  64 sequences of V = 131072,
-// 4 CTAs of 512 threads each: 21.6 us; 2: 30.0, 8: 28.5; 4 of 1024: 31.1, 8 of
-// 256: 21.6 (where 16 trees of V = 100003 take 23.5 us, 21.0 with 512).
+// 4 CTAs of 512 threads each: 21.6 us; 2: 30.0, 8: 28.5; 4 of 1024: 31.1; 8 of 256
+// the same 21.6, but 16 trees of V = 100003 then take 23.5 us, with 512 21.0.
 int verify_cluster(int B, int sm_count) {
   int c = 1;
   while (c < 8 && B * c * 2 <= 2 * sm_count) c *= 2;

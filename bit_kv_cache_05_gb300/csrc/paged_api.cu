@@ -206,13 +206,13 @@ bool overlap(const HeadRows &h, int64_t tokens, int D, int elem) {
 // products take; there it is the faster one at both head sizes.  Replayed
 // graphs, 8 kv heads, cold caches, split-KV against tensor-memory kernel, us:
 //   D = 128     1 x 1024     1 x 32768    16 x 8192     64 x 2048
-//   8 rows     15.5 / 23.7   33.9 / 49.3   56.5 / 118   62.6 / 148
-//   16 rows    19.6 / 23.7   35.9 / 51.4   65.7 / 117   75.9 / 150
-//   20, 32        23.7, 25      53, 56      120, 120     151, 153
+//   8 rows     16.5 / 23.7   34.0 / 51.4   57.5 / 115   62.6 / 169
+//   16 rows    19.6 / 25.7   36.0 / 54.4   66.7 / 117   76.9 / 171
+//   20, 32      25.7, 25.8    54.4, 57.5    117, 118     173, 174
 //   D = 64
-//   8 rows     15.5 / 19.6   25.8 / 44.1   40.1 / 108   44.2 / 128
-//   16 rows    17.5 / 21.6   29.8 / 44.2   46.2 / 108   56.4 / 128
-//   20, 32        21.6, 22      46, 46      107, 109     128, 129
+//   8 rows     16.5 / 20.6   27.8 / 44.2   42.1 / 104   46.2 / 127
+//   16 rows    18.6 / 21.6   29.9 / 44.2   48.3 / 104   58.5 / 127
+//   20, 32      20.6, 21.7    44.2, 44.3    104, 104     128, 128
 bool few_rows(const vq_kivi_paged *p, int max_new) {
   return (int64_t)max_new * (p->H_q / p->H_kv) <= 16;
 }

@@ -453,15 +453,26 @@ cudaError_t evict_t(const PagedArgs &a, const PagedEvict &v, int cluster, cudaSt
   return e;
 }
 
-// Short rows, and longer ones of which few tokens go, take one CTA of few
-// threads: no barriers of a cluster.  Others are shared by as many CTAs as there
-// is room for.  One CTA of 256 threads against clusters of up to 8 of 512, with
-// the read-back, us (8 kv heads of D = 128):
+// Short rows, longer ones of which few tokens go, and any when there are many
+// take one CTA of few threads: no barriers of a cluster, and four on an SM.
+// Others are shared by as many CTAs as there is room for.  One CTA of 256 threads
+// against clusters of up to 8 of 512 (one of 512 from 256 rows on), with the
+// read-back, us (8 kv heads of D = 128; tables as long as the sequences):
 //             1025 > 1024  1025 > 512  2049 > 2048  2049 > 1024  4097 > 4096  4097 > 2048
-//   8 rows    10.5 / 15.1  15.6 / 16.1  12.6 / 16.8  23.9 / 17.2  17.3 / 18.8  41.6 / 18.6
-//   64 rows   15.4 / 20.3  18.5 / 19.3  24.6 / 30.7  32.6 / 27.6  46.0 / 48.7  64.3 / 42.2
-//   256 rows  42.2 / 43.8  37.2 / 37.3  73.3 / 74.1  65.0 / 63.4   128 / 127    119 / 116
+//   8 rows     9.0 / 13.0  16.1 / 16.7  11.1 / 14.0  24.6 / 17.7  14.6 / 15.7  42.5 / 19.0
+//   64 rows   18.4 / 22.0  21.1 / 20.8  25.8 / 31.6  36.2 / 30.5  44.0 / 46.6  65.9 / 44.4
+//   256 rows  41.2 / 42.4  38.5 / 38.5  71.9 / 72.4  66.1 / 64.3   125 / 125    120 / 117
+//   608       84.6 / 91.7  73.3 / 76.8   149 / 154    135 / 136    276 / 281    254 / 253
+//   1216       156 / 171    136 / 145    283 / 296    253 / 255    540 / 551    483 / 479
+//   2432       300 / 327    255 / 277    553 / 578    478 / 486
 // (at 8193 > 8192, 8 rows: 26.5 / 21.4)
+// The rule goes by the tables' room, as the host does not know the lengths.  Tables
+// of 131072 places take the cluster below 8 rows an SM, which their weights want in
+// any case: all places behind the budget are cleared.
+//             513 > 512    1025 > 1024  1025 > 512   2049 > 2048  4097 > 2048
+//   8 rows    16.8 / 13.5  17.4 / 14.0  23.5 / 16.2  18.9 / 14.8  50.5 / 19.7
+//   64 rows   23.1 / 24.6  26.2 / 28.3  30.6 / 27.9  35.8 / 36.7  74.4 / 48.2
+//   256 rows  47.3 / 48.1  61.9 / 62.2  60.7 / 60.1  90.2 / 89.7   144 / 138
 template <int D, int NG>
 cudaError_t evict_d(const PagedArgs &a, const PagedEvict &v, int sm_count, cudaStream_t st) {
   const int64_t rows = (int64_t)a.B * a.H_kv;
