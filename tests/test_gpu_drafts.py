@@ -983,6 +983,75 @@ def test_captured_eviction_loop():
     assert 0 < float(acc.sum()) <= 5 * B * H_q + 1e-3
 
 
+def test_captured_speculative_step():
+    """Append, tree attention, verification and the kept path in one graph: replayed
+    with other lengths, tables, trees, offsets and rows it gives what the calls
+    give one by one."""
+    from bit_kv_cache_05_gb300 import verify_drafts
+    from bit_kv_cache_05_gb300.rope import Rope
+    B, H_q, H_kv, D, page, V, T, most = 3, 8, 2, 64, 16, 501, 40, 24
+    c, rope = new_cache(64, page, H_q, H_kv, D, 32, fill=0), Rope(rot_dim=D)
+    rng = random.Random(12)
+    pool0 = c.pool.random_(0, 256).clone() & 0x3f       # finite scales
+
+    def inputs(seed):
+        n = [rng.randrange(1, most) if seed else 13 for _ in range(B)]
+        while sum(n) > T:
+            n = [max(1, x - 1) for x in n]
+        lens = [rng.randrange(0, 200) for _ in range(B)]
+        pages = rng.sample(range(64), 3 * 14)
+        p, q, tokens, parents, u = draft_case(70 + seed, n, V, "fp32", False, True)
+        trees, at = [], 0
+        for k in n:
+            trees.append(parents[at:at + k])
+            at += k
+        pad = lambda x, v: list(x) + [v] * (T - len(x))
+        rows = lambda x: torch.cat((x, torch.zeros(T - len(x), V))).cuda()
+        x = randn(80 + seed, T, H_q + 2 * H_kv, D).half()
+        seq = [b for b, k in enumerate(n) for _ in range(k)]
+        return dict(table=i32(pages).view(B, 14), lens=i32([a + k for a, k in zip(lens, n)]),
+                    cu=offsets(n), masks=i64(pad([m for t in trees for m in dref.masks_of(t)], 0)),
+                    pos=i32(pad([lens[seq[i]] + d for i, d in enumerate(
+                        d for t in trees for d in dref.depths_of(t))], 0)),
+                    q=x[:, :H_q].contiguous(), k=x[:, H_q:H_q + H_kv].contiguous(),
+                    v=x[:, H_q + H_kv:].contiguous(), p=rows(p), d=rows(q),
+                    tokens=i64(pad(tokens, 0)), parents=i32(pad(parents, 0)),
+                    u=torch.cat((u, torch.zeros(T - len(u)))).cuda())
+
+    def step(s):
+        q = c.append(s["k"], s["v"], s["table"], s["lens"], s["cu"], q=s["q"], rope=rope,
+                     positions=s["pos"], q_out=torch.zeros_like(s["q"]))
+        out = c.attend(q, s["table"], s["lens"], s["cu"], max_new=most, tree=s["masks"],
+                       out=torch.zeros_like(q))
+        path, counts, after = verify_drafts(s["p"], s["tokens"], s["u"], s["cu"],
+                                            parents=s["parents"], draft=s["d"],
+                                            path=torch.full_like(s["parents"], -1))
+        return out, path, counts, after, c.keep(s["table"], s["lens"], s["cu"], path, counts)
+
+    held = inputs(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(held)
+    torch.cuda.current_stream().wait_stream(side)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = step(held)
+    for seed in range(1, 6):
+        new = inputs(seed)
+        for k, t in new.items():
+            held[k].copy_(t)
+        c.pool.copy_(pool0)
+        gr.replay()
+        graph = [t.clone() for t in got] + [c.pool.clone()]
+        c.pool.copy_(pool0)
+        one = list(step(new)) + [c.pool.clone()]
+        c.status()
+        for x, y in zip(graph, one):
+            assert torch.equal(x, y)
+        assert torch.isfinite(one[0].float()).all()
+
+
 def test_other_streams_and_repeatable():
     """On a stream given by argument, the same bits as on the current one."""
     c, table, L = filled([300, 200], 16, 8, 2, 128, 32)
